@@ -295,6 +295,107 @@ dpnorm_status dpnorm_exact(const void* A, const void* G, dpnorm_dtype dt, int64_
  * finite and > 0. c == n (in place) is allowed; other overlap is an error. */
 dpnorm_status dpnorm_clip_factors(const float* n, int64_t B, float C, float* c, hipStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Around the linear layers of a training step: the embedding table (lookup,
+ * per-sample norm, gradient) and causal attention (forward, backward).
+ *
+ * The conventions above hold: device pointers, no allocation, everything
+ * enqueued on `stream`, host checks before anything is enqueued, results
+ * bitwise reproducible (no floating-point atomics).
+ * ------------------------------------------------------------------------- */
+typedef enum dpnorm_index {
+  DPNORM_I32 = 0,
+  DPNORM_I64 = 1,
+  DPNORM_INDEX_RANGE_MIN_ = -2147483647 - 1,
+  DPNORM_INDEX_RANGE_MAX_ = 2147483647
+} dpnorm_index;
+
+/* Scaled embedding lookup: out[q] = scale * W[tok[q]] for q < N, rounded once
+ * to the element type. tok [N] (int32 or int64, aligned to its size), W
+ * [V][d], out [N][d] of type dt, 16-byte aligned; d a multiple of 8 (bf16) or
+ * 4 (fp32). An id outside [0, V) has no row: its out row is zero. N and V in
+ * 1 .. 2^30. scale must be finite. out must not overlap tok or W. */
+dpnorm_status dpnorm_embed_lookup(const void* tok, dpnorm_index it, const void* W, dpnorm_dtype dt, int64_t N,
+                                  int64_t V, int64_t d, float scale, void* out, hipStream_t stream);
+
+/* The order of a batch's ids, which the two calls below read: the positions
+ * i T + t sorted by id, equal ids in position order, positions whose id is
+ * outside [0, V) last. `order` (256-byte aligned, at least order_bytes) is
+ * the caller's and may serve any number of calls on the same tok, B, T and V;
+ * passing it with another B, T or V gives undefined values. ws is scratch of
+ * this call only, and may be NULL when its size is 0. B T and V in 1 .. 2^30. */
+dpnorm_status dpnorm_embed_order_sizes(int64_t B, int64_t T, int64_t V, size_t* order_bytes, size_t* ws_bytes);
+dpnorm_status dpnorm_embed_order(const void* tok, dpnorm_index it, int64_t B, int64_t T, int64_t V, void* order,
+                                 size_t order_bytes, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Exact squared per-sample gradient norm of an embedding table,
+ *   n[i] (+)= scale^2 sum_v || sum_{t: tok[i][t] = v} G[i][t] ||^2,
+ * with G [B][T][d] the gradient of the lookup's output. Row sums are held in
+ * fp32 and each sample's sum over rows in fp64. Positions without a row add
+ * nothing (their G is not read). */
+dpnorm_status dpnorm_embed_norm_workspace(dpnorm_dtype dt, int64_t B, int64_t T, int64_t V, int64_t d, size_t* bytes);
+dpnorm_status dpnorm_embed_norm(const void* order, const void* G, dpnorm_dtype dt, int64_t B, int64_t T, int64_t V,
+                                int64_t d, float scale, float* n, int accumulate, void* ws, size_t ws_bytes,
+                                hipStream_t stream);
+
+/* Gradient of the table, weighted per sample (c float [B], or NULL for 1):
+ *   dW[v] = scale sum_i c[i] sum_{t: tok[i][t] = v} G[i][t],
+ * summed in fp32 and rounded once to dt. accumulate = 0 writes all of dW
+ * [V][d], zeros where an id does not occur; accumulate = 1 adds to the rows of
+ * the ids that occur and leaves the others as they are. */
+dpnorm_status dpnorm_embed_grad_workspace(dpnorm_dtype dt, int64_t B, int64_t T, int64_t V, int64_t d, size_t* bytes);
+dpnorm_status dpnorm_embed_grad(const void* order, const void* G, dpnorm_dtype dt, int64_t B, int64_t T, int64_t V,
+                                int64_t d, float scale, const float* c, void* dW, int accumulate, void* ws,
+                                size_t ws_bytes, hipStream_t stream);
+
+/* Causal attention of S sequences packed one after another in N token rows,
+ * with Hq query heads over Hkv key heads (Hq a multiple of Hkv; query head h
+ * reads key head h / (Hq / Hkv)):
+ *   o_t = sum_{u <= t} exp(scale q_t . k_u - lse_t) v_u,
+ *   lse_t = log sum_{u <= t} exp(scale q_t . k_u),   u in t's sequence.
+ * cu_seqlens is a device array of S + 1 non-decreasing row offsets (sequence s
+ * is rows cu[s] .. cu[s+1] - 1, and may be empty), or NULL: then N is a
+ * multiple of S and every sequence has N / S rows. Its entries are not checked
+ * on the host; offsets outside [0, N] or out of order are clamped, so that no
+ * memory outside the tensors is touched, and give undefined values. Rows that
+ * belong to no sequence are neither read nor written.
+ * D: a multiple of 8 (bf16) or 4 (fp32), at most 128. scale finite and > 0. */
+typedef struct dpnorm_attn_shape {
+  dpnorm_dtype dtype;
+  int64_t N, S, Hq, Hkv, D;
+  const int32_t* cu_seqlens;
+  float scale;
+} dpnorm_attn_shape;
+
+/* A [N][H][D] tensor: row t of head h starts at data + t stride_token +
+ * h stride_head (elements; not negative, multiples of 16 bytes; the D
+ * elements of a row are contiguous), data 16-byte aligned, stride_token below
+ * 2^22 elements. Inputs may overlap each other (views of one q, k, v buffer)
+ * and repeat rows (a stride of 0); the rows of an output must be apart, and an
+ * output's span must not overlap an input's or another output's. */
+typedef struct dpnorm_attn_tensor {
+  const void* data;
+  int64_t stride_token, stride_head;
+} dpnorm_attn_tensor;
+
+/* o [N][Hq][D] of the inputs' type and lse, float [Hq][N]. */
+dpnorm_status dpnorm_attention_forward(const dpnorm_attn_shape* shape, const dpnorm_attn_tensor* q,
+                                       const dpnorm_attn_tensor* k, const dpnorm_attn_tensor* v,
+                                       const dpnorm_attn_tensor* o, float* lse, hipStream_t stream);
+
+/* Gradients of sum(dO * o) for q, k and v, from the forward call's o and lse:
+ * with delta_t = dO_t . o_t, p_tu = exp(scale q_t . k_u - lse_t) and
+ * ds_tu = p_tu (dO_t . v_u - delta_t),
+ *   dq_t = scale sum_u ds_tu k_u, dk_u = scale sum_t ds_tu q_t,
+ *   dv_u = sum_t p_tu dO_t (dk and dv summed over the key head's query heads).
+ * ws holds delta. */
+dpnorm_status dpnorm_attention_backward_workspace(const dpnorm_attn_shape* shape, size_t* bytes);
+dpnorm_status dpnorm_attention_backward(const dpnorm_attn_shape* shape, const dpnorm_attn_tensor* dO,
+                                        const dpnorm_attn_tensor* q, const dpnorm_attn_tensor* k,
+                                        const dpnorm_attn_tensor* v, const dpnorm_attn_tensor* o, const float* lse,
+                                        const dpnorm_attn_tensor* dq, const dpnorm_attn_tensor* dk,
+                                        const dpnorm_attn_tensor* dv, void* ws, size_t ws_bytes, hipStream_t stream);
+
 /* Thin event helpers for profiling (wrap hipEventCreate / Destroy /
  * ElapsedTime / Synchronize); provided so bindings need only this library. */
 dpnorm_status dpnorm_event_create(hipEvent_t* ev);

@@ -24,6 +24,7 @@ import torch
 from . import _lib
 
 __all__ = ["DpnormError", "hutch", "hutch_grouped", "hutchpp", "exact", "clip_factors", "hutchpp_split", "KernelTimer",
+           "embed_lookup", "EmbedOrder", "embed_order", "embed_norm", "embed_grad", "attention_forward", "attention_backward",
            "lib", "hutch_workspace", "hutch_grouped_workspace", "hutchpp_workspace", "exact_workspace"]
 
 
@@ -449,6 +450,273 @@ def hutchpp_split(k: int) -> Tuple[int, int]:
     ms, mt = C.c_int64(0), C.c_int64(0)
     _check(lib().dpnorm_hutchpp_split(k, C.byref(ms), C.byref(mt)), "dpnorm_hutchpp_split")
     return ms.value, mt.value
+
+
+# ---------------------------------------------------------------------------
+# Around the linear layers: the embedding table and causal attention. The calls
+# run on the current stream of the tensors' device; temporaries come from
+# torch's allocator on that stream.
+# ---------------------------------------------------------------------------
+def _index(t: torch.Tensor, name: str) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"{name} must be int32 or int64, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor (libdpnorm runs on the GPU only)")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return _lib.I64 if t.dtype == torch.int64 else _lib.I32
+
+
+def embed_lookup(tokens: torch.Tensor, W: torch.Tensor, scale: float = 1.0,
+                 out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """scale * W[tokens], rounded once to W's type (dpnorm_embed_lookup).
+
+    tokens: int32 or int64 of any shape; W [V][d] bfloat16 or float32. An id
+    outside [0, V) gives a zero row. Returns tokens.shape + (d,).
+    """
+    it = _index(tokens, "tokens")
+    _need(W, "W", 2)
+    code = _code(W.dtype)
+    V, d = W.shape
+    shape = tuple(tokens.shape) + (d,)
+    if out is None:
+        out = torch.empty(shape, dtype=W.dtype, device=W.device)
+    else:
+        _need(out, "out", len(shape), W.dtype)
+        if tuple(out.shape) != shape:
+            raise ValueError(f"out must be {list(shape)}")
+    if tokens.device != W.device or out.device != W.device:
+        raise ValueError("all tensors of a call must be on one device")
+    if out.numel() > 0:
+        with torch.cuda.device(W.device):
+            _check(lib().dpnorm_embed_lookup(tokens.data_ptr(), it, W.data_ptr(), code, tokens.numel(), V, d, float(scale),
+                                             out.data_ptr(), _stream(W.device)), "dpnorm_embed_lookup")
+    return out
+
+
+class EmbedOrder:
+    """The sorted order of a batch's ids [B][T] for a table of V rows
+    (dpnorm_embed_order), read by embed_norm and embed_grad. It describes the
+    ids at the time of the call that made it."""
+
+    def __init__(self, B: int, T: int, V: int, data: torch.Tensor):
+        self.B, self.T, self.V, self.data = B, T, V, data
+
+
+def embed_order(tokens: torch.Tensor, V: int) -> EmbedOrder:
+    """Sorts the positions of tokens [B][T] by id, for any number of
+    embed_norm and embed_grad calls on the same ids."""
+    it = _index(tokens, "tokens")
+    if tokens.dim() != 2:
+        raise ValueError(f"tokens must have 2 dimensions, got shape {tuple(tokens.shape)}")
+    B, T = tokens.shape
+    if tokens.numel() == 0:
+        if not 1 <= V <= 1 << 30:
+            raise ValueError("V must be in 1 .. 2^30")
+        return EmbedOrder(B, T, V, torch.empty(0, dtype=torch.uint8, device=tokens.device))
+    L = lib()
+    ob, wb = C.c_size_t(0), C.c_size_t(0)
+    _check(L.dpnorm_embed_order_sizes(B, T, V, C.byref(ob), C.byref(wb)), "dpnorm_embed_order_sizes")
+    data = torch.empty(ob.value, dtype=torch.uint8, device=tokens.device)
+    ws, wsp = _workspace(wb.value, tokens.device)
+    with torch.cuda.device(tokens.device):
+        _check(L.dpnorm_embed_order(tokens.data_ptr(), it, B, T, V, data.data_ptr(), ob.value, wsp, wb.value,
+                                    _stream(tokens.device)), "dpnorm_embed_order")
+    return EmbedOrder(B, T, V, data)
+
+
+def _embed_args(tokens, G: torch.Tensor, V: Optional[int]) -> EmbedOrder:
+    _need(G, "G", 3)
+    _code(G.dtype)
+    if isinstance(tokens, EmbedOrder):
+        order = tokens
+        if V is not None and V != order.V:
+            raise ValueError(f"the order is of a table of {order.V} rows, not {V}")
+    else:
+        if V is None:
+            raise ValueError("V (the rows of the table) is needed with token ids")
+        order = embed_order(tokens, V)
+    if tuple(G.shape[:2]) != (order.B, order.T):
+        raise ValueError(f"G must be [B={order.B}][T={order.T}][*]")
+    if order.data.device != G.device:
+        raise ValueError("all tensors of a call must be on one device")
+    return order
+
+
+def embed_norm(tokens, G: torch.Tensor, V: Optional[int] = None, scale: float = 1.0, out: Optional[torch.Tensor] = None,
+               accumulate: bool = False, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Exact squared per-sample gradient norm of an embedding table
+    (dpnorm_embed_norm): n_i = scale^2 sum_v ||sum_{t: tokens[i, t] = v} G[i, t]||^2.
+
+    tokens: the ids [B][T] (then V, the table's rows, is needed) or their
+    EmbedOrder. G [B][T][d]: the gradient of the lookup's output. Returns
+    float32 [B]; with accumulate=True the norms are added to ``out``.
+    """
+    order = _embed_args(tokens, G, V)
+    B, T, d = G.shape
+    n = _out(out, B, G.device, accumulate)
+    if n.device != G.device:
+        raise ValueError("all tensors of a call must be on one device")
+    if G.numel() == 0:
+        return n if accumulate else n.zero_()
+    L = lib()
+    nbytes = C.c_size_t(0)
+    _check(L.dpnorm_embed_norm_workspace(_code(G.dtype), B, T, order.V, d, C.byref(nbytes)), "dpnorm_embed_norm_workspace")
+    ws, wsp = _given_workspace(workspace, nbytes.value, G.device)
+    with torch.cuda.device(G.device):
+        _check(L.dpnorm_embed_norm(order.data.data_ptr(), G.data_ptr(), _code(G.dtype), B, T, order.V, d, float(scale),
+                                   n.data_ptr(), int(accumulate), wsp, nbytes.value, _stream(G.device)),
+               "dpnorm_embed_norm")
+    return n
+
+
+def embed_grad(tokens, G: torch.Tensor, V: Optional[int] = None, scale: float = 1.0,
+               weights: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, accumulate: bool = False,
+               workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gradient of an embedding table [V][d] in G's type (dpnorm_embed_grad):
+    scale * sum_i weights_i sum_{t: tokens[i, t] = v} G[i, t] in row v.
+
+    tokens, V, G as for embed_norm; weights: float32 [B] (clip factors), or
+    None for 1. With accumulate=True the rows of the ids that occur are added
+    to ``out`` and its other rows are left as they are.
+    """
+    order = _embed_args(tokens, G, V)
+    B, T, d = G.shape
+    if weights is not None:
+        _need(weights, "weights", 1, torch.float32)
+        if weights.shape[0] != B or weights.device != G.device:
+            raise ValueError(f"weights must have {B} entries on G's device")
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate=True needs an existing output tensor")
+        out = torch.empty(order.V, d, dtype=G.dtype, device=G.device)
+    else:
+        _need(out, "out", 2, G.dtype)
+        if tuple(out.shape) != (order.V, d) or out.device != G.device:
+            raise ValueError(f"out must be [V={order.V}][d={d}] on G's device")
+    if G.numel() == 0:
+        return out if accumulate else out.zero_()
+    L = lib()
+    nbytes = C.c_size_t(0)
+    _check(L.dpnorm_embed_grad_workspace(_code(G.dtype), B, T, order.V, d, C.byref(nbytes)), "dpnorm_embed_grad_workspace")
+    ws, wsp = _given_workspace(workspace, nbytes.value, G.device)
+    with torch.cuda.device(G.device):
+        _check(L.dpnorm_embed_grad(order.data.data_ptr(), G.data_ptr(), _code(G.dtype), B, T, order.V, d, float(scale),
+                                   weights.data_ptr() if weights is not None else None, out.data_ptr(), int(accumulate), wsp,
+                                   nbytes.value, _stream(G.device)), "dpnorm_embed_grad")
+    return out
+
+
+def _heads(t: torch.Tensor, name: str, like: Optional[torch.Tensor] = None) -> _lib.AttnTensor:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [N][heads][D], got shape {tuple(t.shape)}")
+    if like is not None and t.dtype != like.dtype:
+        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor (libdpnorm runs on the GPU only)")
+    if like is not None and t.device != like.device:
+        raise ValueError("all tensors of a call must be on one device")
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    return _lib.AttnTensor(t.data_ptr(), t.stride(0), t.stride(1))
+
+
+def _attn_shape(q, k, v, cu_seqlens, sequences, scale):
+    tq, tk, tv = _heads(q, "q"), _heads(k, "k", like=q), _heads(v, "v", like=q)
+    code = _code(q.dtype)
+    N, Hq, D = q.shape
+    if k.shape != v.shape or k.shape[0] != N or k.shape[2] != D:
+        raise ValueError("shapes must be q [N][Hq][D], k and v [N][Hkv][D]")
+    if k.shape[1] == 0 or Hq % k.shape[1] != 0:
+        raise ValueError(f"{Hq} query heads are not a multiple of {k.shape[1]} key heads")
+    if cu_seqlens is not None:
+        if sequences is not None:
+            raise ValueError("give cu_seqlens or sequences, not both")
+        _need(cu_seqlens, "cu_seqlens", 1, torch.int32)
+        if cu_seqlens.device != q.device or cu_seqlens.shape[0] < 1:
+            raise ValueError("cu_seqlens must be the S + 1 row offsets on the tensors' device")
+        S, cup = cu_seqlens.shape[0] - 1, cu_seqlens.data_ptr()
+    else:
+        S, cup = (1 if sequences is None else int(sequences)), None
+        if S < 1 or N % S != 0:
+            raise ValueError(f"{N} rows are not a multiple of {S} sequences")
+    if scale is None:
+        scale = 1.0 / (D ** 0.5) if D else 1.0
+    return _lib.AttnShape(code, N, S, Hq, k.shape[1], D, cup, float(scale)), tq, tk, tv
+
+
+def attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None,
+                      sequences: Optional[int] = None, scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                      lse: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Causal attention of packed sequences (dpnorm_attention_forward).
+
+    q [N][Hq][D], k and v [N][Hkv][D], bfloat16 or float32, any token and head
+    strides; Hq a multiple of Hkv. cu_seqlens: int32 [S + 1] row offsets on
+    the GPU; without it the N rows are ``sequences`` (default 1) sequences of
+    equal length. scale defaults to 1 / sqrt(D). Returns (o [N][Hq][D],
+    lse float32 [Hq][N]). Rows that belong to no sequence are left as they
+    are in ``out`` and ``lse``, and are zero where these are made here.
+    """
+    shape, tq, tk, tv = _attn_shape(q, k, v, cu_seqlens, sequences, scale)
+    N, Hq, D = q.shape
+    make = torch.empty if cu_seqlens is None else torch.zeros
+    if out is None:
+        out = make(N, Hq, D, dtype=q.dtype, device=q.device)
+    elif tuple(out.shape) != (N, Hq, D):
+        raise ValueError(f"out must be [N={N}][Hq={Hq}][D={D}]")
+    to = _heads(out, "out", like=q)
+    if lse is None:
+        lse = make(Hq, N, dtype=torch.float32, device=q.device)
+    else:
+        _need(lse, "lse", 2, torch.float32)
+        if tuple(lse.shape) != (Hq, N) or lse.device != q.device:
+            raise ValueError(f"lse must be [Hq={Hq}][N={N}] on q's device")
+    if N > 0 and shape.S > 0:
+        with torch.cuda.device(q.device):
+            _check(lib().dpnorm_attention_forward(C.byref(shape), C.byref(tq), C.byref(tk), C.byref(tv), C.byref(to),
+                                                  lse.data_ptr(), _stream(q.device)), "dpnorm_attention_forward")
+    return out, lse
+
+
+def attention_backward(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
+                       lse: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None, sequences: Optional[int] = None,
+                       scale: Optional[float] = None, out: Optional[Sequence[torch.Tensor]] = None,
+                       workspace: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """(dq, dk, dv) of attention_forward for the output gradient ``do``
+    (dpnorm_attention_backward). q, k, v, cu_seqlens, sequences and scale are
+    the forward call's, o and lse its results. ``out``: three tensors to write
+    to. Rows that belong to no sequence are left as they are in ``out``, and
+    are zero where it is made here.
+    """
+    shape, tq, tk, tv = _attn_shape(q, k, v, cu_seqlens, sequences, scale)
+    N, Hq, D = q.shape
+    if tuple(do.shape) != (N, Hq, D) or tuple(o.shape) != (N, Hq, D):
+        raise ValueError(f"do and o must be [N={N}][Hq={Hq}][D={D}]")
+    tdo, to = _heads(do, "do", like=q), _heads(o, "o", like=q)
+    _need(lse, "lse", 2, torch.float32)
+    if tuple(lse.shape) != (Hq, N) or lse.device != q.device:
+        raise ValueError(f"lse must be [Hq={Hq}][N={N}] on q's device")
+    if out is None:
+        make = torch.empty if cu_seqlens is None else torch.zeros
+        out = tuple(make(t.shape, dtype=q.dtype, device=q.device) for t in (q, k, v))
+    dq, dk, dv = out
+    if dq.shape != q.shape or dk.shape != k.shape or dv.shape != v.shape:
+        raise ValueError("out must be three tensors of q's, k's and v's shapes")
+    tdq, tdk, tdv = _heads(dq, "dq", like=q), _heads(dk, "dk", like=q), _heads(dv, "dv", like=q)
+    if N > 0 and shape.S > 0:
+        L = lib()
+        nbytes = C.c_size_t(0)
+        _check(L.dpnorm_attention_backward_workspace(C.byref(shape), C.byref(nbytes)), "dpnorm_attention_backward_workspace")
+        ws, wsp = _given_workspace(workspace, nbytes.value, q.device)
+        with torch.cuda.device(q.device):
+            _check(L.dpnorm_attention_backward(C.byref(shape), C.byref(tdo), C.byref(tq), C.byref(tk), C.byref(tv), C.byref(to),
+                                               lse.data_ptr(), C.byref(tdq), C.byref(tdk), C.byref(tdv), wsp, nbytes.value,
+                                               _stream(q.device)), "dpnorm_attention_backward")
+    return dq, dk, dv
 
 
 class KernelTimer:

@@ -19,6 +19,8 @@ STATIC_SCRATCH_BYTES = 64 << 20
 OK, ERR_NULL, ERR_SIZE, ERR_DTYPE, ERR_VALUE, ERR_WORKSPACE, ERR_ALIGN, ERR_HIP = range(8)
 # dpnorm_dtype
 F32, BF16 = 0, 1
+# dpnorm_index
+I32, I64 = 0, 1
 # dpnorm_route
 EXACT_AUTO, EXACT_EXPLICIT, EXACT_GRAM = 0, 1, 2
 # dpnorm_kernel_kind
@@ -37,8 +39,20 @@ class Trace(C.Structure):
                 ("capacity", C.c_int64), ("count", C.c_int64)]
 
 
+class AttnShape(C.Structure):
+    """struct dpnorm_attn_shape."""
+    _fields_ = [("dtype", C.c_int), ("N", C.c_int64), ("S", C.c_int64), ("Hq", C.c_int64), ("Hkv", C.c_int64),
+                ("D", C.c_int64), ("cu_seqlens", C.c_void_p), ("scale", C.c_float)]
+
+
+class AttnTensor(C.Structure):
+    """struct dpnorm_attn_tensor: element strides of a [N][H][D] device tensor."""
+    _fields_ = [("data", C.c_void_p), ("stride_token", C.c_int64), ("stride_head", C.c_int64)]
+
+
 _vp, _i64, _i32, _f32, _sz = C.c_void_p, C.c_int64, C.c_int, C.c_float, C.c_size_t
 _fp = C.POINTER(C.c_float)
+_szp, _shp, _tp = C.POINTER(C.c_size_t), C.POINTER(AttnShape), C.POINTER(AttnTensor)
 
 SIGNATURES = {
     "dpnorm_version": ([], C.c_int),
@@ -68,6 +82,16 @@ SIGNATURES = {
     "dpnorm_exact_workspace": ([C.c_int, _i64, _i64, _i64, _i64, C.c_int, C.POINTER(_sz)], C.c_int),
     "dpnorm_exact": ([_vp, _vp, C.c_int, _i64, _i64, _i64, _i64, C.c_int, _vp, C.c_int, _vp, _sz, _vp], C.c_int),
     "dpnorm_clip_factors": ([_vp, _i64, _f32, _vp, _vp], C.c_int),
+    "dpnorm_embed_lookup": ([_vp, C.c_int, _vp, C.c_int, _i64, _i64, _i64, _f32, _vp, _vp], C.c_int),
+    "dpnorm_embed_order_sizes": ([_i64, _i64, _i64, _szp, _szp], C.c_int),
+    "dpnorm_embed_order": ([_vp, C.c_int, _i64, _i64, _i64, _vp, _sz, _vp, _sz, _vp], C.c_int),
+    "dpnorm_embed_norm_workspace": ([C.c_int, _i64, _i64, _i64, _i64, _szp], C.c_int),
+    "dpnorm_embed_norm": ([_vp, _vp, C.c_int, _i64, _i64, _i64, _i64, _f32, _vp, C.c_int, _vp, _sz, _vp], C.c_int),
+    "dpnorm_embed_grad_workspace": ([C.c_int, _i64, _i64, _i64, _i64, _szp], C.c_int),
+    "dpnorm_embed_grad": ([_vp, _vp, C.c_int, _i64, _i64, _i64, _i64, _f32, _vp, _vp, C.c_int, _vp, _sz, _vp], C.c_int),
+    "dpnorm_attention_forward": ([_shp, _tp, _tp, _tp, _tp, _vp, _vp], C.c_int),
+    "dpnorm_attention_backward_workspace": ([_shp, _szp], C.c_int),
+    "dpnorm_attention_backward": ([_shp, _tp, _tp, _tp, _tp, _tp, _vp, _tp, _tp, _tp, _vp, _sz, _vp], C.c_int),
     "dpnorm_event_create": ([C.POINTER(_vp)], C.c_int),
     "dpnorm_event_destroy": ([_vp], C.c_int),
     "dpnorm_event_elapsed_ms": ([_vp, _vp, _fp], C.c_int),

@@ -1,0 +1,185 @@
+// Host layer of the attention calls: argument checks and launches. Included by
+// dpnorm.cpp, whose helpers it uses.
+#pragma once
+#include "attention_kernels.h"
+
+namespace {
+
+struct AttnCheck {
+  attn::Args a{};
+  bool bf16 = true;
+};
+
+// Bytes that a [N][H][D] tensor with the given element strides spans.
+size_t span(const dpnorm_attn_tensor& t, int64_t N, int64_t H, int64_t D, size_t e) {
+  return (size_t)((N - 1) * t.stride_token + (H - 1) * t.stride_head + D) * e;
+}
+
+// Whether the rows of an output are all apart (no element written twice).
+bool rows_apart(const dpnorm_attn_tensor& t, int64_t N, int64_t H, int64_t D) {
+  if (t.stride_token >= t.stride_head)
+    return (H == 1 || t.stride_head >= D) && (N == 1 || t.stride_token >= (H - 1) * t.stride_head + D);
+  return (N == 1 || t.stride_token >= D) && (H == 1 || t.stride_head >= (N - 1) * t.stride_token + D);
+}
+
+dpnorm_status check_shape(const dpnorm_attn_shape* s) {
+  if (!s) return DPNORM_ERR_NULL;
+  if (s->dtype != DPNORM_BF16 && s->dtype != DPNORM_F32) return DPNORM_ERR_DTYPE;
+  const int64_t lim = (int64_t)1 << 30;
+  if (s->N < 1 || s->N > lim || s->S < 1 || s->S > lim || s->Hq < 1 || s->Hkv < 1 || s->Hq > 65536 || s->Hq % s->Hkv != 0)
+    return DPNORM_ERR_SIZE;
+  const int64_t g = s->dtype == DPNORM_BF16 ? 8 : 4;
+  if (s->D < 1 || s->D > 128 || s->D % g != 0) return DPNORM_ERR_SIZE;
+  if (!s->cu_seqlens && s->N % s->S != 0) return DPNORM_ERR_SIZE;
+  if (!aligned(s->cu_seqlens, 4)) return DPNORM_ERR_ALIGN;
+  if (!(s->scale > 0.f) || !std::isfinite(s->scale)) return DPNORM_ERR_VALUE;
+  // a block a head and slot: the grid's x dimension holds them
+  if ((s->N / attn::kRows + s->S + 1) * s->Hq > 0x7fffffff) return DPNORM_ERR_SIZE;
+  return DPNORM_OK;
+}
+
+dpnorm_status check_tensor(const dpnorm_attn_tensor* t, const dpnorm_attn_shape* s, int64_t H, bool output) {
+  if (!t || !t->data) return DPNORM_ERR_NULL;
+  if (!aligned(t->data, 16)) return DPNORM_ERR_ALIGN;
+  const int64_t g = s->dtype == DPNORM_BF16 ? 8 : 4;
+  // 128 rows of a tile are addressed with 31-bit byte offsets
+  const int64_t lim = ((int64_t)1 << 31) / 128 / 4 - 256;
+  if (t->stride_token < 0 || t->stride_head < 0 || t->stride_token > lim || t->stride_head > ((int64_t)1 << 40) / H)
+    return DPNORM_ERR_SIZE;
+  if (t->stride_token % g != 0 || t->stride_head % g != 0) return DPNORM_ERR_ALIGN;
+  if (output && !rows_apart(*t, s->N, H, s->D)) return DPNORM_ERR_VALUE;
+  return DPNORM_OK;
+}
+
+attn::Tensor tensor_of(const dpnorm_attn_tensor* t, size_t e) {
+  return attn::Tensor{(char*)t->data, t->stride_token * (int64_t)e, t->stride_head * (int64_t)e};
+}
+
+attn::Args attn_args(const dpnorm_attn_shape* s) {
+  attn::Args a{};
+  a.cu = s->cu_seqlens;
+  a.S = (int32_t)s->S;
+  a.N = (int32_t)s->N;
+  a.T = (int32_t)(s->N / s->S);
+  a.Hq = (int32_t)s->Hq;
+  a.Hkv = (int32_t)s->Hkv;
+  a.D = (int32_t)s->D;
+  a.scale = s->scale;
+  // sequences of any lengths have at most N / rows + S tiles
+  const int64_t per = (a.T + attn::kRows - 1) / attn::kRows;
+  a.slots = (int32_t)(s->cu_seqlens ? s->N / attn::kRows + s->S : s->S * per);
+  return a;
+}
+
+// Every output apart from every input and from the other outputs.
+struct Region {
+  const void* p;
+  size_t bytes;
+};
+bool outputs_overlap(const std::vector<Region>& in, const std::vector<Region>& out) {
+  for (size_t j = 0; j < out.size(); ++j) {
+    for (const Region& r : in)
+      if (overlaps(out[j].p, out[j].bytes, r.p, r.bytes)) return true;
+    for (size_t i = 0; i < j; ++i)
+      if (overlaps(out[j].p, out[j].bytes, out[i].p, out[i].bytes)) return true;
+  }
+  return false;
+}
+
+template <bool BF16, int DP>
+hipError_t launch_attn_forward(const attn::Args& a, hipStream_t stream) {
+  attn::k_forward<BF16, DP><<<(uint32_t)(a.slots * a.Hq), attn::kThreads, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+template <bool BF16, int DP>
+hipError_t launch_attn_backward(const attn::Args& a, hipStream_t stream) {
+  attn::k_backward_q<BF16, DP><<<(uint32_t)(a.slots * a.Hq), attn::kThreads, 0, stream>>>(a);
+  attn::k_backward_kv<BF16, DP><<<(uint32_t)(a.slots * a.Hkv), attn::kThreads, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+extern "C" {
+
+dpnorm_status dpnorm_attention_forward(const dpnorm_attn_shape* shape, const dpnorm_attn_tensor* q, const dpnorm_attn_tensor* k,
+                                       const dpnorm_attn_tensor* v, const dpnorm_attn_tensor* o, float* lse,
+                                       hipStream_t stream) {
+  dpnorm_status st = check_shape(shape);
+  if (st == DPNORM_OK) st = check_tensor(q, shape, shape->Hq, false);
+  if (st == DPNORM_OK) st = check_tensor(k, shape, shape->Hkv, false);
+  if (st == DPNORM_OK) st = check_tensor(v, shape, shape->Hkv, false);
+  if (st == DPNORM_OK) st = check_tensor(o, shape, shape->Hq, true);
+  if (st != DPNORM_OK) return st;
+  if (!lse) return DPNORM_ERR_NULL;
+  if (!aligned(lse, 4)) return DPNORM_ERR_ALIGN;
+  const size_t e = esize(shape->dtype);
+  const int64_t N = shape->N, Hq = shape->Hq, Hkv = shape->Hkv, D = shape->D;
+  if (outputs_overlap({{q->data, span(*q, N, Hq, D, e)}, {k->data, span(*k, N, Hkv, D, e)}, {v->data, span(*v, N, Hkv, D, e)},
+                       {shape->cu_seqlens, (size_t)(shape->S + 1) * 4}},
+                      {{o->data, span(*o, N, Hq, D, e)}, {lse, (size_t)N * Hq * 4}}))
+    return DPNORM_ERR_VALUE;
+  attn::Args a = attn_args(shape);
+  a.q = tensor_of(q, e);
+  a.k = tensor_of(k, e);
+  a.v = tensor_of(v, e);
+  a.o = tensor_of(o, e);
+  a.lse = lse;
+  const bool wide = D > 64;
+  if (shape->dtype == DPNORM_BF16)
+    return hip_status(wide ? launch_attn_forward<true, 128>(a, stream) : launch_attn_forward<true, 64>(a, stream));
+  return hip_status(wide ? launch_attn_forward<false, 128>(a, stream) : launch_attn_forward<false, 64>(a, stream));
+}
+
+dpnorm_status dpnorm_attention_backward_workspace(const dpnorm_attn_shape* shape, size_t* bytes) {
+  if (!bytes) return DPNORM_ERR_NULL;
+  const dpnorm_status st = check_shape(shape);
+  if (st != DPNORM_OK) return st;
+  *bytes = align_up((size_t)shape->N * shape->Hq * 4);
+  return DPNORM_OK;
+}
+
+dpnorm_status dpnorm_attention_backward(const dpnorm_attn_shape* shape, const dpnorm_attn_tensor* dO, const dpnorm_attn_tensor* q,
+                                        const dpnorm_attn_tensor* k, const dpnorm_attn_tensor* v, const dpnorm_attn_tensor* o,
+                                        const float* lse, const dpnorm_attn_tensor* dq, const dpnorm_attn_tensor* dk,
+                                        const dpnorm_attn_tensor* dv, void* ws, size_t ws_bytes, hipStream_t stream) {
+  size_t bytes = 0;
+  dpnorm_status st = dpnorm_attention_backward_workspace(shape, &bytes);
+  for (const dpnorm_attn_tensor* t : {dO, q, o})
+    if (st == DPNORM_OK) st = check_tensor(t, shape, shape->Hq, false);
+  for (const dpnorm_attn_tensor* t : {k, v})
+    if (st == DPNORM_OK) st = check_tensor(t, shape, shape->Hkv, false);
+  if (st == DPNORM_OK) st = check_tensor(dq, shape, shape->Hq, true);
+  for (const dpnorm_attn_tensor* t : {dk, dv})
+    if (st == DPNORM_OK) st = check_tensor(t, shape, shape->Hkv, true);
+  if (st != DPNORM_OK) return st;
+  if (!lse || !ws) return DPNORM_ERR_NULL;
+  if (!aligned(lse, 4) || !aligned(ws, kAlign)) return DPNORM_ERR_ALIGN;
+  if (ws_bytes < bytes) return DPNORM_ERR_WORKSPACE;
+  const size_t e = esize(shape->dtype);
+  const int64_t N = shape->N, Hq = shape->Hq, Hkv = shape->Hkv, D = shape->D;
+  if (outputs_overlap({{dO->data, span(*dO, N, Hq, D, e)}, {q->data, span(*q, N, Hq, D, e)}, {o->data, span(*o, N, Hq, D, e)},
+                       {k->data, span(*k, N, Hkv, D, e)}, {v->data, span(*v, N, Hkv, D, e)}, {lse, (size_t)N * Hq * 4},
+                       {shape->cu_seqlens, (size_t)(shape->S + 1) * 4}},
+                      {{dq->data, span(*dq, N, Hq, D, e)}, {dk->data, span(*dk, N, Hkv, D, e)}, {dv->data, span(*dv, N, Hkv, D, e)},
+                       {ws, bytes}}))
+    return DPNORM_ERR_VALUE;
+  attn::Args a = attn_args(shape);
+  a.dO = tensor_of(dO, e);
+  a.q = tensor_of(q, e);
+  a.k = tensor_of(k, e);
+  a.v = tensor_of(v, e);
+  a.o = tensor_of(o, e);
+  a.dq = tensor_of(dq, e);
+  a.dk = tensor_of(dk, e);
+  a.dv = tensor_of(dv, e);
+  a.lse = const_cast<float*>(lse);
+  a.delta = (float*)ws;
+  const bool wide = D > 64;
+  if (shape->dtype == DPNORM_BF16)
+    return hip_status(wide ? launch_attn_backward<true, 128>(a, stream) : launch_attn_backward<true, 64>(a, stream));
+  return hip_status(wide ? launch_attn_backward<false, 128>(a, stream) : launch_attn_backward<false, 64>(a, stream));
+}
+
+}  // extern "C"

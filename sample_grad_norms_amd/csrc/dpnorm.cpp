@@ -866,7 +866,7 @@ dpnorm_status static_scratch(hipStream_t stream, void** out) {
 // ===========================================================================
 extern "C" {
 
-int dpnorm_version(void) { return 100; }
+int dpnorm_version(void) { return 200; }
 
 const char* dpnorm_status_string(int status) {
   switch (status) {
@@ -1140,3 +1140,8 @@ dpnorm_status dpnorm_event_synchronize(hipEvent_t ev) {
 }
 
 }  // extern "C"
+
+// The calls around the linear layers. They are compiled with the host layer as
+// one unit, so that a build of the library's host side alone has them too.
+#include "embed_api.h"
+#include "attention_api.h"

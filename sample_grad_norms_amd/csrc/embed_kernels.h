@@ -1,0 +1,584 @@
+// Embedding kernels: scaled lookup, the order of a batch's ids, and sums of
+// gradient rows over runs of equal ids, for the per-sample norm and for the
+// gradient of the table.
+//
+//   lookup  out[q] = s W[tok[q]]
+//   norm    n_i = s^2 sum_v || sum_{q in sample i, tok[q] = v} G[q] ||^2
+//   grad    dW[v] = s sum_q c_{sample(q)} [tok[q] = v] G[q]
+//
+// q = i T + t numbers the N = B T positions of a batch. Ids outside [0, V)
+// have no row: they are given the key V, sort behind every row and are skipped.
+//
+// All three are bound by HBM: the rows are read once, sums are held in fp32
+// registers, 16 bytes a lane and row, and there are no atomics, so every
+// result is bitwise reproducible.
+#pragma once
+#include "device_common.h"
+
+namespace dpn {
+namespace embed {
+
+// ---------------------------------------------------------------------------
+// Order: a stable sort of the positions by key (least significant digit first)
+// ---------------------------------------------------------------------------
+constexpr int kSortThreads = 1024;
+constexpr int kSortWaves = kSortThreads / kWave;
+constexpr int kMaxDigits = 512;          // 9 bits a pass: two passes up to V = 2^18 - 1
+constexpr int kSmallSort = 8192;         // positions that one work group sorts alone
+constexpr int kSmallRounds = kSmallSort / kSortThreads;
+constexpr int kMaxSortBlocks = 64;
+
+struct SortShared {
+  uint32_t cnt[kSortWaves][kMaxDigits];
+  uint32_t base[kMaxDigits];
+  uint32_t scan[kSortWaves];
+};
+
+__device__ __forceinline__ int32_t id_key(const void* tok, int idx64, int64_t q, int32_t V) {
+  const int64_t t = idx64 ? ((const int64_t*)tok)[q] : (int64_t)((const int32_t*)tok)[q];
+  return (t >= 0 && t < (int64_t)V) ? (int32_t)t : V;
+}
+
+// Lanes of the wave (among `valid`) whose digit equals this lane's.
+__device__ __forceinline__ uint64_t match_digit(uint32_t digit, int bits, uint64_t valid) {
+  uint64_t m = valid;
+  for (int b = 0; b < bits; ++b) {
+    const uint64_t has = __ballot((digit >> b) & 1u);
+    m &= ((digit >> b) & 1u) ? has : ~has;
+  }
+  return m;
+}
+
+// Counts one round of a wave's keys into its counters and returns the lane's
+// rank among the wave's equal digits so far (stable: in position order).
+__device__ __forceinline__ uint32_t count_round(uint32_t* cnt, uint32_t digit, int bits, bool valid) {
+  const uint64_t m = match_digit(digit, bits, __ballot(valid));
+  uint32_t rank = 0;
+  if (valid) {
+    const int lane = __lane_id();
+    const uint32_t before = (uint32_t)__popcll(m & ((1ull << lane) - 1ull));
+    const uint32_t old = cnt[digit];
+    rank = old + before;
+    if (before == 0) cnt[digit] = old + (uint32_t)__popcll(m);
+  }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // the next round reads what this one counted
+  __builtin_amdgcn_wave_barrier();
+  return rank;
+}
+
+__device__ __forceinline__ void zero_counts(SortShared& sh, int digits) {
+  for (int j = threadIdx.x; j < kSortWaves * digits; j += kSortThreads) sh.cnt[j / digits][j % digits] = 0;
+  __syncthreads();
+}
+
+// cnt[w][digit] becomes the wave's exclusive offset among the block's equal
+// digits; returns the block's total of digit threadIdx.x (0 past the digits).
+__device__ __forceinline__ uint32_t scan_waves(SortShared& sh, int digits) {
+  __syncthreads();
+  uint32_t run = 0;
+  if ((int)threadIdx.x < digits) {
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) {
+      const uint32_t c = sh.cnt[w][threadIdx.x];
+      sh.cnt[w][threadIdx.x] = run;
+      run += c;
+    }
+  }
+  return run;
+}
+
+// Exclusive sum of v over the threads of the block.
+__device__ __forceinline__ uint32_t scan_block(SortShared& sh, uint32_t v) {
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  uint32_t inc = v;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const uint32_t up = __shfl_up(inc, o);
+    if (lane >= o) inc += up;
+  }
+  if (lane == 63) sh.scan[wv] = inc;
+  __syncthreads();
+  uint32_t before = 0;
+  for (int w = 0; w < wv; ++w) before += sh.scan[w];
+  return before + inc - v;
+}
+
+// Up to kSmallSort positions: one work group, every pass through LDS. Each
+// wave keeps a contiguous segment, so waves in order are positions in order.
+__global__ __launch_bounds__(kSortThreads) void k_order_small(const void* tok, int idx64, int32_t N, int32_t V, int passes,
+                                                              int bits, int32_t* keys, int32_t* pos) {
+  __shared__ SortShared sh;
+  __shared__ int32_t lkey[kSmallSort], lpos[kSmallSort];
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  const int rounds = (N + kSortThreads - 1) / kSortThreads;
+  const int seg0 = wv * rounds * kWave;
+  const int digits = 1 << bits;
+  int32_t key[kSmallRounds], ps[kSmallRounds];
+#pragma unroll
+  for (int r = 0; r < kSmallRounds; ++r) {
+    const int q = seg0 + r * kWave + lane;
+    const bool in = r < rounds && q < N;
+    key[r] = in ? id_key(tok, idx64, q, V) : 0;
+    ps[r] = q;
+  }
+  for (int p = 0; p < passes; ++p) {
+    zero_counts(sh, digits);
+    uint32_t rank[kSmallRounds];
+#pragma unroll
+    for (int r = 0; r < kSmallRounds; ++r) {
+      if (r < rounds)
+        rank[r] = count_round(sh.cnt[wv], ((uint32_t)key[r] >> (p * bits)) & (digits - 1), bits,
+                              seg0 + r * kWave + lane < N);
+    }
+    const uint32_t total = scan_waves(sh, digits);
+    const uint32_t base = scan_block(sh, total);
+    if ((int)threadIdx.x < digits) sh.base[threadIdx.x] = base;
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kSmallRounds; ++r) {
+      const int q = seg0 + r * kWave + lane;
+      if (r < rounds && q < N) {
+        const uint32_t dg = ((uint32_t)key[r] >> (p * bits)) & (digits - 1);
+        const uint32_t to = sh.base[dg] + sh.cnt[wv][dg] + rank[r];
+        lkey[to] = key[r];
+        lpos[to] = ps[r];
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kSmallRounds; ++r) {
+      const int q = seg0 + r * kWave + lane;
+      if (r < rounds && q < N) {
+        key[r] = lkey[q];
+        ps[r] = lpos[q];
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < kSmallRounds; ++r) {
+    const int q = seg0 + r * kWave + lane;
+    if (r < rounds && q < N) {
+      keys[q] = key[r];
+      pos[q] = ps[r];
+    }
+  }
+}
+
+// Larger batches, one pass over `per` positions a block: digit counts of every
+// block first (hist[digit][block]), then the stable scatter. src_keys is null
+// in the first pass, which reads the ids.
+__device__ __forceinline__ int32_t load_key(const void* tok, int idx64, const int32_t* src_keys, int64_t q, int32_t V) {
+  return src_keys ? src_keys[q] : id_key(tok, idx64, q, V);
+}
+
+__global__ __launch_bounds__(kSortThreads) void k_order_count(const void* tok, int idx64, const int32_t* src_keys, int32_t N,
+                                                              int32_t V, int shift, int bits, int per, uint32_t* hist) {
+  __shared__ uint32_t cnt[kMaxDigits];
+  const int digits = 1 << bits;
+  for (int j = threadIdx.x; j < digits; j += kSortThreads) cnt[j] = 0;
+  __syncthreads();
+  const int64_t lo = (int64_t)blockIdx.x * per, hi = lo + per < N ? lo + per : N;
+  for (int64_t q = lo + threadIdx.x; q < hi; q += kSortThreads)
+    atomicAdd(&cnt[((uint32_t)load_key(tok, idx64, src_keys, q, V) >> shift) & (digits - 1)], 1u);
+  __syncthreads();
+  for (int j = threadIdx.x; j < digits; j += kSortThreads) hist[(int64_t)j * gridDim.x + blockIdx.x] = cnt[j];
+}
+
+__global__ __launch_bounds__(kSortThreads) void k_order_scatter(const void* tok, int idx64, const int32_t* src_keys,
+                                                                const int32_t* src_pos, int32_t N, int32_t V, int shift,
+                                                                int bits, int per, const uint32_t* hist, int32_t* keys,
+                                                                int32_t* pos) {
+  __shared__ SortShared sh;
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  const int digits = 1 << bits, nb = gridDim.x;
+  const int64_t lo = (int64_t)blockIdx.x * per, hi = lo + per < N ? lo + per : N;
+  const int seg = (per + kSortWaves - 1) / kSortWaves;   // positions a wave walks, in order
+  const int64_t wlo = lo + (int64_t)wv * seg < hi ? lo + (int64_t)wv * seg : hi;
+  const int64_t whi = wlo + seg < hi ? wlo + seg : hi;
+  // where this block's elements of each digit go
+  uint32_t total = 0, before = 0;
+  if ((int)threadIdx.x < digits) {
+    for (int b = 0; b < nb; ++b) {
+      const uint32_t h = hist[(int64_t)threadIdx.x * nb + b];
+      if (b < (int)blockIdx.x) before += h;
+      total += h;
+    }
+  }
+  const uint32_t base = scan_block(sh, total) + before;
+  if ((int)threadIdx.x < digits) sh.base[threadIdx.x] = base;
+  zero_counts(sh, digits);
+  for (int64_t q0 = wlo; q0 < whi; q0 += kWave) {
+    const int64_t q = q0 + lane;
+    const bool in = q < whi;
+    const uint32_t dg = in ? ((uint32_t)load_key(tok, idx64, src_keys, q, V) >> shift) & (digits - 1) : 0;
+    count_round(sh.cnt[wv], dg, bits, in);
+  }
+  scan_waves(sh, digits);
+  __syncthreads();
+  // the same walk again, now from each wave's offsets
+  for (int64_t q0 = wlo; q0 < whi; q0 += kWave) {
+    const int64_t q = q0 + lane;
+    const bool in = q < whi;
+    const int32_t key = in ? load_key(tok, idx64, src_keys, q, V) : 0;
+    const uint32_t dg = ((uint32_t)key >> shift) & (digits - 1);
+    const uint32_t rank = count_round(sh.cnt[wv], dg, bits, in);
+    if (in) {
+      const uint32_t to = sh.base[dg] + rank;
+      keys[to] = key;
+      pos[to] = src_pos ? src_pos[q] : (int32_t)q;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Rows: 16 bytes a lane, 8 bf16 or 4 fp32 columns; a slice is one wave's width
+// ---------------------------------------------------------------------------
+template <bool BF16>
+struct Row {
+  static constexpr int kElems = BF16 ? 8 : 4;
+  static constexpr int kSlice = kElems * kWave;
+  static constexpr int kBytes = BF16 ? 2 : 4;
+  __device__ static void add(float (&acc)[kElems], const uint4& v, float w) {
+    if constexpr (BF16) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t x = word(v, j);
+        acc[2 * j] = fmaf(w, __uint_as_float(x << 16), acc[2 * j]);
+        acc[2 * j + 1] = fmaf(w, __uint_as_float(x & 0xffff0000u), acc[2 * j + 1]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[j] = fmaf(w, __uint_as_float(word(v, j)), acc[j]);
+    }
+  }
+  // rounded once to the element type (to nearest even)
+  __device__ static uint4 pack(const float (&a)[kElems]) {
+    if constexpr (BF16) {
+      uint32_t b[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) b[j] = f32_to_bf16_bits(a[j]);
+      return pack8(b);
+    } else {
+      return make_uint4(__float_as_uint(a[0]), __float_as_uint(a[1]), __float_as_uint(a[2]), __float_as_uint(a[3]));
+    }
+  }
+};
+
+// Sum of v over the wave in a fixed order, the same in every lane.
+__device__ __forceinline__ float wave_sum_f32(float v) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o);
+  return v;
+}
+
+constexpr int kLookupRows = 4;   // rows a wave has in flight
+
+template <bool BF16>
+__global__ __launch_bounds__(256) void k_lookup(const void* tok, int idx64, const char* W, char* out, int64_t N, int32_t V,
+                                                int32_t d, int32_t slices, float scale) {
+  using R = Row<BF16>;
+  const int lane = threadIdx.x & 63;
+  const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int64_t q0 = item / slices * kLookupRows;
+  const int col = (int)(item % slices) * R::kSlice + lane * R::kElems;
+  if (q0 >= N || col >= d) return;
+  uint4 v[kLookupRows];
+#pragma unroll
+  for (int r = 0; r < kLookupRows; ++r) {
+    v[r] = make_uint4(0, 0, 0, 0);
+    if (q0 + r < N) {
+      const int32_t id = id_key(tok, idx64, q0 + r, V);
+      if (id < V) v[r] = ldg16(W + ((int64_t)id * d + col) * R::kBytes);
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < kLookupRows; ++r) {
+    if (q0 + r < N) {
+      float a[R::kElems] = {};
+      R::add(a, v[r], scale);
+      stg16(out + ((q0 + r) * d + col) * R::kBytes, R::pack(a));
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Sums over runs of equal keys
+//
+// The sorted positions are cut into chunks of about R, one wave to a chunk and
+// column slice. A chunk boundary at x = c R moves on to the next run start
+// within R positions, so only runs of R positions and more are ever cut. The
+// pieces of a cut run go to the workspace and a second launch joins them.
+// Runs are of equal (id, sample) for the norm and of equal id for the gradient.
+// ---------------------------------------------------------------------------
+struct Runs {
+  const int32_t* keys;   // sorted, V for positions without a row
+  const int32_t* pos;
+  int32_t N, T, V;
+  int R;                 // at most 32, so that a chunk fits the lanes of a wave
+  int32_t chunks;
+};
+
+enum { RUN_NORM = 0, RUN_GRAD = 1 };
+
+__device__ __forceinline__ int32_t in_batch(const Runs& a, int32_t q) { return (int32_t)min((uint32_t)q, (uint32_t)a.N - 1u); }
+__device__ __forceinline__ int32_t in_table(const Runs& a, int32_t key) { return (int32_t)min((uint32_t)key, (uint32_t)a.V); }
+
+template <int MODE>
+__device__ __forceinline__ bool run_starts(const Runs& a, int32_t j) {
+  if (j <= 0 || j >= a.N) return true;
+  if (a.keys[j] != a.keys[j - 1]) return true;
+  return MODE == RUN_NORM && a.pos[j] / a.T != a.pos[j - 1] / a.T;
+}
+
+// The boundary that x = c R moves to; `cut` when it lies inside a run.
+template <int MODE>
+__device__ __forceinline__ int32_t boundary(const Runs& a, int64_t x, bool& cut) {
+  cut = false;
+  if (x <= 0) return 0;
+  if (x >= a.N) return a.N;
+  const int lane = __lane_id();
+  const uint64_t m = __ballot(lane < a.R && run_starts<MODE>(a, (int32_t)min(x + lane, (int64_t)a.N)));
+  if (m == 0) {
+    cut = true;
+    return (int32_t)x;
+  }
+  return (int32_t)(x + __builtin_ctzll(m));
+}
+
+// End of the run that holds sorted position j: a search by all 64 lanes.
+template <int MODE>
+__device__ __forceinline__ int32_t run_end(const Runs& a, int32_t j) {
+  const int32_t key = a.keys[j], smp = MODE == RUN_NORM ? a.pos[j] / a.T : 0;
+  const int lane = __lane_id();
+  int64_t lo = j, hi = a.N;   // position lo is in the run, hi is not
+  while (hi - lo > 1) {
+    const int64_t step = (hi - lo + 63) / 64;
+    const int64_t p = lo + step * (lane + 1);
+    const bool in = p < hi && a.keys[p] == key && (MODE != RUN_NORM || a.pos[p] / a.T == smp);
+    const int cnt = __popcll(__ballot(in));   // the lanes inside are the first ones
+    const int64_t nlo = lo + step * cnt;
+    hi = min(hi, nlo + step);
+    lo = nlo;
+  }
+  return (int32_t)hi;
+}
+
+struct RunArgs {
+  Runs runs;
+  const char* G;        // [N][d]
+  const float* c;       // per-sample weights or null (grad)
+  float scale;          // grad
+  char* out;            // grad: table [V][d]
+  float* val;           // norm: [slices][N] squared sums, at the position that starts the run
+  float* part;          // [chunks][2][d]: pieces of runs that started before the chunk / that go on after it
+  int32_t d, slices;
+  int accumulate;       // grad: add to the table's touched rows
+  int64_t items;        // chunks x slices
+  int64_t fill_blocks;  // grad: blocks behind the items' that clear rows without an id
+};
+
+template <bool BF16>
+__device__ __forceinline__ void put_row(const RunArgs& a, int32_t key, int col, const float (&acc)[Row<BF16>::kElems]) {
+  using R = Row<BF16>;
+  char* p = a.out + ((int64_t)key * a.d + col) * R::kBytes;
+  if (a.accumulate) {
+    float s[R::kElems];
+#pragma unroll
+    for (int j = 0; j < R::kElems; ++j) s[j] = acc[j];
+    R::add(s, ldg16(p), 1.f);
+    stg16(p, R::pack(s));
+  } else {
+    stg16(p, R::pack(acc));
+  }
+}
+
+template <bool BF16>
+__device__ __forceinline__ void put_part(const RunArgs& a, int32_t chunk, int slot, int col,
+                                         const float (&acc)[Row<BF16>::kElems]) {
+  float* p = a.part + ((int64_t)chunk * 2 + slot) * a.d + col;
+#pragma unroll
+  for (int j = 0; j < Row<BF16>::kElems; j += 4)
+    stg16(p + j, make_uint4(__float_as_uint(acc[j]), __float_as_uint(acc[j + 1]), __float_as_uint(acc[j + 2]),
+                            __float_as_uint(acc[j + 3])));
+}
+
+constexpr int kRowsAhead = 8;    // rows a wave loads ahead of adding them
+constexpr int kFillRows = 64;    // table rows a clearing block looks at
+
+template <bool BF16, int MODE>
+__global__ __launch_bounds__(256) void k_run_sums(RunArgs a) {
+  using R = Row<BF16>;
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  const int64_t item_blocks = (a.items + 3) / 4;
+  if (MODE == RUN_GRAD && (int64_t)blockIdx.x >= item_blocks) {
+    // clear the rows of ids that do not occur: lane r looks for row v0 + r
+    const int64_t v0 = ((int64_t)blockIdx.x - item_blocks) * kFillRows;
+    const int64_t v = v0 + lane;
+    int32_t lo = 0, hi = a.runs.N;
+    while (lo < hi) {
+      const int32_t mid = lo + (hi - lo) / 2;
+      if (a.runs.keys[mid] < v) lo = mid + 1;
+      else hi = mid;
+    }
+    const bool absent = v < a.runs.V && !(lo < a.runs.N && a.runs.keys[lo] == v);
+    uint64_t m = __ballot(absent);
+    for (int j = 0; m; ++j) {
+      const int r = __builtin_ctzll(m);
+      m &= m - 1;
+      if ((j & 3) != wv) continue;   // the block's waves take rows in turn
+      char* p = a.out + (v0 + r) * a.d * R::kBytes;
+      for (int col = lane * R::kElems; col < a.d; col += R::kSlice) stg16(p + (int64_t)col * R::kBytes, make_uint4(0, 0, 0, 0));
+    }
+    return;
+  }
+  const int64_t item = (int64_t)blockIdx.x * 4 + wv;
+  if (item >= a.items) return;
+  const int32_t chunk = (int32_t)(item / a.slices);
+  const int slice = (int)(item % a.slices);
+  const int col = slice * R::kSlice + lane * R::kElems;
+  const bool on = col < a.d;
+  bool cut0, cut1;
+  const int32_t x0 = boundary<MODE>(a.runs, (int64_t)chunk * a.runs.R, cut0);
+  const int32_t x1 = boundary<MODE>(a.runs, ((int64_t)chunk + 1) * a.runs.R, cut1);
+  const int len = x1 - x0;   // at most 2 R - 1 <= 63
+  // lane j describes sorted position x0 + j
+  // (values outside the batch or the table, which no order of this batch holds, are kept in bounds)
+  const int32_t mine = lane < len ? in_batch(a.runs, a.runs.pos[x0 + lane]) : 0;
+  const int32_t mkey = lane < len ? in_table(a.runs, a.runs.keys[x0 + lane]) : a.runs.V;
+  const uint64_t rows = __ballot(mkey < a.runs.V);   // the first ones: V sorts last
+  const uint64_t starts = __ballot(lane < len && run_starts<MODE>(a.runs, x0 + lane));
+  const int n = __popcll(rows);
+  if (MODE == RUN_NORM) {
+    // every position's value is written once: 0 unless it starts a run
+    if (lane < len && !(mkey < a.runs.V && ((starts >> lane) & 1))) a.val[(int64_t)slice * a.runs.N + mine] = 0.f;
+  }
+  if (n == 0) return;
+  float wgt = 1.f;
+  if (MODE == RUN_GRAD) wgt = a.c && lane < n ? a.scale * a.c[mine / a.runs.T] : a.scale;
+  float acc[R::kElems] = {};
+  int first = 0;
+  for (int j0 = 0; j0 < n; j0 += kRowsAhead) {
+    uint4 v[kRowsAhead];
+#pragma unroll
+    for (int u = 0; u < kRowsAhead; ++u) {
+      v[u] = make_uint4(0, 0, 0, 0);
+      if (j0 + u < n && on) {
+        const int32_t q = __builtin_amdgcn_readlane(mine, j0 + u);
+        v[u] = ldg16(a.G + ((int64_t)q * a.d + col) * R::kBytes);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kRowsAhead; ++u) {
+      const int j = j0 + u;
+      if (j < n) {
+        float w = 1.f;
+        if (MODE == RUN_GRAD) w = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wgt), j));
+        R::add(acc, v[u], w);
+        // the run ends here, or the chunk does
+        if (j + 1 == n || ((starts >> (j + 1)) & 1)) {
+          const bool head = first == 0 && cut0;                 // started before the chunk
+          const bool tail = j + 1 == len && cut1;               // goes on after it
+          if (head || tail) {
+            if (on) put_part<BF16>(a, chunk, head ? 0 : 1, col, acc);
+          } else if (MODE == RUN_NORM) {
+            float s = 0.f;
+#pragma unroll
+            for (int e = 0; e < R::kElems; ++e) s = fmaf(acc[e], acc[e], s);
+            s = wave_sum_f32(s);
+            if (lane == 0) a.val[(int64_t)slice * a.runs.N + __builtin_amdgcn_readlane(mine, first)] = s;
+          } else if (on) {
+            put_row<BF16>(a, __builtin_amdgcn_readlane(mkey, first), col, acc);
+          }
+          first = j + 1;
+#pragma unroll
+          for (int e = 0; e < R::kElems; ++e) acc[e] = 0.f;
+        }
+      }
+    }
+  }
+}
+
+// Joins the pieces of each cut run: the block of the chunk that the run starts
+// in adds that chunk's tail and the heads of the chunks after it, four waves
+// in turn, their sums added in wave order.
+template <bool BF16, int MODE>
+__global__ __launch_bounds__(256) void k_run_join(RunArgs a) {
+  using R = Row<BF16>;
+  __shared__ float sums[3][R::kElems][kWave];
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  const int32_t chunk = (int32_t)(blockIdx.x / a.slices);
+  const int slice = (int)(blockIdx.x % a.slices);
+  bool cut0, cut1;
+  const int64_t x = ((int64_t)chunk + 1) * a.runs.R;
+  boundary<MODE>(a.runs, x, cut1);
+  if (!cut1) return;
+  const int32_t x0 = boundary<MODE>(a.runs, (int64_t)chunk * a.runs.R, cut0);
+  // the run at x started in this chunk unless the chunk holds it whole, cut on both sides
+  const uint64_t inner = __ballot(lane < x - x0 && run_starts<MODE>(a.runs, x0 + lane));
+  if (inner == 0) return;
+  const int32_t s = x0 + 63 - __builtin_clzll(inner);
+  const int32_t key = in_table(a.runs, a.runs.keys[s]);
+  if (key >= a.runs.V) return;
+  const int32_t e = run_end<MODE>(a.runs, (int32_t)x);
+  const int32_t last = min(e / a.runs.R, a.runs.chunks) - 1;   // the last boundary with R positions of the run behind it
+  const int col = slice * R::kSlice + lane * R::kElems;
+  const bool on = col < a.d;
+  float acc[R::kElems] = {};
+  if (on) {
+    for (int32_t ch = chunk + wv; ch <= last; ch += 4) {
+      const float* p = a.part + ((int64_t)ch * 2 + (ch == chunk ? 1 : 0)) * a.d + col;
+#pragma unroll
+      for (int j = 0; j < R::kElems; j += 4) {
+        const float4 f = ldg_f32x4(p + j);
+        acc[j] += f.x;
+        acc[j + 1] += f.y;
+        acc[j + 2] += f.z;
+        acc[j + 3] += f.w;
+      }
+    }
+  }
+  if (wv > 0) {
+#pragma unroll
+    for (int j = 0; j < R::kElems; ++j) sums[wv - 1][j][lane] = acc[j];
+  }
+  __syncthreads();
+  if (wv > 0) return;
+#pragma unroll
+  for (int w = 0; w < 3; ++w)
+#pragma unroll
+    for (int j = 0; j < R::kElems; ++j) acc[j] += sums[w][j][lane];
+  if (MODE == RUN_NORM) {
+    float t = 0.f;
+#pragma unroll
+    for (int j = 0; j < R::kElems; ++j) t = fmaf(acc[j], acc[j], t);
+    t = wave_sum_f32(t);
+    if (lane == 0) a.val[(int64_t)slice * a.runs.N + in_batch(a.runs, a.runs.pos[s])] = t;
+  } else if (on) {
+    put_row<BF16>(a, key, col, acc);
+  }
+}
+
+// n_i (+)= s^2 times the sum of the sample's values, in fp64.
+__global__ __launch_bounds__(1024) void k_norm_sum(const float* val, int64_t N, int32_t T, int32_t slices, double scale2,
+                                                   float* n, int accumulate) {
+  __shared__ double part[16];
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  double s = 0.0;
+  for (int sl = 0; sl < slices; ++sl) {
+    const float* p = val + (int64_t)sl * N + (int64_t)blockIdx.x * T;
+    for (int t = threadIdx.x; t < T; t += 1024) s += (double)p[t];
+  }
+  s = wave_sum(s);
+  if (lane == 0) part[wv] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double t = 0.0;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) t += part[w];
+    t *= scale2;
+    n[blockIdx.x] = (float)(accumulate ? (double)n[blockIdx.x] + t : t);
+  }
+}
+
+}  // namespace embed
+}  // namespace dpn

@@ -1,0 +1,204 @@
+"""The C ABI of the embedding and attention calls without a GPU: sizes of
+orders and workspaces, and every host-side check returning its documented
+status before anything is enqueued (every call here fails a check). The file
+also runs against the host layer built with sanitizers."""
+import ctypes as C
+import os
+import subprocess
+import sys
+
+import pytest
+
+from sample_grad_norms_amd import _lib
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+TOK, W, OUT, ORDER, G, N, CW, WS = (0x10000000 * j for j in range(1, 9))   # aligned addresses, never read
+BIG = 1 << 40
+
+
+def order_sizes(lib, B=3, T=100, V=50):
+    ob, wb = C.c_size_t(0), C.c_size_t(0)
+    return lib.dpnorm_embed_order_sizes(B, T, V, C.byref(ob), C.byref(wb)), ob.value, wb.value
+
+
+def test_order_sizes(lib):
+    st, ob, wb = order_sizes(lib)
+    assert st == _lib.OK and ob >= 3 * 100 * 8 and ob % 256 == 0 and wb == 0
+    st, ob, wb = order_sizes(lib, 4, 4096, 131072)
+    assert st == _lib.OK and ob >= 4 * 4096 * 8 and wb >= 4 * 4096 * 8
+    for bad in ((0, 1, 1), (1, 0, 1), (1, 1, 0), (1, 1, 2 ** 30 + 1), (2 ** 16, 2 ** 15, 1), (2 ** 62, 2 ** 62, 1), (-1, 5, 5)):
+        assert order_sizes(lib, *bad)[0] == _lib.ERR_SIZE
+    assert lib.dpnorm_embed_order_sizes(1, 1, 1, None, None) == _lib.ERR_NULL
+
+
+def test_lookup_checks(lib):
+    def call(tok=TOK, it=_lib.I64, w=W, dt=_lib.BF16, n=300, v=50, d=64, scale=1.0, out=OUT):
+        return lib.dpnorm_embed_lookup(tok, it, w, dt, n, v, d, scale, out, None)
+    assert call(tok=None) == call(w=None) == call(out=None) == _lib.ERR_NULL
+    assert call(dt=2) == call(it=2) == call(it=-1) == _lib.ERR_DTYPE
+    assert call(n=0) == call(v=0) == call(d=0) == call(d=12) == call(d=2 ** 25) == call(n=2 ** 30 + 1) == _lib.ERR_SIZE
+    assert call(dt=_lib.F32, d=6) == _lib.ERR_SIZE
+    assert call(tok=TOK + 4) == call(w=W + 8) == call(out=OUT + 2) == _lib.ERR_ALIGN
+    assert call(scale=float("nan")) == call(scale=float("-inf")) == _lib.ERR_VALUE
+    assert call(out=W) == call(out=TOK) == call(out=W + 50 * 64 * 2 - 16) == _lib.ERR_VALUE
+
+
+def test_order_checks(lib):
+    _, ob, _ = order_sizes(lib)
+    _, ob2, wb2 = order_sizes(lib, 4, 4096, 1000)
+
+    def call(tok=TOK, it=_lib.I32, B=3, T=100, V=50, order=ORDER, size=ob, ws=None, ws_size=0):
+        return lib.dpnorm_embed_order(tok, it, B, T, V, order, size, ws, ws_size, None)
+    assert call(tok=None) == call(order=None) == _lib.ERR_NULL
+    assert call(it=5) == _lib.ERR_DTYPE
+    assert call(B=0) == call(V=-1) == _lib.ERR_SIZE
+    assert call(tok=TOK + 2) == call(order=ORDER + 16) == _lib.ERR_ALIGN
+    assert call(it=_lib.I64, tok=TOK + 4) == _lib.ERR_ALIGN
+    assert call(size=ob - 1) == _lib.ERR_WORKSPACE
+    assert call(order=TOK) == _lib.ERR_VALUE
+    big = dict(B=4, T=4096, V=1000, size=ob2, ws=WS, ws_size=wb2)
+    assert call(**{**big, "ws": None}) == _lib.ERR_NULL
+    assert call(**{**big, "ws_size": wb2 - 1}) == _lib.ERR_WORKSPACE
+    assert call(**{**big, "ws": WS + 64}) == _lib.ERR_ALIGN
+    assert call(**{**big, "ws": ORDER}) == call(**{**big, "ws": TOK}) == _lib.ERR_VALUE
+
+
+@pytest.mark.parametrize("which", ["norm", "grad"])
+def test_norm_and_grad_checks(lib, which):
+    query = getattr(lib, f"dpnorm_embed_{which}_workspace")
+    nb = C.c_size_t(0)
+    assert query(_lib.BF16, 3, 100, 50, 64, C.byref(nb)) == _lib.OK and nb.value > 0 and nb.value % 256 == 0
+    assert query(_lib.BF16, 3, 100, 50, 64, None) == _lib.ERR_NULL
+    assert query(7, 3, 100, 50, 64, C.byref(nb)) == _lib.ERR_DTYPE
+    for bad in ((0, 100, 50, 64), (3, 100, 0, 64), (3, 100, 50, 60), (2 ** 20, 2 ** 11, 5, 8), (1, 2 ** 30, 1, 2 ** 24)):
+        assert query(_lib.BF16, *bad, C.byref(nb)) == _lib.ERR_SIZE
+
+    def call(order=ORDER, g=G, dt=_lib.BF16, B=3, T=100, V=50, d=64, scale=1.0, out=OUT, c=CW, acc=0, ws=WS, ws_size=BIG):
+        if which == "norm":
+            return lib.dpnorm_embed_norm(order, g, dt, B, T, V, d, scale, out, acc, ws, ws_size, None)
+        return lib.dpnorm_embed_grad(order, g, dt, B, T, V, d, scale, c, out, acc, ws, ws_size, None)
+    assert call(order=None) == call(g=None) == call(out=None) == call(ws=None) == _lib.ERR_NULL
+    assert call(dt=-3) == _lib.ERR_DTYPE
+    assert call(T=0) == call(d=4) == _lib.ERR_SIZE
+    assert call(order=ORDER + 4) == call(g=G + 8) == call(out=OUT + 2) == call(ws=WS + 16) == _lib.ERR_ALIGN
+    assert call(scale=float("inf")) == call(acc=2) == call(acc=-1) == _lib.ERR_VALUE
+    assert call(ws_size=nb.value - 1 if which == "norm" else 255) == _lib.ERR_WORKSPACE
+    assert call(out=G) == call(out=ORDER) == call(out=WS) == call(ws=G) == call(ws=ORDER) == _lib.ERR_VALUE
+    if which == "grad":
+        assert call(c=CW + 2) == _lib.ERR_ALIGN
+        assert call(c=OUT) == call(c=WS) == _lib.ERR_VALUE
+
+
+Q, K, V_, O, LSE, DO, DQ, DK, DV, CU = (0x100000000 * j for j in range(1, 11))
+
+
+def shape(dtype=_lib.BF16, n=200, s=2, hq=4, hkv=2, d=64, cu=CU, scale=0.125):
+    return _lib.AttnShape(dtype, n, s, hq, hkv, d, cu, scale)
+
+
+def tensor(p, h, d=64, st=None, sh=None):
+    return _lib.AttnTensor(p, h * d if st is None else st, d if sh is None else sh)
+
+
+def forward(lib, sh=None, q=None, k=None, v=None, o=None, lse=LSE):
+    args = [q or tensor(Q, 4), k or tensor(K, 2), v or tensor(V_, 2), o or tensor(O, 4)]
+    return lib.dpnorm_attention_forward(C.byref(sh or shape()), *(C.byref(t) for t in args), lse, None)
+
+
+def test_attention_forward_checks(lib):
+    assert lib.dpnorm_attention_forward(None, None, None, None, None, None, None) == _lib.ERR_NULL
+    assert lib.dpnorm_attention_forward(C.byref(shape()), None, None, None, None, LSE, None) == _lib.ERR_NULL
+    assert forward(lib, lse=None) == forward(lib, q=tensor(None, 4)) == forward(lib, o=tensor(None, 4)) == _lib.ERR_NULL
+    assert forward(lib, shape(dtype=2)) == _lib.ERR_DTYPE
+    for bad in (dict(n=0), dict(s=0), dict(hq=0), dict(hkv=0), dict(hkv=3), dict(d=0), dict(d=136), dict(d=12),
+                dict(n=2 ** 31), dict(s=2 ** 31), dict(hq=2 ** 17, hkv=1), dict(n=201, cu=None), dict(n=2 ** 30, hq=512, hkv=1)):
+        assert forward(lib, shape(**bad)) == _lib.ERR_SIZE, bad
+    assert forward(lib, shape(cu=CU + 2)) == _lib.ERR_ALIGN
+    for scale in (0.0, -1.0, float("nan"), float("inf")):
+        assert forward(lib, shape(scale=scale)) == _lib.ERR_VALUE
+    assert forward(lib, q=tensor(Q + 8, 4)) == forward(lib, lse=LSE + 2) == _lib.ERR_ALIGN
+    assert forward(lib, k=tensor(K, 2, st=129)) == forward(lib, k=tensor(K, 2, sh=68)) == _lib.ERR_ALIGN
+    assert forward(lib, v=tensor(V_, 2, st=-128)) == forward(lib, v=tensor(V_, 2, st=2 ** 23)) == _lib.ERR_SIZE
+    # outputs that repeat rows, or lie on inputs or on each other
+    assert forward(lib, o=tensor(O, 4, st=0)) == forward(lib, o=tensor(O, 4, sh=0)) == _lib.ERR_VALUE
+    assert forward(lib, o=tensor(O, 4, st=64, sh=64)) == forward(lib, o=tensor(O, 4, st=192)) == _lib.ERR_VALUE
+    assert forward(lib, o=tensor(Q, 4)) == forward(lib, o=tensor(V_, 4)) == forward(lib, o=tensor(CU, 4)) == _lib.ERR_VALUE
+    assert forward(lib, lse=O) == forward(lib, lse=K) == forward(lib, o=tensor(Q + (200 * 256 - 64) * 2, 4)) == _lib.ERR_VALUE
+
+
+def test_attention_backward_checks(lib):
+    nb = C.c_size_t(0)
+    assert lib.dpnorm_attention_backward_workspace(C.byref(shape()), C.byref(nb)) == _lib.OK
+    assert nb.value >= 200 * 4 * 4 and nb.value % 256 == 0
+    assert lib.dpnorm_attention_backward_workspace(C.byref(shape()), None) == _lib.ERR_NULL
+    assert lib.dpnorm_attention_backward_workspace(None, C.byref(nb)) == _lib.ERR_NULL
+    assert lib.dpnorm_attention_backward_workspace(C.byref(shape(d=7)), C.byref(nb)) == _lib.ERR_SIZE
+
+    base = dict(do=tensor(DO, 4), q=tensor(Q, 4), k=tensor(K, 2), v=tensor(V_, 2), o=tensor(O, 4), dq=tensor(DQ, 4),
+                dk=tensor(DK, 2), dv=tensor(DV, 2))
+
+    def call(lse=LSE, ws=WS, size=BIG, sh=None, **kw):
+        a = {**base, **kw}
+        return lib.dpnorm_attention_backward(C.byref(sh or shape()), C.byref(a["do"]), C.byref(a["q"]), C.byref(a["k"]),
+                                             C.byref(a["v"]), C.byref(a["o"]), lse, C.byref(a["dq"]), C.byref(a["dk"]),
+                                             C.byref(a["dv"]), ws, size, None)
+    assert call(lse=None) == call(ws=None) == call(do=tensor(None, 4)) == call(dv=tensor(None, 2)) == _lib.ERR_NULL
+    assert call(ws=WS + 8) == call(lse=LSE + 1) == call(dk=tensor(DK + 8, 2)) == call(do=tensor(DO, 4, st=257)) == _lib.ERR_ALIGN
+    assert call(size=nb.value - 1) == _lib.ERR_WORKSPACE
+    assert call(o=tensor(O, 4, st=-8)) == call(sh=shape(d=200)) == _lib.ERR_SIZE
+    assert call(dq=tensor(DQ, 4, st=0)) == call(dk=tensor(DK, 2, sh=0)) == _lib.ERR_VALUE
+    for name in ("q", "k", "v", "o", "do"):
+        assert call(dq=tensor(base[name].data, 4)) == _lib.ERR_VALUE
+        assert call(ws=base[name].data) == _lib.ERR_VALUE
+    assert call(dv=tensor(DK, 2)) == call(dk=tensor(LSE, 2)) == call(ws=DQ) == _lib.ERR_VALUE
+
+
+@pytest.mark.skipif("DPNORM_TEST_LIB" in os.environ, reason="already the sanitized library")
+def test_under_sanitizers(tmp_path):
+    """This file and valid calls of every entry point against the host layer
+    built with AddressSanitizer and UndefinedBehaviorSanitizer."""
+    sys.path.insert(0, os.path.join(HERE, "hostcheck"))
+    import build as hostcheck_build
+    built = hostcheck_build.build(str(tmp_path))
+    env = dict(os.environ, LD_PRELOAD=built["asan_runtime"], ASAN_OPTIONS="detect_leaks=0",
+               UBSAN_OPTIONS="print_stacktrace=1:halt_on_error=1", DPNORM_TEST_LIB=built["lib"])
+    res = subprocess.run([sys.executable, "-m", "pytest", "-q", "-p", "no:cacheprovider", os.path.abspath(__file__)],
+                         capture_output=True, text=True, timeout=600, env=env, cwd=os.path.dirname(HERE))
+    assert res.returncode == 0, res.stdout[-4000:] + res.stderr[-4000:]
+
+
+@pytest.mark.skipif("DPNORM_TEST_LIB" not in os.environ, reason="launches are only counted by the sanitized library's stand-in")
+@pytest.mark.parametrize("seed", range(40))
+def test_valid_calls_launch_valid_grids(lib, seed):
+    """Random valid sizes up to the limits: the call succeeds with the queried
+    workspace (a launch that the stand-in refuses fails the call)."""
+    import random
+    rng = random.Random(seed)
+
+    def log(lo, hi):
+        return int(lo * (hi / lo) ** rng.random())
+    dt = rng.choice([_lib.BF16, _lib.F32])
+    B, V, d = log(1, 300), log(1, 2 ** 30), 8 * log(1, 1000)
+    T = log(1, 2 ** 24 // B)
+    st, ob, wb = order_sizes(lib, B, T, V)
+    assert st == _lib.OK
+    far = 1 << 44
+    p = [far * (j + 1) for j in range(12)]
+    assert lib.dpnorm_embed_order(p[0], _lib.I64, B, T, V, p[1], ob, p[2], wb, None) == _lib.OK
+    nb = C.c_size_t(0)
+    st = lib.dpnorm_embed_norm_workspace(dt, B, T, V, d, C.byref(nb))
+    assert st in (_lib.OK, _lib.ERR_SIZE)
+    assert lib.dpnorm_embed_norm(p[1], p[3], dt, B, T, V, d, 2.0, p[4], 0, p[5], nb.value, None) == st
+    assert lib.dpnorm_embed_grad_workspace(dt, B, T, V, d, C.byref(nb)) == st
+    assert lib.dpnorm_embed_grad(p[1], p[3], dt, B, T, V, d, 2.0, p[6], p[7], seed % 2, p[5], nb.value, None) == st
+    assert lib.dpnorm_embed_lookup(p[0], _lib.I32, p[7], dt, B * T, V, d, 1.0, p[8], None) == _lib.OK
+    hkv = rng.choice([1, 2, 3, 8])
+    hq, D, S = hkv * rng.randint(1, 8), 8 * rng.randint(1, 16), log(1, 5000)
+    n = log(1, 2 ** 22)
+    sh = shape(dt, n, S, hq, hkv, D, p[9])
+    ten = [tensor(x, h, D) for x, h in ((p[0], hq), (p[1], hkv), (p[2], hkv), (p[3], hq), (p[4], hq), (p[5], hq), (p[6], hkv),
+                                        (p[7], hkv))]
+    q, k, v, o, do, dq, dk, dv = (C.byref(t) for t in ten)
+    assert lib.dpnorm_attention_forward(C.byref(sh), q, k, v, o, p[8], None) == _lib.OK
+    assert lib.dpnorm_attention_backward_workspace(C.byref(sh), C.byref(nb)) == _lib.OK
+    assert lib.dpnorm_attention_backward(C.byref(sh), do, q, k, v, o, p[8], dq, dk, dv, p[10], nb.value, None) == _lib.OK
