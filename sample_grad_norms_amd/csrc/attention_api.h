@@ -34,7 +34,7 @@ dpnorm_status check_shape(const dpnorm_attn_shape* s) {
   if (!aligned(s->cu_seqlens, 4)) return DPNORM_ERR_ALIGN;
   if (!(s->scale > 0.f) || !std::isfinite(s->scale)) return DPNORM_ERR_VALUE;
   // a block a head and slot: the grid's x dimension holds them
-  if ((s->N / attn::kRows + s->S + 1) * s->Hq > 0x7fffffff) return DPNORM_ERR_SIZE;
+  if ((s->N / 32 + s->S + 1) * s->Hq > 0x7fffffff) return DPNORM_ERR_SIZE;
   return DPNORM_OK;
 }
 
@@ -65,9 +65,6 @@ attn::Args attn_args(const dpnorm_attn_shape* s) {
   a.Hkv = (int32_t)s->Hkv;
   a.D = (int32_t)s->D;
   a.scale = s->scale;
-  // sequences of any lengths have at most N / rows + S tiles
-  const int64_t per = (a.T + attn::kRows - 1) / attn::kRows;
-  a.slots = (int32_t)(s->cu_seqlens ? s->N / attn::kRows + s->S : s->S * per);
   return a;
 }
 
@@ -86,17 +83,47 @@ bool outputs_overlap(const std::vector<Region>& in, const std::vector<Region>& o
   return false;
 }
 
-template <bool BF16, int DP>
-hipError_t launch_attn_forward(const attn::Args& a, hipStream_t stream) {
-  attn::k_forward<BF16, DP><<<(uint32_t)(a.slots * a.Hq), attn::kThreads, 0, stream>>>(a);
+// Slots of tiles of `rows` rows: sequences of any lengths have at most
+// N / rows + S of them.
+int64_t slots_of(const attn::Args& a, int rows) {
+  return a.cu ? (int64_t)a.N / rows + a.S : (int64_t)a.S * ((a.T + rows - 1) / rows);
+}
+
+template <bool BF16, int DC, int GR, int NS>
+hipError_t launch_attn_forward(attn::Args a, hipStream_t stream) {
+  using P = attn::Split<BF16, DC, GR, NS>;
+  a.slots = (int32_t)slots_of(a, P::kRows);
+  attn::k_forward<BF16, DC, GR, NS><<<(uint32_t)((int64_t)a.slots * a.Hq), P::kThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 
-template <bool BF16, int DP>
-hipError_t launch_attn_backward(const attn::Args& a, hipStream_t stream) {
-  attn::k_backward_q<BF16, DP><<<(uint32_t)(a.slots * a.Hq), attn::kThreads, 0, stream>>>(a);
-  attn::k_backward_kv<BF16, DP><<<(uint32_t)(a.slots * a.Hkv), attn::kThreads, 0, stream>>>(a);
+template <bool BF16, int DC, int GR, int NS>
+hipError_t launch_attn_backward_q(attn::Args a, hipStream_t stream) {
+  using P = attn::Split<BF16, DC, GR, NS>;
+  a.slots = (int32_t)slots_of(a, P::kRows);
+  attn::k_backward_q<BF16, DC, GR, NS><<<(uint32_t)((int64_t)a.slots * a.Hq), P::kThreads, 0, stream>>>(a);
   return hipGetLastError();
+}
+
+template <bool BF16, int DC, int GR, int NS>
+hipError_t launch_attn_backward_kv(attn::Args a, hipStream_t stream) {
+  using P = attn::Split<BF16, DC, GR, NS>;
+  a.slots = (int32_t)slots_of(a, P::kRows);
+  attn::k_backward_kv<BF16, DC, GR, NS><<<(uint32_t)((int64_t)a.slots * a.Hkv), P::kThreads, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+template <bool BF16, int DC>
+hipError_t run_attn_forward(const attn::Args& a, hipStream_t stream) {
+  return launch_attn_forward<BF16, DC, 4, 1>(a, stream);
+}
+
+template <bool BF16, int DC>
+hipError_t run_attn_backward(const attn::Args& a, hipStream_t stream) {
+  hipError_t he = launch_attn_backward_q<BF16, DC, 4, 1>(a, stream);
+  if (he != hipSuccess) return he;
+  if constexpr (BF16) return launch_attn_backward_kv<BF16, DC, 4, 2>(a, stream);
+  else return launch_attn_backward_kv<BF16, DC, 2, 2>(a, stream);
 }
 
 }  // namespace
@@ -126,17 +153,18 @@ dpnorm_status dpnorm_attention_forward(const dpnorm_attn_shape* shape, const dpn
   a.v = tensor_of(v, e);
   a.o = tensor_of(o, e);
   a.lse = lse;
-  const bool wide = D > 64;
   if (shape->dtype == DPNORM_BF16)
-    return hip_status(wide ? launch_attn_forward<true, 128>(a, stream) : launch_attn_forward<true, 64>(a, stream));
-  return hip_status(wide ? launch_attn_forward<false, 128>(a, stream) : launch_attn_forward<false, 64>(a, stream));
+    return hip_status(D <= 64 ? run_attn_forward<true, 64>(a, stream) : D <= 96 ? run_attn_forward<true, 96>(a, stream)
+                                                                           : run_attn_forward<true, 128>(a, stream));
+  return hip_status(D <= 64 ? run_attn_forward<false, 64>(a, stream) : D <= 96 ? run_attn_forward<false, 96>(a, stream)
+                                                                          : run_attn_forward<false, 128>(a, stream));
 }
 
 dpnorm_status dpnorm_attention_backward_workspace(const dpnorm_attn_shape* shape, size_t* bytes) {
   if (!bytes) return DPNORM_ERR_NULL;
   const dpnorm_status st = check_shape(shape);
   if (st != DPNORM_OK) return st;
-  *bytes = align_up((size_t)shape->N * shape->Hq * 4);
+  *bytes = 2 * align_up((size_t)shape->N * shape->Hq * 4);
   return DPNORM_OK;
 }
 
@@ -176,10 +204,12 @@ dpnorm_status dpnorm_attention_backward(const dpnorm_attn_shape* shape, const dp
   a.dv = tensor_of(dv, e);
   a.lse = const_cast<float*>(lse);
   a.delta = (float*)ws;
-  const bool wide = D > 64;
+  a.lse2 = (float*)((char*)ws + bytes / 2);
   if (shape->dtype == DPNORM_BF16)
-    return hip_status(wide ? launch_attn_backward<true, 128>(a, stream) : launch_attn_backward<true, 64>(a, stream));
-  return hip_status(wide ? launch_attn_backward<false, 128>(a, stream) : launch_attn_backward<false, 64>(a, stream));
+    return hip_status(D <= 64 ? run_attn_backward<true, 64>(a, stream) : D <= 96 ? run_attn_backward<true, 96>(a, stream)
+                                                                           : run_attn_backward<true, 128>(a, stream));
+  return hip_status(D <= 64 ? run_attn_backward<false, 64>(a, stream) : D <= 96 ? run_attn_backward<false, 96>(a, stream)
+                                                                          : run_attn_backward<false, 128>(a, stream));
 }
 
 }  // extern "C"

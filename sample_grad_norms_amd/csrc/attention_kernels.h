@@ -43,7 +43,8 @@ struct Tensor {     // [token][head][D], strides in bytes
 struct Args {
   Tensor q, k, v, o, dO, dq, dk, dv;
   float* lse;         // [Hq][N]
-  float* delta;       // [Hq][N], backward
+  float* delta;       // [Hq][N], backward: written with lse2 by the first launch for the second
+  float* lse2;        // [Hq][N], lse in units of log 2
   const int32_t* cu;  // [S + 1], or null: S sequences of T tokens
   int32_t S, T, N;
   int32_t Hq, Hkv, D;
@@ -51,9 +52,6 @@ struct Args {
   int32_t slots;      // tile slots per head
 };
 
-constexpr int kThreads = 256;
-constexpr int kRows = 128;   // stationary rows of a work group: 32 a wave
-constexpr int kStep = 64;    // streamed rows a step
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint32_t kOutside = 0x80000000u;   // an offset past every buffer's range: reads as zero
 
@@ -100,66 +98,90 @@ __device__ __forceinline__ bool find_tile(const Args& a, int32_t slot, int rows,
   return false;
 }
 
-template <bool BF16, int DP>
+// DC: columns computed, 64, 96 or 128 (D filled up with zeros).
+template <bool BF16, int DC>
 struct Geo {
   static constexpr int kElem = BF16 ? 2 : 4;
-  static constexpr int kChunks = DP * kElem / 16;    // 16-byte chunks of a row
-  static constexpr int kPairs = kChunks / 2;         // chunk pairs: one chunk for each half of the wave
-  static constexpr int kPitch = DP * kElem;          // LDS bytes of a row
-  static constexpr int kTiles = DP / 32;             // 32-column tiles of a row
-  static constexpr int kStage = kStep * kPitch;
+  static constexpr int kPitch = (DC == 96 ? 128 : DC) * kElem;   // LDS bytes of a row
+  static constexpr int kChunks = kPitch / 16;                    // 16-byte chunks of an LDS row
+  static constexpr int kPairs = DC * kElem / 32;                 // chunk pairs: one chunk for each half of the wave
+  static constexpr int kTiles = DC / 32;                         // 32-column tiles of a row
 };
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const char* p) {
-  return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, 0x7fffffff, 0x00027000);
+// Buffer descriptor of the rows from p on (wave-uniform): raw, no stride, all
+// that an offset below 2^31 reaches.
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ i32x4_t rows_of(const char* p) {
+  const uint64_t u = (uint64_t)p;
+  i32x4_t r;
+  r.x = __builtin_amdgcn_readfirstlane((int)(uint32_t)u);
+  r.y = __builtin_amdgcn_readfirstlane((int)(uint32_t)(u >> 32) & 0xffff);
+  r.z = 0x7fffffff;
+  r.w = 0x00027000;
+  return r;
 }
 
-// Pointer to row `row` of sequence start `start`, head h (all wave-uniform).
+// Pointer to row `row` of the tensor, head h (all wave-uniform).
 __device__ __forceinline__ char* row_ptr(const Tensor& t, int64_t row, int32_t h) { return t.p + row * t.st + h * t.sh; }
 
-// Rows r0 .. r0 + 63 of a sequence into LDS, row-major with the 16-byte chunks
-// of row r at chunk ^ (r & 7): reads of one chunk of eight rows then fall on
-// different banks. Rows past `len` and columns past D read as zero.
-template <bool BF16, int DP>
+// 16 or 4 bytes a lane from a buffer straight to LDS at lds + 16 (4) * lane.
+// Written out so that the compiler adds no waits for them: `staged` waits.
+__device__ __forceinline__ void dma_rows(i32x4_t rows, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(off), "s"(rows),
+               "s"(__builtin_amdgcn_readfirstlane(lds))
+               : "memory");
+}
+__device__ __forceinline__ void dma_words(i32x4_t rows, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds" ::"v"(off), "s"(rows),
+               "s"(__builtin_amdgcn_readfirstlane(lds))
+               : "memory");
+}
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
+}
+
+// ROWS rows from r0 on of a sequence into LDS by W waves, row-major with the
+// 16-byte chunks of row r at chunk ^ (r & 7): reads of one chunk of eight rows
+// then fall on different banks. Rows past `len` and columns past D read as zero.
+template <bool BF16, int DC, int ROWS, int W>
 __device__ __forceinline__ void stage(const Tensor& t, int64_t start, int32_t h, int32_t r0, int32_t len, int32_t D,
-                                      unsigned char* lds) {
-  using G = Geo<BF16, DP>;
-  const __amdgpu_buffer_rsrc_t rs = rows_of(row_ptr(t, start + r0, h));
-  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+                                      uint32_t lds) {
+  using G = Geo<BF16, DC>;
+  const i32x4_t rows = rows_of(row_ptr(t, start + r0, h));
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int32_t left = len - r0;
+  static_assert(ROWS * G::kChunks % (64 * W) == 0, "whole loads of every wave");
 #pragma unroll
-  for (int i = 0; i < kStep * G::kChunks / kThreads; ++i) {
-    const int at = i * kThreads + threadIdx.x;
+  for (int i = 0; i < ROWS * G::kChunks / (64 * W); ++i) {
+    const int at = (i * W + wv) * 64 + lane;
     const int row = at / G::kChunks, ch = (at % G::kChunks) ^ (row & 7);
-    const bool in = r0 + row < len && ch * 16 < D * G::kElem;
-    const uint32_t off = in ? (uint32_t)(row * (int32_t)t.st + ch * 16) : kOutside;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        rs, (__attribute__((address_space(3))) void*)(lds + (i * kThreads + wv * 64) * 16), 16, off, 0, 0, 0);
+    const bool in = row < left && ch * 16 < D * G::kElem;
+    dma_rows(rows, in ? (uint32_t)(row * (int32_t)t.st + ch * 16) : kOutside, lds + (i * W + wv) * 1024);
   }
 }
 
-// The wave's direct loads have landed, and then every wave's.
+// This wave's direct loads have landed, and then every wave's; and every wave
+// has read what it read from LDS before.
 __device__ __forceinline__ void staged() {
   DPN_WAIT_VMCNT(0);
   __syncthreads();
 }
 
-__device__ __forceinline__ uint4 buffer16(__amdgpu_buffer_rsrc_t rs, uint32_t off) {
-  return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0));
-}
-
 // The wave's 32 stationary rows as an operand: lane l has row l % 32, chunk
 // 2 i + l / 32 of pair i.
-template <bool BF16, int DP>
+template <bool BF16, int DC>
 __device__ __forceinline__ void load_operand(const Tensor& t, int64_t start, int32_t h, int32_t r0, int32_t len, int32_t D,
-                                             uint4 (&f)[Geo<BF16, DP>::kPairs]) {
-  using G = Geo<BF16, DP>;
-  const __amdgpu_buffer_rsrc_t rs = rows_of(row_ptr(t, start + r0, h));
+                                             uint4 (&f)[Geo<BF16, DC>::kPairs]) {
+  using G = Geo<BF16, DC>;
+  const __amdgpu_buffer_rsrc_t rs =
+      __builtin_amdgcn_make_buffer_rsrc((void*)row_ptr(t, start + r0, h), 0, 0x7fffffff, 0x00027000);
   const int lane = threadIdx.x & 63, row = lane & 31, g = lane >> 5;
 #pragma unroll
   for (int i = 0; i < G::kPairs; ++i) {
     const int ch = 2 * i + g;
     const bool in = r0 + row < len && ch * 16 < D * G::kElem;
-    f[i] = buffer16(rs, in ? (uint32_t)(row * (int32_t)t.st + ch * 16) : kOutside);
+    f[i] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(
+                                         rs, in ? (uint32_t)(row * (int32_t)t.st + ch * 16) : kOutside, 0, 0));
   }
 }
 
@@ -175,15 +197,15 @@ __device__ __forceinline__ f32x16_t mfma_chunk(const uint4& a, const uint4& b, f
   }
 }
 
-// 32 rows of LDS (at row r0) times the stationary operand: X f^T, 32 x 32.
-template <bool BF16, int DP>
-__device__ __forceinline__ f32x16_t rows_times(const unsigned char* lds, int r0, const uint4 (&f)[Geo<BF16, DP>::kPairs]) {
-  using G = Geo<BF16, DP>;
-  const int lane = threadIdx.x & 63, row = r0 + (lane & 31), g = lane >> 5;
+// 32 rows of LDS (at row r0, a multiple of 8) times the stationary operand: X f^T.
+template <bool BF16, int DC>
+__device__ __forceinline__ f32x16_t rows_times(const unsigned char* lds, int r0, const uint4 (&f)[Geo<BF16, DC>::kPairs]) {
+  using G = Geo<BF16, DC>;
+  const int lane = threadIdx.x & 63, row = lane & 31, g = lane >> 5;
   f32x16_t c = {};
 #pragma unroll
   for (int i = 0; i < G::kPairs; ++i) {
-    const uint4 a = *(const uint4*)(lds + row * G::kPitch + (((2 * i + g) ^ (row & 7)) << 4));
+    const uint4 a = *(const uint4*)(lds + (row * G::kPitch + (((2 * i + g) ^ (row & 7)) << 4)) + r0 * G::kPitch);
     c = mfma_chunk<BF16>(a, f[i], c);
   }
   return c;
@@ -199,33 +221,34 @@ __device__ __forceinline__ uint4 pack_weights(const f32x16_t& w, int j) {
 }
 
 // acc[tile] += (rows r0 .. r0 + 31 of LDS)^T w, where w's rows are those rows.
-template <bool BF16, int DP>
+template <bool BF16, int DC>
 __device__ __forceinline__ void columns_times(const unsigned char* lds, int r0, const f32x16_t& w,
-                                              f32x16_t (&acc)[Geo<BF16, DP>::kTiles]) {
-  using G = Geo<BF16, DP>;
+                                              f32x16_t (&acc)[Geo<BF16, DC>::kTiles]) {
+  using G = Geo<BF16, DC>;
   const int lane = threadIdx.x & 63, g = lane >> 5;
   if constexpr (BF16) {
     const int j = (lane >> 2) & 3, q = lane & 3, m0 = ((lane >> 4) & 1) * 16;
+    const int row = 4 * g + j;
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
       const uint4 b = pack_weights(w, ks * 8);
-      const int ra = r0 + ks * 16 + 4 * g + j, rb = ra + 8;
 #pragma unroll
       for (int t = 0; t < G::kTiles; ++t) {
         const int ch = (t * 32 + m0 + 4 * q) >> 3;
-        const uint2 lo = lds_read_tr16(lds + ra * G::kPitch + ((ch ^ (ra & 7)) << 4) + (q & 1) * 8);
-        const uint2 hi = lds_read_tr16(lds + rb * G::kPitch + ((ch ^ (rb & 7)) << 4) + (q & 1) * 8);
+        const unsigned char* p = lds + (row * G::kPitch + ((ch ^ row) << 4) + (q & 1) * 8) + (r0 + ks * 16) * G::kPitch;
+        const uint2 lo = lds_read_tr16(p), hi = lds_read_tr16(p + 8 * G::kPitch);
         acc[t] = mfma_chunk<true>(make_uint4(lo.x, lo.y, hi.x, hi.y), b, acc[t]);
       }
     }
   } else {
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
-      const int row = r0 + 8 * (r >> 2) + 4 * g + (r & 3);
+      const int row = 4 * g + (r & 3);
 #pragma unroll
       for (int t = 0; t < G::kTiles; ++t) {
         const int col = t * 32 + (lane & 31);
-        const float x = *(const float*)(lds + row * G::kPitch + (((col >> 2) ^ (row & 7)) << 4) + (col & 3) * 4);
+        const float x = *(const float*)(lds + (row * G::kPitch + (((col >> 2) ^ row) << 4) + (col & 3) * 4) +
+                                        (r0 + 8 * (r >> 2)) * G::kPitch);
         acc[t] = __builtin_amdgcn_mfma_f32_32x32x2f32(x, w[r], acc[t], 0, 0, 0);
       }
     }
@@ -237,11 +260,15 @@ __device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32);
 // Row r (0 .. 15) of a lane's half in a 32 x 32 result.
 __device__ __forceinline__ int result_row(int r, int g) { return 8 * (r >> 2) + 4 * g + (r & 3); }
 
+// Keeps a uniform branch a branch: without it the compiler computes the masks
+// of every step, of which one or two at the diagonal need them.
+__device__ __forceinline__ void keep_branch() { asm volatile(""); }
+
 // Columns of acc (transposed: rows are the D index) to row `row` of t, times f.
-template <bool BF16, int DP>
+template <bool BF16, int DC>
 __device__ __forceinline__ void store_rows(const Tensor& t, int64_t row, int32_t h, int32_t D,
-                                           const f32x16_t (&acc)[Geo<BF16, DP>::kTiles], float f) {
-  using G = Geo<BF16, DP>;
+                                           const f32x16_t (&acc)[Geo<BF16, DC>::kTiles], float f) {
+  using G = Geo<BF16, DC>;
   char* p = t.p + row * t.st + h * t.sh;
   const int g = (threadIdx.x & 63) >> 5;
 #pragma unroll
@@ -250,13 +277,14 @@ __device__ __forceinline__ void store_rows(const Tensor& t, int64_t row, int32_t
     for (int r4 = 0; r4 < 4; ++r4) {
       const int col = i * 32 + 8 * r4 + 4 * g;
       if (col >= D) continue;
+      const float x[4] = {acc[i][4 * r4] * f, acc[i][4 * r4 + 1] * f, acc[i][4 * r4 + 2] * f, acc[i][4 * r4 + 3] * f};
       if constexpr (BF16) {
-        uint2 x;
-        x.x = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t){acc[i][4 * r4] * f, acc[i][4 * r4 + 1] * f}, bf16x2_t));
-        x.y = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t){acc[i][4 * r4 + 2] * f, acc[i][4 * r4 + 3] * f}, bf16x2_t));
-        *(uint2*)(p + col * 2) = x;
+        uint2 y;
+        y.x = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t){x[0], x[1]}, bf16x2_t));
+        y.y = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t){x[2], x[3]}, bf16x2_t));
+        *(uint2*)(p + col * 2) = y;
       } else {
-        *(float4*)(p + col * 4) = make_float4(acc[i][4 * r4] * f, acc[i][4 * r4 + 1] * f, acc[i][4 * r4 + 2] * f, acc[i][4 * r4 + 3] * f);
+        *(float4*)(p + col * 4) = make_float4(x[0], x[1], x[2], x[3]);
       }
     }
   }
@@ -271,69 +299,166 @@ __device__ __forceinline__ void block_head(const Args& a, int32_t& h, int32_t& s
   slot = b / a.Hq;
 }
 
-template <bool BF16, int DP>
-__global__ __launch_bounds__(kThreads) void k_forward(Args a) {
-  using G = Geo<BF16, DP>;
-  __shared__ __align__(16) unsigned char lk[G::kStage], lv[G::kStage];
+// Work groups: GR groups of 32 stationary rows, each taken by NS waves that
+// split the streamed rows of a step. With NS = 1 a wave takes 64 rows a step,
+// else 32. The steps' rows are double buffered in LDS where two fit.
+template <bool BF16, int DC, int GR, int NS>
+struct Split {
+  using G = Geo<BF16, DC>;
+  static constexpr int kWaves = GR * NS, kThreads = 64 * kWaves;
+  static constexpr int kRows = 32 * GR;              // stationary rows
+  static constexpr int kSub = NS == 1 ? 2 : 1;       // 32-row tiles of a wave and step
+  static constexpr int kStep = 32 * NS * kSub;       // streamed rows a step
+  static constexpr int kStage = kStep * G::kPitch;   // bytes of one tensor's step
+  static constexpr int kBuffers = 4 * kStage + 4 * kStep * 4 <= 128 * 1024 ? 2 : 1;
+  static constexpr int kWords = 2 * kStep * 4;       // lse2 and delta of a step (dk and dv)
+  static constexpr int kLds = kBuffers * (2 * kStage + kWords);
+  static constexpr int kJoin = 64 * 16 * 4;          // bytes of a wave's 32 x 32 tile
+};
+
+// Adds the accumulators of the waves of one row group, in split order, to the
+// first one's. `lds` is free; every wave of the block calls it.
+template <int GR, int NS, int TILES>
+__device__ __forceinline__ void join(f32x16_t (&acc)[TILES], int grp, int split, unsigned char* lds) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int t = 0; t < TILES; ++t) {
+    __syncthreads();
+    if (split > 0) {
+      f32x4_t* p = (f32x4_t*)(lds + ((split - 1) * GR + grp) * 4096) + lane;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        p[64 * j] = f32x4_t{acc[t][4 * j], acc[t][4 * j + 1], acc[t][4 * j + 2], acc[t][4 * j + 3]};
+    }
+    __syncthreads();
+    if (split == 0) {
+#pragma unroll
+      for (int s = 1; s < NS; ++s) {
+        const f32x4_t* p = (const f32x4_t*)(lds + ((s - 1) * GR + grp) * 4096) + lane;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const f32x4_t x = p[64 * j];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[t][4 * j + i] += x[i];
+        }
+      }
+    }
+  }
+}
+
+template <bool BF16, int DC, int GR, int NS>
+__global__ __launch_bounds__(64 * GR * NS, BF16 ? 2 : 1) void k_forward(Args a) {
+  using G = Geo<BF16, DC>;
+  using P = Split<BF16, DC, GR, NS>;
+  __shared__ __align__(1024) unsigned char lds[P::kBuffers * 2 * P::kStage];
   int32_t h, slot, start, len, tile, tiles;
   block_head(a, h, slot);
-  if (!find_tile(a, slot, kRows, start, len, tile, tiles)) return;
+  if (!find_tile(a, slot, P::kRows, start, len, tile, tiles)) return;
   tile = tiles - 1 - tile;   // the longest rows first
   const int32_t kh = h / (a.Hq / a.Hkv);
   const int lane = threadIdx.x & 63, g = lane >> 5;
-  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int32_t w0 = tile * kRows + wv * 32;   // the wave's first query
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), grp = wv % GR, split = wv / GR;
+  const int32_t w0 = tile * P::kRows + grp * 32;   // the wave's first query
   const int32_t query = w0 + (lane & 31);
+  const uint32_t base = lds_address(lds);
+  const int32_t end = min(tile * P::kRows + P::kRows, len);   // keys that some query of the block sees
+  stage<BF16, DC, P::kStep, P::kWaves>(a.k, start, kh, 0, len, a.D, base);
+  stage<BF16, DC, P::kStep, P::kWaves>(a.v, start, kh, 0, len, a.D, base + P::kStage);
   uint4 q[G::kPairs];
-  load_operand<BF16, DP>(a.q, start, h, w0, len, a.D, q);
+  load_operand<BF16, DC>(a.q, start, h, w0, len, a.D, q);
   const float c = a.scale * kLog2e;
   float m = -INFINITY, l = 0.f;
   f32x16_t acc[G::kTiles] = {};
-  const int32_t end = min(tile * kRows + kRows, len);   // keys that some query of the block sees
-  for (int32_t k0 = 0; k0 < end; k0 += kStep) {
-    __syncthreads();
-    stage<BF16, DP>(a.k, start, kh, k0, len, a.D, lk);
-    stage<BF16, DP>(a.v, start, kh, k0, len, a.D, lv);
-    staged();
-    if (k0 > w0 + 31) continue;
-    f32x16_t s[2];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) s[t] = rows_times<BF16, DP>(lk, t * 32, q);
-    if (k0 + kStep - 1 > w0) {
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int r = 0; r < 16; ++r)
-          if (k0 + t * 32 + result_row(r, g) > query) s[t][r] = -INFINITY;
+  staged();
+  int buf = 0;
+  for (int32_t r0 = 0; r0 < end; r0 += P::kStep) {
+    const bool more = r0 + P::kStep < end;
+    if (P::kBuffers == 2 && more) {
+      const uint32_t to = base + (buf ^ 1) * 2 * P::kStage;
+      stage<BF16, DC, P::kStep, P::kWaves>(a.k, start, kh, r0 + P::kStep, len, a.D, to);
+      stage<BF16, DC, P::kStep, P::kWaves>(a.v, start, kh, r0 + P::kStep, len, a.D, to + P::kStage);
     }
-    float top = s[0][0];
+    const int32_t k0 = r0 + split * 32;   // (one split: 0)
+    if (k0 <= w0 + 31) {
+      const unsigned char* lk = lds + buf * 2 * P::kStage + split * 32 * G::kPitch;
+      const unsigned char* lv = lk + P::kStage;
+      f32x16_t s[P::kSub];
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+      for (int t = 0; t < P::kSub; ++t) s[t] = rows_times<BF16, DC>(lk, t * 32, q);
+      if (k0 + 32 * P::kSub - 1 > w0) {
+        keep_branch();
 #pragma unroll
-      for (int r = 0; r < 16; ++r) top = fmaxf(top, s[t][r]);
-    top = fmaxf(m, fmaxf(top, other_half(top)));
-    const float f = __builtin_amdgcn_exp2f((m - top) * c);
-    const float mc = top * c;
-    m = top;
-    float sum = 0.f;
+        for (int t = 0; t < P::kSub; ++t)
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        s[t][r] = __builtin_amdgcn_exp2f(fmaf(s[t][r], c, -mc));
-        sum += s[t][r];
+          for (int r = 0; r < 16; ++r)
+            if (k0 + t * 32 + result_row(r, g) > query) s[t][r] = -INFINITY;
       }
-    l = fmaf(l, f, sum);
+      float top = s[0][0];
+#pragma unroll
+      for (int t = 0; t < P::kSub; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) top = fmaxf(top, s[t][r]);
+      top = fmaxf(top, other_half(top));
+      // a new largest score of some query rescales the wave's sums
+      if (__any(top > m)) {
+        keep_branch();
+        top = fmaxf(m, top);
+        const float f = top == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - top) * c);
+        m = top;
+        l *= f;
+#pragma unroll
+        for (int t = 0; t < G::kTiles; ++t)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) acc[t][r] *= f;
+      }
+      // (queries that see none of a split's keys so far: every weight 0)
+      const float mc = m == -INFINITY ? 0.f : m * c;
+      float sum = 0.f;
+#pragma unroll
+      for (int t = 0; t < P::kSub; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          s[t][r] = __builtin_amdgcn_exp2f(fmaf(s[t][r], c, -mc));
+          sum += s[t][r];
+        }
+      l += sum;
+#pragma unroll
+      for (int t = 0; t < P::kSub; ++t) columns_times<BF16, DC>(lv, t * 32, s[t], acc);
+    }
+    if (P::kBuffers == 1 && more) {
+      __syncthreads();
+      stage<BF16, DC, P::kStep, P::kWaves>(a.k, start, kh, r0 + P::kStep, len, a.D, base);
+      stage<BF16, DC, P::kStep, P::kWaves>(a.v, start, kh, r0 + P::kStep, len, a.D, base + P::kStage);
+    }
+    staged();
+    if (P::kBuffers == 2) buf ^= 1;
+  }
+  l += other_half(l);
+  if constexpr (NS > 1) {
+    // the splits' sums on the scale of their common largest score
+    float* st = (float*)lds;
+    st[(split * GR + grp) * 64 + lane] = m;
+    __syncthreads();
+    float top = -INFINITY;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) top = fmaxf(top, st[(s * GR + grp) * 64 + lane]);
+    const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - top) * c);
+    m = top;
+    __syncthreads();
+    st[(split * GR + grp) * 64 + lane] = l * f;
+    __syncthreads();
+    l = 0.f;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) l += st[(s * GR + grp) * 64 + lane];
 #pragma unroll
     for (int t = 0; t < G::kTiles; ++t)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[t][r] *= f;
-#pragma unroll
-    for (int t = 0; t < 2; ++t) columns_times<BF16, DP>(lv, t * 32, s[t], acc);
+    join<GR, NS, G::kTiles>(acc, grp, split, lds);
+    if (split > 0) return;
   }
-  l += other_half(l);
   if (query >= len) return;
-  store_rows<BF16, DP>(a.o, (int64_t)start + query, h, a.D, acc, 1.f / l);
+  store_rows<BF16, DC>(a.o, (int64_t)start + query, h, a.D, acc, 1.f / l);
   if (g == 0) a.lse[(int64_t)h * a.N + start + query] = fmaf(m, a.scale, logf(l));
 }
 
@@ -353,123 +478,189 @@ __device__ __forceinline__ float dot_chunk(const uint4& x, const uint4& y, float
   return s;
 }
 
-// dq, and delta for the second launch.
-template <bool BF16, int DP>
-__global__ __launch_bounds__(kThreads) void k_backward_q(Args a) {
-  using G = Geo<BF16, DP>;
-  __shared__ __align__(16) unsigned char lk[G::kStage], lv[G::kStage];
+// dq, and delta and lse2 for the second launch.
+template <bool BF16, int DC, int GR, int NS>
+__global__ __launch_bounds__(64 * GR * NS, BF16 ? 2 : 1) void k_backward_q(Args a) {
+  using G = Geo<BF16, DC>;
+  using P = Split<BF16, DC, GR, NS>;
+  __shared__ __align__(1024) unsigned char lds[P::kBuffers * 2 * P::kStage];
   int32_t h, slot, start, len, tile, tiles;
   block_head(a, h, slot);
-  if (!find_tile(a, slot, kRows, start, len, tile, tiles)) return;
+  if (!find_tile(a, slot, P::kRows, start, len, tile, tiles)) return;
   tile = tiles - 1 - tile;
   const int32_t kh = h / (a.Hq / a.Hkv);
   const int lane = threadIdx.x & 63, g = lane >> 5;
-  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int32_t w0 = tile * kRows + wv * 32;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), grp = wv % GR, split = wv / GR;
+  const int32_t w0 = tile * P::kRows + grp * 32;
   const int32_t query = w0 + (lane & 31);
+  const uint32_t base = lds_address(lds);
+  const int32_t end = min(tile * P::kRows + P::kRows, len);
+  stage<BF16, DC, P::kStep, P::kWaves>(a.k, start, kh, 0, len, a.D, base);
+  stage<BF16, DC, P::kStep, P::kWaves>(a.v, start, kh, 0, len, a.D, base + P::kStage);
   uint4 q[G::kPairs], dO[G::kPairs];
   float delta = 0.f;
   {
     uint4 o[G::kPairs];
-    load_operand<BF16, DP>(a.dO, start, h, w0, len, a.D, dO);
-    load_operand<BF16, DP>(a.o, start, h, w0, len, a.D, o);
-    load_operand<BF16, DP>(a.q, start, h, w0, len, a.D, q);
+    load_operand<BF16, DC>(a.dO, start, h, w0, len, a.D, dO);
+    load_operand<BF16, DC>(a.o, start, h, w0, len, a.D, o);
+    load_operand<BF16, DC>(a.q, start, h, w0, len, a.D, q);
 #pragma unroll
     for (int i = 0; i < G::kPairs; ++i) delta = dot_chunk<BF16>(dO[i], o[i], delta);
     delta += other_half(delta);
   }
-  float lse = INFINITY;   // queries past the end: every weight 0
+  float lse = 0.f;
   if (query < len) {
     const int64_t at = (int64_t)h * a.N + start + query;
     lse = a.lse[at] * kLog2e;
-    if (g == 0) a.delta[at] = delta;
+    if (g == 0 && split == 0) {
+      a.delta[at] = delta;
+      a.lse2[at] = lse;
+    }
   }
   const float c = a.scale * kLog2e;
   f32x16_t acc[G::kTiles] = {};
-  const int32_t end = min(tile * kRows + kRows, len);
-  for (int32_t k0 = 0; k0 < end; k0 += kStep) {
-    __syncthreads();
-    stage<BF16, DP>(a.k, start, kh, k0, len, a.D, lk);
-    stage<BF16, DP>(a.v, start, kh, k0, len, a.D, lv);
-    staged();
-    if (k0 > w0 + 31) continue;
-    const bool diag = k0 + kStep - 1 > w0;
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      f32x16_t s = rows_times<BF16, DP>(lk, t * 32, q);
-      const f32x16_t dp = rows_times<BF16, DP>(lv, t * 32, dO);
-#pragma unroll
-      for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, -lse)) * (dp[r] - delta);
-      if (diag) {
-#pragma unroll
-        for (int r = 0; r < 16; ++r)
-          if (k0 + t * 32 + result_row(r, g) > query) s[r] = 0.f;
-      }
-      columns_times<BF16, DP>(lk, t * 32, s, acc);
+  staged();
+  int buf = 0;
+  for (int32_t r0 = 0; r0 < end; r0 += P::kStep) {
+    const bool more = r0 + P::kStep < end;
+    if (P::kBuffers == 2 && more) {
+      const uint32_t to = base + (buf ^ 1) * 2 * P::kStage;
+      stage<BF16, DC, P::kStep, P::kWaves>(a.k, start, kh, r0 + P::kStep, len, a.D, to);
+      stage<BF16, DC, P::kStep, P::kWaves>(a.v, start, kh, r0 + P::kStep, len, a.D, to + P::kStage);
     }
+    const int32_t k0 = r0 + split * 32;
+    if (k0 <= w0 + 31) {
+      const unsigned char* lk = lds + buf * 2 * P::kStage + split * 32 * G::kPitch;
+      const unsigned char* lv = lk + P::kStage;
+      const bool diag = k0 + 32 * P::kSub - 1 > w0;
+#pragma unroll
+      for (int t = 0; t < P::kSub; ++t) {
+        f32x16_t s = rows_times<BF16, DC>(lk, t * 32, q);
+        const f32x16_t dp = rows_times<BF16, DC>(lv, t * 32, dO);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, -lse)) * (dp[r] - delta);
+        if (diag) {
+          keep_branch();
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            if (k0 + t * 32 + result_row(r, g) > query) s[r] = 0.f;
+        }
+        columns_times<BF16, DC>(lk, t * 32, s, acc);
+      }
+    }
+    if (P::kBuffers == 1 && more) {
+      __syncthreads();
+      stage<BF16, DC, P::kStep, P::kWaves>(a.k, start, kh, r0 + P::kStep, len, a.D, base);
+      stage<BF16, DC, P::kStep, P::kWaves>(a.v, start, kh, r0 + P::kStep, len, a.D, base + P::kStage);
+    }
+    staged();
+    if (P::kBuffers == 2) buf ^= 1;
+  }
+  if constexpr (NS > 1) {
+    join<GR, NS, G::kTiles>(acc, grp, split, lds);
+    if (split > 0) return;
   }
   if (query >= len) return;
-  store_rows<BF16, DP>(a.dq, (int64_t)start + query, h, a.D, acc, a.scale);
+  store_rows<BF16, DC>(a.dq, (int64_t)start + query, h, a.D, acc, a.scale);
 }
 
-// dk and dv of 128 keys of one key head: 32 keys a wave, all query heads of the
-// key head and all queries from the diagonal on.
-template <bool BF16, int DP>
-__global__ __launch_bounds__(kThreads) void k_backward_kv(Args a) {
-  using G = Geo<BF16, DP>;
-  __shared__ __align__(16) unsigned char lq[G::kStage], lo[G::kStage];
-  __shared__ __align__(16) float llse[kStep], ldelta[kStep];
+// dk and dv of 32 GR keys of one key head: all query heads of the key head and
+// all queries from the diagonal on.
+template <bool BF16, int DC, int GR, int NS>
+__global__ __launch_bounds__(64 * GR * NS, BF16 ? 2 : 1) void k_backward_kv(Args a) {
+  using G = Geo<BF16, DC>;
+  using P = Split<BF16, DC, GR, NS>;
+  constexpr int kBuf = 2 * P::kStage + P::kWords;
+  __shared__ __align__(1024) unsigned char lds[P::kBuffers * kBuf];
   int32_t start, len, tile, tiles;
   const int32_t kh = blockIdx.x % a.Hkv, slot = blockIdx.x / a.Hkv, rep = a.Hq / a.Hkv;
-  if (!find_tile(a, slot, kRows, start, len, tile, tiles)) return;
+  if (!find_tile(a, slot, P::kRows, start, len, tile, tiles)) return;
   const int lane = threadIdx.x & 63, g = lane >> 5;
-  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int32_t w0 = tile * kRows + wv * 32;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), grp = wv % GR, split = wv / GR;
+  const int32_t w0 = tile * P::kRows + grp * 32;
   const int32_t key = w0 + (lane & 31);
+  const uint32_t base = lds_address(lds);
+  // queries q0 .. of head h, with their lse2 and delta: zeros past the end,
+  // whose dO and q rows are zero too and so add nothing
+  const auto fetch = [&](int32_t h, int32_t q0, uint32_t to) {
+    stage<BF16, DC, P::kStep, P::kWaves>(a.q, start, h, q0, len, a.D, to);
+    stage<BF16, DC, P::kStep, P::kWaves>(a.dO, start, h, q0, len, a.D, to + P::kStage);
+    constexpr int parts = P::kStep / 64;
+#pragma unroll
+    for (int i = 0; i < 2 * parts; ++i) {
+      if (i % P::kWaves != wv) continue;
+      const float* src = (i < parts ? a.lse2 : a.delta) + (int64_t)h * a.N + start + q0;
+      const int row = (i % parts) * 64 + lane;
+      dma_words(rows_of((const char*)src), q0 + row < len ? row * 4 : kOutside, to + 2 * P::kStage + i * 256);
+    }
+  };
+  const int32_t first = tile * P::kRows / P::kStep * P::kStep;   // a step's start at or before the first key
+  int32_t h = kh * rep, q0 = first;
+  fetch(h, q0, base);
   uint4 k[G::kPairs], v[G::kPairs];
-  load_operand<BF16, DP>(a.k, start, kh, w0, len, a.D, k);
-  load_operand<BF16, DP>(a.v, start, kh, w0, len, a.D, v);
+  load_operand<BF16, DC>(a.k, start, kh, w0, len, a.D, k);
+  load_operand<BF16, DC>(a.v, start, kh, w0, len, a.D, v);
   const float c = a.scale * kLog2e;
   f32x16_t dk[G::kTiles] = {}, dv[G::kTiles] = {};
-  for (int32_t h = kh * rep; h < kh * rep + rep; ++h) {
-    for (int32_t q0 = tile * kRows; q0 < len; q0 += kStep) {
-      __syncthreads();
-      stage<BF16, DP>(a.q, start, h, q0, len, a.D, lq);
-      stage<BF16, DP>(a.dO, start, h, q0, len, a.D, lo);
-      if (threadIdx.x < kStep) {
-        const int32_t t = q0 + threadIdx.x;
-        const int64_t at = (int64_t)h * a.N + start + t;
-        llse[threadIdx.x] = t < len ? a.lse[at] * kLog2e : INFINITY;   // queries past the end: every weight 0
-        ldelta[threadIdx.x] = t < len ? a.delta[at] : 0.f;
-      }
-      staged();
-      if (q0 + kStep - 1 < w0) continue;
-      const bool diag = q0 < w0 + 31;
+  staged();
+  int buf = 0;
+  for (;;) {
+    int32_t nh = h, nq = q0 + P::kStep;
+    if (nq >= len) {
+      nq = first;
+      ++nh;
+    }
+    const bool more = nh < kh * rep + rep;
+    if (P::kBuffers == 2 && more) fetch(nh, nq, base + (buf ^ 1) * kBuf);
+    const int32_t t0 = q0 + split * 32;
+    if (t0 + 32 * P::kSub - 1 >= w0) {
+      const unsigned char* lq = lds + buf * kBuf + split * 32 * G::kPitch;
+      const unsigned char* lo = lq + P::kStage;
+      const float* words = (const float*)(lds + buf * kBuf + 2 * P::kStage) + split * 32;
+      const bool diag = t0 < w0 + 31;
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        f32x16_t p = rows_times<BF16, DP>(lq, t * 32, k);
-        f32x16_t ds = rows_times<BF16, DP>(lo, t * 32, v);
+      for (int t = 0; t < P::kSub; ++t) {
+        f32x16_t p = rows_times<BF16, DC>(lq, t * 32, k);
+        f32x16_t ds = rows_times<BF16, DC>(lo, t * 32, v);
 #pragma unroll
         for (int r4 = 0; r4 < 4; ++r4) {
-          const float4 z = *(const float4*)(llse + t * 32 + 8 * r4 + 4 * g);
-          const float4 e = *(const float4*)(ldelta + t * 32 + 8 * r4 + 4 * g);
-          const float zz[4] = {z.x, z.y, z.z, z.w}, ee[4] = {e.x, e.y, e.z, e.w};
+          const f32x4_t z = *(const f32x4_t*)(words + t * 32 + 8 * r4 + 4 * g);
+          const f32x4_t e = *(const f32x4_t*)(words + P::kStep + t * 32 + 8 * r4 + 4 * g);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int r = 4 * r4 + i;
-            p[r] = __builtin_amdgcn_exp2f(fmaf(p[r], c, -zz[i]));
-            ds[r] = p[r] * (ds[r] - ee[i]);
-            if (diag && q0 + t * 32 + result_row(r, g) < key) p[r] = 0.f, ds[r] = 0.f;
+            p[r] = __builtin_amdgcn_exp2f(fmaf(p[r], c, -z[i]));
+            ds[r] = p[r] * (ds[r] - e[i]);
           }
         }
-        columns_times<BF16, DP>(lo, t * 32, p, dv);
-        columns_times<BF16, DP>(lq, t * 32, ds, dk);
+        if (diag) {
+          keep_branch();
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            if (t0 + t * 32 + result_row(r, g) < key) p[r] = 0.f, ds[r] = 0.f;
+        }
+        columns_times<BF16, DC>(lo, t * 32, p, dv);
+        columns_times<BF16, DC>(lq, t * 32, ds, dk);
       }
     }
+    if (P::kBuffers == 1 && more) {
+      __syncthreads();
+      fetch(nh, nq, base);
+    }
+    staged();
+    if (!more) break;
+    h = nh;
+    q0 = nq;
+    if (P::kBuffers == 2) buf ^= 1;
+  }
+  if constexpr (NS > 1) {
+    join<GR, NS, G::kTiles>(dk, grp, split, lds);
+    join<GR, NS, G::kTiles>(dv, grp, split, lds);
+    if (split > 0) return;
   }
   if (key >= len) return;
-  store_rows<BF16, DP>(a.dk, (int64_t)start + key, kh, a.D, dk, a.scale);
-  store_rows<BF16, DP>(a.dv, (int64_t)start + key, kh, a.D, dv, 1.f);
+  store_rows<BF16, DC>(a.dk, (int64_t)start + key, kh, a.D, dk, a.scale);
+  store_rows<BF16, DC>(a.dv, (int64_t)start + key, kh, a.D, dv, 1.f);
 }
 
 }  // namespace attn
