@@ -26,15 +26,13 @@ dpnorm_status check_shape(const dpnorm_attn_shape* s) {
   if (!s) return DPNORM_ERR_NULL;
   if (s->dtype != DPNORM_BF16 && s->dtype != DPNORM_F32) return DPNORM_ERR_DTYPE;
   const int64_t lim = (int64_t)1 << 30;
-  if (s->N < 1 || s->N > lim || s->S < 1 || s->S > lim || s->Hq < 1 || s->Hkv < 1 || s->Hq > 65536 || s->Hq % s->Hkv != 0)
+  if (s->N < 1 || s->N > lim || s->S < 1 || s->S > lim || s->Hq < 1 || s->Hkv < 1 || s->Hq > 65535 || s->Hq % s->Hkv != 0)
     return DPNORM_ERR_SIZE;
   const int64_t g = s->dtype == DPNORM_BF16 ? 8 : 4;
   if (s->D < 1 || s->D > 128 || s->D % g != 0) return DPNORM_ERR_SIZE;
   if (!s->cu_seqlens && s->N % s->S != 0) return DPNORM_ERR_SIZE;
   if (!aligned(s->cu_seqlens, 4)) return DPNORM_ERR_ALIGN;
   if (!(s->scale > 0.f) || !std::isfinite(s->scale)) return DPNORM_ERR_VALUE;
-  // a block a head and slot: the grid's x dimension holds them
-  if ((s->N / 32 + s->S + 1) * s->Hq > 0x7fffffff) return DPNORM_ERR_SIZE;
   return DPNORM_OK;
 }
 
@@ -89,28 +87,39 @@ int64_t slots_of(const attn::Args& a, int rows) {
   return a.cu ? (int64_t)a.N / rows + a.S : (int64_t)a.S * ((a.T + rows - 1) / rows);
 }
 
-template <bool BF16, int DC, int GR, int NS>
-hipError_t launch_attn_forward(attn::Args a, hipStream_t stream) {
-  using P = attn::Split<BF16, DC, GR, NS>;
-  a.slots = (int32_t)slots_of(a, P::kRows);
-  attn::k_forward<BF16, DC, GR, NS><<<(uint32_t)((int64_t)a.slots * a.Hq), P::kThreads, 0, stream>>>(a);
+// One launch, or more where a grid's z dimension does not hold the slots.
+template <typename F>
+hipError_t launch_slots(attn::Args a, int rows, int rep, F launch) {
+  const int64_t slots = slots_of(a, rows);
+  for (int64_t s = 0; s < slots; s += 65535) {
+    a.slot0 = (int32_t)s;
+    launch(a, dim3((uint32_t)a.Hkv, (uint32_t)rep, (uint32_t)std::min<int64_t>(65535, slots - s)));
+  }
   return hipGetLastError();
 }
 
 template <bool BF16, int DC, int GR, int NS>
-hipError_t launch_attn_backward_q(attn::Args a, hipStream_t stream) {
+hipError_t launch_attn_forward(const attn::Args& a, hipStream_t stream) {
   using P = attn::Split<BF16, DC, GR, NS>;
-  a.slots = (int32_t)slots_of(a, P::kRows);
-  attn::k_backward_q<BF16, DC, GR, NS><<<(uint32_t)((int64_t)a.slots * a.Hq), P::kThreads, 0, stream>>>(a);
-  return hipGetLastError();
+  return launch_slots(a, P::kRows, a.Hq / a.Hkv, [&](const attn::Args& x, dim3 grid) {
+    attn::k_forward<BF16, DC, GR, NS><<<grid, P::kThreads, 0, stream>>>(x);
+  });
 }
 
 template <bool BF16, int DC, int GR, int NS>
-hipError_t launch_attn_backward_kv(attn::Args a, hipStream_t stream) {
+hipError_t launch_attn_backward_q(const attn::Args& a, hipStream_t stream) {
   using P = attn::Split<BF16, DC, GR, NS>;
-  a.slots = (int32_t)slots_of(a, P::kRows);
-  attn::k_backward_kv<BF16, DC, GR, NS><<<(uint32_t)((int64_t)a.slots * a.Hkv), P::kThreads, 0, stream>>>(a);
-  return hipGetLastError();
+  return launch_slots(a, P::kRows, a.Hq / a.Hkv, [&](const attn::Args& x, dim3 grid) {
+    attn::k_backward_q<BF16, DC, GR, NS><<<grid, P::kThreads, 0, stream>>>(x);
+  });
+}
+
+template <bool BF16, int DC, int GR, int NS>
+hipError_t launch_attn_backward_kv(const attn::Args& a, hipStream_t stream) {
+  using P = attn::Split<BF16, DC, GR, NS>;
+  return launch_slots(a, P::kRows, 1, [&](const attn::Args& x, dim3 grid) {
+    attn::k_backward_kv<BF16, DC, GR, NS><<<grid, P::kThreads, 0, stream>>>(x);
+  });
 }
 
 template <bool BF16, int DC>

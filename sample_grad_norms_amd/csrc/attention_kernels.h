@@ -26,6 +26,8 @@
 // are rounded to bf16 for bf16 inputs (half a step, 2^-9 relative, as the
 // inputs themselves are); the sum of the weights takes them unrounded.
 #pragma once
+#include <type_traits>
+
 #include "device_common.h"
 
 namespace dpn {
@@ -49,7 +51,7 @@ struct Args {
   int32_t S, T, N;
   int32_t Hq, Hkv, D;
   float scale;        // a
-  int32_t slots;      // tile slots per head
+  int32_t slot0;      // first slot of the launch
 };
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -104,9 +106,18 @@ struct Geo {
   static constexpr int kElem = BF16 ? 2 : 4;
   static constexpr int kPitch = (DC == 96 ? 128 : DC) * kElem;   // LDS bytes of a row
   static constexpr int kChunks = kPitch / 16;                    // 16-byte chunks of an LDS row
+  static constexpr int kSwz = kChunks >= 16 ? 1 : 0;             // see swizzle
   static constexpr int kPairs = DC * kElem / 32;                 // chunk pairs: one chunk for each half of the wave
   static constexpr int kTiles = DC / 32;                         // 32-column tiles of a row
 };
+
+// Where row r keeps its chunk c: at c ^ (r & 7), and in rows of 256 bytes and
+// more at c ^ 2 (r & 7). Eight rows' reads of one chunk, and the four rows x 32
+// bytes of a transposing read, then fall on different banks.
+template <bool BF16, int DC>
+__device__ __forceinline__ int swizzle(int ch, int row) {
+  return ch ^ ((row & 7) << Geo<BF16, DC>::kSwz);
+}
 
 // Buffer descriptor of the rows from p on (wave-uniform): raw, no stride, all
 // that an offset below 2^31 reaches.
@@ -126,9 +137,9 @@ __device__ __forceinline__ char* row_ptr(const Tensor& t, int64_t row, int32_t h
 
 // 16 or 4 bytes a lane from a buffer straight to LDS at lds + 16 (4) * lane.
 // Written out so that the compiler adds no waits for them: `staged` waits.
-__device__ __forceinline__ void dma_rows(i32x4_t rows, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(off), "s"(rows),
-               "s"(__builtin_amdgcn_readfirstlane(lds))
+__device__ __forceinline__ void dma_rows(i32x4_t rows, uint32_t off, int32_t more, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %3 offen lds" ::"v"(off), "s"(rows),
+               "s"(__builtin_amdgcn_readfirstlane(lds)), "s"(more)
                : "memory");
 }
 __device__ __forceinline__ void dma_words(i32x4_t rows, uint32_t off, uint32_t lds) {
@@ -140,25 +151,39 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
 }
 
-// ROWS rows from r0 on of a sequence into LDS by W waves, row-major with the
-// 16-byte chunks of row r at chunk ^ (r & 7): reads of one chunk of eight rows
-// then fall on different banks. Rows past `len` and columns past D read as zero.
+// Steps of ROWS rows of one head of a sequence into LDS by W waves, row-major
+// with swizzled chunks. Rows past the sequence and columns past D read as zero.
 template <bool BF16, int DC, int ROWS, int W>
-__device__ __forceinline__ void stage(const Tensor& t, int64_t start, int32_t h, int32_t r0, int32_t len, int32_t D,
-                                      uint32_t lds) {
+struct Stream {
   using G = Geo<BF16, DC>;
-  const i32x4_t rows = rows_of(row_ptr(t, start + r0, h));
-  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int32_t left = len - r0;
-  static_assert(ROWS * G::kChunks % (64 * W) == 0, "whole loads of every wave");
-#pragma unroll
-  for (int i = 0; i < ROWS * G::kChunks / (64 * W); ++i) {
-    const int at = (i * W + wv) * 64 + lane;
-    const int row = at / G::kChunks, ch = (at % G::kChunks) ^ (row & 7);
-    const bool in = row < left && ch * 16 < D * G::kElem;
-    dma_rows(rows, in ? (uint32_t)(row * (int32_t)t.st + ch * 16) : kOutside, lds + (i * W + wv) * 1024);
+  static constexpr int kLoads = ROWS * G::kChunks / (64 * W);    // of a wave
+  static constexpr int kApart = 64 * W / G::kChunks;             // rows between a lane's loads
+  static_assert(kLoads * 64 * W == ROWS * G::kChunks && kApart % 8 == 0, "whole loads, one swizzle a lane");
+  const char* p;      // the sequence's first row
+  int64_t st;
+  uint32_t off;       // the lane's first load: row, chunk
+  int row;
+  __device__ __forceinline__ Stream(const Tensor& t, int64_t start, int32_t h, int32_t D) {
+    p = row_ptr(t, start, h);
+    st = t.st;
+    row = threadIdx.x / G::kChunks;
+    const int ch = swizzle<BF16, DC>(threadIdx.x % G::kChunks, row);
+    off = ch * 16 < D * G::kElem ? (uint32_t)(row * (int32_t)st + ch * 16) : kOutside;
   }
-}
+  __device__ __forceinline__ void head(const Tensor& t, int64_t start, int32_t h) { p = row_ptr(t, start, h); }
+  __device__ __forceinline__ void fetch(int32_t r0, int32_t len, uint32_t lds) const {
+    const i32x4_t rows = rows_of(p + r0 * st);
+    const uint32_t to = lds + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 1024;
+    if (len - r0 >= ROWS) {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) dma_rows(rows, off, i * kApart * (int32_t)st, to + i * W * 1024);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i)
+        dma_rows(rows, row + i * kApart < len - r0 ? off : kOutside, i * kApart * (int32_t)st, to + i * W * 1024);
+    }
+  }
+};
 
 // This wave's direct loads have landed, and then every wave's; and every wave
 // has read what it read from LDS before.
@@ -205,7 +230,7 @@ __device__ __forceinline__ f32x16_t rows_times(const unsigned char* lds, int r0,
   f32x16_t c = {};
 #pragma unroll
   for (int i = 0; i < G::kPairs; ++i) {
-    const uint4 a = *(const uint4*)(lds + (row * G::kPitch + (((2 * i + g) ^ (row & 7)) << 4)) + r0 * G::kPitch);
+    const uint4 a = *(const uint4*)(lds + (row * G::kPitch + (swizzle<BF16, DC>(2 * i + g, row) << 4)) + r0 * G::kPitch);
     c = mfma_chunk<BF16>(a, f[i], c);
   }
   return c;
@@ -235,7 +260,7 @@ __device__ __forceinline__ void columns_times(const unsigned char* lds, int r0, 
 #pragma unroll
       for (int t = 0; t < G::kTiles; ++t) {
         const int ch = (t * 32 + m0 + 4 * q) >> 3;
-        const unsigned char* p = lds + (row * G::kPitch + ((ch ^ row) << 4) + (q & 1) * 8) + (r0 + ks * 16) * G::kPitch;
+        const unsigned char* p = lds + (row * G::kPitch + (swizzle<BF16, DC>(ch, row) << 4) + (q & 1) * 8) + (r0 + ks * 16) * G::kPitch;
         const uint2 lo = lds_read_tr16(p), hi = lds_read_tr16(p + 8 * G::kPitch);
         acc[t] = mfma_chunk<true>(make_uint4(lo.x, lo.y, hi.x, hi.y), b, acc[t]);
       }
@@ -247,7 +272,7 @@ __device__ __forceinline__ void columns_times(const unsigned char* lds, int r0, 
 #pragma unroll
       for (int t = 0; t < G::kTiles; ++t) {
         const int col = t * 32 + (lane & 31);
-        const float x = *(const float*)(lds + (row * G::kPitch + (((col >> 2) ^ row) << 4) + (col & 3) * 4) +
+        const float x = *(const float*)(lds + (row * G::kPitch + (swizzle<BF16, DC>(col >> 2, row) << 4) + (col & 3) * 4) +
                                         (r0 + 8 * (r >> 2)) * G::kPitch);
         acc[t] = __builtin_amdgcn_mfma_f32_32x32x2f32(x, w[r], acc[t], 0, 0, 0);
       }
@@ -255,7 +280,11 @@ __device__ __forceinline__ void columns_times(const unsigned char* lds, int r0, 
   }
 }
 
-__device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32); }
+// The value of the lane's column in the other half of the wave.
+__device__ __forceinline__ float other_half(float x) {
+  const auto y = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float((threadIdx.x & 32) ? y[0] : y[1]);
+}
 
 // Row r (0 .. 15) of a lane's half in a 32 x 32 result.
 __device__ __forceinline__ int result_row(int r, int g) { return 8 * (r >> 2) + 4 * g + (r & 3); }
@@ -263,6 +292,11 @@ __device__ __forceinline__ int result_row(int r, int g) { return 8 * (r >> 2) + 
 // Keeps a uniform branch a branch: without it the compiler computes the masks
 // of every step, of which one or two at the diagonal need them.
 __device__ __forceinline__ void keep_branch() { asm volatile(""); }
+
+// Wide rows leave no registers for a backward step as one block of
+// instructions: they keep one copy of it, with the mask as a branch.
+template <bool BF16, int DC>
+constexpr bool kWide = !BF16 || DC > 64;
 
 // Columns of acc (transposed: rows are the D index) to row `row` of t, times f.
 template <bool BF16, int DC>
@@ -290,14 +324,10 @@ __device__ __forceinline__ void store_rows(const Tensor& t, int64_t row, int32_t
   }
 }
 
-// Head and slot of a block. Blocks go to the 8 XCDs in turn; with the key head
-// as the fastest index, the blocks that read one key head meet in one L2 when
-// Hkv is a multiple or a divisor of 8.
-__device__ __forceinline__ void block_head(const Args& a, int32_t& h, int32_t& slot) {
-  const int32_t b = blockIdx.x, x = b % a.Hq, rep = a.Hq / a.Hkv;
-  h = (x % a.Hkv) * rep + x / a.Hkv;
-  slot = b / a.Hq;
-}
+// Blocks: x is the key head, y the query head of that key head, z the slot
+// (from slot0 on). Blocks go to the 8 XCDs in turn, so the blocks that read one
+// key head meet in one L2 when Hkv is a multiple or a divisor of 8.
+__device__ __forceinline__ int32_t block_slot(const Args& a) { return a.slot0 + (int32_t)blockIdx.z; }
 
 // Work groups: GR groups of 32 stationary rows, each taken by NS waves that
 // split the streamed rows of a step. With NS = 1 a wave takes 64 rows a step,
@@ -310,10 +340,9 @@ struct Split {
   static constexpr int kSub = NS == 1 ? 2 : 1;       // 32-row tiles of a wave and step
   static constexpr int kStep = 32 * NS * kSub;       // streamed rows a step
   static constexpr int kStage = kStep * G::kPitch;   // bytes of one tensor's step
-  static constexpr int kBuffers = 4 * kStage + 4 * kStep * 4 <= 128 * 1024 ? 2 : 1;
   static constexpr int kWords = 2 * kStep * 4;       // lse2 and delta of a step (dk and dv)
-  static constexpr int kLds = kBuffers * (2 * kStage + kWords);
-  static constexpr int kJoin = 64 * 16 * 4;          // bytes of a wave's 32 x 32 tile
+  static constexpr int kBuffers = 2 * (2 * kStage + kWords) <= 132 * 1024 ? 2 : 1;
+  using Rows = Stream<BF16, DC, kStep, kWaves>;
 };
 
 // Adds the accumulators of the waves of one row group, in split order, to the
@@ -346,45 +375,47 @@ __device__ __forceinline__ void join(f32x16_t (&acc)[TILES], int grp, int split,
   }
 }
 
+// Largest growth of a score, in powers of two, that a wave lets pass without
+// rescaling its sums: the weights stay below 2^8 and the sums far inside fp32.
+constexpr float kGrowth = 8.f;
+
 template <bool BF16, int DC, int GR, int NS>
 __global__ __launch_bounds__(64 * GR * NS, BF16 ? 2 : 1) void k_forward(Args a) {
   using G = Geo<BF16, DC>;
   using P = Split<BF16, DC, GR, NS>;
-  __shared__ __align__(1024) unsigned char lds[P::kBuffers * 2 * P::kStage];
-  int32_t h, slot, start, len, tile, tiles;
-  block_head(a, h, slot);
-  if (!find_tile(a, slot, P::kRows, start, len, tile, tiles)) return;
+  // keys are needed a step ahead of their values, whose scores they give
+  __shared__ __align__(1024) unsigned char lds[4 * P::kStage];
+  int32_t start, len, tile, tiles;
+  if (!find_tile(a, block_slot(a), P::kRows, start, len, tile, tiles)) return;
   tile = tiles - 1 - tile;   // the longest rows first
-  const int32_t kh = h / (a.Hq / a.Hkv);
+  const int32_t kh = blockIdx.x, h = kh * gridDim.y + blockIdx.y;
   const int lane = threadIdx.x & 63, g = lane >> 5;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), grp = wv % GR, split = wv / GR;
   const int32_t w0 = tile * P::kRows + grp * 32;   // the wave's first query
   const int32_t query = w0 + (lane & 31);
   const uint32_t base = lds_address(lds);
   const int32_t end = min(tile * P::kRows + P::kRows, len);   // keys that some query of the block sees
-  stage<BF16, DC, P::kStep, P::kWaves>(a.k, start, kh, 0, len, a.D, base);
-  stage<BF16, DC, P::kStep, P::kWaves>(a.v, start, kh, 0, len, a.D, base + P::kStage);
+  const typename P::Rows ks(a.k, start, kh, a.D), vs(a.v, start, kh, a.D);
+  ks.fetch(0, len, base);
+  vs.fetch(0, len, base + 2 * P::kStage);
+  if (P::kStep < end) ks.fetch(P::kStep, len, base + P::kStage);
   uint4 q[G::kPairs];
   load_operand<BF16, DC>(a.q, start, h, w0, len, a.D, q);
   const float c = a.scale * kLog2e;
   float m = -INFINITY, l = 0.f;
   f32x16_t acc[G::kTiles] = {};
+  f32x16_t s[P::kSub];
   staged();
-  int buf = 0;
-  for (int32_t r0 = 0; r0 < end; r0 += P::kStep) {
-    const bool more = r0 + P::kStep < end;
-    if (P::kBuffers == 2 && more) {
-      const uint32_t to = base + (buf ^ 1) * 2 * P::kStage;
-      stage<BF16, DC, P::kStep, P::kWaves>(a.k, start, kh, r0 + P::kStep, len, a.D, to);
-      stage<BF16, DC, P::kStep, P::kWaves>(a.v, start, kh, r0 + P::kStep, len, a.D, to + P::kStage);
-    }
-    const int32_t k0 = r0 + split * 32;   // (one split: 0)
-    if (k0 <= w0 + 31) {
-      const unsigned char* lk = lds + buf * 2 * P::kStage + split * 32 * G::kPitch;
-      const unsigned char* lv = lk + P::kStage;
-      f32x16_t s[P::kSub];
+  const unsigned char* mine = lds + split * 32 * G::kPitch;
 #pragma unroll
-      for (int t = 0; t < P::kSub; ++t) s[t] = rows_times<BF16, DC>(lk, t * 32, q);
+  for (int t = 0; t < P::kSub; ++t) s[t] = rows_times<BF16, DC>(mine, t * 32, q);
+  __syncthreads();
+  int buf = 0;
+  for (int32_t r0 = 0; r0 < end; r0 += P::kStep, buf ^= 1) {
+    if (r0 + P::kStep < end) vs.fetch(r0 + P::kStep, len, base + (2 + (buf ^ 1)) * P::kStage);
+    if (r0 + 2 * P::kStep < end) ks.fetch(r0 + 2 * P::kStep, len, base + buf * P::kStage);
+    const int32_t k0 = r0 + split * 32;
+    if (k0 <= w0 + 31) {
       if (k0 + 32 * P::kSub - 1 > w0) {
         keep_branch();
 #pragma unroll
@@ -393,14 +424,14 @@ __global__ __launch_bounds__(64 * GR * NS, BF16 ? 2 : 1) void k_forward(Args a) 
           for (int r = 0; r < 16; ++r)
             if (k0 + t * 32 + result_row(r, g) > query) s[t][r] = -INFINITY;
       }
-      float top = s[0][0];
+      float x[4] = {s[0][0], s[0][1], s[0][2], s[0][3]};
 #pragma unroll
       for (int t = 0; t < P::kSub; ++t)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) top = fmaxf(top, s[t][r]);
+        for (int r = 0; r < 16; ++r) x[r & 3] = fmaxf(x[r & 3], s[t][r]);
+      float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
       top = fmaxf(top, other_half(top));
-      // a new largest score of some query rescales the wave's sums
-      if (__any(top > m)) {
+      if (__any((top - m) * c > kGrowth)) {
         keep_branch();
         top = fmaxf(m, top);
         const float f = top == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - top) * c);
@@ -413,25 +444,26 @@ __global__ __launch_bounds__(64 * GR * NS, BF16 ? 2 : 1) void k_forward(Args a) 
       }
       // (queries that see none of a split's keys so far: every weight 0)
       const float mc = m == -INFINITY ? 0.f : m * c;
-      float sum = 0.f;
+      // the next step's scores fill the matrix unit while this step's weights are computed
+      f32x16_t next[P::kSub];
+#pragma unroll
+      for (int t = 0; t < P::kSub; ++t) next[t] = rows_times<BF16, DC>(mine + (buf ^ 1) * P::kStage, t * 32, q);
+      float sum[2] = {0.f, 0.f};
 #pragma unroll
       for (int t = 0; t < P::kSub; ++t)
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
           s[t][r] = __builtin_amdgcn_exp2f(fmaf(s[t][r], c, -mc));
-          sum += s[t][r];
+          sum[r & 1] += s[t][r];
         }
-      l += sum;
+      l += sum[0] + sum[1];
 #pragma unroll
-      for (int t = 0; t < P::kSub; ++t) columns_times<BF16, DC>(lv, t * 32, s[t], acc);
-    }
-    if (P::kBuffers == 1 && more) {
-      __syncthreads();
-      stage<BF16, DC, P::kStep, P::kWaves>(a.k, start, kh, r0 + P::kStep, len, a.D, base);
-      stage<BF16, DC, P::kStep, P::kWaves>(a.v, start, kh, r0 + P::kStep, len, a.D, base + P::kStage);
+      for (int t = 0; t < P::kSub; ++t) {
+        columns_times<BF16, DC>(mine + (2 + buf) * P::kStage, t * 32, s[t], acc);
+        s[t] = next[t];
+      }
     }
     staged();
-    if (P::kBuffers == 2) buf ^= 1;
   }
   l += other_half(l);
   if constexpr (NS > 1) {
@@ -441,7 +473,7 @@ __global__ __launch_bounds__(64 * GR * NS, BF16 ? 2 : 1) void k_forward(Args a) 
     __syncthreads();
     float top = -INFINITY;
 #pragma unroll
-    for (int s = 0; s < NS; ++s) top = fmaxf(top, st[(s * GR + grp) * 64 + lane]);
+    for (int i = 0; i < NS; ++i) top = fmaxf(top, st[(i * GR + grp) * 64 + lane]);
     const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - top) * c);
     m = top;
     __syncthreads();
@@ -449,7 +481,7 @@ __global__ __launch_bounds__(64 * GR * NS, BF16 ? 2 : 1) void k_forward(Args a) 
     __syncthreads();
     l = 0.f;
 #pragma unroll
-    for (int s = 0; s < NS; ++s) l += st[(s * GR + grp) * 64 + lane];
+    for (int i = 0; i < NS; ++i) l += st[(i * GR + grp) * 64 + lane];
 #pragma unroll
     for (int t = 0; t < G::kTiles; ++t)
 #pragma unroll
@@ -484,19 +516,19 @@ __global__ __launch_bounds__(64 * GR * NS, BF16 ? 2 : 1) void k_backward_q(Args 
   using G = Geo<BF16, DC>;
   using P = Split<BF16, DC, GR, NS>;
   __shared__ __align__(1024) unsigned char lds[P::kBuffers * 2 * P::kStage];
-  int32_t h, slot, start, len, tile, tiles;
-  block_head(a, h, slot);
-  if (!find_tile(a, slot, P::kRows, start, len, tile, tiles)) return;
+  int32_t start, len, tile, tiles;
+  if (!find_tile(a, block_slot(a), P::kRows, start, len, tile, tiles)) return;
   tile = tiles - 1 - tile;
-  const int32_t kh = h / (a.Hq / a.Hkv);
+  const int32_t kh = blockIdx.x, h = kh * gridDim.y + blockIdx.y;
   const int lane = threadIdx.x & 63, g = lane >> 5;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), grp = wv % GR, split = wv / GR;
   const int32_t w0 = tile * P::kRows + grp * 32;
   const int32_t query = w0 + (lane & 31);
   const uint32_t base = lds_address(lds);
   const int32_t end = min(tile * P::kRows + P::kRows, len);
-  stage<BF16, DC, P::kStep, P::kWaves>(a.k, start, kh, 0, len, a.D, base);
-  stage<BF16, DC, P::kStep, P::kWaves>(a.v, start, kh, 0, len, a.D, base + P::kStage);
+  const typename P::Rows ks(a.k, start, kh, a.D), vs(a.v, start, kh, a.D);
+  ks.fetch(0, len, base);
+  vs.fetch(0, len, base + P::kStage);
   uint4 q[G::kPairs], dO[G::kPairs];
   float delta = 0.f;
   {
@@ -525,33 +557,39 @@ __global__ __launch_bounds__(64 * GR * NS, BF16 ? 2 : 1) void k_backward_q(Args 
     const bool more = r0 + P::kStep < end;
     if (P::kBuffers == 2 && more) {
       const uint32_t to = base + (buf ^ 1) * 2 * P::kStage;
-      stage<BF16, DC, P::kStep, P::kWaves>(a.k, start, kh, r0 + P::kStep, len, a.D, to);
-      stage<BF16, DC, P::kStep, P::kWaves>(a.v, start, kh, r0 + P::kStep, len, a.D, to + P::kStage);
+      ks.fetch(r0 + P::kStep, len, to);
+      vs.fetch(r0 + P::kStep, len, to + P::kStage);
     }
     const int32_t k0 = r0 + split * 32;
     if (k0 <= w0 + 31) {
       const unsigned char* lk = lds + buf * 2 * P::kStage + split * 32 * G::kPitch;
       const unsigned char* lv = lk + P::kStage;
-      const bool diag = k0 + 32 * P::kSub - 1 > w0;
+      // (two copies, so that a step off the diagonal is one block of instructions)
+      const auto step = [&](auto diag) {
 #pragma unroll
-      for (int t = 0; t < P::kSub; ++t) {
-        f32x16_t s = rows_times<BF16, DC>(lk, t * 32, q);
-        const f32x16_t dp = rows_times<BF16, DC>(lv, t * 32, dO);
+        for (int t = 0; t < P::kSub; ++t) {
+          f32x16_t s = rows_times<BF16, DC>(lk, t * 32, q);
+          const f32x16_t dp = rows_times<BF16, DC>(lv, t * 32, dO);
 #pragma unroll
-        for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, -lse)) * (dp[r] - delta);
-        if (diag) {
-          keep_branch();
+          for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, -lse)) * (dp[r] - delta);
+          if (diag) {
+            keep_branch();
 #pragma unroll
-          for (int r = 0; r < 16; ++r)
-            if (k0 + t * 32 + result_row(r, g) > query) s[r] = 0.f;
+            for (int r = 0; r < 16; ++r)
+              if (k0 + t * 32 + result_row(r, g) > query) s[r] = 0.f;
+          }
+          columns_times<BF16, DC>(lk, t * 32, s, acc);
         }
-        columns_times<BF16, DC>(lk, t * 32, s, acc);
-      }
+      };
+      const bool diag = k0 + 32 * P::kSub - 1 > w0;
+      if (kWide<BF16, DC>) step(diag);
+      else if (diag) step(std::true_type{});
+      else step(std::false_type{});
     }
     if (P::kBuffers == 1 && more) {
       __syncthreads();
-      stage<BF16, DC, P::kStep, P::kWaves>(a.k, start, kh, r0 + P::kStep, len, a.D, base);
-      stage<BF16, DC, P::kStep, P::kWaves>(a.v, start, kh, r0 + P::kStep, len, a.D, base + P::kStage);
+      ks.fetch(r0 + P::kStep, len, base);
+      vs.fetch(r0 + P::kStep, len, base + P::kStage);
     }
     staged();
     if (P::kBuffers == 2) buf ^= 1;
@@ -573,8 +611,8 @@ __global__ __launch_bounds__(64 * GR * NS, BF16 ? 2 : 1) void k_backward_kv(Args
   constexpr int kBuf = 2 * P::kStage + P::kWords;
   __shared__ __align__(1024) unsigned char lds[P::kBuffers * kBuf];
   int32_t start, len, tile, tiles;
-  const int32_t kh = blockIdx.x % a.Hkv, slot = blockIdx.x / a.Hkv, rep = a.Hq / a.Hkv;
-  if (!find_tile(a, slot, P::kRows, start, len, tile, tiles)) return;
+  const int32_t kh = blockIdx.x, rep = a.Hq / a.Hkv;
+  if (!find_tile(a, block_slot(a), P::kRows, start, len, tile, tiles)) return;
   const int lane = threadIdx.x & 63, g = lane >> 5;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), grp = wv % GR, split = wv / GR;
   const int32_t w0 = tile * P::kRows + grp * 32;
@@ -582,9 +620,12 @@ __global__ __launch_bounds__(64 * GR * NS, BF16 ? 2 : 1) void k_backward_kv(Args
   const uint32_t base = lds_address(lds);
   // queries q0 .. of head h, with their lse2 and delta: zeros past the end,
   // whose dO and q rows are zero too and so add nothing
+  typename P::Rows qs(a.q, start, kh * rep, a.D), os(a.dO, start, kh * rep, a.D);
   const auto fetch = [&](int32_t h, int32_t q0, uint32_t to) {
-    stage<BF16, DC, P::kStep, P::kWaves>(a.q, start, h, q0, len, a.D, to);
-    stage<BF16, DC, P::kStep, P::kWaves>(a.dO, start, h, q0, len, a.D, to + P::kStage);
+    qs.head(a.q, start, h);
+    os.head(a.dO, start, h);
+    qs.fetch(q0, len, to);
+    os.fetch(q0, len, to + P::kStage);
     constexpr int parts = P::kStep / 64;
 #pragma unroll
     for (int i = 0; i < 2 * parts; ++i) {
@@ -617,31 +658,36 @@ __global__ __launch_bounds__(64 * GR * NS, BF16 ? 2 : 1) void k_backward_kv(Args
       const unsigned char* lq = lds + buf * kBuf + split * 32 * G::kPitch;
       const unsigned char* lo = lq + P::kStage;
       const float* words = (const float*)(lds + buf * kBuf + 2 * P::kStage) + split * 32;
-      const bool diag = t0 < w0 + 31;
+      const auto step = [&](auto diag) {
 #pragma unroll
-      for (int t = 0; t < P::kSub; ++t) {
-        f32x16_t p = rows_times<BF16, DC>(lq, t * 32, k);
-        f32x16_t ds = rows_times<BF16, DC>(lo, t * 32, v);
+        for (int t = 0; t < P::kSub; ++t) {
+          f32x16_t p = rows_times<BF16, DC>(lq, t * 32, k);
+          f32x16_t ds = rows_times<BF16, DC>(lo, t * 32, v);
 #pragma unroll
-        for (int r4 = 0; r4 < 4; ++r4) {
-          const f32x4_t z = *(const f32x4_t*)(words + t * 32 + 8 * r4 + 4 * g);
-          const f32x4_t e = *(const f32x4_t*)(words + P::kStep + t * 32 + 8 * r4 + 4 * g);
+          for (int r4 = 0; r4 < 4; ++r4) {
+            const f32x4_t z = *(const f32x4_t*)(words + t * 32 + 8 * r4 + 4 * g);
+            const f32x4_t e = *(const f32x4_t*)(words + P::kStep + t * 32 + 8 * r4 + 4 * g);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int r = 4 * r4 + i;
-            p[r] = __builtin_amdgcn_exp2f(fmaf(p[r], c, -z[i]));
-            ds[r] = p[r] * (ds[r] - e[i]);
+            for (int i = 0; i < 4; ++i) {
+              const int r = 4 * r4 + i;
+              p[r] = __builtin_amdgcn_exp2f(fmaf(p[r], c, -z[i]));
+              ds[r] = p[r] * (ds[r] - e[i]);
+            }
           }
-        }
-        if (diag) {
-          keep_branch();
+          if (diag) {
+            keep_branch();
 #pragma unroll
-          for (int r = 0; r < 16; ++r)
-            if (t0 + t * 32 + result_row(r, g) < key) p[r] = 0.f, ds[r] = 0.f;
+            for (int r = 0; r < 16; ++r)
+              if (t0 + t * 32 + result_row(r, g) < key) p[r] = 0.f, ds[r] = 0.f;
+          }
+          columns_times<BF16, DC>(lo, t * 32, p, dv);
+          columns_times<BF16, DC>(lq, t * 32, ds, dk);
         }
-        columns_times<BF16, DC>(lo, t * 32, p, dv);
-        columns_times<BF16, DC>(lq, t * 32, ds, dk);
-      }
+      };
+      const bool diag = t0 < w0 + 31;
+      if (kWide<BF16, DC>) step(diag);
+      else if (diag) step(std::true_type{});
+      else step(std::false_type{});
     }
     if (P::kBuffers == 1 && more) {
       __syncthreads();
