@@ -404,14 +404,14 @@ __global__ __launch_bounds__(64 * GR * NS, BF16 ? 2 : 1) void k_forward(Args a) 
   const float c = a.scale * kLog2e;
   float m = -INFINITY, l = 0.f;
   f32x16_t acc[G::kTiles] = {};
-  f32x16_t s[P::kSub];
+  f32x16_t even[P::kSub], odd[P::kSub];   // scores of the even and the odd steps
   staged();
   const unsigned char* mine = lds + split * 32 * G::kPitch;
 #pragma unroll
-  for (int t = 0; t < P::kSub; ++t) s[t] = rows_times<BF16, DC>(mine, t * 32, q);
+  for (int t = 0; t < P::kSub; ++t) even[t] = rows_times<BF16, DC>(mine, t * 32, q);
   __syncthreads();
-  int buf = 0;
-  for (int32_t r0 = 0; r0 < end; r0 += P::kStep, buf ^= 1) {
+  const auto step = [&](int32_t r0, f32x16_t (&s)[P::kSub], f32x16_t (&next)[P::kSub], auto buffer) {
+    constexpr int buf = buffer.value;
     if (r0 + P::kStep < end) vs.fetch(r0 + P::kStep, len, base + (2 + (buf ^ 1)) * P::kStage);
     if (r0 + 2 * P::kStep < end) ks.fetch(r0 + 2 * P::kStep, len, base + buf * P::kStage);
     const int32_t k0 = r0 + split * 32;
@@ -445,7 +445,6 @@ __global__ __launch_bounds__(64 * GR * NS, BF16 ? 2 : 1) void k_forward(Args a) 
       // (queries that see none of a split's keys so far: every weight 0)
       const float mc = m == -INFINITY ? 0.f : m * c;
       // the next step's scores fill the matrix unit while this step's weights are computed
-      f32x16_t next[P::kSub];
 #pragma unroll
       for (int t = 0; t < P::kSub; ++t) next[t] = rows_times<BF16, DC>(mine + (buf ^ 1) * P::kStage, t * 32, q);
       float sum[2] = {0.f, 0.f};
@@ -458,12 +457,16 @@ __global__ __launch_bounds__(64 * GR * NS, BF16 ? 2 : 1) void k_forward(Args a) 
         }
       l += sum[0] + sum[1];
 #pragma unroll
-      for (int t = 0; t < P::kSub; ++t) {
-        columns_times<BF16, DC>(mine + (2 + buf) * P::kStage, t * 32, s[t], acc);
-        s[t] = next[t];
-      }
+      for (int t = 0; t < P::kSub; ++t) columns_times<BF16, DC>(mine + (2 + buf) * P::kStage, t * 32, s[t], acc);
     }
     staged();
+  };
+  for (int32_t r0 = 0; r0 < end;) {
+    step(r0, even, odd, std::integral_constant<int, 0>{});
+    r0 += P::kStep;
+    if (r0 >= end) break;
+    step(r0, odd, even, std::integral_constant<int, 1>{});
+    r0 += P::kStep;
   }
   l += other_half(l);
   if constexpr (NS > 1) {
