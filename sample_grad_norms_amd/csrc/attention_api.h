@@ -87,6 +87,23 @@ int64_t slots_of(const attn::Args& a, int rows) {
   return a.cu ? (int64_t)a.N / rows + a.S : (int64_t)a.S * ((a.T + rows - 1) / rows);
 }
 
+// Tiles or rows (see attention_kernels.h) for the forward pass and dq, by the
+// work groups that rows give. Rows have the shorter chains and win while the
+// work groups are few (us, rows against tiles: forward T = 1024, 16/4 heads,
+// D = 64 11.6 against 18.7; T = 2048, 16 heads 26 against 33; T = 2048, 32 heads
+// 48 against 37); float32 rows of up to 64 columns, where two of their work groups
+// fit a CU, always (B = 2, T = 2048, 16/4 heads 182 against 275; 128 columns 410
+// against 367).
+constexpr int64_t kRowsMost = 1536;
+template <bool BF16, int DC>
+constexpr bool kRowsAlways = !BF16 && DC == 64;
+
+// dk and dv: eight waves a work group instead of four while the work groups are
+// few, for chains half as long (T = 2048, 32/4 heads: D = 64 88 us against 132,
+// D = 128 156 against 259; B = 4, 32/8 heads, D = 64, 2080 work groups: 242
+// against 208). float32 rows of eight waves do not fit the LDS.
+constexpr int64_t kKeysMost = 600;
+
 // One launch, or more where a grid's z dimension does not hold the slots.
 template <typename F>
 hipError_t launch_slots(attn::Args a, int rows, int rep, F launch) {
@@ -98,41 +115,47 @@ hipError_t launch_slots(attn::Args a, int rows, int rep, F launch) {
   return hipGetLastError();
 }
 
-template <bool BF16, int DC, int GR, int NS>
-hipError_t launch_attn_forward(const attn::Args& a, hipStream_t stream) {
-  using P = attn::Split<BF16, DC, GR, NS>;
-  return launch_slots(a, P::kRows, a.Hq / a.Hkv, [&](const attn::Args& x, dim3 grid) {
-    attn::k_forward<BF16, DC, GR, NS><<<grid, P::kThreads, 0, stream>>>(x);
-  });
-}
-
-template <bool BF16, int DC, int GR, int NS>
-hipError_t launch_attn_backward_q(const attn::Args& a, hipStream_t stream) {
-  using P = attn::Split<BF16, DC, GR, NS>;
-  return launch_slots(a, P::kRows, a.Hq / a.Hkv, [&](const attn::Args& x, dim3 grid) {
-    attn::k_backward_q<BF16, DC, GR, NS><<<grid, P::kThreads, 0, stream>>>(x);
-  });
-}
-
-template <bool BF16, int DC, int GR, int NS>
-hipError_t launch_attn_backward_kv(const attn::Args& a, hipStream_t stream) {
-  using P = attn::Split<BF16, DC, GR, NS>;
-  return launch_slots(a, P::kRows, 1, [&](const attn::Args& x, dim3 grid) {
-    attn::k_backward_kv<BF16, DC, GR, NS><<<grid, P::kThreads, 0, stream>>>(x);
+template <bool BF16, int DC>
+hipError_t run_attn_forward(const attn::Args& a, hipStream_t stream) {
+  const int rep = a.Hq / a.Hkv;
+  if constexpr (!kRowsAlways<BF16, DC>) {
+    if (slots_of(a, 32) * a.Hq > kRowsMost)
+      return launch_slots(a, 128, rep, [&](const attn::Args& x, dim3 grid) {
+        attn::k_forward<BF16, DC><<<grid, 256, 0, stream>>>(x);
+      });
+  }
+  return launch_slots(a, 32, rep, [&](const attn::Args& x, dim3 grid) {
+    attn::k_forward_rows<BF16, DC, 4><<<grid, 256, 0, stream>>>(x);
   });
 }
 
 template <bool BF16, int DC>
-hipError_t run_attn_forward(const attn::Args& a, hipStream_t stream) {
-  return launch_attn_forward<BF16, DC, 4, 1>(a, stream);
+hipError_t run_attn_backward_q(const attn::Args& a, hipStream_t stream) {
+  const int rep = a.Hq / a.Hkv;
+  if constexpr (!kRowsAlways<BF16, DC>) {
+    if (slots_of(a, 32) * a.Hq > kRowsMost)
+      return launch_slots(a, 128, rep, [&](const attn::Args& x, dim3 grid) {
+        attn::k_backward_q<BF16, DC><<<grid, 256, 0, stream>>>(x);
+      });
+  }
+  return launch_slots(a, 32, rep, [&](const attn::Args& x, dim3 grid) {
+    attn::k_backward_q_rows<BF16, DC, 4><<<grid, 256, 0, stream>>>(x);
+  });
 }
 
 template <bool BF16, int DC>
 hipError_t run_attn_backward(const attn::Args& a, hipStream_t stream) {
-  hipError_t he = launch_attn_backward_q<BF16, DC, 4, 1>(a, stream);
+  const hipError_t he = run_attn_backward_q<BF16, DC>(a, stream);
   if (he != hipSuccess) return he;
-  if constexpr (BF16) return launch_attn_backward_kv<BF16, DC, 4, 2>(a, stream);
-  else return launch_attn_backward_kv<BF16, DC, 2, 2>(a, stream);
+  if constexpr (BF16) {
+    if (slots_of(a, 32) * a.Hkv <= kKeysMost)
+      return launch_slots(a, 32, 1, [&](const attn::Args& x, dim3 grid) {
+        attn::k_backward_kv<BF16, DC, 8><<<grid, 512, 0, stream>>>(x);
+      });
+  }
+  return launch_slots(a, 32, 1, [&](const attn::Args& x, dim3 grid) {
+    attn::k_backward_kv<BF16, DC, 4><<<grid, 256, 0, stream>>>(x);
+  });
 }
 
 }  // namespace
@@ -173,7 +196,7 @@ dpnorm_status dpnorm_attention_backward_workspace(const dpnorm_attn_shape* shape
   if (!bytes) return DPNORM_ERR_NULL;
   const dpnorm_status st = check_shape(shape);
   if (st != DPNORM_OK) return st;
-  *bytes = 2 * align_up((size_t)shape->N * shape->Hq * 4);
+  *bytes = align_up((size_t)shape->N * shape->Hq * 8);
   return DPNORM_OK;
 }
 
@@ -212,8 +235,7 @@ dpnorm_status dpnorm_attention_backward(const dpnorm_attn_shape* shape, const dp
   a.dk = tensor_of(dk, e);
   a.dv = tensor_of(dv, e);
   a.lse = const_cast<float*>(lse);
-  a.delta = (float*)ws;
-  a.lse2 = (float*)((char*)ws + bytes / 2);
+  a.pairs = (float*)ws;
   if (shape->dtype == DPNORM_BF16)
     return hip_status(D <= 64 ? run_attn_backward<true, 64>(a, stream) : D <= 96 ? run_attn_backward<true, 96>(a, stream)
                                                                            : run_attn_backward<true, 128>(a, stream));

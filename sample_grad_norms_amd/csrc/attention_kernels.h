@@ -45,8 +45,7 @@ struct Tensor {     // [token][head][D], strides in bytes
 struct Args {
   Tensor q, k, v, o, dO, dq, dk, dv;
   float* lse;         // [Hq][N]
-  float* delta;       // [Hq][N], backward: written with lse2 by the first launch for the second
-  float* lse2;        // [Hq][N], lse in units of log 2
+  float* pairs;       // [Hq][N][2], backward: lse in units of log 2 and delta, of the first launch for the second
   const int32_t* cu;  // [S + 1], or null: S sequences of T tokens
   int32_t S, T, N;
   int32_t Hq, Hkv, D;
@@ -158,29 +157,34 @@ struct Stream {
   using G = Geo<BF16, DC>;
   static constexpr int kLoads = ROWS * G::kChunks / (64 * W);    // of a wave
   static constexpr int kApart = 64 * W / G::kChunks;             // rows between a lane's loads
-  static_assert(kLoads * 64 * W == ROWS * G::kChunks && kApart % 8 == 0, "whole loads, one swizzle a lane");
+  static constexpr int kKinds = kApart >= 8 ? 1 : 8 / kApart;    // loads until the swizzle of a lane's row repeats
+  static_assert(kLoads * 64 * W == ROWS * G::kChunks && kLoads % kKinds == 0, "whole loads");
   const char* p;      // the sequence's first row
   int64_t st;
-  uint32_t off;       // the lane's first load: row, chunk
+  uint32_t off[kKinds];   // the lane's first loads: row, chunk
   int row;
   __device__ __forceinline__ Stream(const Tensor& t, int64_t start, int32_t h, int32_t D) {
     p = row_ptr(t, start, h);
     st = t.st;
-    row = threadIdx.x / G::kChunks;
-    const int ch = swizzle<BF16, DC>(threadIdx.x % G::kChunks, row);
-    off = ch * 16 < D * G::kElem ? (uint32_t)(row * (int32_t)st + ch * 16) : kOutside;
+    const int at = W == 1 ? threadIdx.x & 63 : threadIdx.x;
+    row = at / G::kChunks;
+#pragma unroll
+    for (int j = 0; j < kKinds; ++j) {
+      const int r = row + j * kApart, ch = swizzle<BF16, DC>(at % G::kChunks, r);
+      off[j] = ch * 16 < D * G::kElem ? (uint32_t)(r * (int32_t)st + ch * 16) : kOutside;
+    }
   }
   __device__ __forceinline__ void head(const Tensor& t, int64_t start, int32_t h) { p = row_ptr(t, start, h); }
   __device__ __forceinline__ void fetch(int32_t r0, int32_t len, uint32_t lds) const {
     const i32x4_t rows = rows_of(p + r0 * st);
-    const uint32_t to = lds + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 1024;
-    if (len - r0 >= ROWS) {
+    const uint32_t to = lds + (W == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 1024);
+    const int32_t left = len - r0;
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) dma_rows(rows, off, i * kApart * (int32_t)st, to + i * W * 1024);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i)
-        dma_rows(rows, row + i * kApart < len - r0 ? off : kOutside, i * kApart * (int32_t)st, to + i * W * 1024);
+    for (int i = 0; i < kLoads; ++i) {
+      const uint32_t o = off[i % kKinds];
+      const int32_t more = i / kKinds * kKinds * kApart * (int32_t)st;
+      if (left >= ROWS) dma_rows(rows, o, more, to + i * W * 1024);
+      else dma_rows(rows, row + i * kApart < left ? o : kOutside, more, to + i * W * 1024);
     }
   }
 };
@@ -190,6 +194,12 @@ struct Stream {
 __device__ __forceinline__ void staged() {
   DPN_WAIT_VMCNT(0);
   __syncthreads();
+}
+
+// The same for rows that only this wave loads and reads.
+__device__ __forceinline__ void own_staged() {
+  __builtin_amdgcn_s_waitcnt(0x70);   // vmcnt(0) lgkmcnt(0)
+  asm volatile("" ::: "memory");
 }
 
 // The wave's 32 stationary rows as an operand: lane l has row l % 32, chunk
@@ -293,11 +303,6 @@ __device__ __forceinline__ int result_row(int r, int g) { return 8 * (r >> 2) + 
 // of every step, of which one or two at the diagonal need them.
 __device__ __forceinline__ void keep_branch() { asm volatile(""); }
 
-// Wide rows leave no registers for a backward step as one block of
-// instructions: they keep one copy of it, with the mask as a branch.
-template <bool BF16, int DC>
-constexpr bool kWide = !BF16 || DC > 64;
-
 // Columns of acc (transposed: rows are the D index) to row `row` of t, times f.
 template <bool BF16, int DC>
 __device__ __forceinline__ void store_rows(const Tensor& t, int64_t row, int32_t h, int32_t D,
@@ -329,32 +334,46 @@ __device__ __forceinline__ void store_rows(const Tensor& t, int64_t row, int32_t
 // key head meet in one L2 when Hkv is a multiple or a divisor of 8.
 __device__ __forceinline__ int32_t block_slot(const Args& a) { return a.slot0 + (int32_t)blockIdx.z; }
 
-// Work groups: GR groups of 32 stationary rows, each taken by NS waves that
-// split the streamed rows of a step. With NS = 1 a wave takes 64 rows a step,
-// else 32. The steps' rows are double buffered in LDS where two fit.
-template <bool BF16, int DC, int GR, int NS>
-struct Split {
+// Two forms of work groups.
+//
+// Tiles: 128 stationary rows, 32 a wave, whose four waves share 64 streamed rows
+// a step in LDS. The least traffic and LDS writing a product.
+//
+// Rows: 32 stationary rows, whose NS waves take 32 streamed rows each in turn,
+// from LDS of their own, so that no wave waits for another; their sums are joined
+// at the end. Four times the work groups and shorter chains of steps.
+template <bool BF16, int DC>
+struct Tiles {
   using G = Geo<BF16, DC>;
-  static constexpr int kWaves = GR * NS, kThreads = 64 * kWaves;
-  static constexpr int kRows = 32 * GR;              // stationary rows
-  static constexpr int kSub = NS == 1 ? 2 : 1;       // 32-row tiles of a wave and step
-  static constexpr int kStep = 32 * NS * kSub;       // streamed rows a step
+  static constexpr int kWaves = 4, kThreads = 64 * kWaves, kRows = 128, kStep = 64;
   static constexpr int kStage = kStep * G::kPitch;   // bytes of one tensor's step
-  static constexpr int kWords = 2 * kStep * 4;       // lse2 and delta of a step (dk and dv)
-  static constexpr int kBuffers = 2 * (2 * kStage + kWords) <= 132 * 1024 ? 2 : 1;
+  static constexpr int kBuffers = 4 * kStage <= 132 * 1024 ? 2 : 1;
   using Rows = Stream<BF16, DC, kStep, kWaves>;
 };
 
-// Adds the accumulators of the waves of one row group, in split order, to the
+// Bytes of a wave's own step are kBuf, for two tensors and the kExtra of dk and
+// dv. Two buffers where two work groups of them fit a CU: a second work group
+// hides more of the loads' latency than a second buffer (dk and dv of
+// B = 4, T = 2048, 16/4 heads, D = 128: 273 us with one buffer, 343 with two).
+template <bool BF16, int DC, int NS, int EXTRA>
+struct OwnRows {
+  using G = Geo<BF16, DC>;
+  static constexpr int kStage = 32 * G::kPitch, kBuf = 2 * kStage + EXTRA;
+  static constexpr int kBuffers = NS * 2 * kBuf <= 80 * 1024 ? 2 : 1;
+  static constexpr int kLds = NS * kBuffers * kBuf;
+  using Rows = Stream<BF16, DC, 32, 1>;
+};
+
+// Adds the accumulators of the waves of a work group, in wave order, to the
 // first one's. `lds` is free; every wave of the block calls it.
-template <int GR, int NS, int TILES>
-__device__ __forceinline__ void join(f32x16_t (&acc)[TILES], int grp, int split, unsigned char* lds) {
+template <int NS, int TILES>
+__device__ __forceinline__ void join(f32x16_t (&acc)[TILES], int split, unsigned char* lds) {
   const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int t = 0; t < TILES; ++t) {
     __syncthreads();
     if (split > 0) {
-      f32x4_t* p = (f32x4_t*)(lds + ((split - 1) * GR + grp) * 4096) + lane;
+      f32x4_t* p = (f32x4_t*)(lds + (split - 1) * 4096) + lane;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         p[64 * j] = f32x4_t{acc[t][4 * j], acc[t][4 * j + 1], acc[t][4 * j + 2], acc[t][4 * j + 3]};
@@ -363,7 +382,7 @@ __device__ __forceinline__ void join(f32x16_t (&acc)[TILES], int grp, int split,
     if (split == 0) {
 #pragma unroll
       for (int s = 1; s < NS; ++s) {
-        const f32x4_t* p = (const f32x4_t*)(lds + ((s - 1) * GR + grp) * 4096) + lane;
+        const f32x4_t* p = (const f32x4_t*)(lds + (s - 1) * 4096) + lane;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const f32x4_t x = p[64 * j];
@@ -379,10 +398,113 @@ __device__ __forceinline__ void join(f32x16_t (&acc)[TILES], int grp, int split,
 // rescaling its sums: the weights stay below 2^8 and the sums far inside fp32.
 constexpr float kGrowth = 8.f;
 
-template <bool BF16, int DC, int GR, int NS>
-__global__ __launch_bounds__(64 * GR * NS, BF16 ? 2 : 1) void k_forward(Args a) {
+template <bool BF16, int DC, int NS>
+__global__ __launch_bounds__(64 * NS, BF16 ? 2 : 1) void k_forward_rows(Args a) {
   using G = Geo<BF16, DC>;
-  using P = Split<BF16, DC, GR, NS>;
+  using P = OwnRows<BF16, DC, NS, 0>;
+  __shared__ __align__(1024) unsigned char lds[P::kLds];
+  int32_t start, len, tile, tiles;
+  if (!find_tile(a, block_slot(a), 32, start, len, tile, tiles)) return;
+  tile = tiles - 1 - tile;
+  const int32_t kh = blockIdx.x, h = kh * gridDim.y + blockIdx.y;
+  const int lane = threadIdx.x & 63, g = lane >> 5;
+  const int split = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int32_t w0 = tile * 32, query = w0 + (lane & 31);
+  const unsigned char* mine = lds + split * P::kBuffers * P::kBuf;
+  const uint32_t base = lds_address(mine);
+  const typename P::Rows ks(a.k, start, kh, a.D), vs(a.v, start, kh, a.D);
+  const auto fetch = [&](int32_t r0, uint32_t to) {
+    ks.fetch(r0, len, to);
+    vs.fetch(r0, len, to + P::kStage);
+  };
+  int32_t k0 = 32 * split;
+  if (k0 <= w0) fetch(k0, base);
+  uint4 q[G::kPairs];
+  load_operand<BF16, DC>(a.q, start, h, w0, len, a.D, q);
+  const float c = a.scale * kLog2e;
+  float m = -INFINITY, l = 0.f;
+  f32x16_t acc[G::kTiles] = {};
+  int buf = 0;
+  for (; k0 <= w0; k0 += 32 * NS) {
+    own_staged();
+    const bool more = k0 + 32 * NS <= w0;
+    if (P::kBuffers == 2 && more) fetch(k0 + 32 * NS, base + (buf ^ 1) * P::kBuf);
+    const unsigned char* lk = mine + buf * P::kBuf;
+    const unsigned char* lv = lk + P::kStage;
+    f32x16_t s = rows_times<BF16, DC>(lk, 0, q);
+    if (k0 == w0) {
+      keep_branch();
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        if (k0 + result_row(r, g) > query) s[r] = -INFINITY;
+    }
+    float x[2] = {s[0], s[1]};
+#pragma unroll
+    for (int r = 2; r < 16; ++r) x[r & 1] = fmaxf(x[r & 1], s[r]);
+    float top = fmaxf(x[0], x[1]);
+    top = fmaxf(top, other_half(top));
+    if (__any((top - m) * c > kGrowth)) {
+      keep_branch();
+      top = fmaxf(m, top);
+      const float f = top == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - top) * c);
+      m = top;
+      l *= f;
+#pragma unroll
+      for (int t = 0; t < G::kTiles; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[t][r] *= f;
+    }
+    // (queries that see none of a split's keys so far: every weight 0)
+    const float mc = m == -INFINITY ? 0.f : m * c;
+    float sum[2] = {0.f, 0.f};
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, -mc));
+      sum[r & 1] += s[r];
+    }
+    l += sum[0] + sum[1];
+    columns_times<BF16, DC>(lv, 0, s, acc);
+    if (P::kBuffers == 2) {
+      buf ^= 1;
+    } else if (more) {
+      own_staged();   // (the reads of this step are done)
+      fetch(k0 + 32 * NS, base);
+    }
+  }
+  l += other_half(l);
+  if constexpr (NS > 1) {
+    // the splits' sums on the scale of their common largest score
+    float* st = (float*)lds;
+    __syncthreads();
+    st[split * 64 + lane] = m;
+    __syncthreads();
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NS; ++i) top = fmaxf(top, st[i * 64 + lane]);
+    const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - top) * c);
+    m = top;
+    __syncthreads();
+    st[split * 64 + lane] = l * f;
+    __syncthreads();
+    l = 0.f;
+#pragma unroll
+    for (int i = 0; i < NS; ++i) l += st[i * 64 + lane];
+#pragma unroll
+    for (int t = 0; t < G::kTiles; ++t)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[t][r] *= f;
+    join<NS, G::kTiles>(acc, split, lds);
+    if (split > 0) return;
+  }
+  if (query >= len) return;
+  store_rows<BF16, DC>(a.o, (int64_t)start + query, h, a.D, acc, 1.f / l);
+  if (g == 0) a.lse[(int64_t)h * a.N + start + query] = fmaf(m, a.scale, logf(l));
+}
+
+template <bool BF16, int DC>
+__global__ __launch_bounds__(256, BF16 ? 2 : 1) void k_forward(Args a) {
+  using G = Geo<BF16, DC>;
+  using P = Tiles<BF16, DC>;
   // keys are needed a step ahead of their values, whose scores they give
   __shared__ __align__(1024) unsigned char lds[4 * P::kStage];
   int32_t start, len, tile, tiles;
@@ -390,8 +512,8 @@ __global__ __launch_bounds__(64 * GR * NS, BF16 ? 2 : 1) void k_forward(Args a) 
   tile = tiles - 1 - tile;   // the longest rows first
   const int32_t kh = blockIdx.x, h = kh * gridDim.y + blockIdx.y;
   const int lane = threadIdx.x & 63, g = lane >> 5;
-  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), grp = wv % GR, split = wv / GR;
-  const int32_t w0 = tile * P::kRows + grp * 32;   // the wave's first query
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int32_t w0 = tile * P::kRows + wv * 32;   // the wave's first query
   const int32_t query = w0 + (lane & 31);
   const uint32_t base = lds_address(lds);
   const int32_t end = min(tile * P::kRows + P::kRows, len);   // keys that some query of the block sees
@@ -404,29 +526,27 @@ __global__ __launch_bounds__(64 * GR * NS, BF16 ? 2 : 1) void k_forward(Args a) 
   const float c = a.scale * kLog2e;
   float m = -INFINITY, l = 0.f;
   f32x16_t acc[G::kTiles] = {};
-  f32x16_t even[P::kSub], odd[P::kSub];   // scores of the even and the odd steps
+  f32x16_t even[2], odd[2];   // scores of the even and the odd steps
   staged();
-  const unsigned char* mine = lds + split * 32 * G::kPitch;
 #pragma unroll
-  for (int t = 0; t < P::kSub; ++t) even[t] = rows_times<BF16, DC>(mine, t * 32, q);
+  for (int t = 0; t < 2; ++t) even[t] = rows_times<BF16, DC>(lds, t * 32, q);
   __syncthreads();
-  const auto step = [&](int32_t r0, f32x16_t (&s)[P::kSub], f32x16_t (&next)[P::kSub], auto buffer) {
+  const auto step = [&](int32_t r0, f32x16_t (&s)[2], f32x16_t (&next)[2], auto buffer) {
     constexpr int buf = buffer.value;
     if (r0 + P::kStep < end) vs.fetch(r0 + P::kStep, len, base + (2 + (buf ^ 1)) * P::kStage);
     if (r0 + 2 * P::kStep < end) ks.fetch(r0 + 2 * P::kStep, len, base + buf * P::kStage);
-    const int32_t k0 = r0 + split * 32;
-    if (k0 <= w0 + 31) {
-      if (k0 + 32 * P::kSub - 1 > w0) {
+    if (r0 <= w0 + 31) {
+      if (r0 + 63 > w0) {
         keep_branch();
 #pragma unroll
-        for (int t = 0; t < P::kSub; ++t)
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
           for (int r = 0; r < 16; ++r)
-            if (k0 + t * 32 + result_row(r, g) > query) s[t][r] = -INFINITY;
+            if (r0 + t * 32 + result_row(r, g) > query) s[t][r] = -INFINITY;
       }
       float x[4] = {s[0][0], s[0][1], s[0][2], s[0][3]};
 #pragma unroll
-      for (int t = 0; t < P::kSub; ++t)
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int r = 0; r < 16; ++r) x[r & 3] = fmaxf(x[r & 3], s[t][r]);
       float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
@@ -434,7 +554,7 @@ __global__ __launch_bounds__(64 * GR * NS, BF16 ? 2 : 1) void k_forward(Args a) 
       if (__any((top - m) * c > kGrowth)) {
         keep_branch();
         top = fmaxf(m, top);
-        const float f = top == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - top) * c);
+        const float f = __builtin_amdgcn_exp2f((m - top) * c);
         m = top;
         l *= f;
 #pragma unroll
@@ -442,14 +562,13 @@ __global__ __launch_bounds__(64 * GR * NS, BF16 ? 2 : 1) void k_forward(Args a) 
 #pragma unroll
           for (int r = 0; r < 16; ++r) acc[t][r] *= f;
       }
-      // (queries that see none of a split's keys so far: every weight 0)
-      const float mc = m == -INFINITY ? 0.f : m * c;
+      const float mc = m * c;
       // the next step's scores fill the matrix unit while this step's weights are computed
 #pragma unroll
-      for (int t = 0; t < P::kSub; ++t) next[t] = rows_times<BF16, DC>(mine + (buf ^ 1) * P::kStage, t * 32, q);
+      for (int t = 0; t < 2; ++t) next[t] = rows_times<BF16, DC>(lds + (buf ^ 1) * P::kStage, t * 32, q);
       float sum[2] = {0.f, 0.f};
 #pragma unroll
-      for (int t = 0; t < P::kSub; ++t)
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
           s[t][r] = __builtin_amdgcn_exp2f(fmaf(s[t][r], c, -mc));
@@ -457,7 +576,7 @@ __global__ __launch_bounds__(64 * GR * NS, BF16 ? 2 : 1) void k_forward(Args a) 
         }
       l += sum[0] + sum[1];
 #pragma unroll
-      for (int t = 0; t < P::kSub; ++t) columns_times<BF16, DC>(mine + (2 + buf) * P::kStage, t * 32, s[t], acc);
+      for (int t = 0; t < 2; ++t) columns_times<BF16, DC>(lds + (2 + buf) * P::kStage, t * 32, s[t], acc);
     }
     staged();
   };
@@ -469,29 +588,6 @@ __global__ __launch_bounds__(64 * GR * NS, BF16 ? 2 : 1) void k_forward(Args a) 
     r0 += P::kStep;
   }
   l += other_half(l);
-  if constexpr (NS > 1) {
-    // the splits' sums on the scale of their common largest score
-    float* st = (float*)lds;
-    st[(split * GR + grp) * 64 + lane] = m;
-    __syncthreads();
-    float top = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < NS; ++i) top = fmaxf(top, st[(i * GR + grp) * 64 + lane]);
-    const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - top) * c);
-    m = top;
-    __syncthreads();
-    st[(split * GR + grp) * 64 + lane] = l * f;
-    __syncthreads();
-    l = 0.f;
-#pragma unroll
-    for (int i = 0; i < NS; ++i) l += st[(i * GR + grp) * 64 + lane];
-#pragma unroll
-    for (int t = 0; t < G::kTiles; ++t)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[t][r] *= f;
-    join<GR, NS, G::kTiles>(acc, grp, split, lds);
-    if (split > 0) return;
-  }
   if (query >= len) return;
   store_rows<BF16, DC>(a.o, (int64_t)start + query, h, a.D, acc, 1.f / l);
   if (g == 0) a.lse[(int64_t)h * a.N + start + query] = fmaf(m, a.scale, logf(l));
@@ -513,19 +609,19 @@ __device__ __forceinline__ float dot_chunk(const uint4& x, const uint4& y, float
   return s;
 }
 
-// dq, and delta and lse2 for the second launch.
-template <bool BF16, int DC, int GR, int NS>
-__global__ __launch_bounds__(64 * GR * NS, BF16 ? 2 : 1) void k_backward_q(Args a) {
+// dq, and the pairs for the second launch, by tiles.
+template <bool BF16, int DC>
+__global__ __launch_bounds__(256, BF16 ? 2 : 1) void k_backward_q(Args a) {
   using G = Geo<BF16, DC>;
-  using P = Split<BF16, DC, GR, NS>;
+  using P = Tiles<BF16, DC>;
   __shared__ __align__(1024) unsigned char lds[P::kBuffers * 2 * P::kStage];
   int32_t start, len, tile, tiles;
   if (!find_tile(a, block_slot(a), P::kRows, start, len, tile, tiles)) return;
   tile = tiles - 1 - tile;
   const int32_t kh = blockIdx.x, h = kh * gridDim.y + blockIdx.y;
   const int lane = threadIdx.x & 63, g = lane >> 5;
-  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), grp = wv % GR, split = wv / GR;
-  const int32_t w0 = tile * P::kRows + grp * 32;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int32_t w0 = tile * P::kRows + wv * 32;
   const int32_t query = w0 + (lane & 31);
   const uint32_t base = lds_address(lds);
   const int32_t end = min(tile * P::kRows + P::kRows, len);
@@ -547,9 +643,8 @@ __global__ __launch_bounds__(64 * GR * NS, BF16 ? 2 : 1) void k_backward_q(Args 
   if (query < len) {
     const int64_t at = (int64_t)h * a.N + start + query;
     lse = a.lse[at] * kLog2e;
-    if (g == 0 && split == 0) {
-      a.delta[at] = delta;
-      a.lse2[at] = lse;
+    if (g == 0) {
+      *(float2*)(a.pairs + 2 * at) = make_float2(lse, delta);
     }
   }
   const float c = a.scale * kLog2e;
@@ -563,14 +658,12 @@ __global__ __launch_bounds__(64 * GR * NS, BF16 ? 2 : 1) void k_backward_q(Args 
       ks.fetch(r0 + P::kStep, len, to);
       vs.fetch(r0 + P::kStep, len, to + P::kStage);
     }
-    const int32_t k0 = r0 + split * 32;
-    if (k0 <= w0 + 31) {
-      const unsigned char* lk = lds + buf * 2 * P::kStage + split * 32 * G::kPitch;
+    if (r0 <= w0 + 31) {
+      const unsigned char* lk = lds + buf * 2 * P::kStage;
       const unsigned char* lv = lk + P::kStage;
-      // (two copies, so that a step off the diagonal is one block of instructions)
-      const auto step = [&](auto diag) {
+      const auto step = [&](bool diag) {
 #pragma unroll
-        for (int t = 0; t < P::kSub; ++t) {
+        for (int t = 0; t < 2; ++t) {
           f32x16_t s = rows_times<BF16, DC>(lk, t * 32, q);
           const f32x16_t dp = rows_times<BF16, DC>(lv, t * 32, dO);
 #pragma unroll
@@ -579,15 +672,13 @@ __global__ __launch_bounds__(64 * GR * NS, BF16 ? 2 : 1) void k_backward_q(Args 
             keep_branch();
 #pragma unroll
             for (int r = 0; r < 16; ++r)
-              if (k0 + t * 32 + result_row(r, g) > query) s[r] = 0.f;
+              if (r0 + t * 32 + result_row(r, g) > query) s[r] = 0.f;
           }
           columns_times<BF16, DC>(lk, t * 32, s, acc);
         }
       };
-      const bool diag = k0 + 32 * P::kSub - 1 > w0;
-      if (kWide<BF16, DC>) step(diag);
-      else if (diag) step(std::true_type{});
-      else step(std::false_type{});
+      const bool diag = r0 + 63 > w0;
+      step(diag);
     }
     if (P::kBuffers == 1 && more) {
       __syncthreads();
@@ -597,114 +688,166 @@ __global__ __launch_bounds__(64 * GR * NS, BF16 ? 2 : 1) void k_backward_q(Args 
     staged();
     if (P::kBuffers == 2) buf ^= 1;
   }
+  if (query >= len) return;
+  store_rows<BF16, DC>(a.dq, (int64_t)start + query, h, a.D, acc, a.scale);
+}
+
+// The same by rows.
+template <bool BF16, int DC, int NS>
+__global__ __launch_bounds__(64 * NS, BF16 ? 2 : 1) void k_backward_q_rows(Args a) {
+  using G = Geo<BF16, DC>;
+  using P = OwnRows<BF16, DC, NS, 0>;
+  __shared__ __align__(1024) unsigned char lds[P::kLds];
+  int32_t start, len, tile, tiles;
+  if (!find_tile(a, block_slot(a), 32, start, len, tile, tiles)) return;
+  tile = tiles - 1 - tile;
+  const int32_t kh = blockIdx.x, h = kh * gridDim.y + blockIdx.y;
+  const int lane = threadIdx.x & 63, g = lane >> 5;
+  const int split = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int32_t w0 = tile * 32, query = w0 + (lane & 31);
+  const unsigned char* mine = lds + split * P::kBuffers * P::kBuf;
+  const uint32_t base = lds_address(mine);
+  const typename P::Rows ks(a.k, start, kh, a.D), vs(a.v, start, kh, a.D);
+  const auto fetch = [&](int32_t r0, uint32_t to) {
+    ks.fetch(r0, len, to);
+    vs.fetch(r0, len, to + P::kStage);
+  };
+  int32_t k0 = 32 * split;
+  if (k0 <= w0) fetch(k0, base);
+  uint4 q[G::kPairs], dO[G::kPairs];
+  float delta = 0.f;
+  {
+    uint4 o[G::kPairs];
+    load_operand<BF16, DC>(a.dO, start, h, w0, len, a.D, dO);
+    load_operand<BF16, DC>(a.o, start, h, w0, len, a.D, o);
+    load_operand<BF16, DC>(a.q, start, h, w0, len, a.D, q);
+#pragma unroll
+    for (int i = 0; i < G::kPairs; ++i) delta = dot_chunk<BF16>(dO[i], o[i], delta);
+    delta += other_half(delta);
+  }
+  float lse = 0.f;
+  if (query < len) {
+    const int64_t at = (int64_t)h * a.N + start + query;
+    lse = a.lse[at] * kLog2e;
+    if (g == 0 && split == 0) *(float2*)(a.pairs + 2 * at) = make_float2(lse, delta);
+  }
+  const float c = a.scale * kLog2e;
+  f32x16_t acc[G::kTiles] = {};
+  int buf = 0;
+  for (; k0 <= w0; k0 += 32 * NS) {
+    own_staged();
+    const bool more = k0 + 32 * NS <= w0;
+    if (P::kBuffers == 2 && more) fetch(k0 + 32 * NS, base + (buf ^ 1) * P::kBuf);
+    const unsigned char* lk = mine + buf * P::kBuf;
+    const unsigned char* lv = lk + P::kStage;
+    f32x16_t s = rows_times<BF16, DC>(lk, 0, q);
+    const f32x16_t dp = rows_times<BF16, DC>(lv, 0, dO);
+#pragma unroll
+    for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, -lse)) * (dp[r] - delta);
+    if (k0 == w0) {
+      keep_branch();
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        if (k0 + result_row(r, g) > query) s[r] = 0.f;
+    }
+    columns_times<BF16, DC>(lk, 0, s, acc);
+    if (P::kBuffers == 2) {
+      buf ^= 1;
+    } else if (more) {
+      own_staged();   // (the reads of this step are done)
+      fetch(k0 + 32 * NS, base);
+    }
+  }
   if constexpr (NS > 1) {
-    join<GR, NS, G::kTiles>(acc, grp, split, lds);
+    join<NS, G::kTiles>(acc, split, lds);
     if (split > 0) return;
   }
   if (query >= len) return;
   store_rows<BF16, DC>(a.dq, (int64_t)start + query, h, a.D, acc, a.scale);
 }
 
-// dk and dv of 32 GR keys of one key head: all query heads of the key head and
+// dk and dv by rows: 32 keys of one key head, all query heads of the key head and
 // all queries from the diagonal on.
-template <bool BF16, int DC, int GR, int NS>
-__global__ __launch_bounds__(64 * GR * NS, BF16 ? 2 : 1) void k_backward_kv(Args a) {
+template <bool BF16, int DC, int NS>
+__global__ __launch_bounds__(64 * NS, BF16 ? 2 : 1) void k_backward_kv(Args a) {
   using G = Geo<BF16, DC>;
-  using P = Split<BF16, DC, GR, NS>;
-  constexpr int kBuf = 2 * P::kStage + P::kWords;
-  __shared__ __align__(1024) unsigned char lds[P::kBuffers * kBuf];
+  using P = OwnRows<BF16, DC, NS, 256>;
+  __shared__ __align__(1024) unsigned char lds[P::kLds];
   int32_t start, len, tile, tiles;
   const int32_t kh = blockIdx.x, rep = a.Hq / a.Hkv;
-  if (!find_tile(a, block_slot(a), P::kRows, start, len, tile, tiles)) return;
+  if (!find_tile(a, block_slot(a), 32, start, len, tile, tiles)) return;
   const int lane = threadIdx.x & 63, g = lane >> 5;
-  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), grp = wv % GR, split = wv / GR;
-  const int32_t w0 = tile * P::kRows + grp * 32;
-  const int32_t key = w0 + (lane & 31);
-  const uint32_t base = lds_address(lds);
-  // queries q0 .. of head h, with their lse2 and delta: zeros past the end,
-  // whose dO and q rows are zero too and so add nothing
+  const int split = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int32_t w0 = tile * 32, key = w0 + (lane & 31);
+  const unsigned char* mine = lds + split * P::kBuffers * P::kBuf;
+  const uint32_t base = lds_address(mine);
+  // 32 queries from q0 on of head h, with their lse and delta: zeros past the
+  // end, whose dO and q rows are zero too and so add nothing
   typename P::Rows qs(a.q, start, kh * rep, a.D), os(a.dO, start, kh * rep, a.D);
   const auto fetch = [&](int32_t h, int32_t q0, uint32_t to) {
     qs.head(a.q, start, h);
     os.head(a.dO, start, h);
     qs.fetch(q0, len, to);
     os.fetch(q0, len, to + P::kStage);
-    constexpr int parts = P::kStep / 64;
-#pragma unroll
-    for (int i = 0; i < 2 * parts; ++i) {
-      if (i % P::kWaves != wv) continue;
-      const float* src = (i < parts ? a.lse2 : a.delta) + (int64_t)h * a.N + start + q0;
-      const int row = (i % parts) * 64 + lane;
-      dma_words(rows_of((const char*)src), q0 + row < len ? row * 4 : kOutside, to + 2 * P::kStage + i * 256);
-    }
+    const char* at = (const char*)(a.pairs + 2 * ((int64_t)h * a.N + start + q0));
+    dma_words(rows_of(at), q0 + (lane >> 1) < len ? lane * 4 : kOutside, to + 2 * P::kStage);
   };
-  const int32_t first = tile * P::kRows / P::kStep * P::kStep;   // a step's start at or before the first key
-  int32_t h = kh * rep, q0 = first;
-  fetch(h, q0, base);
+  const int32_t first = w0 + 32 * split;
+  const int32_t per = first < len ? (len - first + 32 * NS - 1) / (32 * NS) : 0;   // steps a head
+  const int32_t steps = per * rep;
   uint4 k[G::kPairs], v[G::kPairs];
+  if (steps > 0) fetch(kh * rep, first, base);
   load_operand<BF16, DC>(a.k, start, kh, w0, len, a.D, k);
   load_operand<BF16, DC>(a.v, start, kh, w0, len, a.D, v);
   const float c = a.scale * kLog2e;
   f32x16_t dk[G::kTiles] = {}, dv[G::kTiles] = {};
-  staged();
+  int32_t h = kh * rep, q0 = first;
   int buf = 0;
-  for (;;) {
-    int32_t nh = h, nq = q0 + P::kStep;
+  for (int32_t i = 0; i < steps; ++i) {
+    int32_t nh = h, nq = q0 + 32 * NS;
     if (nq >= len) {
       nq = first;
       ++nh;
     }
-    const bool more = nh < kh * rep + rep;
-    if (P::kBuffers == 2 && more) fetch(nh, nq, base + (buf ^ 1) * kBuf);
-    const int32_t t0 = q0 + split * 32;
-    if (t0 + 32 * P::kSub - 1 >= w0) {
-      const unsigned char* lq = lds + buf * kBuf + split * 32 * G::kPitch;
-      const unsigned char* lo = lq + P::kStage;
-      const float* words = (const float*)(lds + buf * kBuf + 2 * P::kStage) + split * 32;
-      const auto step = [&](auto diag) {
+    own_staged();
+    if (P::kBuffers == 2 && i + 1 < steps) fetch(nh, nq, base + (buf ^ 1) * P::kBuf);
+    const unsigned char* lq = mine + buf * P::kBuf;
+    const unsigned char* lo = lq + P::kStage;
+    const float* words = (const float*)(lq + 2 * P::kStage);
+    f32x16_t p = rows_times<BF16, DC>(lq, 0, k);
+    f32x16_t ds = rows_times<BF16, DC>(lo, 0, v);
 #pragma unroll
-        for (int t = 0; t < P::kSub; ++t) {
-          f32x16_t p = rows_times<BF16, DC>(lq, t * 32, k);
-          f32x16_t ds = rows_times<BF16, DC>(lo, t * 32, v);
+    for (int r4 = 0; r4 < 4; ++r4) {
 #pragma unroll
-          for (int r4 = 0; r4 < 4; ++r4) {
-            const f32x4_t z = *(const f32x4_t*)(words + t * 32 + 8 * r4 + 4 * g);
-            const f32x4_t e = *(const f32x4_t*)(words + P::kStep + t * 32 + 8 * r4 + 4 * g);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int r = 4 * r4 + i;
-              p[r] = __builtin_amdgcn_exp2f(fmaf(p[r], c, -z[i]));
-              ds[r] = p[r] * (ds[r] - e[i]);
-            }
-          }
-          if (diag) {
-            keep_branch();
-#pragma unroll
-            for (int r = 0; r < 16; ++r)
-              if (t0 + t * 32 + result_row(r, g) < key) p[r] = 0.f, ds[r] = 0.f;
-          }
-          columns_times<BF16, DC>(lo, t * 32, p, dv);
-          columns_times<BF16, DC>(lq, t * 32, ds, dk);
-        }
-      };
-      const bool diag = t0 < w0 + 31;
-      if (kWide<BF16, DC>) step(diag);
-      else if (diag) step(std::true_type{});
-      else step(std::false_type{});
+      for (int i = 0; i < 4; i += 2) {
+        const f32x4_t x = *(const f32x4_t*)(words + 2 * (8 * r4 + 4 * g + i));   // lse, delta of two queries
+        const int r = 4 * r4 + i;
+        p[r] = __builtin_amdgcn_exp2f(fmaf(p[r], c, -x[0]));
+        ds[r] = p[r] * (ds[r] - x[1]);
+        p[r + 1] = __builtin_amdgcn_exp2f(fmaf(p[r + 1], c, -x[2]));
+        ds[r + 1] = p[r + 1] * (ds[r + 1] - x[3]);
+      }
     }
-    if (P::kBuffers == 1 && more) {
-      __syncthreads();
-      fetch(nh, nq, base);
+    if (q0 == w0) {
+      keep_branch();
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        if (q0 + result_row(r, g) < key) p[r] = 0.f, ds[r] = 0.f;
     }
-    staged();
-    if (!more) break;
+    columns_times<BF16, DC>(lo, 0, p, dv);
+    columns_times<BF16, DC>(lq, 0, ds, dk);
     h = nh;
     q0 = nq;
-    if (P::kBuffers == 2) buf ^= 1;
+    if (P::kBuffers == 2) {
+      buf ^= 1;
+    } else if (i + 1 < steps) {
+      own_staged();   // (the reads of this step are done)
+      fetch(nh, nq, base);
+    }
   }
   if constexpr (NS > 1) {
-    join<GR, NS, G::kTiles>(dk, grp, split, lds);
-    join<GR, NS, G::kTiles>(dv, grp, split, lds);
+    join<NS, G::kTiles>(dk, split, lds);
+    join<NS, G::kTiles>(dv, split, lds);
     if (split > 0) return;
   }
   if (key >= len) return;
