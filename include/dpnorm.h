@@ -332,21 +332,27 @@ dpnorm_status dpnorm_embed_order(const void* tok, dpnorm_index it, int64_t B, in
  *   n[i] (+)= scale^2 sum_v || sum_{t: tok[i][t] = v} G[i][t] ||^2,
  * with G [B][T][d] the gradient of the lookup's output. Row sums are held in
  * fp32 and each sample's sum over rows in fp64. Positions without a row add
- * nothing (their G is not read). */
-dpnorm_status dpnorm_embed_norm_workspace(dpnorm_dtype dt, int64_t B, int64_t T, int64_t V, int64_t d, size_t* bytes);
-dpnorm_status dpnorm_embed_norm(const void* order, const void* G, dpnorm_dtype dt, int64_t B, int64_t T, int64_t V,
-                                int64_t d, float scale, float* n, int accumulate, void* ws, size_t ws_bytes,
-                                hipStream_t stream);
+ * nothing (their G is not read). The ids are given as tok [B][T], or by their
+ * order (then tok is not read and may be NULL). If order is NULL the call
+ * orders the ids itself where it needs to, in ws; `ordered` of the workspace
+ * query is 1 when an order will be given, else 0. */
+dpnorm_status dpnorm_embed_norm_workspace(dpnorm_dtype dt, int64_t B, int64_t T, int64_t V, int64_t d, int ordered,
+                                          size_t* bytes);
+dpnorm_status dpnorm_embed_norm(const void* tok, dpnorm_index it, const void* order, const void* G, dpnorm_dtype dt,
+                                int64_t B, int64_t T, int64_t V, int64_t d, float scale, float* n, int accumulate,
+                                void* ws, size_t ws_bytes, hipStream_t stream);
 
 /* Gradient of the table, weighted per sample (c float [B], or NULL for 1):
  *   dW[v] = scale sum_i c[i] sum_{t: tok[i][t] = v} G[i][t],
  * summed in fp32 and rounded once to dt. accumulate = 0 writes all of dW
  * [V][d], zeros where an id does not occur; accumulate = 1 adds to the rows of
- * the ids that occur and leaves the others as they are. */
-dpnorm_status dpnorm_embed_grad_workspace(dpnorm_dtype dt, int64_t B, int64_t T, int64_t V, int64_t d, size_t* bytes);
-dpnorm_status dpnorm_embed_grad(const void* order, const void* G, dpnorm_dtype dt, int64_t B, int64_t T, int64_t V,
-                                int64_t d, float scale, const float* c, void* dW, int accumulate, void* ws,
-                                size_t ws_bytes, hipStream_t stream);
+ * the ids that occur and leaves the others as they are. tok, order and
+ * `ordered` as for dpnorm_embed_norm. */
+dpnorm_status dpnorm_embed_grad_workspace(dpnorm_dtype dt, int64_t B, int64_t T, int64_t V, int64_t d, int ordered,
+                                          size_t* bytes);
+dpnorm_status dpnorm_embed_grad(const void* tok, dpnorm_index it, const void* order, const void* G, dpnorm_dtype dt,
+                                int64_t B, int64_t T, int64_t V, int64_t d, float scale, const float* c, void* dW,
+                                int accumulate, void* ws, size_t ws_bytes, hipStream_t stream);
 
 /* Causal attention of S sequences packed one after another in N token rows,
  * with Hq query heads over Hkv key heads (Hq a multiple of Hkv; query head h
@@ -358,13 +364,15 @@ dpnorm_status dpnorm_embed_grad(const void* order, const void* G, dpnorm_dtype d
  * multiple of S and every sequence has N / S rows. Its entries are not checked
  * on the host; offsets outside [0, N] or out of order are clamped, so that no
  * memory outside the tensors is touched, and give undefined values. Rows that
- * belong to no sequence are neither read nor written.
+ * belong to no sequence (before the first and behind the last) are not read;
+ * they are left as they are in the outputs, or set to zero with clear_rest = 1.
  * D: a multiple of 8 (bf16) or 4 (fp32), at most 128. scale finite and > 0. */
 typedef struct dpnorm_attn_shape {
   dpnorm_dtype dtype;
   int64_t N, S, Hq, Hkv, D;
   const int32_t* cu_seqlens;
   float scale;
+  int32_t clear_rest;
 } dpnorm_attn_shape;
 
 /* A [N][H][D] tensor: row t of head h starts at data + t stride_token +

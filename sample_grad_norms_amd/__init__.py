@@ -457,16 +457,36 @@ def hutchpp_split(k: int) -> Tuple[int, int]:
 # run on the current stream of the tensors' device; temporaries come from
 # torch's allocator on that stream.
 # ---------------------------------------------------------------------------
+def _run(device: torch.device, name: str, *args) -> None:
+    """One library call on `device` and its current stream."""
+    if torch.cuda.current_device() == device.index:
+        status = getattr(lib(), name)(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            status = getattr(lib(), name)(*args, torch.cuda.current_stream(device).cuda_stream)
+    if status != _lib.OK:
+        raise DpnormError(status, name)
+
+
+def _one_device(device: torch.device, *tensors) -> None:
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError("all tensors of a call must be on one device")
+
+
+_INDEX = {torch.int64: _lib.I64, torch.int32: _lib.I32}
+
+
 def _index(t: torch.Tensor, name: str) -> int:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if t.dtype not in (torch.int32, torch.int64):
+    if t.dtype not in _INDEX:
         raise TypeError(f"{name} must be int32 or int64, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor (libdpnorm runs on the GPU only)")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return _lib.I64 if t.dtype == torch.int64 else _lib.I32
+    return _INDEX[t.dtype]
 
 
 def embed_lookup(tokens: torch.Tensor, W: torch.Tensor, scale: float = 1.0,
@@ -480,19 +500,17 @@ def embed_lookup(tokens: torch.Tensor, W: torch.Tensor, scale: float = 1.0,
     _need(W, "W", 2)
     code = _code(W.dtype)
     V, d = W.shape
-    shape = tuple(tokens.shape) + (d,)
+    shape = (*tokens.shape, d)
     if out is None:
         out = torch.empty(shape, dtype=W.dtype, device=W.device)
     else:
         _need(out, "out", len(shape), W.dtype)
-        if tuple(out.shape) != shape:
+        if out.shape != shape:
             raise ValueError(f"out must be {list(shape)}")
-    if tokens.device != W.device or out.device != W.device:
-        raise ValueError("all tensors of a call must be on one device")
-    if out.numel() > 0:
-        with torch.cuda.device(W.device):
-            _check(lib().dpnorm_embed_lookup(tokens.data_ptr(), it, W.data_ptr(), code, tokens.numel(), V, d, float(scale),
-                                             out.data_ptr(), _stream(W.device)), "dpnorm_embed_lookup")
+    _one_device(W.device, tokens, out)
+    n = tokens.numel()
+    if n * d > 0:
+        _run(W.device, "dpnorm_embed_lookup", tokens.data_ptr(), it, W.data_ptr(), code, n, V, d, scale, out.data_ptr())
     return out
 
 
@@ -512,37 +530,37 @@ def embed_order(tokens: torch.Tensor, V: int) -> EmbedOrder:
     if tokens.dim() != 2:
         raise ValueError(f"tokens must have 2 dimensions, got shape {tuple(tokens.shape)}")
     B, T = tokens.shape
-    if tokens.numel() == 0:
+    if B * T == 0:
         if not 1 <= V <= 1 << 30:
             raise ValueError("V must be in 1 .. 2^30")
         return EmbedOrder(B, T, V, torch.empty(0, dtype=torch.uint8, device=tokens.device))
-    L = lib()
     ob, wb = C.c_size_t(0), C.c_size_t(0)
-    _check(L.dpnorm_embed_order_sizes(B, T, V, C.byref(ob), C.byref(wb)), "dpnorm_embed_order_sizes")
+    _check(lib().dpnorm_embed_order_sizes(B, T, V, C.byref(ob), C.byref(wb)), "dpnorm_embed_order_sizes")
     data = torch.empty(ob.value, dtype=torch.uint8, device=tokens.device)
     ws, wsp = _workspace(wb.value, tokens.device)
-    with torch.cuda.device(tokens.device):
-        _check(L.dpnorm_embed_order(tokens.data_ptr(), it, B, T, V, data.data_ptr(), ob.value, wsp, wb.value,
-                                    _stream(tokens.device)), "dpnorm_embed_order")
+    _run(tokens.device, "dpnorm_embed_order", tokens.data_ptr(), it, B, T, V, data.data_ptr(), ob.value, wsp, wb.value)
     return EmbedOrder(B, T, V, data)
 
 
-def _embed_args(tokens, G: torch.Tensor, V: Optional[int]) -> EmbedOrder:
+def _embed_ids(tokens, G: torch.Tensor, V: Optional[int]):
+    """(tok pointer, index type, order pointer, ordered, V) of a norm or gradient call."""
     _need(G, "G", 3)
-    _code(G.dtype)
     if isinstance(tokens, EmbedOrder):
-        order = tokens
-        if V is not None and V != order.V:
-            raise ValueError(f"the order is of a table of {order.V} rows, not {V}")
+        if V is not None and V != tokens.V:
+            raise ValueError(f"the order is of a table of {tokens.V} rows, not {V}")
+        shape, V, res = (tokens.B, tokens.T), tokens.V, (None, 0, tokens.data.data_ptr(), 1, tokens.V)
+        _one_device(G.device, tokens.data)
     else:
+        it = _index(tokens, "tokens")
+        if tokens.dim() != 2:
+            raise ValueError(f"tokens must have 2 dimensions, got shape {tuple(tokens.shape)}")
         if V is None:
             raise ValueError("V (the rows of the table) is needed with token ids")
-        order = embed_order(tokens, V)
-    if tuple(G.shape[:2]) != (order.B, order.T):
-        raise ValueError(f"G must be [B={order.B}][T={order.T}][*]")
-    if order.data.device != G.device:
-        raise ValueError("all tensors of a call must be on one device")
-    return order
+        shape, res = tokens.shape, (tokens.data_ptr(), it, None, 0, V)
+        _one_device(G.device, tokens)
+    if tuple(G.shape[:2]) != tuple(shape):
+        raise ValueError(f"G must be [B={shape[0]}][T={shape[1]}][*]")
+    return res
 
 
 def embed_norm(tokens, G: torch.Tensor, V: Optional[int] = None, scale: float = 1.0, out: Optional[torch.Tensor] = None,
@@ -554,21 +572,17 @@ def embed_norm(tokens, G: torch.Tensor, V: Optional[int] = None, scale: float = 
     EmbedOrder. G [B][T][d]: the gradient of the lookup's output. Returns
     float32 [B]; with accumulate=True the norms are added to ``out``.
     """
-    order = _embed_args(tokens, G, V)
-    B, T, d = G.shape
-    n = _out(out, B, G.device, accumulate)
-    if n.device != G.device:
-        raise ValueError("all tensors of a call must be on one device")
-    if G.numel() == 0:
+    tok, it, order, ordered, V = _embed_ids(tokens, G, V)
+    code, (B, T, d), device = _code(G.dtype), G.shape, G.device
+    n = _out(out, B, device, accumulate)
+    _one_device(device, n)
+    if B * T * d == 0:
         return n if accumulate else n.zero_()
-    L = lib()
     nbytes = C.c_size_t(0)
-    _check(L.dpnorm_embed_norm_workspace(_code(G.dtype), B, T, order.V, d, C.byref(nbytes)), "dpnorm_embed_norm_workspace")
-    ws, wsp = _given_workspace(workspace, nbytes.value, G.device)
-    with torch.cuda.device(G.device):
-        _check(L.dpnorm_embed_norm(order.data.data_ptr(), G.data_ptr(), _code(G.dtype), B, T, order.V, d, float(scale),
-                                   n.data_ptr(), int(accumulate), wsp, nbytes.value, _stream(G.device)),
-               "dpnorm_embed_norm")
+    _check(lib().dpnorm_embed_norm_workspace(code, B, T, V, d, ordered, C.byref(nbytes)), "dpnorm_embed_norm_workspace")
+    ws, wsp = _given_workspace(workspace, nbytes.value, device)
+    _run(device, "dpnorm_embed_norm", tok, it, order, G.data_ptr(), code, B, T, V, d, scale, n.data_ptr(), int(accumulate),
+         wsp, nbytes.value)
     return n
 
 
@@ -582,62 +596,67 @@ def embed_grad(tokens, G: torch.Tensor, V: Optional[int] = None, scale: float = 
     None for 1. With accumulate=True the rows of the ids that occur are added
     to ``out`` and its other rows are left as they are.
     """
-    order = _embed_args(tokens, G, V)
-    B, T, d = G.shape
+    tok, it, order, ordered, V = _embed_ids(tokens, G, V)
+    code, (B, T, d), device = _code(G.dtype), G.shape, G.device
     if weights is not None:
         _need(weights, "weights", 1, torch.float32)
-        if weights.shape[0] != B or weights.device != G.device:
-            raise ValueError(f"weights must have {B} entries on G's device")
+        if weights.shape[0] != B:
+            raise ValueError(f"weights must have {B} entries")
     if out is None:
         if accumulate:
             raise ValueError("accumulate=True needs an existing output tensor")
-        out = torch.empty(order.V, d, dtype=G.dtype, device=G.device)
+        out = torch.empty(V, d, dtype=G.dtype, device=device)
     else:
         _need(out, "out", 2, G.dtype)
-        if tuple(out.shape) != (order.V, d) or out.device != G.device:
-            raise ValueError(f"out must be [V={order.V}][d={d}] on G's device")
-    if G.numel() == 0:
+        if tuple(out.shape) != (V, d):
+            raise ValueError(f"out must be [V={V}][d={d}]")
+    _one_device(device, weights, out)
+    if B * T * d == 0:
         return out if accumulate else out.zero_()
-    L = lib()
     nbytes = C.c_size_t(0)
-    _check(L.dpnorm_embed_grad_workspace(_code(G.dtype), B, T, order.V, d, C.byref(nbytes)), "dpnorm_embed_grad_workspace")
-    ws, wsp = _given_workspace(workspace, nbytes.value, G.device)
-    with torch.cuda.device(G.device):
-        _check(L.dpnorm_embed_grad(order.data.data_ptr(), G.data_ptr(), _code(G.dtype), B, T, order.V, d, float(scale),
-                                   weights.data_ptr() if weights is not None else None, out.data_ptr(), int(accumulate), wsp,
-                                   nbytes.value, _stream(G.device)), "dpnorm_embed_grad")
+    _check(lib().dpnorm_embed_grad_workspace(code, B, T, V, d, ordered, C.byref(nbytes)), "dpnorm_embed_grad_workspace")
+    ws, wsp = _given_workspace(workspace, nbytes.value, device)
+    _run(device, "dpnorm_embed_grad", tok, it, order, G.data_ptr(), code, B, T, V, d, scale,
+         weights.data_ptr() if weights is not None else None, out.data_ptr(), int(accumulate), wsp, nbytes.value)
     return out
 
 
-def _heads(t: torch.Tensor, name: str, like: Optional[torch.Tensor] = None) -> _lib.AttnTensor:
+def _heads(t: torch.Tensor, name: str, dtype: torch.dtype, device: torch.device, shape) -> _lib.AttnTensor:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [N][heads][D], got shape {tuple(t.shape)}")
-    if like is not None and t.dtype != like.dtype:
-        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor (libdpnorm runs on the GPU only)")
-    if like is not None and t.device != like.device:
+    if t.device != device:
         raise ValueError("all tensors of a call must be on one device")
-    if t.shape[2] > 1 and t.stride(2) != 1:
+    if t.shape != shape:
+        raise ValueError(f"{name} must be [N][heads][D] = {list(shape)}, got {list(t.shape)}")
+    st, sh, sd = t.stride()
+    if sd != 1 and shape[2] > 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
-    return _lib.AttnTensor(t.data_ptr(), t.stride(0), t.stride(1))
+    return _lib.AttnTensor(t.data_ptr(), st, sh)
 
 
-def _attn_shape(q, k, v, cu_seqlens, sequences, scale):
-    tq, tk, tv = _heads(q, "q"), _heads(k, "k", like=q), _heads(v, "v", like=q)
-    code = _code(q.dtype)
+def _attn_shape(q, k, v, cu_seqlens, sequences, scale, clear):
+    """The shape record, and q's, k's and v's."""
+    for t, name in ((q, "q"), (k, "k")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch tensor")
+        if t.dim() != 3:
+            raise ValueError(f"{name} must be [N][heads][D], got shape {tuple(t.shape)}")
+    code, dtype, device = _code(q.dtype), q.dtype, q.device
     N, Hq, D = q.shape
-    if k.shape != v.shape or k.shape[0] != N or k.shape[2] != D:
-        raise ValueError("shapes must be q [N][Hq][D], k and v [N][Hkv][D]")
-    if k.shape[1] == 0 or Hq % k.shape[1] != 0:
-        raise ValueError(f"{Hq} query heads are not a multiple of {k.shape[1]} key heads")
+    Hkv = k.shape[1]
+    if Hkv == 0 or Hq % Hkv != 0:
+        raise ValueError(f"{Hq} query heads are not a multiple of {Hkv} key heads")
+    kv = torch.Size((N, Hkv, D))
+    tq, tk, tv = _heads(q, "q", dtype, device, q.shape), _heads(k, "k", dtype, device, kv), _heads(v, "v", dtype, device, kv)
     if cu_seqlens is not None:
         if sequences is not None:
             raise ValueError("give cu_seqlens or sequences, not both")
         _need(cu_seqlens, "cu_seqlens", 1, torch.int32)
-        if cu_seqlens.device != q.device or cu_seqlens.shape[0] < 1:
+        if cu_seqlens.device != device or cu_seqlens.shape[0] < 1:
             raise ValueError("cu_seqlens must be the S + 1 row offsets on the tensors' device")
         S, cup = cu_seqlens.shape[0] - 1, cu_seqlens.data_ptr()
     else:
@@ -645,8 +664,8 @@ def _attn_shape(q, k, v, cu_seqlens, sequences, scale):
         if S < 1 or N % S != 0:
             raise ValueError(f"{N} rows are not a multiple of {S} sequences")
     if scale is None:
-        scale = 1.0 / (D ** 0.5) if D else 1.0
-    return _lib.AttnShape(code, N, S, Hq, k.shape[1], D, cup, float(scale)), tq, tk, tv
+        scale = D ** -0.5 if D else 1.0
+    return _lib.AttnShape(code, N, S, Hq, Hkv, D, cup, scale, int(clear)), tq, tk, tv
 
 
 def attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None,
@@ -659,26 +678,26 @@ def attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seql
     the GPU; without it the N rows are ``sequences`` (default 1) sequences of
     equal length. scale defaults to 1 / sqrt(D). Returns (o [N][Hq][D],
     lse float32 [Hq][N]). Rows that belong to no sequence are left as they
-    are in ``out`` and ``lse``, and are zero where these are made here.
+    are in a given ``out`` and ``lse`` (give both or neither), and are zero
+    where the call makes them.
     """
-    shape, tq, tk, tv = _attn_shape(q, k, v, cu_seqlens, sequences, scale)
+    if (out is None) != (lse is None):
+        raise ValueError("give out and lse both, or neither")
+    shape, tq, tk, tv = _attn_shape(q, k, v, cu_seqlens, sequences, scale, out is None)
     N, Hq, D = q.shape
-    make = torch.empty if cu_seqlens is None else torch.zeros
+    device = q.device
     if out is None:
-        out = make(N, Hq, D, dtype=q.dtype, device=q.device)
-    elif tuple(out.shape) != (N, Hq, D):
-        raise ValueError(f"out must be [N={N}][Hq={Hq}][D={D}]")
-    to = _heads(out, "out", like=q)
-    if lse is None:
-        lse = make(Hq, N, dtype=torch.float32, device=q.device)
+        out = torch.empty((N, Hq, D), dtype=q.dtype, device=device)
+        lse = torch.empty((Hq, N), dtype=torch.float32, device=device)
     else:
         _need(lse, "lse", 2, torch.float32)
-        if tuple(lse.shape) != (Hq, N) or lse.device != q.device:
+        if tuple(lse.shape) != (Hq, N) or lse.device != device:
             raise ValueError(f"lse must be [Hq={Hq}][N={N}] on q's device")
+    to = _heads(out, "out", q.dtype, device, q.shape)
     if N > 0 and shape.S > 0:
-        with torch.cuda.device(q.device):
-            _check(lib().dpnorm_attention_forward(C.byref(shape), C.byref(tq), C.byref(tk), C.byref(tv), C.byref(to),
-                                                  lse.data_ptr(), _stream(q.device)), "dpnorm_attention_forward")
+        _run(device, "dpnorm_attention_forward", shape, tq, tk, tv, to, lse.data_ptr())
+    elif shape.clear_rest:
+        out.zero_(), lse.zero_()
     return out, lse
 
 
@@ -690,32 +709,27 @@ def attention_backward(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: to
     (dpnorm_attention_backward). q, k, v, cu_seqlens, sequences and scale are
     the forward call's, o and lse its results. ``out``: three tensors to write
     to. Rows that belong to no sequence are left as they are in ``out``, and
-    are zero where it is made here.
+    are zero where the call makes it.
     """
-    shape, tq, tk, tv = _attn_shape(q, k, v, cu_seqlens, sequences, scale)
+    shape, tq, tk, tv = _attn_shape(q, k, v, cu_seqlens, sequences, scale, out is None)
     N, Hq, D = q.shape
-    if tuple(do.shape) != (N, Hq, D) or tuple(o.shape) != (N, Hq, D):
-        raise ValueError(f"do and o must be [N={N}][Hq={Hq}][D={D}]")
-    tdo, to = _heads(do, "do", like=q), _heads(o, "o", like=q)
+    dtype, device = q.dtype, q.device
+    tdo, to = _heads(do, "do", dtype, device, q.shape), _heads(o, "o", dtype, device, q.shape)
     _need(lse, "lse", 2, torch.float32)
-    if tuple(lse.shape) != (Hq, N) or lse.device != q.device:
+    if tuple(lse.shape) != (Hq, N) or lse.device != device:
         raise ValueError(f"lse must be [Hq={Hq}][N={N}] on q's device")
     if out is None:
-        make = torch.empty if cu_seqlens is None else torch.zeros
-        out = tuple(make(t.shape, dtype=q.dtype, device=q.device) for t in (q, k, v))
-    dq, dk, dv = out
-    if dq.shape != q.shape or dk.shape != k.shape or dv.shape != v.shape:
-        raise ValueError("out must be three tensors of q's, k's and v's shapes")
-    tdq, tdk, tdv = _heads(dq, "dq", like=q), _heads(dk, "dk", like=q), _heads(dv, "dv", like=q)
+        dq, dk, dv = (torch.empty(t.shape, dtype=dtype, device=device) for t in (q, k, v))
+    else:
+        dq, dk, dv = out
+    tdq, tdk, tdv = (_heads(t, n, dtype, device, x.shape) for t, n, x in ((dq, "dq", q), (dk, "dk", k), (dv, "dv", k)))
     if N > 0 and shape.S > 0:
-        L = lib()
         nbytes = C.c_size_t(0)
-        _check(L.dpnorm_attention_backward_workspace(C.byref(shape), C.byref(nbytes)), "dpnorm_attention_backward_workspace")
-        ws, wsp = _given_workspace(workspace, nbytes.value, q.device)
-        with torch.cuda.device(q.device):
-            _check(L.dpnorm_attention_backward(C.byref(shape), C.byref(tdo), C.byref(tq), C.byref(tk), C.byref(tv), C.byref(to),
-                                               lse.data_ptr(), C.byref(tdq), C.byref(tdk), C.byref(tdv), wsp, nbytes.value,
-                                               _stream(q.device)), "dpnorm_attention_backward")
+        _check(lib().dpnorm_attention_backward_workspace(shape, C.byref(nbytes)), "dpnorm_attention_backward_workspace")
+        ws, wsp = _given_workspace(workspace, nbytes.value, device)
+        _run(device, "dpnorm_attention_backward", shape, tdo, tq, tk, tv, to, lse.data_ptr(), tdq, tdk, tdv, wsp, nbytes.value)
+    elif shape.clear_rest:
+        dq.zero_(), dk.zero_(), dv.zero_()
     return dq, dk, dv
 
 

@@ -42,7 +42,7 @@ class Trace(C.Structure):
 class AttnShape(C.Structure):
     """struct dpnorm_attn_shape."""
     _fields_ = [("dtype", C.c_int), ("N", C.c_int64), ("S", C.c_int64), ("Hq", C.c_int64), ("Hkv", C.c_int64),
-                ("D", C.c_int64), ("cu_seqlens", C.c_void_p), ("scale", C.c_float)]
+                ("D", C.c_int64), ("cu_seqlens", C.c_void_p), ("scale", C.c_float), ("clear_rest", C.c_int32)]
 
 
 class AttnTensor(C.Structure):
@@ -85,10 +85,12 @@ SIGNATURES = {
     "dpnorm_embed_lookup": ([_vp, C.c_int, _vp, C.c_int, _i64, _i64, _i64, _f32, _vp, _vp], C.c_int),
     "dpnorm_embed_order_sizes": ([_i64, _i64, _i64, _szp, _szp], C.c_int),
     "dpnorm_embed_order": ([_vp, C.c_int, _i64, _i64, _i64, _vp, _sz, _vp, _sz, _vp], C.c_int),
-    "dpnorm_embed_norm_workspace": ([C.c_int, _i64, _i64, _i64, _i64, _szp], C.c_int),
-    "dpnorm_embed_norm": ([_vp, _vp, C.c_int, _i64, _i64, _i64, _i64, _f32, _vp, C.c_int, _vp, _sz, _vp], C.c_int),
-    "dpnorm_embed_grad_workspace": ([C.c_int, _i64, _i64, _i64, _i64, _szp], C.c_int),
-    "dpnorm_embed_grad": ([_vp, _vp, C.c_int, _i64, _i64, _i64, _i64, _f32, _vp, _vp, C.c_int, _vp, _sz, _vp], C.c_int),
+    "dpnorm_embed_norm_workspace": ([C.c_int, _i64, _i64, _i64, _i64, C.c_int, _szp], C.c_int),
+    "dpnorm_embed_norm": ([_vp, C.c_int, _vp, _vp, C.c_int, _i64, _i64, _i64, _i64, _f32, _vp, C.c_int, _vp, _sz, _vp],
+                          C.c_int),
+    "dpnorm_embed_grad_workspace": ([C.c_int, _i64, _i64, _i64, _i64, C.c_int, _szp], C.c_int),
+    "dpnorm_embed_grad": ([_vp, C.c_int, _vp, _vp, C.c_int, _i64, _i64, _i64, _i64, _f32, _vp, _vp, C.c_int, _vp, _sz, _vp],
+                          C.c_int),
     "dpnorm_attention_forward": ([_shp, _tp, _tp, _tp, _tp, _vp, _vp], C.c_int),
     "dpnorm_attention_backward_workspace": ([_shp, _szp], C.c_int),
     "dpnorm_attention_backward": ([_shp, _tp, _tp, _tp, _tp, _tp, _vp, _tp, _tp, _tp, _vp, _sz, _vp], C.c_int),

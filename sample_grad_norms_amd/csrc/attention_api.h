@@ -32,6 +32,7 @@ dpnorm_status check_shape(const dpnorm_attn_shape* s) {
   if (s->D < 1 || s->D > 128 || s->D % g != 0) return DPNORM_ERR_SIZE;
   if (!s->cu_seqlens && s->N % s->S != 0) return DPNORM_ERR_SIZE;
   if (!aligned(s->cu_seqlens, 4)) return DPNORM_ERR_ALIGN;
+  if (s->clear_rest != 0 && s->clear_rest != 1) return DPNORM_ERR_VALUE;
   if (!(s->scale > 0.f) || !std::isfinite(s->scale)) return DPNORM_ERR_VALUE;
   return DPNORM_OK;
 }
@@ -63,6 +64,7 @@ attn::Args attn_args(const dpnorm_attn_shape* s) {
   a.Hkv = (int32_t)s->Hkv;
   a.D = (int32_t)s->D;
   a.scale = s->scale;
+  a.clear = s->cu_seqlens && s->clear_rest;
   return a;
 }
 
@@ -107,7 +109,8 @@ constexpr int64_t kKeysMost = 600;
 // One launch, or more where a grid's z dimension does not hold the slots.
 template <typename F>
 hipError_t launch_slots(attn::Args a, int rows, int rep, F launch) {
-  const int64_t slots = slots_of(a, rows);
+  const int64_t slots = slots_of(a, rows) + (a.clear ? 1 : 0);   // one without a tile at least
+  a.slots = (int32_t)slots;
   for (int64_t s = 0; s < slots; s += 65535) {
     a.slot0 = (int32_t)s;
     launch(a, dim3((uint32_t)a.Hkv, (uint32_t)rep, (uint32_t)std::min<int64_t>(65535, slots - s)));

@@ -50,15 +50,18 @@ struct Args {
   int32_t S, T, N;
   int32_t Hq, Hkv, D;
   float scale;        // a
+  int32_t slots;      // tile slots per head
   int32_t slot0;      // first slot of the launch
+  int32_t clear;      // set rows of no sequence to zero
 };
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint32_t kOutside = 0x80000000u;   // an offset past every buffer's range: reads as zero
 
 // The sequence and tile of a slot. Slots count the tiles of the sequences one
-// after another; a slot past the last tile has none. Offsets outside [0, N] or
-// out of order are clamped, so no row outside the tensors is ever touched.
+// after another; a slot past the last tile has none (tiles is then the number of
+// all). Offsets outside [0, N] or out of order are clamped, so no row outside the
+// tensors is ever touched.
 __device__ __forceinline__ bool find_tile(const Args& a, int32_t slot, int rows, int32_t& start, int32_t& len, int32_t& tile,
                                           int32_t& tiles) {
   if (!a.cu) {
@@ -96,7 +99,22 @@ __device__ __forceinline__ bool find_tile(const Args& a, int32_t slot, int rows,
     }
     before += total;
   }
+  tiles = before;
   return false;
+}
+
+// The slots without a tile share the rows of no sequence (before the first and
+// behind the last) and set them to zero: row(r) is called by the whole block.
+template <typename F>
+__device__ __forceinline__ void clear_rest(const Args& a, int32_t slot, int32_t tiles, F row) {
+  if (!a.clear || !a.cu) return;
+  const int32_t first = min(max(a.cu[0], 0), a.N), last = min(max(a.cu[a.S], first), a.N);
+  for (int64_t i = slot - tiles; i < (int64_t)first + a.N - last; i += a.slots - tiles)
+    row(i < first ? (int32_t)i : (int32_t)(i - first + last));
+}
+__device__ __forceinline__ void clear_row(const Tensor& t, int32_t row, int32_t h, int32_t bytes) {
+  char* p = t.p + row * t.st + h * t.sh;
+  for (int32_t b = threadIdx.x * 16; b < bytes; b += blockDim.x * 16) *(uint4*)(p + b) = make_uint4(0, 0, 0, 0);
 }
 
 // DC: columns computed, 64, 96 or 128 (D filled up with zeros).
@@ -404,7 +422,13 @@ __global__ __launch_bounds__(64 * NS, BF16 ? 2 : 1) void k_forward_rows(Args a) 
   using P = OwnRows<BF16, DC, NS, 0>;
   __shared__ __align__(1024) unsigned char lds[P::kLds];
   int32_t start, len, tile, tiles;
-  if (!find_tile(a, block_slot(a), 32, start, len, tile, tiles)) return;
+  if (!find_tile(a, block_slot(a), 32, start, len, tile, tiles)) {
+    clear_rest(a, block_slot(a), tiles, [&](int32_t r) {
+      clear_row(a.o, r, blockIdx.x * gridDim.y + blockIdx.y, a.D * G::kElem);
+      if (threadIdx.x == 0) a.lse[(int64_t)(blockIdx.x * gridDim.y + blockIdx.y) * a.N + r] = 0.f;
+    });
+    return;
+  }
   tile = tiles - 1 - tile;
   const int32_t kh = blockIdx.x, h = kh * gridDim.y + blockIdx.y;
   const int lane = threadIdx.x & 63, g = lane >> 5;
@@ -508,7 +532,13 @@ __global__ __launch_bounds__(256, BF16 ? 2 : 1) void k_forward(Args a) {
   // keys are needed a step ahead of their values, whose scores they give
   __shared__ __align__(1024) unsigned char lds[4 * P::kStage];
   int32_t start, len, tile, tiles;
-  if (!find_tile(a, block_slot(a), P::kRows, start, len, tile, tiles)) return;
+  if (!find_tile(a, block_slot(a), P::kRows, start, len, tile, tiles)) {
+    clear_rest(a, block_slot(a), tiles, [&](int32_t r) {
+      clear_row(a.o, r, blockIdx.x * gridDim.y + blockIdx.y, a.D * G::kElem);
+      if (threadIdx.x == 0) a.lse[(int64_t)(blockIdx.x * gridDim.y + blockIdx.y) * a.N + r] = 0.f;
+    });
+    return;
+  }
   tile = tiles - 1 - tile;   // the longest rows first
   const int32_t kh = blockIdx.x, h = kh * gridDim.y + blockIdx.y;
   const int lane = threadIdx.x & 63, g = lane >> 5;
@@ -616,7 +646,12 @@ __global__ __launch_bounds__(256, BF16 ? 2 : 1) void k_backward_q(Args a) {
   using P = Tiles<BF16, DC>;
   __shared__ __align__(1024) unsigned char lds[P::kBuffers * 2 * P::kStage];
   int32_t start, len, tile, tiles;
-  if (!find_tile(a, block_slot(a), P::kRows, start, len, tile, tiles)) return;
+  if (!find_tile(a, block_slot(a), P::kRows, start, len, tile, tiles)) {
+    clear_rest(a, block_slot(a), tiles, [&](int32_t r) {
+      clear_row(a.dq, r, blockIdx.x * gridDim.y + blockIdx.y, a.D * G::kElem);
+    });
+    return;
+  }
   tile = tiles - 1 - tile;
   const int32_t kh = blockIdx.x, h = kh * gridDim.y + blockIdx.y;
   const int lane = threadIdx.x & 63, g = lane >> 5;
@@ -699,7 +734,12 @@ __global__ __launch_bounds__(64 * NS, BF16 ? 2 : 1) void k_backward_q_rows(Args 
   using P = OwnRows<BF16, DC, NS, 0>;
   __shared__ __align__(1024) unsigned char lds[P::kLds];
   int32_t start, len, tile, tiles;
-  if (!find_tile(a, block_slot(a), 32, start, len, tile, tiles)) return;
+  if (!find_tile(a, block_slot(a), 32, start, len, tile, tiles)) {
+    clear_rest(a, block_slot(a), tiles, [&](int32_t r) {
+      clear_row(a.dq, r, blockIdx.x * gridDim.y + blockIdx.y, a.D * G::kElem);
+    });
+    return;
+  }
   tile = tiles - 1 - tile;
   const int32_t kh = blockIdx.x, h = kh * gridDim.y + blockIdx.y;
   const int lane = threadIdx.x & 63, g = lane >> 5;
@@ -775,7 +815,13 @@ __global__ __launch_bounds__(64 * NS, BF16 ? 2 : 1) void k_backward_kv(Args a) {
   __shared__ __align__(1024) unsigned char lds[P::kLds];
   int32_t start, len, tile, tiles;
   const int32_t kh = blockIdx.x, rep = a.Hq / a.Hkv;
-  if (!find_tile(a, block_slot(a), 32, start, len, tile, tiles)) return;
+  if (!find_tile(a, block_slot(a), 32, start, len, tile, tiles)) {
+    clear_rest(a, block_slot(a), tiles, [&](int32_t r) {
+      clear_row(a.dk, r, blockIdx.x, a.D * G::kElem);
+      clear_row(a.dv, r, blockIdx.x, a.D * G::kElem);
+    });
+    return;
+  }
   const int lane = threadIdx.x & 63, g = lane >> 5;
   const int split = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int32_t w0 = tile * 32, key = w0 + (lane & 31);

@@ -14,8 +14,9 @@ struct EmbedPlan {
   // order
   int passes = 0, bits = 0, blocks = 0, per = 0;
   size_t off_pos = 0, order_bytes = 0, off_key2 = 0, off_pos2 = 0, off_hist = 0, order_ws = 0;
-  // run sums
-  size_t off_val = 0, off_part = 0, norm_ws = 0, off_part_grad = 0, grad_ws = 0;
+  // run sums: the order and its scratch where the call makes it, then the calls' own
+  bool small_norm = false, small_grad = false;
+  size_t off_order = 0, off_order_ws = 0, off_val = 0, off_part = 0, norm_ws = 0, off_part_grad = 0, grad_ws = 0;
 };
 
 dpnorm_status check_ids(int64_t B, int64_t T, int64_t V) {
@@ -55,19 +56,38 @@ void plan_order(EmbedPlan& pl, int64_t B, int64_t T, int64_t V) {
   pl.order_ws = align_up(w.off);
 }
 
-void plan_runs(EmbedPlan& pl, dpnorm_dtype dt, int64_t d) {
+// One launch without an order: up to 256 ids (of a sample for the norm, in all for
+// the gradient) and, for the norm, samples that one CU reads in a few us
+// (B = 3, T = 61, d = 256 fp32: 8 us against 31 with an order).
+constexpr int64_t kSmallBytes = 256 * 1024;
+
+void plan_runs(EmbedPlan& pl, dpnorm_dtype dt, int64_t d, bool ordered) {
   pl.d = (int32_t)d;
+  pl.small_norm = !ordered && pl.T <= embed::kSmallIds && pl.T * d * (int64_t)esize(dt) <= kSmallBytes;
+  pl.small_grad = !ordered && pl.N <= embed::kSmallIds;
   const int64_t width = dt == DPNORM_BF16 ? embed::Row<true>::kSlice : embed::Row<false>::kSlice;
   pl.slices = (int)((d + width - 1) / width);
   pl.R = 32;
   while (pl.R > 4 && (int64_t)pl.N * pl.slices / pl.R < 4096) pl.R >>= 1;
   pl.chunks = (pl.N + pl.R - 1) / pl.R;
   Bump n;
-  pl.off_val = n.take((size_t)pl.slices * (size_t)pl.N * 4);
-  pl.off_part = n.take((size_t)pl.chunks * 2 * (size_t)d * 4);
+  if (!pl.small_norm) {
+    if (!ordered) {
+      pl.off_order = n.take(pl.order_bytes);
+      pl.off_order_ws = n.take(pl.order_ws);
+    }
+    pl.off_val = n.take((size_t)pl.slices * (size_t)pl.N * 4);
+    pl.off_part = n.take((size_t)pl.chunks * 2 * (size_t)d * 4);
+  }
   pl.norm_ws = align_up(n.off);
   Bump g;
-  pl.off_part_grad = g.take((size_t)pl.chunks * 2 * (size_t)d * 4);
+  if (!pl.small_grad) {
+    if (!ordered) {   // (where the norm has them)
+      pl.off_order = g.take(pl.order_bytes);
+      pl.off_order_ws = g.take(pl.order_ws);
+    }
+    pl.off_part_grad = g.take((size_t)pl.chunks * 2 * (size_t)d * 4);
+  }
   pl.grad_ws = align_up(g.off);
 }
 
@@ -79,13 +99,40 @@ dpnorm_status check_grid(const EmbedPlan& pl) {
   return DPNORM_OK;
 }
 
+hipError_t launch_order(const EmbedPlan& pl, const void* tok, dpnorm_index it, void* order, void* ws, hipStream_t stream) {
+  const int i64 = it == DPNORM_I64;
+  int32_t* keys = (int32_t*)order;
+  int32_t* pos = (int32_t*)((char*)order + pl.off_pos);
+  if (pl.N <= embed::kSmallSort) {
+    embed::k_order_small<<<1, embed::kSortThreads, 0, stream>>>(tok, i64, pl.N, pl.V, pl.passes, pl.bits, keys, pos);
+    return hipGetLastError();
+  }
+  int32_t* key2 = (int32_t*)((char*)ws + pl.off_key2);
+  int32_t* pos2 = (int32_t*)((char*)ws + pl.off_pos2);
+  uint32_t* hist = (uint32_t*)((char*)ws + pl.off_hist);
+  const int32_t *sk = nullptr, *sp = nullptr;
+  for (int p = 0; p < pl.passes; ++p) {
+    // the last pass writes the order; the ones before it alternate
+    const bool to_order = (pl.passes - 1 - p) % 2 == 0;
+    int32_t *dk = to_order ? keys : key2, *dp = to_order ? pos : pos2;
+    embed::k_order_count<<<pl.blocks, embed::kSortThreads, 0, stream>>>(tok, i64, sk, pl.N, pl.V, p * pl.bits, pl.bits, pl.per,
+                                                                       hist);
+    embed::k_order_scatter<<<pl.blocks, embed::kSortThreads, 0, stream>>>(tok, i64, sk, sp, pl.N, pl.V, p * pl.bits, pl.bits,
+                                                                         pl.per, hist, dk, dp);
+    sk = dk;
+    sp = dp;
+  }
+  return hipGetLastError();
+}
+
 embed::RunArgs run_args(const EmbedPlan& pl, const void* order, const void* G) {
   embed::RunArgs a{};
   a.runs.keys = (const int32_t*)order;
-  a.runs.pos = (const int32_t*)((const char*)order + pl.off_pos);
+  a.runs.pos = order ? (const int32_t*)((const char*)order + pl.off_pos) : nullptr;   // (none: a small gradient)
   a.runs.N = pl.N;
   a.runs.T = pl.T;
   a.runs.V = pl.V;
+  a.runs.per = 1.0 / pl.T;
   a.runs.R = pl.R;
   a.runs.chunks = (int32_t)pl.chunks;
   a.G = (const char*)G;
@@ -164,113 +211,128 @@ dpnorm_status dpnorm_embed_order(const void* tok, dpnorm_index it, int64_t B, in
   if (overlaps(order, pl.order_bytes, tok, (size_t)pl.N * ib) || overlaps(ws, pl.order_ws, tok, (size_t)pl.N * ib) ||
       overlaps(order, pl.order_bytes, ws, pl.order_ws))
     return DPNORM_ERR_VALUE;
-  const int i64 = it == DPNORM_I64;
-  int32_t* keys = (int32_t*)order;
-  int32_t* pos = (int32_t*)((char*)order + pl.off_pos);
-  if (pl.N <= embed::kSmallSort) {
-    embed::k_order_small<<<1, embed::kSortThreads, 0, stream>>>(tok, i64, pl.N, pl.V, pl.passes, pl.bits, keys, pos);
-    return hip_status(hipGetLastError());
-  }
-  int32_t* key2 = (int32_t*)((char*)ws + pl.off_key2);
-  int32_t* pos2 = (int32_t*)((char*)ws + pl.off_pos2);
-  uint32_t* hist = (uint32_t*)((char*)ws + pl.off_hist);
-  const int32_t *sk = nullptr, *sp = nullptr;
-  for (int p = 0; p < pl.passes; ++p) {
-    // the last pass writes the order; the ones before it alternate
-    const bool to_order = (pl.passes - 1 - p) % 2 == 0;
-    int32_t *dk = to_order ? keys : key2, *dp = to_order ? pos : pos2;
-    embed::k_order_count<<<pl.blocks, embed::kSortThreads, 0, stream>>>(tok, i64, sk, pl.N, pl.V, p * pl.bits, pl.bits, pl.per,
-                                                                       hist);
-    embed::k_order_scatter<<<pl.blocks, embed::kSortThreads, 0, stream>>>(tok, i64, sk, sp, pl.N, pl.V, p * pl.bits, pl.bits,
-                                                                         pl.per, hist, dk, dp);
-    sk = dk;
-    sp = dp;
-  }
-  return hip_status(hipGetLastError());
+  return hip_status(launch_order(pl, tok, it, order, ws, stream));
 }
 
-dpnorm_status dpnorm_embed_norm_workspace(dpnorm_dtype dt, int64_t B, int64_t T, int64_t V, int64_t d, size_t* bytes) {
-  if (!bytes) return DPNORM_ERR_NULL;
+static dpnorm_status plan_embed(dpnorm_dtype dt, int64_t B, int64_t T, int64_t V, int64_t d, bool ordered, EmbedPlan& pl) {
   dpnorm_status st = check_ids(B, T, V);
   if (st == DPNORM_OK) st = check_rows(dt, std::max(B * T, V), d);
   if (st != DPNORM_OK) return st;
-  EmbedPlan pl;
   plan_order(pl, B, T, V);
-  plan_runs(pl, dt, d);
-  st = check_grid(pl);
-  if (st != DPNORM_OK) return st;
-  *bytes = pl.norm_ws;
+  plan_runs(pl, dt, d, ordered);
+  return check_grid(pl);
+}
+
+// The checks that both calls share, and that the ids come from one place.
+static dpnorm_status check_embed(const EmbedPlan& pl, const void* tok, dpnorm_index it, const void* order, const void* G,
+                                 const void* out, const void* ws, size_t need, size_t ws_bytes, float scale, int accumulate) {
+  if (!order && it != DPNORM_I32 && it != DPNORM_I64) return DPNORM_ERR_DTYPE;
+  if ((!order && !tok) || !G || !out || (!ws && need)) return DPNORM_ERR_NULL;
+  if (!aligned(order, kAlign) || (!order && !aligned(tok, it == DPNORM_I64 ? 8 : 4)) || !aligned(G, 16) || !aligned(ws, kAlign))
+    return DPNORM_ERR_ALIGN;
+  if (!std::isfinite(scale) || (accumulate != 0 && accumulate != 1)) return DPNORM_ERR_VALUE;
+  if (ws_bytes < need) return DPNORM_ERR_WORKSPACE;
   return DPNORM_OK;
 }
 
-dpnorm_status dpnorm_embed_norm(const void* order, const void* G, dpnorm_dtype dt, int64_t B, int64_t T, int64_t V, int64_t d,
-                                float scale, float* n, int accumulate, void* ws, size_t ws_bytes, hipStream_t stream) {
-  size_t bytes = 0;
-  const dpnorm_status st = dpnorm_embed_norm_workspace(dt, B, T, V, d, &bytes);
-  if (st != DPNORM_OK) return st;
-  if (!order || !G || !n || !ws) return DPNORM_ERR_NULL;
-  if (!aligned(order, kAlign) || !aligned(G, 16) || !aligned(n, 4) || !aligned(ws, kAlign)) return DPNORM_ERR_ALIGN;
-  if (!std::isfinite(scale) || (accumulate != 0 && accumulate != 1)) return DPNORM_ERR_VALUE;
-  if (ws_bytes < bytes) return DPNORM_ERR_WORKSPACE;
+dpnorm_status dpnorm_embed_norm_workspace(dpnorm_dtype dt, int64_t B, int64_t T, int64_t V, int64_t d, int ordered,
+                                          size_t* bytes) {
+  if (!bytes) return DPNORM_ERR_NULL;
+  if (ordered != 0 && ordered != 1) return DPNORM_ERR_VALUE;
   EmbedPlan pl;
-  plan_order(pl, B, T, V);
-  plan_runs(pl, dt, d);
+  const dpnorm_status st = plan_embed(dt, B, T, V, d, ordered != 0, pl);
+  if (st == DPNORM_OK) *bytes = pl.norm_ws;
+  return st;
+}
+
+dpnorm_status dpnorm_embed_norm(const void* tok, dpnorm_index it, const void* order, const void* G, dpnorm_dtype dt, int64_t B,
+                                int64_t T, int64_t V, int64_t d, float scale, float* n, int accumulate, void* ws,
+                                size_t ws_bytes, hipStream_t stream) {
+  EmbedPlan pl;
+  dpnorm_status st = plan_embed(dt, B, T, V, d, order != nullptr, pl);
+  if (st == DPNORM_OK) st = check_embed(pl, tok, it, order, G, n, ws, pl.norm_ws, ws_bytes, scale, accumulate);
+  if (st != DPNORM_OK) return st;
+  if (!aligned(n, 4)) return DPNORM_ERR_ALIGN;
   const size_t nb = (size_t)B * 4, gb = (size_t)pl.N * d * esize(dt);
-  if (overlaps(n, nb, order, pl.order_bytes) || overlaps(n, nb, G, gb) || overlaps(n, nb, ws, bytes) ||
-      overlaps(ws, bytes, order, pl.order_bytes) || overlaps(ws, bytes, G, gb))
+  const void* ids = order ? order : tok;
+  const size_t ib = order ? pl.order_bytes : (size_t)pl.N * (it == DPNORM_I64 ? 8 : 4);
+  if (overlaps(n, nb, ids, ib) || overlaps(n, nb, G, gb) || overlaps(n, nb, ws, pl.norm_ws) ||
+      overlaps(ws, pl.norm_ws, ids, ib) || overlaps(ws, pl.norm_ws, G, gb))
     return DPNORM_ERR_VALUE;
+  const bool bf16 = dt == DPNORM_BF16;
+  const double scale2 = (double)scale * (double)scale;
+  if (pl.small_norm) {
+    if (bf16)
+      embed::k_norm_small<true><<<(uint32_t)B, 1024, 0, stream>>>(tok, it == DPNORM_I64, (const char*)G, pl.T, pl.V, pl.d, scale2,
+                                                                  n, accumulate);
+    else
+      embed::k_norm_small<false><<<(uint32_t)B, 1024, 0, stream>>>(tok, it == DPNORM_I64, (const char*)G, pl.T, pl.V, pl.d, scale2,
+                                                                   n, accumulate);
+    return hip_status(hipGetLastError());
+  }
+  hipError_t he = hipSuccess;
+  char* base = (char*)ws;
+  if (!order) {
+    he = launch_order(pl, tok, it, base + pl.off_order, base + pl.off_order_ws, stream);
+    order = base + pl.off_order;
+  }
   embed::RunArgs a = run_args(pl, order, G);
-  a.val = (float*)((char*)ws + pl.off_val);
-  a.part = (float*)((char*)ws + pl.off_part);
-  hipError_t he = launch_runs<embed::RUN_NORM>(a, dt == DPNORM_BF16, stream);
+  a.val = (float*)(base + pl.off_val);
+  a.part = (float*)(base + pl.off_part);
+  if (he == hipSuccess) he = launch_runs<embed::RUN_NORM>(a, bf16, stream);
   if (he == hipSuccess) {
-    embed::k_norm_sum<<<(uint32_t)B, 1024, 0, stream>>>(a.val, pl.N, pl.T, pl.slices, (double)scale * (double)scale, n, accumulate);
+    embed::k_norm_sum<<<(uint32_t)B, 1024, 0, stream>>>(a.val, pl.N, pl.T, pl.slices, scale2, n, accumulate);
     he = hipGetLastError();
   }
   return hip_status(he);
 }
 
-dpnorm_status dpnorm_embed_grad_workspace(dpnorm_dtype dt, int64_t B, int64_t T, int64_t V, int64_t d, size_t* bytes) {
+dpnorm_status dpnorm_embed_grad_workspace(dpnorm_dtype dt, int64_t B, int64_t T, int64_t V, int64_t d, int ordered,
+                                          size_t* bytes) {
   if (!bytes) return DPNORM_ERR_NULL;
-  dpnorm_status st = check_ids(B, T, V);
-  if (st == DPNORM_OK) st = check_rows(dt, std::max(B * T, V), d);
-  if (st != DPNORM_OK) return st;
+  if (ordered != 0 && ordered != 1) return DPNORM_ERR_VALUE;
   EmbedPlan pl;
-  plan_order(pl, B, T, V);
-  plan_runs(pl, dt, d);
-  st = check_grid(pl);
-  if (st != DPNORM_OK) return st;
-  *bytes = pl.grad_ws;
-  return DPNORM_OK;
+  const dpnorm_status st = plan_embed(dt, B, T, V, d, ordered != 0, pl);
+  if (st == DPNORM_OK) *bytes = pl.grad_ws;
+  return st;
 }
 
-dpnorm_status dpnorm_embed_grad(const void* order, const void* G, dpnorm_dtype dt, int64_t B, int64_t T, int64_t V, int64_t d,
-                                float scale, const float* c, void* dW, int accumulate, void* ws, size_t ws_bytes,
-                                hipStream_t stream) {
-  size_t bytes = 0;
-  const dpnorm_status st = dpnorm_embed_grad_workspace(dt, B, T, V, d, &bytes);
-  if (st != DPNORM_OK) return st;
-  if (!order || !G || !dW || !ws) return DPNORM_ERR_NULL;
-  if (!aligned(order, kAlign) || !aligned(G, 16) || !aligned(c, 4) || !aligned(dW, 16) || !aligned(ws, kAlign))
-    return DPNORM_ERR_ALIGN;
-  if (!std::isfinite(scale) || (accumulate != 0 && accumulate != 1)) return DPNORM_ERR_VALUE;
-  if (ws_bytes < bytes) return DPNORM_ERR_WORKSPACE;
+dpnorm_status dpnorm_embed_grad(const void* tok, dpnorm_index it, const void* order, const void* G, dpnorm_dtype dt, int64_t B,
+                                int64_t T, int64_t V, int64_t d, float scale, const float* c, void* dW, int accumulate,
+                                void* ws, size_t ws_bytes, hipStream_t stream) {
   EmbedPlan pl;
-  plan_order(pl, B, T, V);
-  plan_runs(pl, dt, d);
-  const size_t e = esize(dt), wb = (size_t)V * d * e, gb = (size_t)pl.N * d * e;
-  if (overlaps(dW, wb, order, pl.order_bytes) || overlaps(dW, wb, G, gb) || overlaps(dW, wb, ws, bytes) ||
-      (c && (overlaps(dW, wb, c, (size_t)B * 4) || overlaps(ws, bytes, c, (size_t)B * 4))) ||
-      overlaps(ws, bytes, order, pl.order_bytes) || overlaps(ws, bytes, G, gb))
+  dpnorm_status st = plan_embed(dt, B, T, V, d, order != nullptr, pl);
+  if (st == DPNORM_OK) st = check_embed(pl, tok, it, order, G, dW, ws, pl.grad_ws, ws_bytes, scale, accumulate);
+  if (st != DPNORM_OK) return st;
+  if (!aligned(c, 4) || !aligned(dW, 16)) return DPNORM_ERR_ALIGN;
+  const size_t e = esize(dt), wb = (size_t)V * d * e, gb = (size_t)pl.N * d * e, cb = (size_t)B * 4;
+  const void* ids = order ? order : tok;
+  const size_t ib = order ? pl.order_bytes : (size_t)pl.N * (it == DPNORM_I64 ? 8 : 4);
+  if (overlaps(dW, wb, ids, ib) || overlaps(dW, wb, G, gb) || overlaps(dW, wb, c, cb) || overlaps(dW, wb, ws, pl.grad_ws) ||
+      overlaps(ws, pl.grad_ws, ids, ib) || overlaps(ws, pl.grad_ws, G, gb) || overlaps(ws, pl.grad_ws, c, cb))
     return DPNORM_ERR_VALUE;
+  const bool bf16 = dt == DPNORM_BF16;
+  hipError_t he = hipSuccess;
+  char* base = (char*)ws;
+  if (!order && !pl.small_grad) {
+    he = launch_order(pl, tok, it, base + pl.off_order, base + pl.off_order_ws, stream);
+    order = base + pl.off_order;
+  }
   embed::RunArgs a = run_args(pl, order, G);
   a.c = c;
   a.scale = scale;
   a.out = (char*)dW;
   a.accumulate = accumulate;
-  a.part = (float*)((char*)ws + pl.off_part_grad);
+  if (pl.small_grad) {
+    const uint32_t blocks = (uint32_t)((pl.V + embed::kSmallRows - 1) / embed::kSmallRows);
+    if (bf16) embed::k_grad_small<true><<<blocks, 256, 0, stream>>>(tok, it == DPNORM_I64, a);
+    else embed::k_grad_small<false><<<blocks, 256, 0, stream>>>(tok, it == DPNORM_I64, a);
+    return hip_status(hipGetLastError());
+  }
+  a.part = (float*)(base + pl.off_part_grad);
   a.fill_blocks = accumulate ? 0 : (pl.V + embed::kFillRows - 1) / embed::kFillRows;
-  return hip_status(launch_runs<embed::RUN_GRAD>(a, dt == DPNORM_BF16, stream));
+  if (he == hipSuccess) he = launch_runs<embed::RUN_GRAD>(a, bf16, stream);
+  return hip_status(he);
 }
 
 }  // extern "C"

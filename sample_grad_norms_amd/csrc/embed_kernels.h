@@ -198,10 +198,15 @@ __global__ __launch_bounds__(kSortThreads) void k_order_scatter(const void* tok,
   // where this block's elements of each digit go
   uint32_t total = 0, before = 0;
   if ((int)threadIdx.x < digits) {
-    for (int b = 0; b < nb; ++b) {
-      const uint32_t h = hist[(int64_t)threadIdx.x * nb + b];
-      if (b < (int)blockIdx.x) before += h;
-      total += h;
+    for (int b0 = 0; b0 < nb; b0 += 16) {   // (16 loads in flight)
+      uint32_t h[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) h[j] = b0 + j < nb ? hist[(int64_t)threadIdx.x * nb + b0 + j] : 0u;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        if (b0 + j < (int)blockIdx.x) before += h[j];
+        total += h[j];
+      }
     }
   }
   const uint32_t base = scan_block(sh, total) + before;
@@ -314,6 +319,7 @@ struct Runs {
   const int32_t* keys;   // sorted, V for positions without a row
   const int32_t* pos;
   int32_t N, T, V;
+  double per;            // 1 / T
   int R;                 // at most 32, so that a chunk fits the lanes of a wave
   int32_t chunks;
 };
@@ -323,11 +329,18 @@ enum { RUN_NORM = 0, RUN_GRAD = 1 };
 __device__ __forceinline__ int32_t in_batch(const Runs& a, int32_t q) { return (int32_t)min((uint32_t)q, (uint32_t)a.N - 1u); }
 __device__ __forceinline__ int32_t in_table(const Runs& a, int32_t key) { return (int32_t)min((uint32_t)key, (uint32_t)a.V); }
 
+// Sample of position q, q / T: the fp64 quotient is off by less than one part in
+// 2^51, so at most the last whole step of an exact multiple is missed.
+__device__ __forceinline__ int32_t sample_of(const Runs& a, int32_t q) {
+  const int32_t i = (int32_t)((double)q * a.per);
+  return q - i * a.T >= a.T ? i + 1 : i;
+}
+
 template <int MODE>
 __device__ __forceinline__ bool run_starts(const Runs& a, int32_t j) {
   if (j <= 0 || j >= a.N) return true;
   if (a.keys[j] != a.keys[j - 1]) return true;
-  return MODE == RUN_NORM && a.pos[j] / a.T != a.pos[j - 1] / a.T;
+  return MODE == RUN_NORM && sample_of(a, a.pos[j]) != sample_of(a, a.pos[j - 1]);
 }
 
 // The boundary that x = c R moves to; `cut` when it lies inside a run.
@@ -348,13 +361,13 @@ __device__ __forceinline__ int32_t boundary(const Runs& a, int64_t x, bool& cut)
 // End of the run that holds sorted position j: a search by all 64 lanes.
 template <int MODE>
 __device__ __forceinline__ int32_t run_end(const Runs& a, int32_t j) {
-  const int32_t key = a.keys[j], smp = MODE == RUN_NORM ? a.pos[j] / a.T : 0;
+  const int32_t key = a.keys[j], smp = MODE == RUN_NORM ? sample_of(a, a.pos[j]) : 0;
   const int lane = __lane_id();
   int64_t lo = j, hi = a.N;   // position lo is in the run, hi is not
   while (hi - lo > 1) {
     const int64_t step = (hi - lo + 63) / 64;
     const int64_t p = lo + step * (lane + 1);
-    const bool in = p < hi && a.keys[p] == key && (MODE != RUN_NORM || a.pos[p] / a.T == smp);
+    const bool in = p < hi && a.keys[p] == key && (MODE != RUN_NORM || sample_of(a, a.pos[p]) == smp);
     const int cnt = __popcll(__ballot(in));   // the lanes inside are the first ones
     const int64_t nlo = lo + step * cnt;
     hi = min(hi, nlo + step);
@@ -454,7 +467,7 @@ __global__ __launch_bounds__(256) void k_run_sums(RunArgs a) {
   }
   if (n == 0) return;
   float wgt = 1.f;
-  if (MODE == RUN_GRAD) wgt = a.c && lane < n ? a.scale * a.c[mine / a.runs.T] : a.scale;
+  if (MODE == RUN_GRAD) wgt = a.c && lane < n ? a.scale * a.c[sample_of(a.runs, mine)] : a.scale;
   float acc[R::kElems] = {};
   int first = 0;
   for (int j0 = 0; j0 < n; j0 += kRowsAhead) {
@@ -525,16 +538,24 @@ __global__ __launch_bounds__(256) void k_run_join(RunArgs a) {
   const bool on = col < a.d;
   float acc[R::kElems] = {};
   if (on) {
-    for (int32_t ch = chunk + wv; ch <= last; ch += 4) {
-      const float* p = a.part + ((int64_t)ch * 2 + (ch == chunk ? 1 : 0)) * a.d + col;
+    for (int32_t ch = chunk + wv; ch <= last; ch += 32) {
+      float4 f[8][R::kElems / 4];
 #pragma unroll
-      for (int j = 0; j < R::kElems; j += 4) {
-        const float4 f = ldg_f32x4(p + j);
-        acc[j] += f.x;
-        acc[j + 1] += f.y;
-        acc[j + 2] += f.z;
-        acc[j + 3] += f.w;
+      for (int u = 0; u < 8; ++u) {
+        const int32_t c = ch + 4 * u;
+        const float* p = a.part + ((int64_t)c * 2 + (c == chunk ? 1 : 0)) * a.d + col;
+#pragma unroll
+        for (int j = 0; j < R::kElems / 4; ++j) f[u][j] = c <= last ? ldg_f32x4(p + 4 * j) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+#pragma unroll
+        for (int j = 0; j < R::kElems / 4; ++j) {
+          acc[4 * j] += f[u][j].x;
+          acc[4 * j + 1] += f[u][j].y;
+          acc[4 * j + 2] += f[u][j].z;
+          acc[4 * j + 3] += f[u][j].w;
+        }
     }
   }
   if (wv > 0) {
@@ -566,7 +587,13 @@ __global__ __launch_bounds__(1024) void k_norm_sum(const float* val, int64_t N, 
   double s = 0.0;
   for (int sl = 0; sl < slices; ++sl) {
     const float* p = val + (int64_t)sl * N + (int64_t)blockIdx.x * T;
-    for (int t = threadIdx.x; t < T; t += 1024) s += (double)p[t];
+    for (int t = threadIdx.x; t < T; t += 8 * 1024) {
+      float x[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) x[u] = t + u * 1024 < T ? p[t + u * 1024] : 0.f;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) s += (double)x[u];
+    }
   }
   s = wave_sum(s);
   if (lane == 0) part[wv] = s;
@@ -577,6 +604,122 @@ __global__ __launch_bounds__(1024) void k_norm_sum(const float* val, int64_t N, 
     for (int w = 0; w < 16; ++w) t += part[w];
     t *= scale2;
     n[blockIdx.x] = (float)(accumulate ? (double)n[blockIdx.x] + t : t);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Small batches in one launch, without an order: each wave looks for the equal
+// ids itself among at most kSmallIds of them.
+// ---------------------------------------------------------------------------
+constexpr int kSmallIds = 256;
+
+// Sum of the rows at the positions in `mask` of each 64 ids, weighted.
+template <bool BF16, typename W>
+__device__ __forceinline__ void add_rows(float (&acc)[Row<BF16>::kElems], const uint64_t (&mask)[kSmallIds / 64],
+                                         const char* G, int64_t row_bytes, bool on, W weight) {
+#pragma unroll
+  for (int k = 0; k < kSmallIds / 64; ++k) {
+    uint64_t m = mask[k];
+    while (m) {
+      int at[kRowsAhead];
+      uint4 v[kRowsAhead];
+#pragma unroll
+      for (int u = 0; u < kRowsAhead; ++u) {
+        at[u] = m ? 64 * k + __builtin_ctzll(m) : -1;
+        if (m) m &= m - 1;
+        v[u] = at[u] >= 0 && on ? ldg16(G + at[u] * row_bytes) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int u = 0; u < kRowsAhead; ++u)
+        if (at[u] >= 0) Row<BF16>::add(acc, v[u], weight(at[u]));
+    }
+  }
+}
+
+// Norm of samples of at most kSmallIds positions, a block a sample. The first
+// position of an id stands for its row.
+template <bool BF16>
+__global__ __launch_bounds__(1024) void k_norm_small(const void* tok, int idx64, const char* G, int32_t T, int32_t V, int32_t d,
+                                                     double scale2, float* n, int accumulate) {
+  using R = Row<BF16>;
+  __shared__ int32_t keys[kSmallIds];
+  __shared__ double part[16];
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t q0 = (int64_t)blockIdx.x * T;
+  if (threadIdx.x < kSmallIds) keys[threadIdx.x] = (int)threadIdx.x < T ? id_key(tok, idx64, q0 + threadIdx.x, V) : V;
+  __syncthreads();
+  int32_t mine[kSmallIds / 64];
+#pragma unroll
+  for (int k = 0; k < kSmallIds / 64; ++k) mine[k] = keys[64 * k + lane];
+  double sum = 0.0;
+  for (int t = wv; t < T; t += 16) {
+    const int32_t key = __builtin_amdgcn_readfirstlane(keys[t]);
+    if (key >= V) continue;
+    uint64_t mask[kSmallIds / 64];
+    bool first = true;
+#pragma unroll
+    for (int k = 0; k < kSmallIds / 64; ++k) {
+      mask[k] = __ballot(mine[k] == key);
+      if (64 * k + 63 < t) first = first && mask[k] == 0;
+      else if (64 * k <= t) first = first && (mask[k] & ((1ull << (t & 63)) - 1ull)) == 0;
+    }
+    if (!first) continue;
+    for (int c0 = 0; c0 < d; c0 += R::kSlice) {
+      const int col = c0 + lane * R::kElems;
+      float acc[R::kElems] = {};
+      add_rows<BF16>(acc, mask, G + (q0 * d + col) * R::kBytes, (int64_t)d * R::kBytes, col < d, [](int) { return 1.f; });
+      float s = 0.f;
+#pragma unroll
+      for (int e = 0; e < R::kElems; ++e) s = fmaf(acc[e], acc[e], s);
+      sum += (double)wave_sum_f32(s);
+    }
+  }
+  if (lane == 0) part[wv] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double t = 0.0;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) t += part[w];
+    t *= scale2;
+    n[blockIdx.x] = (float)(accumulate ? (double)n[blockIdx.x] + t : t);
+  }
+}
+
+constexpr int kSmallRows = 16;   // table rows of a block, four a wave
+
+// Gradient of the table from at most kSmallIds positions in all.
+template <bool BF16>
+__global__ __launch_bounds__(256) void k_grad_small(const void* tok, int idx64, RunArgs a) {
+  using R = Row<BF16>;
+  __shared__ int32_t keys[kSmallIds];
+  __shared__ float wgt[kSmallIds];
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int32_t v0 = blockIdx.x * kSmallRows;
+  {
+    const int q = threadIdx.x;
+    keys[q] = q < a.runs.N ? id_key(tok, idx64, q, a.runs.V) : a.runs.V;
+    wgt[q] = a.c && q < a.runs.N ? a.scale * a.c[sample_of(a.runs, q)] : a.scale;
+  }
+  __syncthreads();
+  int32_t mine[kSmallIds / 64];
+#pragma unroll
+  for (int k = 0; k < kSmallIds / 64; ++k) mine[k] = keys[64 * k + lane];
+  for (int32_t v = v0 + wv; v < min(v0 + kSmallRows, a.runs.V); v += 4) {
+    uint64_t mask[kSmallIds / 64], any = 0;
+#pragma unroll
+    for (int k = 0; k < kSmallIds / 64; ++k) {
+      mask[k] = __ballot(mine[k] == v);
+      any |= mask[k];
+    }
+    if (!any && a.accumulate) continue;
+    for (int c0 = 0; c0 < a.d; c0 += R::kSlice) {
+      const int col = c0 + lane * R::kElems;
+      float acc[R::kElems] = {};
+      if (any)
+        add_rows<BF16>(acc, mask, a.G + (int64_t)col * R::kBytes, (int64_t)a.d * R::kBytes, col < a.d,
+                       [&](int q) { return wgt[q]; });
+      if (col < a.d) put_row<BF16>(a, v, col, acc);
+    }
   }
 }
 

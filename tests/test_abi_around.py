@@ -66,24 +66,33 @@ def test_order_checks(lib):
 @pytest.mark.parametrize("which", ["norm", "grad"])
 def test_norm_and_grad_checks(lib, which):
     query = getattr(lib, f"dpnorm_embed_{which}_workspace")
-    nb = C.c_size_t(0)
-    assert query(_lib.BF16, 3, 100, 50, 64, C.byref(nb)) == _lib.OK and nb.value > 0 and nb.value % 256 == 0
-    assert query(_lib.BF16, 3, 100, 50, 64, None) == _lib.ERR_NULL
-    assert query(7, 3, 100, 50, 64, C.byref(nb)) == _lib.ERR_DTYPE
+    sizes = []
+    for ordered in (0, 1):
+        nb = C.c_size_t(0)
+        assert query(_lib.BF16, 3, 100, 50, 64, ordered, C.byref(nb)) == _lib.OK and nb.value % 256 == 0
+        sizes.append(nb.value)
+    # 100 ids a sample and 300 in all: the norm needs no order and no workspace, the gradient both
+    assert sizes[0] == 0 < sizes[1] if which == "norm" else sizes[0] >= sizes[1] + order_sizes(lib)[1] > 0
+    assert query(_lib.BF16, 3, 100, 50, 64, 0, None) == _lib.ERR_NULL
+    assert query(_lib.BF16, 3, 100, 50, 64, 2, C.byref(nb)) == _lib.ERR_VALUE
+    assert query(7, 3, 100, 50, 64, 0, C.byref(nb)) == _lib.ERR_DTYPE
     for bad in ((0, 100, 50, 64), (3, 100, 0, 64), (3, 100, 50, 60), (2 ** 20, 2 ** 11, 5, 8), (1, 2 ** 30, 1, 2 ** 24)):
-        assert query(_lib.BF16, *bad, C.byref(nb)) == _lib.ERR_SIZE
+        assert query(_lib.BF16, *bad, 0, C.byref(nb)) == _lib.ERR_SIZE
 
-    def call(order=ORDER, g=G, dt=_lib.BF16, B=3, T=100, V=50, d=64, scale=1.0, out=OUT, c=CW, acc=0, ws=WS, ws_size=BIG):
+    def call(tok=None, it=_lib.I64, order=ORDER, g=G, dt=_lib.BF16, B=3, T=100, V=50, d=64, scale=1.0, out=OUT, c=CW, acc=0,
+             ws=WS, ws_size=BIG):
         if which == "norm":
-            return lib.dpnorm_embed_norm(order, g, dt, B, T, V, d, scale, out, acc, ws, ws_size, None)
-        return lib.dpnorm_embed_grad(order, g, dt, B, T, V, d, scale, c, out, acc, ws, ws_size, None)
+            return lib.dpnorm_embed_norm(tok, it, order, g, dt, B, T, V, d, scale, out, acc, ws, ws_size, None)
+        return lib.dpnorm_embed_grad(tok, it, order, g, dt, B, T, V, d, scale, c, out, acc, ws, ws_size, None)
     assert call(order=None) == call(g=None) == call(out=None) == call(ws=None) == _lib.ERR_NULL
-    assert call(dt=-3) == _lib.ERR_DTYPE
+    assert call(dt=-3) == call(order=None, tok=TOK, it=3) == _lib.ERR_DTYPE
     assert call(T=0) == call(d=4) == _lib.ERR_SIZE
     assert call(order=ORDER + 4) == call(g=G + 8) == call(out=OUT + 2) == call(ws=WS + 16) == _lib.ERR_ALIGN
+    assert call(order=None, tok=TOK + 4) == _lib.ERR_ALIGN
     assert call(scale=float("inf")) == call(acc=2) == call(acc=-1) == _lib.ERR_VALUE
-    assert call(ws_size=nb.value - 1 if which == "norm" else 255) == _lib.ERR_WORKSPACE
+    assert call(ws_size=sizes[1] - 1) == call(order=None, tok=TOK, T=300, ws_size=255) == _lib.ERR_WORKSPACE
     assert call(out=G) == call(out=ORDER) == call(out=WS) == call(ws=G) == call(ws=ORDER) == _lib.ERR_VALUE
+    assert call(order=None, tok=TOK, out=TOK) == call(order=None, tok=TOK, T=300, ws=TOK) == _lib.ERR_VALUE
     if which == "grad":
         assert call(c=CW + 2) == _lib.ERR_ALIGN
         assert call(c=OUT) == call(c=WS) == _lib.ERR_VALUE
@@ -92,8 +101,8 @@ def test_norm_and_grad_checks(lib, which):
 Q, K, V_, O, LSE, DO, DQ, DK, DV, CU = (0x100000000 * j for j in range(1, 11))
 
 
-def shape(dtype=_lib.BF16, n=200, s=2, hq=4, hkv=2, d=64, cu=CU, scale=0.125):
-    return _lib.AttnShape(dtype, n, s, hq, hkv, d, cu, scale)
+def shape(dtype=_lib.BF16, n=200, s=2, hq=4, hkv=2, d=64, cu=CU, scale=0.125, clear=0):
+    return _lib.AttnShape(dtype, n, s, hq, hkv, d, cu, scale, clear)
 
 
 def tensor(p, h, d=64, st=None, sh=None):
@@ -114,6 +123,7 @@ def test_attention_forward_checks(lib):
                 dict(n=2 ** 31), dict(s=2 ** 31), dict(hq=2 ** 17, hkv=1), dict(n=201, cu=None)):
         assert forward(lib, shape(**bad)) == _lib.ERR_SIZE, bad
     assert forward(lib, shape(cu=CU + 2)) == _lib.ERR_ALIGN
+    assert forward(lib, shape(clear=2)) == forward(lib, shape(clear=-1)) == _lib.ERR_VALUE
     for scale in (0.0, -1.0, float("nan"), float("inf")):
         assert forward(lib, shape(scale=scale)) == _lib.ERR_VALUE
     assert forward(lib, q=tensor(Q + 8, 4)) == forward(lib, lse=LSE + 2) == _lib.ERR_ALIGN
@@ -186,16 +196,18 @@ def test_valid_calls_launch_valid_grids(lib, seed):
     p = [far * (j + 1) for j in range(12)]
     assert lib.dpnorm_embed_order(p[0], _lib.I64, B, T, V, p[1], ob, p[2], wb, None) == _lib.OK
     nb = C.c_size_t(0)
-    st = lib.dpnorm_embed_norm_workspace(dt, B, T, V, d, C.byref(nb))
-    assert st in (_lib.OK, _lib.ERR_SIZE)
-    assert lib.dpnorm_embed_norm(p[1], p[3], dt, B, T, V, d, 2.0, p[4], 0, p[5], nb.value, None) == st
-    assert lib.dpnorm_embed_grad_workspace(dt, B, T, V, d, C.byref(nb)) == st
-    assert lib.dpnorm_embed_grad(p[1], p[3], dt, B, T, V, d, 2.0, p[6], p[7], seed % 2, p[5], nb.value, None) == st
+    for ordered in (0, 1):
+        ids = (None, 0, p[1]) if ordered else (p[0], _lib.I64, None)
+        st = lib.dpnorm_embed_norm_workspace(dt, B, T, V, d, ordered, C.byref(nb))
+        assert st in (_lib.OK, _lib.ERR_SIZE)
+        assert lib.dpnorm_embed_norm(*ids, p[3], dt, B, T, V, d, 2.0, p[4], 0, p[5], nb.value, None) == st
+        assert lib.dpnorm_embed_grad_workspace(dt, B, T, V, d, ordered, C.byref(nb)) == st
+        assert lib.dpnorm_embed_grad(*ids, p[3], dt, B, T, V, d, 2.0, p[6], p[7], seed % 2, p[5], nb.value, None) == st
     assert lib.dpnorm_embed_lookup(p[0], _lib.I32, p[7], dt, B * T, V, d, 1.0, p[8], None) == _lib.OK
     hkv = rng.choice([1, 2, 3, 8])
     hq, D, S = hkv * rng.randint(1, 8), 8 * rng.randint(1, 16), log(1, 5000)
     n = log(1, 2 ** 22)
-    sh = shape(dt, n, S, hq, hkv, D, p[9])
+    sh = shape(dt, n, S, hq, hkv, D, p[9], clear=seed % 2)
     ten = [tensor(x, h, D) for x, h in ((p[0], hq), (p[1], hkv), (p[2], hkv), (p[3], hq), (p[4], hq), (p[5], hq), (p[6], hkv),
                                         (p[7], hkv))]
     q, k, v, o, do, dq, dk, dv = (C.byref(t) for t in ten)

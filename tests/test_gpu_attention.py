@@ -125,6 +125,8 @@ CASES = [   # lengths, Hq, Hkv, D
     ([500, 1, 2, 3], 8, 2, 96),
     ([1030], 2, 1, 128),
     ([1029], 2, 2, 64),
+    ([400, 1, 299], 64, 32, 64),        # many heads: work groups of 128 queries, and of four waves for dk and dv
+    ([333, 370], 64, 32, 104),
 ]
 
 
@@ -192,7 +194,7 @@ def test_strided_and_repeated_rows(dtype):
     hnd = tuple(x.transpose(0, 1).contiguous().transpose(0, 1) for x in (q, k, v))
     for a, b, c in (views, hnd):
         out = torch.empty(Hq, N, D, dtype=dtype, device=dev()).transpose(0, 1)
-        o2, lse2 = dp.attention_forward(a, b, c, cu_seqlens=cu, out=out)
+        o2, lse2 = dp.attention_forward(a, b, c, cu_seqlens=cu, out=out, lse=torch.empty_like(lse))
         assert o2 is out and torch.equal(o2, o) and torch.equal(lse2, lse)
         grads = tuple(torch.empty(x.shape[1], N, D, dtype=dtype, device=dev()).transpose(0, 1) for x in (a, b, c))
         g2 = dp.attention_backward(do.transpose(0, 1).contiguous().transpose(0, 1), a, b, c, o2, lse2, cu_seqlens=cu, out=grads)
@@ -231,13 +233,35 @@ def test_rows_of_no_sequence(dtype):
         assert bool((x.cpu()[free] == 7).all())
         inside(x[3:201], w[3:201], b[3:201], name)
     # made by the call, such rows are zero
+    dirty = [torch.full_like(x, 9.0) for x in (out, lse, *args)]   # the allocator hands these out again
+    del dirty
     o2, lse2 = dp.attention_forward(*args, cu_seqlens=cud)
     assert bool((o2.cpu()[free] == 0).all()) and bool((lse2.cpu()[:, free] == 0).all())
+    for x, y in zip(dp.attention_backward(do.to(dev()), *args, out, lse, cu_seqlens=cud), grads):
+        assert bool((x.cpu()[free] == 0).all()) and torch.equal(x[3:201], y[3:201])
     # a NaN in one sequence leaves the other as it was
     for x in args:
         x[3:70] = math.nan
     o3, _ = dp.attention_forward(*args, cu_seqlens=cud)
     assert torch.equal(o3[70:201], o2[70:201]) and bool(o3[3:70].isnan().all())
+
+
+@pytest.mark.parametrize("cu", [[0, 0, 0], [130, 130], [0, 64, 128], [100, 101, 133]])
+def test_rows_of_no_sequence_are_cleared(cu):
+    """No sequence at all, tiles that fill every slot, one row among many."""
+    import sample_grad_norms_amd as dp
+    for Hq, Hkv in ((2, 1), (64, 64)):
+        N = 133 if Hq == 2 else 900
+        q, k, v, do = (x.to(dev()) for x in make(N, Hq, Hkv, 64, torch.bfloat16, 17))
+        cud = torch.tensor(cu, dtype=torch.int32, device=dev())
+        dirty = [torch.full_like(x, 9.0) for x in (q, q, k, v)]
+        del dirty
+        o, lse = dp.attention_forward(q, k, v, cu_seqlens=cud)
+        grads = dp.attention_backward(do, q, k, v, o, lse, cu_seqlens=cud)
+        free = torch.ones(N, dtype=torch.bool)
+        free[cu[0]:cu[-1]] = False
+        for x in (o, lse.t(), *grads):
+            assert bool((x.cpu()[free] == 0).all()) and bool(x.isfinite().all())
 
 
 def test_offsets_outside_the_rows_are_clamped():
@@ -266,7 +290,7 @@ def test_byte_offsets_past_32_bits():
         o2, lse2 = dp.attention_forward(*args[:3])
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
         assert all(torch.equal(x, y) for x, y in zip(g, dp.attention_backward(args[3], *args[:3], o, lse)))
-    dp.attention_forward(*small[:3], out=wide)
+    dp.attention_forward(*small[:3], out=wide, lse=lse2)
     assert torch.equal(wide, o)
 
 
@@ -344,8 +368,8 @@ def test_refusals():
     buf = torch.zeros(12 * 4 * 64 + 8, device=dev())
     for call in (lambda: dp.attention_forward(wide, wide, wide), lambda: dp.attention_forward(odd, odd, odd),
                  lambda: dp.attention_forward(q, k, k, scale=0.0), lambda: dp.attention_forward(q, k, k, scale=float("nan")),
-                 lambda: dp.attention_forward(q, k, k, out=q),                                        # an output over an input
-                 lambda: dp.attention_forward(q, k, k, out=torch.zeros(1, 4, 64, device=dev()).expand(12, 4, 64)),
+                 lambda: dp.attention_forward(q, k, k, out=q, lse=lse),                                        # an output over an input
+                 lambda: dp.attention_forward(q, k, k, out=torch.zeros(1, 4, 64, device=dev()).expand(12, 4, 64), lse=lse),
                  lambda: dp.attention_forward(buf[1:1 + q.numel()].view(q.shape), k, k),              # not 16-byte aligned
                  lambda: dp.attention_backward(q.clone(), q, k, k, q.clone(), lse, out=(q.clone(), k, k.clone()))):
         with pytest.raises(dp.DpnormError):
@@ -354,7 +378,8 @@ def test_refusals():
                  lambda: dp.attention_forward(q, k[:11], k[:11]), lambda: dp.attention_forward(q, k, k, sequences=5),
                  lambda: dp.attention_forward(q, k, k, sequences=1, cu_seqlens=cu),
                  lambda: dp.attention_forward(q.transpose(1, 2), k, k), lambda: dp.attention_forward(q.cpu(), k, k),
-                 lambda: dp.attention_forward(q, k, k, out=q[:11]), lambda: dp.attention_forward(q, k, k, lse=lse.t()),
+                 lambda: dp.attention_forward(q, k, k, out=q[:11], lse=lse), lambda: dp.attention_forward(q, k, k, lse=lse),
+                 lambda: dp.attention_forward(q, k, k, out=q.clone(), lse=lse.t()),
                  lambda: dp.attention_backward(q[:11], q, k, k, q, lse),
                  lambda: dp.attention_backward(q, q, k, k, q, lse, workspace=torch.zeros(8, device=dev()))):
         with pytest.raises(ValueError):
