@@ -67,7 +67,7 @@ void plan_runs(EmbedPlan& pl, dpnorm_dtype dt, int64_t d, bool ordered) {
   pl.small_grad = !ordered && pl.N <= embed::kSmallIds;
   const int64_t width = dt == DPNORM_BF16 ? embed::Row<true>::kSlice : embed::Row<false>::kSlice;
   pl.slices = (int)((d + width - 1) / width);
-  pl.R = 32;
+  pl.R = 16;
   while (pl.R > 4 && (int64_t)pl.N * pl.slices / pl.R < 4096) pl.R >>= 1;
   pl.chunks = (pl.N + pl.R - 1) / pl.R;
   Bump n;

@@ -66,8 +66,8 @@ __device__ __forceinline__ uint32_t count_round(uint32_t* cnt, uint32_t digit, i
   return rank;
 }
 
-__device__ __forceinline__ void zero_counts(SortShared& sh, int digits) {
-  for (int j = threadIdx.x; j < kSortWaves * digits; j += kSortThreads) sh.cnt[j / digits][j % digits] = 0;
+__device__ __forceinline__ void zero_counts(SortShared& sh, int bits) {
+  for (int j = threadIdx.x; j < kSortWaves << bits; j += kSortThreads) sh.cnt[j >> bits][j & ((1 << bits) - 1)] = 0;
   __syncthreads();
 }
 
@@ -77,11 +77,13 @@ __device__ __forceinline__ uint32_t scan_waves(SortShared& sh, int digits) {
   __syncthreads();
   uint32_t run = 0;
   if ((int)threadIdx.x < digits) {
+    uint32_t c[kSortWaves];
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) c[w] = sh.cnt[w][threadIdx.x];
 #pragma unroll
     for (int w = 0; w < kSortWaves; ++w) {
-      const uint32_t c = sh.cnt[w][threadIdx.x];
       sh.cnt[w][threadIdx.x] = run;
-      run += c;
+      run += c[w];
     }
   }
   return run;
@@ -98,8 +100,11 @@ __device__ __forceinline__ uint32_t scan_block(SortShared& sh, uint32_t v) {
   }
   if (lane == 63) sh.scan[wv] = inc;
   __syncthreads();
-  uint32_t before = 0;
-  for (int w = 0; w < wv; ++w) before += sh.scan[w];
+  uint32_t all[kSortWaves], before = 0;
+#pragma unroll
+  for (int w = 0; w < kSortWaves; ++w) all[w] = sh.scan[w];
+#pragma unroll
+  for (int w = 0; w < kSortWaves; ++w) before += w < wv ? all[w] : 0u;
   return before + inc - v;
 }
 
@@ -122,7 +127,7 @@ __global__ __launch_bounds__(kSortThreads) void k_order_small(const void* tok, i
     ps[r] = q;
   }
   for (int p = 0; p < passes; ++p) {
-    zero_counts(sh, digits);
+    zero_counts(sh, bits);
     uint32_t rank[kSmallRounds];
 #pragma unroll
     for (int r = 0; r < kSmallRounds; ++r) {
@@ -184,6 +189,8 @@ __global__ __launch_bounds__(kSortThreads) void k_order_count(const void* tok, i
   for (int j = threadIdx.x; j < digits; j += kSortThreads) hist[(int64_t)j * gridDim.x + blockIdx.x] = cnt[j];
 }
 
+constexpr int kHeldRounds = 4;   // rounds of a wave whose keys stay in registers between the two walks
+
 __global__ __launch_bounds__(kSortThreads) void k_order_scatter(const void* tok, int idx64, const int32_t* src_keys,
                                                                 const int32_t* src_pos, int32_t N, int32_t V, int shift,
                                                                 int bits, int per, const uint32_t* hist, int32_t* keys,
@@ -195,6 +202,16 @@ __global__ __launch_bounds__(kSortThreads) void k_order_scatter(const void* tok,
   const int seg = (per + kSortWaves - 1) / kSortWaves;   // positions a wave walks, in order
   const int64_t wlo = lo + (int64_t)wv * seg < hi ? lo + (int64_t)wv * seg : hi;
   const int64_t whi = wlo + seg < hi ? wlo + seg : hi;
+  const bool held = seg <= kHeldRounds * kWave;
+  int32_t key[kHeldRounds], ps[kHeldRounds];
+  if (held) {
+#pragma unroll
+    for (int r = 0; r < kHeldRounds; ++r) {
+      const int64_t q = wlo + r * kWave + lane;
+      key[r] = q < whi ? load_key(tok, idx64, src_keys, q, V) : 0;
+      ps[r] = q < whi && src_pos ? src_pos[q] : (int32_t)q;
+    }
+  }
   // where this block's elements of each digit go
   uint32_t total = 0, before = 0;
   if ((int)threadIdx.x < digits) {
@@ -211,7 +228,27 @@ __global__ __launch_bounds__(kSortThreads) void k_order_scatter(const void* tok,
   }
   const uint32_t base = scan_block(sh, total) + before;
   if ((int)threadIdx.x < digits) sh.base[threadIdx.x] = base;
-  zero_counts(sh, digits);
+  zero_counts(sh, bits);
+  if (held) {
+    uint32_t rank[kHeldRounds];
+#pragma unroll
+    for (int r = 0; r < kHeldRounds; ++r) {
+      if (wlo + r * kWave < whi)
+        rank[r] = count_round(sh.cnt[wv], ((uint32_t)key[r] >> shift) & (digits - 1), bits, wlo + r * kWave + lane < whi);
+    }
+    scan_waves(sh, digits);
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kHeldRounds; ++r) {
+      if (wlo + r * kWave + lane < whi) {
+        const uint32_t dg = ((uint32_t)key[r] >> shift) & (digits - 1);
+        const uint32_t to = sh.base[dg] + sh.cnt[wv][dg] + rank[r];
+        keys[to] = key[r];
+        pos[to] = ps[r];
+      }
+    }
+    return;
+  }
   for (int64_t q0 = wlo; q0 < whi; q0 += kWave) {
     const int64_t q = q0 + lane;
     const bool in = q < whi;
@@ -224,12 +261,12 @@ __global__ __launch_bounds__(kSortThreads) void k_order_scatter(const void* tok,
   for (int64_t q0 = wlo; q0 < whi; q0 += kWave) {
     const int64_t q = q0 + lane;
     const bool in = q < whi;
-    const int32_t key = in ? load_key(tok, idx64, src_keys, q, V) : 0;
-    const uint32_t dg = ((uint32_t)key >> shift) & (digits - 1);
+    const int32_t k = in ? load_key(tok, idx64, src_keys, q, V) : 0;
+    const uint32_t dg = ((uint32_t)k >> shift) & (digits - 1);
     const uint32_t rank = count_round(sh.cnt[wv], dg, bits, in);
     if (in) {
       const uint32_t to = sh.base[dg] + rank;
-      keys[to] = key;
+      keys[to] = k;
       pos[to] = src_pos ? src_pos[q] : (int32_t)q;
     }
   }
@@ -320,7 +357,7 @@ struct Runs {
   const int32_t* pos;
   int32_t N, T, V;
   double per;            // 1 / T
-  int R;                 // at most 32, so that a chunk fits the lanes of a wave
+  int R;                 // at most 16, so that a wave's lanes see both ends of a chunk
   int32_t chunks;
 };
 
@@ -336,26 +373,38 @@ __device__ __forceinline__ int32_t sample_of(const Runs& a, int32_t q) {
   return q - i * a.T >= a.T ? i + 1 : i;
 }
 
-template <int MODE>
-__device__ __forceinline__ bool run_starts(const Runs& a, int32_t j) {
-  if (j <= 0 || j >= a.N) return true;
-  if (a.keys[j] != a.keys[j - 1]) return true;
-  return MODE == RUN_NORM && sample_of(a, a.pos[j]) != sample_of(a, a.pos[j - 1]);
-}
+// What a wave knows of chunk c: lane l describes sorted position c R - 1 + l, and
+// the chunk reaches from x0 to x1. One round of loads covers both boundaries.
+// (Values outside the batch or the table, which no order of this batch holds, are
+// kept in bounds.)
+struct Chunk {
+  int32_t at;            // position of lane 0
+  int32_t key, pos, smp;
+  uint64_t starts;       // lanes whose position starts a run (positions past the end do)
+  int32_t x0, x1;
+  bool cut0, cut1;       // the boundary lies inside a run
+};
 
-// The boundary that x = c R moves to; `cut` when it lies inside a run.
 template <int MODE>
-__device__ __forceinline__ int32_t boundary(const Runs& a, int64_t x, bool& cut) {
-  cut = false;
-  if (x <= 0) return 0;
-  if (x >= a.N) return a.N;
+__device__ __forceinline__ Chunk look_at(const Runs& a, int32_t c) {
+  Chunk w;
   const int lane = __lane_id();
-  const uint64_t m = __ballot(lane < a.R && run_starts<MODE>(a, (int32_t)min(x + lane, (int64_t)a.N)));
-  if (m == 0) {
-    cut = true;
-    return (int32_t)x;
-  }
-  return (int32_t)(x + __builtin_ctzll(m));
+  w.at = (int32_t)((int64_t)c * a.R - 1);
+  const int64_t j = (int64_t)w.at + lane;
+  const bool in = j >= 0 && j < a.N;
+  w.key = in ? in_table(a, a.keys[j]) : a.V;
+  w.pos = in ? in_batch(a, a.pos[j]) : 0;
+  w.smp = sample_of(a, w.pos);
+  const int32_t key = __shfl_up(w.key, 1), smp = __shfl_up(w.smp, 1);
+  w.starts = __ballot(!in || j == 0 || w.key != key || (MODE == RUN_NORM && w.smp != smp));
+  const uint64_t window = (1ull << a.R) - 1;
+  const uint64_t m0 = (w.starts >> 1) & window, m1 = (w.starts >> (1 + a.R)) & window;
+  w.cut0 = m0 == 0;
+  w.cut1 = m1 == 0;
+  w.x0 = (int32_t)min((int64_t)w.at + 1 + (m0 ? __builtin_ctzll(m0) : 0), (int64_t)a.N);
+  w.x1 = (int32_t)min((int64_t)w.at + 1 + a.R + (m1 ? __builtin_ctzll(m1) : 0), (int64_t)a.N);
+  if (c == 0) w.x0 = 0, w.cut0 = false;
+  return w;
 }
 
 // End of the run that holds sorted position j: a search by all 64 lanes.
@@ -364,14 +413,29 @@ __device__ __forceinline__ int32_t run_end(const Runs& a, int32_t j) {
   const int32_t key = a.keys[j], smp = MODE == RUN_NORM ? sample_of(a, a.pos[j]) : 0;
   const int lane = __lane_id();
   int64_t lo = j, hi = a.N;   // position lo is in the run, hi is not
+  bool near = true;           // most runs end within 64 positions
   while (hi - lo > 1) {
-    const int64_t step = (hi - lo + 63) / 64;
+    const int64_t step = near ? 1 : (hi - lo + 63) / 64;
+    near = false;
     const int64_t p = lo + step * (lane + 1);
     const bool in = p < hi && a.keys[p] == key && (MODE != RUN_NORM || sample_of(a, a.pos[p]) == smp);
     const int cnt = __popcll(__ballot(in));   // the lanes inside are the first ones
-    const int64_t nlo = lo + step * cnt;
-    hi = min(hi, nlo + step);
-    lo = nlo;
+    lo += step * cnt;
+    if (cnt < 64) hi = min(hi, lo + step);
+  }
+  return (int32_t)hi;
+}
+
+// First sorted position whose key is at least v: a search by all 64 lanes.
+__device__ __forceinline__ int32_t lower_bound(const Runs& a, int64_t v) {
+  const int lane = __lane_id();
+  int64_t lo = -1, hi = a.N;   // position lo is below v, hi is not
+  while (hi - lo > 1) {
+    const int64_t step = (hi - lo + 63) / 64;
+    const int64_t p = lo + step * (lane + 1);
+    const int cnt = __popcll(__ballot(p < hi && a.keys[p] < v));
+    lo += step * cnt;
+    hi = min(hi, lo + step);
   }
   return (int32_t)hi;
 }
@@ -424,16 +488,18 @@ __global__ __launch_bounds__(256) void k_run_sums(RunArgs a) {
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
   const int64_t item_blocks = (a.items + 3) / 4;
   if (MODE == RUN_GRAD && (int64_t)blockIdx.x >= item_blocks) {
-    // clear the rows of ids that do not occur: lane r looks for row v0 + r
+    // clear the rows of ids that do not occur: lane r looks for row v0 + r, among
+    // the keys from v0 to v0 + 63, found by the whole wave
     const int64_t v0 = ((int64_t)blockIdx.x - item_blocks) * kFillRows;
     const int64_t v = v0 + lane;
-    int32_t lo = 0, hi = a.runs.N;
+    int32_t lo = lower_bound(a.runs, v0), hi = lower_bound(a.runs, v0 + kFillRows);
+    const int32_t end = hi;
     while (lo < hi) {
       const int32_t mid = lo + (hi - lo) / 2;
       if (a.runs.keys[mid] < v) lo = mid + 1;
       else hi = mid;
     }
-    const bool absent = v < a.runs.V && !(lo < a.runs.N && a.runs.keys[lo] == v);
+    const bool absent = v < a.runs.V && !(lo < end && a.runs.keys[lo] == v);
     uint64_t m = __ballot(absent);
     for (int j = 0; m; ++j) {
       const int r = __builtin_ctzll(m);
@@ -450,24 +516,18 @@ __global__ __launch_bounds__(256) void k_run_sums(RunArgs a) {
   const int slice = (int)(item % a.slices);
   const int col = slice * R::kSlice + lane * R::kElems;
   const bool on = col < a.d;
-  bool cut0, cut1;
-  const int32_t x0 = boundary<MODE>(a.runs, (int64_t)chunk * a.runs.R, cut0);
-  const int32_t x1 = boundary<MODE>(a.runs, ((int64_t)chunk + 1) * a.runs.R, cut1);
-  const int len = x1 - x0;   // at most 2 R - 1 <= 63
-  // lane j describes sorted position x0 + j
-  // (values outside the batch or the table, which no order of this batch holds, are kept in bounds)
-  const int32_t mine = lane < len ? in_batch(a.runs, a.runs.pos[x0 + lane]) : 0;
-  const int32_t mkey = lane < len ? in_table(a.runs, a.runs.keys[x0 + lane]) : a.runs.V;
-  const uint64_t rows = __ballot(mkey < a.runs.V);   // the first ones: V sorts last
-  const uint64_t starts = __ballot(lane < len && run_starts<MODE>(a.runs, x0 + lane));
-  const int n = __popcll(rows);
+  const Chunk w = look_at<MODE>(a.runs, chunk);
+  const int off = w.x0 - w.at, len = w.x1 - w.x0;   // the chunk's first lane; at most 2 R - 1 rows
+  const bool mine = lane >= off && lane < off + len;
+  const int n = __popcll(__ballot(mine && w.key < a.runs.V));   // rows: the first ones, as V sorts last
+  const uint64_t starts = w.starts >> off;
   if (MODE == RUN_NORM) {
     // every position's value is written once: 0 unless it starts a run
-    if (lane < len && !(mkey < a.runs.V && ((starts >> lane) & 1))) a.val[(int64_t)slice * a.runs.N + mine] = 0.f;
+    if (mine && !(w.key < a.runs.V && ((w.starts >> lane) & 1))) a.val[(int64_t)slice * a.runs.N + w.pos] = 0.f;
   }
   if (n == 0) return;
   float wgt = 1.f;
-  if (MODE == RUN_GRAD) wgt = a.c && lane < n ? a.scale * a.c[sample_of(a.runs, mine)] : a.scale;
+  if (MODE == RUN_GRAD) wgt = a.c && mine ? a.scale * a.c[w.smp] : a.scale;
   float acc[R::kElems] = {};
   int first = 0;
   for (int j0 = 0; j0 < n; j0 += kRowsAhead) {
@@ -476,7 +536,7 @@ __global__ __launch_bounds__(256) void k_run_sums(RunArgs a) {
     for (int u = 0; u < kRowsAhead; ++u) {
       v[u] = make_uint4(0, 0, 0, 0);
       if (j0 + u < n && on) {
-        const int32_t q = __builtin_amdgcn_readlane(mine, j0 + u);
+        const int32_t q = __builtin_amdgcn_readlane(w.pos, off + j0 + u);
         v[u] = ldg16(a.G + ((int64_t)q * a.d + col) * R::kBytes);
       }
     }
@@ -484,13 +544,13 @@ __global__ __launch_bounds__(256) void k_run_sums(RunArgs a) {
     for (int u = 0; u < kRowsAhead; ++u) {
       const int j = j0 + u;
       if (j < n) {
-        float w = 1.f;
-        if (MODE == RUN_GRAD) w = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wgt), j));
-        R::add(acc, v[u], w);
+        float c = 1.f;
+        if (MODE == RUN_GRAD) c = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wgt), off + j));
+        R::add(acc, v[u], c);
         // the run ends here, or the chunk does
         if (j + 1 == n || ((starts >> (j + 1)) & 1)) {
-          const bool head = first == 0 && cut0;                 // started before the chunk
-          const bool tail = j + 1 == len && cut1;               // goes on after it
+          const bool head = first == 0 && w.cut0;                 // started before the chunk
+          const bool tail = j + 1 == len && w.cut1;               // goes on after it
           if (head || tail) {
             if (on) put_part<BF16>(a, chunk, head ? 0 : 1, col, acc);
           } else if (MODE == RUN_NORM) {
@@ -498,9 +558,9 @@ __global__ __launch_bounds__(256) void k_run_sums(RunArgs a) {
 #pragma unroll
             for (int e = 0; e < R::kElems; ++e) s = fmaf(acc[e], acc[e], s);
             s = wave_sum_f32(s);
-            if (lane == 0) a.val[(int64_t)slice * a.runs.N + __builtin_amdgcn_readlane(mine, first)] = s;
+            if (lane == 0) a.val[(int64_t)slice * a.runs.N + __builtin_amdgcn_readlane(w.pos, off + first)] = s;
           } else if (on) {
-            put_row<BF16>(a, __builtin_amdgcn_readlane(mkey, first), col, acc);
+            put_row<BF16>(a, __builtin_amdgcn_readlane(w.key, off + first), col, acc);
           }
           first = j + 1;
 #pragma unroll
@@ -521,18 +581,16 @@ __global__ __launch_bounds__(256) void k_run_join(RunArgs a) {
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
   const int32_t chunk = (int32_t)(blockIdx.x / a.slices);
   const int slice = (int)(blockIdx.x % a.slices);
-  bool cut0, cut1;
-  const int64_t x = ((int64_t)chunk + 1) * a.runs.R;
-  boundary<MODE>(a.runs, x, cut1);
-  if (!cut1) return;
-  const int32_t x0 = boundary<MODE>(a.runs, (int64_t)chunk * a.runs.R, cut0);
-  // the run at x started in this chunk unless the chunk holds it whole, cut on both sides
-  const uint64_t inner = __ballot(lane < x - x0 && run_starts<MODE>(a.runs, x0 + lane));
+  const Chunk w = look_at<MODE>(a.runs, chunk);
+  if (!w.cut1) return;
+  // the run at x1 started in this chunk unless the chunk holds it whole, cut on both sides
+  const int off = w.x0 - w.at;
+  const uint64_t inner = (w.starts >> off) & ((1ull << (w.x1 - w.x0)) - 1);
   if (inner == 0) return;
-  const int32_t s = x0 + 63 - __builtin_clzll(inner);
-  const int32_t key = in_table(a.runs, a.runs.keys[s]);
+  const int s = off + 63 - __builtin_clzll(inner);   // its first lane
+  const int32_t key = __builtin_amdgcn_readlane(w.key, s), pos = __builtin_amdgcn_readlane(w.pos, s);
   if (key >= a.runs.V) return;
-  const int32_t e = run_end<MODE>(a.runs, (int32_t)x);
+  const int32_t e = run_end<MODE>(a.runs, w.x1);
   const int32_t last = min(e / a.runs.R, a.runs.chunks) - 1;   // the last boundary with R positions of the run behind it
   const int col = slice * R::kSlice + lane * R::kElems;
   const bool on = col < a.d;
@@ -573,7 +631,7 @@ __global__ __launch_bounds__(256) void k_run_join(RunArgs a) {
 #pragma unroll
     for (int j = 0; j < R::kElems; ++j) t = fmaf(acc[j], acc[j], t);
     t = wave_sum_f32(t);
-    if (lane == 0) a.val[(int64_t)slice * a.runs.N + in_batch(a.runs, a.runs.pos[s])] = t;
+    if (lane == 0) a.val[(int64_t)slice * a.runs.N + pos] = t;
   } else if (on) {
     put_row<BF16>(a, key, col, acc);
   }
@@ -585,14 +643,17 @@ __global__ __launch_bounds__(1024) void k_norm_sum(const float* val, int64_t N, 
   __shared__ double part[16];
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
   double s = 0.0;
-  for (int sl = 0; sl < slices; ++sl) {
-    const float* p = val + (int64_t)sl * N + (int64_t)blockIdx.x * T;
-    for (int t = threadIdx.x; t < T; t += 8 * 1024) {
-      float x[8];
+  const float* p = val + (int64_t)blockIdx.x * T;
+  for (int s0 = 0; s0 < slices; s0 += 4) {
+    for (int t = threadIdx.x; t < T; t += 4 * 1024) {   // (16 loads in flight)
+      float x[16];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) x[u] = t + u * 1024 < T ? p[t + u * 1024] : 0.f;
+      for (int u = 0; u < 16; ++u) {
+        const int sl = s0 + (u >> 2), tt = t + (u & 3) * 1024;
+        x[u] = sl < slices && tt < T ? p[sl * N + tt] : 0.f;
+      }
 #pragma unroll
-      for (int u = 0; u < 8; ++u) s += (double)x[u];
+      for (int u = 0; u < 16; ++u) s += (double)x[u];
     }
   }
   s = wave_sum(s);
