@@ -319,7 +319,7 @@ dpnorm_status dpnorm_embed_lookup(const void* tok, dpnorm_index it, const void* 
                                   int64_t V, int64_t d, float scale, void* out, hipStream_t stream);
 
 /* The order of a batch's ids, which the two calls below read: the positions
- * i T + t sorted by id, equal ids in position order, positions whose id is
+ * i T + t grouped by id, equal ids in position order, positions whose id is
  * outside [0, V) last. `order` (256-byte aligned, at least order_bytes) is
  * the caller's and may serve any number of calls on the same tok, B, T and V;
  * passing it with another B, T or V gives undefined values. ws is scratch of

@@ -515,7 +515,7 @@ def embed_lookup(tokens: torch.Tensor, W: torch.Tensor, scale: float = 1.0,
 
 
 class EmbedOrder:
-    """The sorted order of a batch's ids [B][T] for a table of V rows
+    """The order of a batch's ids [B][T] for a table of V rows
     (dpnorm_embed_order), read by embed_norm and embed_grad. It describes the
     ids at the time of the call that made it."""
 
@@ -524,7 +524,7 @@ class EmbedOrder:
 
 
 def embed_order(tokens: torch.Tensor, V: int) -> EmbedOrder:
-    """Sorts the positions of tokens [B][T] by id, for any number of
+    """Groups the positions of tokens [B][T] by id, for any number of
     embed_norm and embed_grad calls on the same ids."""
     it = _index(tokens, "tokens")
     if tokens.dim() != 2:

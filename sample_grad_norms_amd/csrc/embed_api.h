@@ -12,11 +12,13 @@ struct EmbedPlan {
   int slices = 0, R = 0;
   int64_t chunks = 0;
   // order
-  int passes = 0, bits = 0, blocks = 0, per = 0;
-  size_t off_pos = 0, order_bytes = 0, off_key2 = 0, off_pos2 = 0, off_hist = 0, order_ws = 0;
+  bool scan = false;   // in one launch
+  int id_bits = 0, passes = 0, bits = 0, blocks = 0, per = 0;
+  size_t off_pos = 0, off_start = 0, order_bytes = 0, off_key2 = 0, off_pos2 = 0, off_hist = 0, order_ws = 0;
   // run sums: the order and its scratch where the call makes it, then the calls' own
   bool small_norm = false, small_grad = false;
-  size_t off_order = 0, off_order_ws = 0, off_val = 0, off_part = 0, norm_ws = 0, off_part_grad = 0, grad_ws = 0;
+  int sum_blocks = 1;  // of a sample
+  size_t off_order = 0, off_order_ws = 0, off_val = 0, off_parts = 0, off_arrived = 0, off_part = 0, norm_ws = 0, off_part_grad = 0, grad_ws = 0;
 };
 
 dpnorm_status check_ids(int64_t B, int64_t T, int64_t V) {
@@ -36,19 +38,22 @@ void plan_order(EmbedPlan& pl, int64_t B, int64_t T, int64_t V) {
   pl.N = (int32_t)(B * T);
   pl.T = (int32_t)T;
   pl.V = (int32_t)V;
-  int bits = 1;
-  while (((int64_t)1 << bits) <= V) ++bits;   // keys 0 .. V
-  pl.passes = (bits + 8) / 9;
-  pl.bits = (bits + pl.passes - 1) / pl.passes;
+  pl.id_bits = 1;
+  while (((int64_t)1 << pl.id_bits) < V) ++pl.id_bits;
+  pl.scan = pl.N <= embed::kScanMost && pl.id_bits <= embed::kScanBits;
+  // radix passes of at most 9 bits over id_bits + 1 (the positions without a row)
+  pl.passes = (pl.id_bits + 9) / 9;
+  pl.bits = (pl.id_bits + pl.passes) / pl.passes;
   // a block for every 1024 positions, up to the 64 whose counts one thread adds up
   pl.blocks = (int)std::min<int64_t>(embed::kMaxSortBlocks, (pl.N + 1023) / 1024);
   pl.per = (pl.N + pl.blocks - 1) / pl.blocks;
   Bump o;
   o.take((size_t)pl.N * 4);
   pl.off_pos = o.take((size_t)pl.N * 4);
+  pl.off_start = o.take((((size_t)1 << embed::kBucketBits) + 1) * 4);
   pl.order_bytes = align_up(o.off);
   Bump w;
-  if (pl.N > embed::kSmallSort) {
+  if (!pl.scan) {
     pl.off_key2 = w.take((size_t)pl.N * 4);
     pl.off_pos2 = w.take((size_t)pl.N * 4);
     pl.off_hist = w.take((size_t)pl.blocks * ((size_t)4 << pl.bits));
@@ -78,6 +83,13 @@ void plan_runs(EmbedPlan& pl, dpnorm_dtype dt, int64_t d, bool ordered) {
     }
     pl.off_val = n.take((size_t)pl.slices * (size_t)pl.N * 4);
     pl.off_part = n.take((size_t)pl.chunks * 2 * (size_t)d * 4);
+    // blocks of at least 4096 values, where a sample has many
+    pl.sum_blocks = (int)std::min<int64_t>(16, std::max<int64_t>(1, (int64_t)pl.T * pl.slices / 4096));
+    if (pl.sum_blocks > 1) {
+      const size_t samples = (size_t)(pl.N / pl.T);
+      pl.off_parts = n.take(samples * pl.sum_blocks * 8);
+      pl.off_arrived = n.take(samples * 4);
+    }
   }
   pl.norm_ws = align_up(n.off);
   Bump g;
@@ -103,8 +115,13 @@ hipError_t launch_order(const EmbedPlan& pl, const void* tok, dpnorm_index it, v
   const int i64 = it == DPNORM_I64;
   int32_t* keys = (int32_t*)order;
   int32_t* pos = (int32_t*)((char*)order + pl.off_pos);
-  if (pl.N <= embed::kSmallSort) {
-    embed::k_order_small<<<1, embed::kSortThreads, 0, stream>>>(tok, i64, pl.N, pl.V, pl.passes, pl.bits, keys, pos);
+  if (pl.scan) {
+    const uint32_t buckets = 1u << std::min(pl.id_bits, embed::kBucketBits);
+    // the factor's inverse modulo 2^32 (each step doubles the bits that are right)
+    uint32_t inverse = 1;
+    for (int i = 0; i < 5; ++i) inverse *= 2u - embed::mix_factor(pl.id_bits) * inverse;
+    embed::k_order_scan<<<buckets, embed::kSortThreads, 0, stream>>>(tok, i64, pl.N, pl.V, pl.id_bits, inverse, keys, pos,
+                                                                    (int32_t*)((char*)order + pl.off_start));
     return hipGetLastError();
   }
   int32_t* key2 = (int32_t*)((char*)ws + pl.off_key2);
@@ -115,9 +132,9 @@ hipError_t launch_order(const EmbedPlan& pl, const void* tok, dpnorm_index it, v
     // the last pass writes the order; the ones before it alternate
     const bool to_order = (pl.passes - 1 - p) % 2 == 0;
     int32_t *dk = to_order ? keys : key2, *dp = to_order ? pos : pos2;
-    embed::k_order_count<<<pl.blocks, embed::kSortThreads, 0, stream>>>(tok, i64, sk, pl.N, pl.V, p * pl.bits, pl.bits, pl.per,
+    embed::k_order_count<<<pl.blocks, embed::kSortThreads, 0, stream>>>(tok, i64, sk, pl.N, pl.V, pl.id_bits, p * pl.bits, pl.bits, pl.per,
                                                                        hist);
-    embed::k_order_scatter<<<pl.blocks, embed::kSortThreads, 0, stream>>>(tok, i64, sk, sp, pl.N, pl.V, p * pl.bits, pl.bits,
+    embed::k_order_scatter<<<pl.blocks, embed::kSortThreads, 0, stream>>>(tok, i64, sk, sp, pl.N, pl.V, pl.id_bits, p * pl.bits, pl.bits,
                                                                          pl.per, hist, dk, dp);
     sk = dk;
     sp = dp;
@@ -129,6 +146,8 @@ embed::RunArgs run_args(const EmbedPlan& pl, const void* order, const void* G) {
   embed::RunArgs a{};
   a.runs.keys = (const int32_t*)order;
   a.runs.pos = order ? (const int32_t*)((const char*)order + pl.off_pos) : nullptr;   // (none: a small gradient)
+  a.runs.start = order && pl.scan ? (const int32_t*)((const char*)order + pl.off_start) : nullptr;
+  a.runs.bits = pl.id_bits;
   a.runs.N = pl.N;
   a.runs.T = pl.T;
   a.runs.V = pl.V;
@@ -279,9 +298,13 @@ dpnorm_status dpnorm_embed_norm(const void* tok, dpnorm_index it, const void* or
   embed::RunArgs a = run_args(pl, order, G);
   a.val = (float*)(base + pl.off_val);
   a.part = (float*)(base + pl.off_part);
+  double* parts = pl.sum_blocks > 1 ? (double*)(base + pl.off_parts) : nullptr;
+  a.arrived = pl.sum_blocks > 1 ? (uint32_t*)(base + pl.off_arrived) : nullptr;
   if (he == hipSuccess) he = launch_runs<embed::RUN_NORM>(a, bf16, stream);
   if (he == hipSuccess) {
-    embed::k_norm_sum<<<(uint32_t)B, 1024, 0, stream>>>(a.val, pl.N, pl.T, pl.slices, scale2, n, accumulate);
+    const int64_t y = std::min<int64_t>(B, 65535);
+    const dim3 grid((uint32_t)pl.sum_blocks, (uint32_t)y, (uint32_t)((B + y - 1) / y));
+    embed::k_norm_sum<<<grid, 1024, 0, stream>>>(a.val, pl.N, pl.T, pl.slices, scale2, n, accumulate, parts, a.arrived);
     he = hipGetLastError();
   }
   return hip_status(he);

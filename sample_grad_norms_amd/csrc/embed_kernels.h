@@ -19,14 +19,24 @@ namespace dpn {
 namespace embed {
 
 // ---------------------------------------------------------------------------
-// Order: a stable sort of the positions by key (least significant digit first)
+// Order: the positions grouped by id, each group in position order. The groups
+// are sorted by a mixed id, which spreads neighbouring ids (the frequent ones of
+// a vocabulary) over the range; positions without a row come last.
 // ---------------------------------------------------------------------------
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / kWave;
-constexpr int kMaxDigits = 512;          // 9 bits a pass: two passes up to V = 2^18 - 1
-constexpr int kSmallSort = 8192;         // positions that one work group sorts alone
-constexpr int kSmallRounds = kSmallSort / kSortThreads;
+constexpr int kMaxDigits = 1024;
+constexpr int kBucketBits = 8;
+constexpr int kScanMost = 24 * kSortThreads;                 // positions of an order made in one launch
+constexpr int kScanBits = kBucketBits + 10;                  // id bits of an order made in one launch
 constexpr int kMaxSortBlocks = 64;
+
+// Ids below 2^bits mixed one to one: a product with an odd number near 2^bits
+// over the golden ratio, modulo 2^bits. Positions without a row get 2^bits.
+__host__ __device__ __forceinline__ uint32_t mix_factor(int bits) { return (0x9e3779b1u >> (32 - bits)) | 1u; }
+__device__ __forceinline__ uint32_t mixed(int32_t id, int32_t V, int bits) {
+  return id < V ? ((uint32_t)id * mix_factor(bits)) & ((1u << bits) - 1u) : 1u << bits;
+}
 
 struct SortShared {
   uint32_t cnt[kSortWaves][kMaxDigits];
@@ -108,68 +118,130 @@ __device__ __forceinline__ uint32_t scan_block(SortShared& sh, uint32_t v) {
   return before + inc - v;
 }
 
-// Up to kSmallSort positions: one work group, every pass through LDS. Each
-// wave keeps a contiguous segment, so waves in order are positions in order.
-__global__ __launch_bounds__(kSortThreads) void k_order_small(const void* tok, int idx64, int32_t N, int32_t V, int passes,
-                                                              int bits, int32_t* keys, int32_t* pos) {
-  __shared__ SortShared sh;
-  __shared__ int32_t lkey[kSmallSort], lpos[kSmallSort];
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  const int rounds = (N + kSortThreads - 1) / kSortThreads;
-  const int seg0 = wv * rounds * kWave;
-  const int digits = 1 << bits;
-  int32_t key[kSmallRounds], ps[kSmallRounds];
+// An order in one launch: every block reads all ids, counts those of the buckets
+// before its own (the leading bits of the mixed id), and sorts those of its own
+// by the remaining bits; the last block places the positions without a row too.
+// A bucket holds one part in 256 of the distinct ids, so that reading and mixing
+// the ids is most of the work. A wave gathers its matches in LDS and ranks them 64
+// at a time.
+constexpr int kAhead = 8;                          // rounds whose ids a wave loads together
+constexpr int kPending = (kAhead + 2) * kWave;     // matches that a wave holds
+
+// A wave's segment of the positions, walked in order: seen(mixed id) for every
+// position (2^bits: no row, all ones: none), take(mixed id, position, lanes) for the
+// matches of bucket b, 64 at a time. Returns the number of matches where pend still
+// holds all of them, else -1.
+template <typename S, typename F>
+__device__ __forceinline__ int walk(const void* tok, int idx64, int32_t N, int32_t V, int bits, int rem, uint32_t b, int seg0,
+                                    int rounds, uint2 (&pend)[kPending], S seen, F take) {
+  const int lane = threadIdx.x & 63;
+  int n = 0;
+  bool whole = true;
+  for (int r0 = 0; r0 < rounds; r0 += kAhead) {
+    if (n > kPending - kAhead * kWave) {   // rank what does not leave room for the next rounds
+      int at = 0;
+      for (; at + 64 <= n; at += 64) take(pend[at + lane].x, pend[at + lane].y, 64);
+      const uint2 x = pend[min(at + lane, kPending - 1)];
+      __builtin_amdgcn_wave_barrier();
+      pend[lane] = x;
+      n -= at;
+      whole = false;
+    }
+    uint32_t h[kAhead];
 #pragma unroll
-  for (int r = 0; r < kSmallRounds; ++r) {
-    const int q = seg0 + r * kWave + lane;
-    const bool in = r < rounds && q < N;
-    key[r] = in ? id_key(tok, idx64, q, V) : 0;
-    ps[r] = q;
+    for (int u = 0; u < kAhead; ++u) {
+      const int q = seg0 + (r0 + u) * kWave + lane;
+      h[u] = r0 + u < rounds && q < N ? mixed(id_key(tok, idx64, q, V), V, bits) : ~0u;
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      seen(h[u], seg0 + (r0 + u) * kWave + lane);
+      const bool match = h[u] >> rem == b;
+      const uint64_t m = __ballot(match);
+      if (match) pend[n + __popcll(m & ((1ull << lane) - 1ull))] = make_uint2(h[u], (uint32_t)(seg0 + (r0 + u) * kWave + lane));
+      n += __popcll(m);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
   }
-  for (int p = 0; p < passes; ++p) {
-    zero_counts(sh, bits);
-    uint32_t rank[kSmallRounds];
-#pragma unroll
-    for (int r = 0; r < kSmallRounds; ++r) {
-      if (r < rounds)
-        rank[r] = count_round(sh.cnt[wv], ((uint32_t)key[r] >> (p * bits)) & (digits - 1), bits,
-                              seg0 + r * kWave + lane < N);
-    }
-    const uint32_t total = scan_waves(sh, digits);
-    const uint32_t base = scan_block(sh, total);
-    if ((int)threadIdx.x < digits) sh.base[threadIdx.x] = base;
-    __syncthreads();
-#pragma unroll
-    for (int r = 0; r < kSmallRounds; ++r) {
-      const int q = seg0 + r * kWave + lane;
-      if (r < rounds && q < N) {
-        const uint32_t dg = ((uint32_t)key[r] >> (p * bits)) & (digits - 1);
-        const uint32_t to = sh.base[dg] + sh.cnt[wv][dg] + rank[r];
-        lkey[to] = key[r];
-        lpos[to] = ps[r];
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int r = 0; r < kSmallRounds; ++r) {
-      const int q = seg0 + r * kWave + lane;
-      if (r < rounds && q < N) {
-        key[r] = lkey[q];
-        ps[r] = lpos[q];
-      }
-    }
+  for (int at = 0; at < n; at += 64) {
+    const uint2 x = pend[min(at + lane, kPending - 1)];
+    take(x.x, x.y, min(64, n - at));
   }
-#pragma unroll
-  for (int r = 0; r < kSmallRounds; ++r) {
-    const int q = seg0 + r * kWave + lane;
-    if (r < rounds && q < N) {
-      keys[q] = key[r];
-      pos[q] = ps[r];
-    }
-  }
+  return whole ? n : -1;
 }
 
-// Larger batches, one pass over `per` positions a block: digit counts of every
+__global__ __launch_bounds__(kSortThreads) void k_order_scan(const void* tok, int idx64, int32_t N, int32_t V, int bits,
+                                                             uint32_t inverse, int32_t* keys, int32_t* pos, int32_t* start) {
+  __shared__ SortShared sh;
+  __shared__ uint2 pend[kSortWaves][kPending];
+  __shared__ uint32_t below[kSortWaves], none[kSortWaves];
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t b = blockIdx.x;
+  const bool last = b + 1 == gridDim.x;
+  const int rem = bits > kBucketBits ? bits - kBucketBits : 0, digits = 1 << rem;
+  const int rounds = (N + kSortThreads - 1) / kSortThreads;
+  const int seg0 = wv * rounds * kWave;   // a contiguous segment a wave, so waves in order are positions in order
+  zero_counts(sh, rem);
+  uint32_t less = 0, without = 0;
+  const int held = walk(tok, idx64, N, V, bits, rem, b, seg0, rounds, pend[wv],
+                        [&](uint32_t h, int) {
+                          less += h >> rem < b ? 1u : 0u;
+                          without += h == 1u << bits ? 1u : 0u;
+                        },
+                        [&](uint32_t x, uint32_t, int n) { count_round(sh.cnt[wv], x & (digits - 1), rem, lane < n); });
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) {
+    less += __shfl_xor(less, o);
+    without += __shfl_xor(without, o);
+  }
+  if (lane == 0) below[wv] = less, none[wv] = without;
+  const uint32_t total = scan_waves(sh, digits);
+  const uint32_t before = scan_block(sh, total);
+  uint32_t offset = 0, ended = 0, tail = 0;   // positions below the bucket; without a row, in all and of the waves before
+#pragma unroll
+  for (int w = 0; w < kSortWaves; ++w) {
+    offset += below[w];
+    ended += none[w];
+    tail += w < wv ? none[w] : 0u;
+  }
+  if ((int)threadIdx.x < digits) sh.base[threadIdx.x] = offset + before;
+  if (threadIdx.x == 0) start[b] = (int32_t)offset;
+  if (last && threadIdx.x == 0) start[b + 1] = N - (int32_t)ended;
+  __syncthreads();
+  tail += (uint32_t)N - ended;
+  const auto place = [&](uint32_t x, uint32_t q, int n) {
+    const uint32_t dg = x & (digits - 1);
+    const uint32_t rank = count_round(sh.cnt[wv], dg, rem, lane < n);
+    if (lane < n) {
+      const uint32_t to = sh.base[dg] + rank;
+      keys[to] = (int32_t)((x * inverse) & ((1u << bits) - 1u));
+      pos[to] = (int32_t)q;
+    }
+  };
+  if (held >= 0 && !(last && ended > 0)) {
+    for (int at = 0; at < held; at += 64) {
+      const uint2 x = pend[wv][min(at + lane, kPending - 1)];
+      place(x.x, x.y, min(64, held - at));
+    }
+    return;
+  }
+  walk(tok, idx64, N, V, bits, rem, b, seg0, rounds, pend[wv],
+       [&](uint32_t h, int q) {
+         if (!last) return;
+         const bool mine = h == 1u << bits;
+         const uint64_t m = __ballot(mine);
+         if (mine) {
+           const uint32_t to = tail + (uint32_t)__popcll(m & ((1ull << lane) - 1ull));
+           keys[to] = V;
+           pos[to] = q;
+         }
+         tail += (uint32_t)__popcll(m);
+       },
+       place);
+}
+
+// Larger batches and tables: radix passes over the mixed ids, `per` positions a block: digit counts of every
 // block first (hist[digit][block]), then the stable scatter. src_keys is null
 // in the first pass, which reads the ids.
 __device__ __forceinline__ int32_t load_key(const void* tok, int idx64, const int32_t* src_keys, int64_t q, int32_t V) {
@@ -177,14 +249,15 @@ __device__ __forceinline__ int32_t load_key(const void* tok, int idx64, const in
 }
 
 __global__ __launch_bounds__(kSortThreads) void k_order_count(const void* tok, int idx64, const int32_t* src_keys, int32_t N,
-                                                              int32_t V, int shift, int bits, int per, uint32_t* hist) {
+                                                              int32_t V, int id_bits, int shift, int bits, int per,
+                                                              uint32_t* hist) {
   __shared__ uint32_t cnt[kMaxDigits];
   const int digits = 1 << bits;
   for (int j = threadIdx.x; j < digits; j += kSortThreads) cnt[j] = 0;
   __syncthreads();
   const int64_t lo = (int64_t)blockIdx.x * per, hi = lo + per < N ? lo + per : N;
   for (int64_t q = lo + threadIdx.x; q < hi; q += kSortThreads)
-    atomicAdd(&cnt[((uint32_t)load_key(tok, idx64, src_keys, q, V) >> shift) & (digits - 1)], 1u);
+    atomicAdd(&cnt[(mixed(load_key(tok, idx64, src_keys, q, V), V, id_bits) >> shift) & (digits - 1)], 1u);
   __syncthreads();
   for (int j = threadIdx.x; j < digits; j += kSortThreads) hist[(int64_t)j * gridDim.x + blockIdx.x] = cnt[j];
 }
@@ -192,8 +265,8 @@ __global__ __launch_bounds__(kSortThreads) void k_order_count(const void* tok, i
 constexpr int kHeldRounds = 4;   // rounds of a wave whose keys stay in registers between the two walks
 
 __global__ __launch_bounds__(kSortThreads) void k_order_scatter(const void* tok, int idx64, const int32_t* src_keys,
-                                                                const int32_t* src_pos, int32_t N, int32_t V, int shift,
-                                                                int bits, int per, const uint32_t* hist, int32_t* keys,
+                                                                const int32_t* src_pos, int32_t N, int32_t V, int id_bits,
+                                                                int shift, int bits, int per, const uint32_t* hist, int32_t* keys,
                                                                 int32_t* pos) {
   __shared__ SortShared sh;
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
@@ -234,14 +307,14 @@ __global__ __launch_bounds__(kSortThreads) void k_order_scatter(const void* tok,
 #pragma unroll
     for (int r = 0; r < kHeldRounds; ++r) {
       if (wlo + r * kWave < whi)
-        rank[r] = count_round(sh.cnt[wv], ((uint32_t)key[r] >> shift) & (digits - 1), bits, wlo + r * kWave + lane < whi);
+        rank[r] = count_round(sh.cnt[wv], (mixed(key[r], V, id_bits) >> shift) & (digits - 1), bits, wlo + r * kWave + lane < whi);
     }
     scan_waves(sh, digits);
     __syncthreads();
 #pragma unroll
     for (int r = 0; r < kHeldRounds; ++r) {
       if (wlo + r * kWave + lane < whi) {
-        const uint32_t dg = ((uint32_t)key[r] >> shift) & (digits - 1);
+        const uint32_t dg = (mixed(key[r], V, id_bits) >> shift) & (digits - 1);
         const uint32_t to = sh.base[dg] + sh.cnt[wv][dg] + rank[r];
         keys[to] = key[r];
         pos[to] = ps[r];
@@ -252,7 +325,7 @@ __global__ __launch_bounds__(kSortThreads) void k_order_scatter(const void* tok,
   for (int64_t q0 = wlo; q0 < whi; q0 += kWave) {
     const int64_t q = q0 + lane;
     const bool in = q < whi;
-    const uint32_t dg = in ? ((uint32_t)load_key(tok, idx64, src_keys, q, V) >> shift) & (digits - 1) : 0;
+    const uint32_t dg = in ? (mixed(load_key(tok, idx64, src_keys, q, V), V, id_bits) >> shift) & (digits - 1) : 0;
     count_round(sh.cnt[wv], dg, bits, in);
   }
   scan_waves(sh, digits);
@@ -262,7 +335,7 @@ __global__ __launch_bounds__(kSortThreads) void k_order_scatter(const void* tok,
     const int64_t q = q0 + lane;
     const bool in = q < whi;
     const int32_t k = in ? load_key(tok, idx64, src_keys, q, V) : 0;
-    const uint32_t dg = ((uint32_t)k >> shift) & (digits - 1);
+    const uint32_t dg = (mixed(k, V, id_bits) >> shift) & (digits - 1);
     const uint32_t rank = count_round(sh.cnt[wv], dg, bits, in);
     if (in) {
       const uint32_t to = sh.base[dg] + rank;
@@ -353,8 +426,10 @@ __global__ __launch_bounds__(256) void k_lookup(const void* tok, int idx64, cons
 // Runs are of equal (id, sample) for the norm and of equal id for the gradient.
 // ---------------------------------------------------------------------------
 struct Runs {
-  const int32_t* keys;   // sorted, V for positions without a row
+  const int32_t* keys;   // grouped by id, V for positions without a row last
   const int32_t* pos;
+  const int32_t* start;  // first position of each bucket, or null
+  int bits;              // of the mixed ids
   int32_t N, T, V;
   double per;            // 1 / T
   int R;                 // at most 16, so that a wave's lanes see both ends of a chunk
@@ -426,18 +501,25 @@ __device__ __forceinline__ int32_t run_end(const Runs& a, int32_t j) {
   return (int32_t)hi;
 }
 
-// First sorted position whose key is at least v: a search by all 64 lanes.
-__device__ __forceinline__ int32_t lower_bound(const Runs& a, int64_t v) {
-  const int lane = __lane_id();
-  int64_t lo = -1, hi = a.N;   // position lo is below v, hi is not
-  while (hi - lo > 1) {
-    const int64_t step = (hi - lo + 63) / 64;
-    const int64_t p = lo + step * (lane + 1);
-    const int cnt = __popcll(__ballot(p < hi && a.keys[p] < v));
-    lo += step * cnt;
-    hi = min(hi, lo + step);
+// Whether id v occurs: a search in its bucket, or in the whole order.
+__device__ __forceinline__ bool occurs(const Runs& a, int32_t v) {
+  const uint32_t h = mixed(v, a.V, a.bits);
+  int32_t lo = 0, hi = a.N;
+  if (a.start) {
+    const uint32_t b = h >> (a.bits > kBucketBits ? a.bits - kBucketBits : 0);
+    lo = a.start[b];
+    hi = a.start[b + 1];
   }
-  return (int32_t)hi;
+  lo = max(lo, 0);
+  hi = min(hi, a.N);
+  while (lo < hi) {
+    const int32_t mid = lo + (hi - lo) / 2;
+    const int32_t key = a.keys[mid];
+    if (key == v) return true;
+    if (mixed(key, a.V, a.bits) < h) lo = mid + 1;
+    else hi = mid;
+  }
+  return false;
 }
 
 struct RunArgs {
@@ -450,6 +532,7 @@ struct RunArgs {
   float* part;          // [chunks][2][d]: pieces of runs that started before the chunk / that go on after it
   int32_t d, slices;
   int accumulate;       // grad: add to the table's touched rows
+  uint32_t* arrived;    // norm: counters to reset for the sum, or null
   int64_t items;        // chunks x slices
   int64_t fill_blocks;  // grad: blocks behind the items' that clear rows without an id
 };
@@ -488,25 +571,17 @@ __global__ __launch_bounds__(256) void k_run_sums(RunArgs a) {
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
   const int64_t item_blocks = (a.items + 3) / 4;
   if (MODE == RUN_GRAD && (int64_t)blockIdx.x >= item_blocks) {
-    // clear the rows of ids that do not occur: lane r looks for row v0 + r, among
-    // the keys from v0 to v0 + 63, found by the whole wave
+    // clear the rows of ids that do not occur: lane r looks for row v0 + r
     const int64_t v0 = ((int64_t)blockIdx.x - item_blocks) * kFillRows;
     const int64_t v = v0 + lane;
-    int32_t lo = lower_bound(a.runs, v0), hi = lower_bound(a.runs, v0 + kFillRows);
-    const int32_t end = hi;
-    while (lo < hi) {
-      const int32_t mid = lo + (hi - lo) / 2;
-      if (a.runs.keys[mid] < v) lo = mid + 1;
-      else hi = mid;
-    }
-    const bool absent = v < a.runs.V && !(lo < end && a.runs.keys[lo] == v);
+    const bool absent = v < a.runs.V && !occurs(a.runs, (int32_t)v);
     uint64_t m = __ballot(absent);
     for (int j = 0; m; ++j) {
       const int r = __builtin_ctzll(m);
       m &= m - 1;
       if ((j & 3) != wv) continue;   // the block's waves take rows in turn
       char* p = a.out + (v0 + r) * a.d * R::kBytes;
-      for (int col = lane * R::kElems; col < a.d; col += R::kSlice) stg16(p + (int64_t)col * R::kBytes, make_uint4(0, 0, 0, 0));
+      for (int col = lane * R::kElems; col < a.d; col += R::kSlice) __builtin_nontemporal_store(u32x4_t{0, 0, 0, 0}, (DPN_GLOBAL u32x4_t*)(p + (int64_t)col * R::kBytes));
     }
     return;
   }
@@ -516,6 +591,9 @@ __global__ __launch_bounds__(256) void k_run_sums(RunArgs a) {
   const int slice = (int)(item % a.slices);
   const int col = slice * R::kSlice + lane * R::kElems;
   const bool on = col < a.d;
+  if (MODE == RUN_NORM && a.arrived && slice == 0 && lane == 0) {
+    for (int64_t i = chunk; i * a.runs.T < a.runs.N; i += a.runs.chunks) a.arrived[i] = 0;
+  }
   const Chunk w = look_at<MODE>(a.runs, chunk);
   const int off = w.x0 - w.at, len = w.x1 - w.x0;   // the chunk's first lane; at most 2 R - 1 rows
   const bool mine = lane >= off && lane < off + len;
@@ -637,20 +715,24 @@ __global__ __launch_bounds__(256) void k_run_join(RunArgs a) {
   }
 }
 
-// n_i (+)= s^2 times the sum of the sample's values, in fp64.
+// n_i (+)= s^2 times the sum of the sample's values, in fp64. Long samples are
+// summed by gridDim.x blocks; the last one to arrive adds their parts in order.
 __global__ __launch_bounds__(1024) void k_norm_sum(const float* val, int64_t N, int32_t T, int32_t slices, double scale2,
-                                                   float* n, int accumulate) {
+                                                   float* n, int accumulate, double* parts, uint32_t* arrived) {
   __shared__ double part[16];
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  const int64_t i = blockIdx.y + (int64_t)blockIdx.z * gridDim.y;
+  if (i * T >= N) return;
   double s = 0.0;
-  const float* p = val + (int64_t)blockIdx.x * T;
+  const float* p = val + i * T;
+  const int32_t per = (T + gridDim.x - 1) / gridDim.x, t0 = blockIdx.x * per, t1 = min(t0 + per, T);
   for (int s0 = 0; s0 < slices; s0 += 4) {
-    for (int t = threadIdx.x; t < T; t += 4 * 1024) {   // (16 loads in flight)
+    for (int t = t0 + threadIdx.x; t < t1; t += 4 * 1024) {   // (16 loads in flight)
       float x[16];
 #pragma unroll
       for (int u = 0; u < 16; ++u) {
         const int sl = s0 + (u >> 2), tt = t + (u & 3) * 1024;
-        x[u] = sl < slices && tt < T ? p[sl * N + tt] : 0.f;
+        x[u] = sl < slices && tt < t1 ? p[sl * N + tt] : 0.f;
       }
 #pragma unroll
       for (int u = 0; u < 16; ++u) s += (double)x[u];
@@ -659,13 +741,20 @@ __global__ __launch_bounds__(1024) void k_norm_sum(const float* val, int64_t N, 
   s = wave_sum(s);
   if (lane == 0) part[wv] = s;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    double t = 0.0;
+  if (threadIdx.x != 0) return;
+  double t = 0.0;
 #pragma unroll
-    for (int w = 0; w < 16; ++w) t += part[w];
-    t *= scale2;
-    n[blockIdx.x] = (float)(accumulate ? (double)n[blockIdx.x] + t : t);
+  for (int w = 0; w < 16; ++w) t += part[w];
+  if (gridDim.x > 1) {
+    double* mine = parts + i * gridDim.x;
+    __hip_atomic_store(mine + blockIdx.x, t, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const uint32_t order = __hip_atomic_fetch_add(arrived + i, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+    if (order != gridDim.x - 1) return;
+    t = 0.0;
+    for (uint32_t b = 0; b < gridDim.x; ++b) t += __hip_atomic_load(mine + b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
+  t *= scale2;
+  n[i] = (float)(accumulate ? (double)n[i] + t : t);
 }
 
 // ---------------------------------------------------------------------------

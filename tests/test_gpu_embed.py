@@ -78,8 +78,12 @@ CASES = [   # B, T, V, d, kind
     (3, 61, 40, 256, "padded"),
     (2, 700, 3, 520, "two"),
     (5, 333, 1000, 264, "zipf"),
-    (4, 2048, 50257, 64, "zipf"),       # the largest batch one work group sorts
-    (3, 3001, 300000, 72, "zipf"),      # several blocks, three passes
+    (4, 2048, 50257, 64, "zipf"),
+    (1, 24576, 262144, 8, "zipf"),      # the largest order made in one launch
+    (1, 24577, 5000, 8, "zipf"),        # one position more: radix passes
+    (3, 3001, 262145, 72, "zipf"),      # one table row more: radix passes
+    (1, 20000, 128, 8, "padded"),       # fewer ids than buckets
+    (2, 66000, 2, 8, "uniform"),        # more positions of a wave than stay in registers
     (2, 5000, 700, 40, "padded"),
     (1, 9001, 9, 48, "same"),
     (70, 150, 11, 24, "uniform"),
