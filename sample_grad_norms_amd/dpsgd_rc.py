@@ -27,9 +27,12 @@ Readings where the pages leave a step open:
     exist for tests only.
 
 Every norm estimate runs in libdpnorm on the GPU; torch runs the model and its
-two backward passes. Only bias-free nn.Linear weights are clipped (Llama has
-no biases). Refused, since part of a gradient would go unclipped: any other
-trainable parameter, and a linear weight that a module of another kind also
+two backward passes. The weights that are clipped are those of bias-free
+nn.Linear modules (Llama has no biases) and of layers.Embedding tables, whose
+per-sample norm is exact whatever the estimator is: row v of sample i's
+gradient is the sum of its output gradients at the positions of id v, so the
+norm costs one pass over the output gradients. Refused, since part of a gradient would go unclipped: any other
+trainable parameter, and a weight that a module of another kind also
 holds (a tied embedding). A use of a weight that the hooks cannot see (the
 weight passed to F.linear outside its module) is caught on the first step:
 the clipped gradient autograd accumulates must equal sum_i c_i G_i^T A_i
@@ -44,6 +47,7 @@ import torch
 from torch import nn
 
 import sample_grad_norms_amd as dp
+from sample_grad_norms_amd.layers import Embedding
 
 ProjectionFn = Callable[[int, int, torch.dtype, torch.device, torch.Generator], torch.Tensor]
 
@@ -57,7 +61,8 @@ def gaussian_projection(p: int, k: int, dtype: torch.dtype, device: torch.device
 
 
 class RandomizedClipping:
-    """Hooks a model's bias-free linear layers and runs the DP-SGD-RC step.
+    """Hooks a model's bias-free linear layers and embedding tables
+    (layers.Embedding) and runs the DP-SGD-RC step.
 
     Usage::
 
@@ -112,8 +117,9 @@ class RandomizedClipping:
         for m in self.modules:
             if m.bias is not None:
                 raise ValueError("linear layers with a bias are not supported (the clipped gradient would miss it)")
+        self.tables: List[Embedding] = [m for m in model.modules() if isinstance(m, Embedding)]
         covered = {id(m.weight) for m in self.modules}
-        # a linear weight that a module of another kind also holds (a tied
+        # a weight that a module of another kind also holds (a tied
         # embedding) gets gradient through that module, which no hook sees
         tied = [f"{name}.{pname}" if name else pname for name, mod in model.named_modules()
                 if not isinstance(mod, nn.Linear)
@@ -121,6 +127,14 @@ class RandomizedClipping:
         if tied:
             raise ValueError(f"linear weights shared with modules that are not linear layers would go partly "
                              f"unclipped: {tied}")
+        covered_tables = {id(m.weight) for m in self.tables}
+        shared = [f"{name}.{pname}" if name else pname for name, mod in model.named_modules()
+                  if not isinstance(mod, Embedding)
+                  for pname, p in mod.named_parameters(recurse=False) if id(p) in covered_tables]
+        if shared:
+            raise ValueError(f"embedding tables shared with modules that are not layers.Embedding would go partly "
+                             f"unclipped: {shared}")
+        covered |= covered_tables
         loose = [name for name, p in model.named_parameters(remove_duplicate=False)
                  if p.requires_grad and id(p) not in covered]
         if loose:
@@ -135,15 +149,20 @@ class RandomizedClipping:
                 if m.weight.requires_grad:
                     self.params.append(m.weight)
             self._users[id(m.weight)].append(m)
+        for t in self.tables:
+            if t.weight.requires_grad and all(p is not t.weight for p in self.params):
+                self.params.append(t.weight)
         self._names = {id(p): name for name, p in model.named_parameters()}
         self._capturing = False
-        self._rec: Dict[nn.Linear, List[Tuple[torch.Tensor, torch.Tensor]]] = {}
+        self._rec: Dict[nn.Module, List[Tuple[torch.Tensor, torch.Tensor]]] = {}
         self._gen: Optional[torch.Generator] = None
         self._noise_gen: Optional[torch.Generator] = None
         self._batch = 0
         self._verify = bool(verify_coverage)
         self._pending: Optional[List[Tuple[nn.Parameter, torch.Tensor, torch.Tensor]]] = None
-        self._handles = [m.register_forward_hook(self._hook) for m in self.modules]
+        # per table of the last step: (weight, order of its ids, output gradients, scale)
+        self._table_recs: List[Tuple[nn.Parameter, dp.EmbedOrder, torch.Tensor, float]] = []
+        self._handles = [m.register_forward_hook(self._hook) for m in [*self.modules, *self.tables]]
 
     # -- capture ---------------------------------------------------------
     def _hook(self, module, inputs, output):
@@ -200,6 +219,12 @@ class RandomizedClipping:
                 if not weights or all(id(w) != key for w, _ in weights):
                     weights.append((m.weight, [r for u in self._users[key] for r in self._rec.get(u, [])]))
         outputs = [o for _, recs in weights for (_, o) in recs]
+        # the uses of every table, by the scale of the look-up
+        looked = {}
+        for m in self.tables:
+            for r in self._rec.get(m, []):
+                looked.setdefault((id(m.weight), m.scale), (m, []))[1].append(r)
+        outputs += [o for _, recs in looked.values() for (_, o) in recs]
         grads = torch.autograd.grad(losses.sum(), outputs, retain_graph=True, allow_unused=True)
         layers, at, cast = [], 0, {}
         for w, recs in weights:
@@ -213,6 +238,22 @@ class RandomizedClipping:
             A = As[0] if len(As) == 1 else torch.cat(As, dim=1)
             G = Gs[0] if len(Gs) == 1 else torch.cat(Gs, dim=1)
             layers.append((A, G))
+        scales = [w for w, _ in looked]
+        split = [w for w in scales if scales.count(w) > 1]
+        if split:
+            raise ValueError("one embedding table looked up with two scales has no norm of its own: use one scale")
+        self._table_recs = []
+        for m, recs in looked.values():
+            toks, Gs = [], []
+            for (tok, out), g in zip(recs, grads[at:at + len(recs)]):
+                if g is None:
+                    g = torch.zeros_like(out)
+                toks.append(tok.detach().reshape(B, -1))
+                Gs.append(self._cast(g.detach().reshape(B, -1, g.shape[-1]), cast))
+            at += len(recs)
+            tok = toks[0] if len(toks) == 1 else torch.cat([t.long() for t in toks], dim=1)
+            G = Gs[0] if len(Gs) == 1 else torch.cat(Gs, dim=1)
+            self._table_recs.append((m.weight, dp.embed_order(tok.contiguous(), m.weight.shape[0]), G, m.scale))
         self._pending = [(w, A, G) for (w, _), (A, G) in zip(weights, layers)] if self._verify else None
         self._batch = B
         self._rec = {}
@@ -222,7 +263,7 @@ class RandomizedClipping:
         """Backward pass 1 and the norm path: returns (n, c), float32 [B]."""
         layers = self._collect(losses)
         B = losses.shape[0]
-        device = layers[0][0].device
+        device = layers[0][0].device if layers else self._table_recs[0][2].device
         gen = self._generator(device)
         n = torch.zeros(B, dtype=torch.float32, device=device)
         used = []
@@ -252,6 +293,8 @@ class RandomizedClipping:
                     P = self.projection(G.shape[2], m_t, A.dtype, device, gen)
                     dp.hutchpp(A, G, S, P, k=self.k, out=n, accumulate=True)
                     used.append((A, G, (S, P)))
+        for (_, order, G, scale) in self._table_recs:
+            dp.embed_norm(order, G, scale=scale, out=n, accumulate=True)
         c = dp.clip_factors(n, self.C)
         self.last_layers = used if self.keep_layers else []
         return n, c
@@ -268,12 +311,18 @@ class RandomizedClipping:
         """Backward pass 2: accumulates sum_i c_i grad l_i into the weights' .grad
         (on the first step, then checked against the recordings)."""
         pending, self._pending = self._pending, None
+        tables, self._table_recs = self._table_recs, []
         before = None
         if pending is not None:
-            before = [w.grad.detach().float().clone() if w.grad is not None else None for w, _, _ in pending]
+            before = [w.grad.detach().float().clone() if w.grad is not None else None
+                      for w in [w for w, _, _ in pending] + [w for w, _, _, _ in tables]]
         (c.detach().to(losses.dtype) * losses).sum().backward()
         if pending is not None:
             self._check_coverage(pending, before, c)
+            cw = c.detach().float()
+            for (w, order, G, scale), g0 in zip(tables, before[len(pending):]):
+                want = dp.embed_grad(order, G, scale=scale, weights=cw).float()
+                self._check_gradient(w, want, g0)
             self._verify = False
 
     def _check_coverage(self, pending, before, c: torch.Tensor) -> None:
@@ -285,17 +334,20 @@ class RandomizedClipping:
                 continue
             B, T, d = A.shape
             p = G.shape[2]
-            want = (G.float() * cw.view(B, 1, 1)).reshape(B * T, p).t() @ A.float().reshape(B * T, d)
-            got = torch.zeros_like(want) if w.grad is None else w.grad.detach().float()
-            if g0 is not None:
-                got = got - g0
-            scale = float(torch.linalg.vector_norm(want))
-            err = float(torch.linalg.vector_norm(got - want))
-            if err > 5e-2 * scale + 1e-30:
-                raise RuntimeError(
-                    f"the gradient of linear weight {self._names.get(id(w), '')} {list(w.shape)} differs from what its "
-                    f"recorded uses give (relative {err / max(scale, 1e-300):.2e}): it has a use the hooks do not "
-                    f"see (e.g. F.linear called with it outside its module), which would go unclipped")
+            self._check_gradient(w, (G.float() * cw.view(B, 1, 1)).reshape(B * T, p).t() @ A.float().reshape(B * T, d), g0)
+
+    def _check_gradient(self, w: nn.Parameter, want: torch.Tensor, g0: Optional[torch.Tensor]) -> None:
+        """The weight's gradient less what it held before (g0) against `want`."""
+        got = torch.zeros_like(want) if w.grad is None else w.grad.detach().float()
+        if g0 is not None:
+            got = got - g0
+        scale = float(torch.linalg.vector_norm(want))
+        err = float(torch.linalg.vector_norm(got - want))
+        if err > 5e-2 * scale + 1e-30:
+            raise RuntimeError(
+                f"the gradient of weight {self._names.get(id(w), '')} {list(w.shape)} differs from what its "
+                f"recorded uses give (relative {err / max(scale, 1e-300):.2e}): it has a use the hooks do not "
+                f"see (e.g. F.linear called with it outside its module), which would go unclipped")
 
     def add_noise(self) -> None:
         """Adds sigma C N(0, I) to each clipped gradient sum and divides by B."""

@@ -16,6 +16,8 @@ NAME is one of:
   dpsgd_step          DP-SGD-RC training steps on a random-init Llama-width stack
                       (2 decoder layers, B=4, T=2048, bf16): forward, backward 1,
                       the norm path, backward 2 of sum c_i l_i, noise, Adam
+  dpsgd_step_tokens   the same from token ids, with the library's embedding table
+                      (32768 rows, trained) and attention
 --calib-copy first runs one 1 GiB device-to-device copy, the reference the
 counter summaries scale FETCH_SIZE and WRITE_SIZE by.
 """
@@ -30,7 +32,7 @@ if ROOT not in sys.path:
     sys.path.insert(0, ROOT)
 
 NAMES = ("long_context_hutch", "long_context_exact", "hutchpp", "single_layer", "single_layer_gram", "shared_stack",
-         "sign_stack", "lora_routed", "dpsgd_step")
+         "sign_stack", "lora_routed", "dpsgd_step", "dpsgd_step_tokens")
 
 
 def main() -> None:
@@ -66,12 +68,16 @@ def main() -> None:
     elif a.name == "lora_routed":
         routed = [(A, G, None) for (A, G, _) in workloads.lora_stack(device=dev)]
         fn = lambda: dp.norms_routed(routed, 32)
-    elif a.name == "dpsgd_step":
+    elif a.name in ("dpsgd_step", "dpsgd_step_tokens"):
         from sample_grad_norms_amd.dpsgd_rc import RandomizedClipping
         from workloads import llama_block as lb
         shape = dict(layers=2, dim=2048, heads=32, kv_heads=8, hidden=8192, vocab=2048)
+        if a.name == "dpsgd_step_tokens":   # from token ids, with the library's table and attention
+            shape.update(vocab_in=32768, embed_scale=45.0, ops="library")
         model = lb.build(90, device=dev, dtype=torch.bfloat16, **shape)
         x, y = lb.batch(91, 4, 2048, shape["dim"], shape["vocab"], device=dev, dtype=torch.bfloat16)
+        if a.name == "dpsgd_step_tokens":
+            x, y = lb.token_batch(91, 4, 2048, shape["vocab_in"], shape["vocab"], device=dev)
         rc = RandomizedClipping(model, C=1.0, noise_multiplier=1.0, k=32)
         opt = torch.optim.Adam(rc.params, lr=1e-5)
 
