@@ -308,6 +308,82 @@ __device__ __forceinline__ void columns_times(const unsigned char* lds, int r0, 
   }
 }
 
+// Keeps a uniform branch a branch: without it the compiler computes the masks
+// of every step, of which one or two at the diagonal need them.
+__device__ __forceinline__ void keep_branch() { asm volatile(""); }
+
+// Halves (bf16) or words (fp32) of x that are infinities or NaN, as a mask.
+template <bool BF16>
+__device__ __forceinline__ uint32_t not_finite(uint32_t x) {
+  if constexpr (BF16) {
+    const uint32_t top = ((x & 0x7f807f80u) + 0x00800080u) & 0x80008000u;   // bit 15 of a half whose exponent is all ones
+    return (top >> 15) * 0xffffu;
+  } else {
+    return (x & 0x7f800000u) == 0x7f800000u ? ~0u : 0u;
+  }
+}
+
+// Whether some sum of the wave is an infinity or NaN (times zero, it is NaN).
+template <int TILES>
+__device__ __forceinline__ bool not_all_finite(const f32x16_t (&acc)[TILES]) {
+  float z[2] = {0.f, 0.f};
+#pragma unroll
+  for (int t = 0; t < TILES; ++t)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) z[r & 1] = fmaf(acc[t][r], 0.f, z[r & 1]);
+  return __builtin_expect(__any(!(z[0] + z[1] == 0.f)), 0);
+}
+
+// Causality holds for infinities and NaN. A masked row has weights of zero, and as a
+// product an infinity or NaN in it would still add NaN; only the 32 rows on a wave's
+// diagonal are masked for some of its columns and not for others. There such entries
+// are set to zero for the product, and added afterwards to the results of the rows
+// that see them. The output and dq do so in a second pass of a wave whose sums come
+// out not finite. dk and dv take each step on the diagonal so: a second pass would
+// cost them registers (D 128, 4 x 1024: 257 us without the guard, 282 with it, 307
+// with a second pass; D 64, 4 x 2048: 239, 252, 262).
+
+// 32 rows in LDS, the wave's own: infinities and NaN become zero. Returns whether any were.
+template <bool BF16, int DC>
+__device__ __forceinline__ bool zero_not_finite(unsigned char* lds) {
+  uint32_t any = 0;
+#pragma unroll 1
+  for (int i = 0; i < 32 * Geo<BF16, DC>::kChunks / 64; ++i) {
+    uint4* p = (uint4*)(lds + (i * 64 + (threadIdx.x & 63)) * 16);
+    const uint4 x = *p;
+    const uint4 n = make_uint4(not_finite<BF16>(x.x), not_finite<BF16>(x.y), not_finite<BF16>(x.z), not_finite<BF16>(x.w));
+    if (__builtin_expect(__any(n.x | n.y | n.z | n.w), 0)) {
+      any = 1;
+      *p = make_uint4(x.x & ~n.x, x.y & ~n.y, x.z & ~n.z, x.w & ~n.w);
+    }
+  }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  return any;
+}
+
+// Adds the infinities and NaN of rows w0 .. w0 + 31 of head hs of src to the results
+// of head ho that see them: those of the same and later rows (UP) or of the same and
+// earlier ones; as they are, or as NaN (weights of either sign). By one wave.
+template <bool BF16, bool UP, bool AS_NAN>
+__device__ __forceinline__ void add_not_finite(const Tensor& src, int32_t hs, const Tensor& out, int32_t ho, int64_t start,
+                                               int32_t len, int32_t w0, int32_t D) {
+  constexpr int e = BF16 ? 2 : 4;
+  for (int32_t d = threadIdx.x & 63; d < D; d += 64) {
+    float bad = 0.f;
+    for (int i = 0; i < 32; ++i) {
+      const int32_t row = w0 + (UP ? i : 31 - i);
+      if (row >= len) continue;
+      const char* p = row_ptr(src, start + row, hs) + d * e;
+      const uint32_t x = BF16 ? (uint32_t)*(const uint16_t*)p << 16 : *(const uint32_t*)p;
+      if ((x & 0x7f800000u) == 0x7f800000u) bad += AS_NAN ? NAN : __uint_as_float(x);
+      if (bad == 0.f) continue;
+      char* q = row_ptr(out, start + row, ho) + d * e;
+      if constexpr (BF16) *(uint16_t*)q = (uint16_t)f32_to_bf16_bits(bf16_bits_to_f32(*(const uint16_t*)q) + bad);
+      else *(float*)q += bad;
+    }
+  }
+}
+
 // The value of the lane's column in the other half of the wave.
 __device__ __forceinline__ float other_half(float x) {
   const auto y = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
@@ -316,10 +392,6 @@ __device__ __forceinline__ float other_half(float x) {
 
 // Row r (0 .. 15) of a lane's half in a 32 x 32 result.
 __device__ __forceinline__ int result_row(int r, int g) { return 8 * (r >> 2) + 4 * g + (r & 3); }
-
-// Keeps a uniform branch a branch: without it the compiler computes the masks
-// of every step, of which one or two at the diagonal need them.
-__device__ __forceinline__ void keep_branch() { asm volatile(""); }
 
 // Columns of acc (transposed: rows are the D index) to row `row` of t, times f.
 template <bool BF16, int DC>
@@ -365,8 +437,7 @@ struct Tiles {
   using G = Geo<BF16, DC>;
   static constexpr int kWaves = 4, kThreads = 64 * kWaves, kRows = 128, kStep = 64;
   static constexpr int kStage = kStep * G::kPitch;   // bytes of one tensor's step
-  static constexpr int kBuffers = 4 * kStage <= 132 * 1024 ? 2 : 1;
-  using Rows = Stream<BF16, DC, kStep, kWaves>;
+  using Rows = Stream<BF16, DC, kStep, kWaves>;      // double buffered
 };
 
 // Bytes of a wave's own step are kBuf, for two tensors and the kExtra of dk and
@@ -416,6 +487,79 @@ __device__ __forceinline__ void join(f32x16_t (&acc)[TILES], int split, unsigned
 // rescaling its sums: the weights stay below 2^8 and the sums far inside fp32.
 constexpr float kGrowth = 8.f;
 
+// One wave's pass over the keys k0, k0 + 32 NS, .. up to its 32 queries from w0 on,
+// from LDS of its own. careful: without the infinities and NaN on the diagonal.
+template <bool BF16, int DC, int NS, int BUFFERS>
+__device__ __forceinline__ void forward_pass(bool careful, const Args& a, int32_t start, int32_t len, int32_t kh,
+                                             int32_t w0, int32_t k0, unsigned char* mine, const uint4 (&q)[Geo<BF16, DC>::kPairs], float& m, float& l,
+                                             f32x16_t (&acc)[Geo<BF16, DC>::kTiles]) {
+  using G = Geo<BF16, DC>;
+  using Rows = Stream<BF16, DC, 32, 1>;
+  constexpr int kStage = 32 * G::kPitch, kBuf = 2 * kStage;
+  const int lane = threadIdx.x & 63, g = lane >> 5;
+  const int32_t query = w0 + (lane & 31);
+  const float c = a.scale * kLog2e;
+  const uint32_t base = lds_address(mine);
+  const Rows ks(a.k, start, kh, a.D), vs(a.v, start, kh, a.D);
+  const auto fetch = [&](int32_t r0, uint32_t to) {
+    ks.fetch(r0, len, to);
+    vs.fetch(r0, len, to + kStage);
+  };
+  if (k0 <= w0) fetch(k0, base);
+  m = -INFINITY;
+  l = 0.f;
+#pragma unroll
+  for (int t = 0; t < G::kTiles; ++t) acc[t] = f32x16_t{};
+  int buf = 0;
+  for (; k0 <= w0; k0 += 32 * NS) {
+    own_staged();
+    const bool more = k0 + 32 * NS <= w0;
+    if (BUFFERS == 2 && more) fetch(k0 + 32 * NS, base + (buf ^ 1) * kBuf);
+    unsigned char* lk = mine + buf * kBuf;
+    unsigned char* lv = lk + kStage;
+    f32x16_t s = rows_times<BF16, DC>(lk, 0, q);
+    if (k0 == w0) {
+      keep_branch();
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        if (k0 + result_row(r, g) > query) s[r] = -INFINITY;
+    }
+    float x[2] = {s[0], s[1]};
+#pragma unroll
+    for (int r = 2; r < 16; ++r) x[r & 1] = fmaxf(x[r & 1], s[r]);
+    float top = fmaxf(x[0], x[1]);
+    top = fmaxf(top, other_half(top));
+    const bool grown = (top - m) * c > kGrowth;
+    if (__any(grown)) {   // (each query by its own scores alone)
+      keep_branch();
+      const float f = grown ? __builtin_amdgcn_exp2f((m - top) * c) : 1.f;
+      m = grown ? top : m;
+      l *= f;
+#pragma unroll
+      for (int t = 0; t < G::kTiles; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[t][r] *= f;
+    }
+    // (queries that see none of a split's keys so far: every weight 0)
+    const float mc = m == -INFINITY ? 0.f : m * c;
+    float sum[2] = {0.f, 0.f};
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, -mc));
+      sum[r & 1] += s[r];
+    }
+    l += sum[0] + sum[1];
+    if (careful && k0 == w0) zero_not_finite<BF16, DC>(lv);
+    columns_times<BF16, DC>(lv, 0, s, acc);
+    if (BUFFERS == 2) {
+      buf ^= 1;
+    } else if (more) {
+      own_staged();   // (the reads of this step are done)
+      fetch(k0 + 32 * NS, base);
+    }
+  }
+}
+
 template <bool BF16, int DC, int NS>
 __global__ __launch_bounds__(64 * NS, BF16 ? 2 : 1) void k_forward_rows(Args a) {
   using G = Geo<BF16, DC>;
@@ -434,67 +578,20 @@ __global__ __launch_bounds__(64 * NS, BF16 ? 2 : 1) void k_forward_rows(Args a) 
   const int lane = threadIdx.x & 63, g = lane >> 5;
   const int split = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int32_t w0 = tile * 32, query = w0 + (lane & 31);
-  const unsigned char* mine = lds + split * P::kBuffers * P::kBuf;
-  const uint32_t base = lds_address(mine);
-  const typename P::Rows ks(a.k, start, kh, a.D), vs(a.v, start, kh, a.D);
-  const auto fetch = [&](int32_t r0, uint32_t to) {
-    ks.fetch(r0, len, to);
-    vs.fetch(r0, len, to + P::kStage);
-  };
-  int32_t k0 = 32 * split;
-  if (k0 <= w0) fetch(k0, base);
   uint4 q[G::kPairs];
   load_operand<BF16, DC>(a.q, start, h, w0, len, a.D, q);
   const float c = a.scale * kLog2e;
-  float m = -INFINITY, l = 0.f;
-  f32x16_t acc[G::kTiles] = {};
-  int buf = 0;
-  for (; k0 <= w0; k0 += 32 * NS) {
-    own_staged();
-    const bool more = k0 + 32 * NS <= w0;
-    if (P::kBuffers == 2 && more) fetch(k0 + 32 * NS, base + (buf ^ 1) * P::kBuf);
-    const unsigned char* lk = mine + buf * P::kBuf;
-    const unsigned char* lv = lk + P::kStage;
-    f32x16_t s = rows_times<BF16, DC>(lk, 0, q);
-    if (k0 == w0) {
-      keep_branch();
-#pragma unroll
-      for (int r = 0; r < 16; ++r)
-        if (k0 + result_row(r, g) > query) s[r] = -INFINITY;
-    }
-    float x[2] = {s[0], s[1]};
-#pragma unroll
-    for (int r = 2; r < 16; ++r) x[r & 1] = fmaxf(x[r & 1], s[r]);
-    float top = fmaxf(x[0], x[1]);
-    top = fmaxf(top, other_half(top));
-    if (__any((top - m) * c > kGrowth)) {
-      keep_branch();
-      top = fmaxf(m, top);
-      const float f = top == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - top) * c);
-      m = top;
-      l *= f;
-#pragma unroll
-      for (int t = 0; t < G::kTiles; ++t)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) acc[t][r] *= f;
-    }
-    // (queries that see none of a split's keys so far: every weight 0)
-    const float mc = m == -INFINITY ? 0.f : m * c;
-    float sum[2] = {0.f, 0.f};
-#pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, -mc));
-      sum[r & 1] += s[r];
-    }
-    l += sum[0] + sum[1];
-    columns_times<BF16, DC>(lv, 0, s, acc);
-    if (P::kBuffers == 2) {
-      buf ^= 1;
-    } else if (more) {
-      own_staged();   // (the reads of this step are done)
-      fetch(k0 + 32 * NS, base);
-    }
+  float m, l;
+  f32x16_t acc[G::kTiles];
+  unsigned char* mine = lds + split * P::kBuffers * P::kBuf;
+  bool careful = false;
+#pragma unroll 1
+  for (;;) {
+    forward_pass<BF16, DC, NS, P::kBuffers>(careful, a, start, len, kh, w0, 32 * split, mine, q, m, l, acc);
+    if (careful || !not_all_finite(acc)) break;
+    careful = true;
   }
+  careful = __syncthreads_or(careful);
   l += other_half(l);
   if constexpr (NS > 1) {
     // the splits' sums on the scale of their common largest score
@@ -520,9 +617,14 @@ __global__ __launch_bounds__(64 * NS, BF16 ? 2 : 1) void k_forward_rows(Args a) 
     join<NS, G::kTiles>(acc, split, lds);
     if (split > 0) return;
   }
-  if (query >= len) return;
-  store_rows<BF16, DC>(a.o, (int64_t)start + query, h, a.D, acc, 1.f / l);
-  if (g == 0) a.lse[(int64_t)h * a.N + start + query] = fmaf(m, a.scale, logf(l));
+  if (query < len) {
+    store_rows<BF16, DC>(a.o, (int64_t)start + query, h, a.D, acc, 1.f / l);
+    if (g == 0) a.lse[(int64_t)h * a.N + start + query] = fmaf(m, a.scale, logf(l));
+  }
+  if (careful) {
+    __threadfence_block();
+    add_not_finite<BF16, true, false>(a.v, kh, a.o, h, start, len, w0, a.D);
+  }
 }
 
 template <bool BF16, int DC>
@@ -581,11 +683,11 @@ __global__ __launch_bounds__(256, BF16 ? 2 : 1) void k_forward(Args a) {
         for (int r = 0; r < 16; ++r) x[r & 3] = fmaxf(x[r & 3], s[t][r]);
       float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
       top = fmaxf(top, other_half(top));
-      if (__any((top - m) * c > kGrowth)) {
+      const bool grown = (top - m) * c > kGrowth;
+      if (__any(grown)) {   // (each query by its own scores alone)
         keep_branch();
-        top = fmaxf(m, top);
-        const float f = __builtin_amdgcn_exp2f((m - top) * c);
-        m = top;
+        const float f = grown ? __builtin_amdgcn_exp2f((m - top) * c) : 1.f;
+        m = grown ? top : m;
         l *= f;
 #pragma unroll
         for (int t = 0; t < G::kTiles; ++t)
@@ -605,8 +707,9 @@ __global__ __launch_bounds__(256, BF16 ? 2 : 1) void k_forward(Args a) {
           sum[r & 1] += s[t][r];
         }
       l += sum[0] + sum[1];
+      const unsigned char* lv = lds + (2 + buf) * P::kStage;
 #pragma unroll
-      for (int t = 0; t < 2; ++t) columns_times<BF16, DC>(lds + (2 + buf) * P::kStage, t * 32, s[t], acc);
+      for (int t = 0; t < 2; ++t) columns_times<BF16, DC>(lv, t * 32, s[t], acc);
     }
     staged();
   };
@@ -617,10 +720,19 @@ __global__ __launch_bounds__(256, BF16 ? 2 : 1) void k_forward(Args a) {
     step(r0, odd, even, std::integral_constant<int, 1>{});
     r0 += P::kStep;
   }
+  // Masked values may have added NaN: the wave takes its queries once more, by rows,
+  // from its quarter of the LDS (every wave is past the last step).
+  const bool careful = not_all_finite(acc);
+  if (careful) forward_pass<BF16, DC, 1, 1>(true, a, start, len, kh, w0, 0, lds + wv * P::kStage, q, m, l, acc);
   l += other_half(l);
-  if (query >= len) return;
-  store_rows<BF16, DC>(a.o, (int64_t)start + query, h, a.D, acc, 1.f / l);
-  if (g == 0) a.lse[(int64_t)h * a.N + start + query] = fmaf(m, a.scale, logf(l));
+  if (query < len) {
+    store_rows<BF16, DC>(a.o, (int64_t)start + query, h, a.D, acc, 1.f / l);
+    if (g == 0) a.lse[(int64_t)h * a.N + start + query] = fmaf(m, a.scale, logf(l));
+  }
+  if (careful) {
+    __threadfence_block();
+    add_not_finite<BF16, true, false>(a.v, kh, a.o, h, start, len, w0, a.D);
+  }
 }
 
 // dot product of two 16-byte chunks
@@ -639,12 +751,61 @@ __device__ __forceinline__ float dot_chunk(const uint4& x, const uint4& y, float
   return s;
 }
 
+// One wave's pass over the keys for dq, as forward_pass.
+template <bool BF16, int DC, int NS, int BUFFERS>
+__device__ __forceinline__ void backward_q_pass(bool careful, const Args& a, int32_t start, int32_t len, int32_t kh,
+                                                int32_t w0, int32_t k0, unsigned char* mine, const uint4 (&q)[Geo<BF16, DC>::kPairs],
+                                                const uint4 (&dO)[Geo<BF16, DC>::kPairs], float lse, float delta,
+                                                f32x16_t (&acc)[Geo<BF16, DC>::kTiles]) {
+  using G = Geo<BF16, DC>;
+  using Rows = Stream<BF16, DC, 32, 1>;
+  constexpr int kStage = 32 * G::kPitch, kBuf = 2 * kStage;
+  const int lane = threadIdx.x & 63, g = lane >> 5;
+  const int32_t query = w0 + (lane & 31);
+  const float c = a.scale * kLog2e;
+  const uint32_t base = lds_address(mine);
+  const Rows ks(a.k, start, kh, a.D), vs(a.v, start, kh, a.D);
+  const auto fetch = [&](int32_t r0, uint32_t to) {
+    ks.fetch(r0, len, to);
+    vs.fetch(r0, len, to + kStage);
+  };
+  if (k0 <= w0) fetch(k0, base);
+#pragma unroll
+  for (int t = 0; t < G::kTiles; ++t) acc[t] = f32x16_t{};
+  int buf = 0;
+  for (; k0 <= w0; k0 += 32 * NS) {
+    own_staged();
+    const bool more = k0 + 32 * NS <= w0;
+    if (BUFFERS == 2 && more) fetch(k0 + 32 * NS, base + (buf ^ 1) * kBuf);
+    unsigned char* lk = mine + buf * kBuf;
+    unsigned char* lv = lk + kStage;
+    f32x16_t s = rows_times<BF16, DC>(lk, 0, q);
+    const f32x16_t dp = rows_times<BF16, DC>(lv, 0, dO);
+#pragma unroll
+    for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, -lse)) * (dp[r] - delta);
+    if (k0 == w0) {
+      keep_branch();
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        if (k0 + result_row(r, g) > query) s[r] = 0.f;
+      if (careful) zero_not_finite<BF16, DC>(lk);
+    }
+    columns_times<BF16, DC>(lk, 0, s, acc);
+    if (BUFFERS == 2) {
+      buf ^= 1;
+    } else if (more) {
+      own_staged();   // (the reads of this step are done)
+      fetch(k0 + 32 * NS, base);
+    }
+  }
+}
+
 // dq, and the pairs for the second launch, by tiles.
 template <bool BF16, int DC>
-__global__ __launch_bounds__(256, BF16 ? 2 : 1) void k_backward_q(Args a) {
+__global__ __launch_bounds__(256, !BF16 ? 1 : DC == 64 ? 3 : 2) void k_backward_q(Args a) {
   using G = Geo<BF16, DC>;
   using P = Tiles<BF16, DC>;
-  __shared__ __align__(1024) unsigned char lds[P::kBuffers * 2 * P::kStage];
+  __shared__ __align__(1024) unsigned char lds[4 * P::kStage];
   int32_t start, len, tile, tiles;
   if (!find_tile(a, block_slot(a), P::kRows, start, len, tile, tiles)) {
     clear_rest(a, block_slot(a), tiles, [&](int32_t r) {
@@ -687,8 +848,7 @@ __global__ __launch_bounds__(256, BF16 ? 2 : 1) void k_backward_q(Args a) {
   staged();
   int buf = 0;
   for (int32_t r0 = 0; r0 < end; r0 += P::kStep) {
-    const bool more = r0 + P::kStep < end;
-    if (P::kBuffers == 2 && more) {
+    if (r0 + P::kStep < end) {
       const uint32_t to = base + (buf ^ 1) * 2 * P::kStage;
       ks.fetch(r0 + P::kStep, len, to);
       vs.fetch(r0 + P::kStep, len, to + P::kStage);
@@ -696,35 +856,33 @@ __global__ __launch_bounds__(256, BF16 ? 2 : 1) void k_backward_q(Args a) {
     if (r0 <= w0 + 31) {
       const unsigned char* lk = lds + buf * 2 * P::kStage;
       const unsigned char* lv = lk + P::kStage;
-      const auto step = [&](bool diag) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          f32x16_t s = rows_times<BF16, DC>(lk, t * 32, q);
-          const f32x16_t dp = rows_times<BF16, DC>(lv, t * 32, dO);
+      for (int t = 0; t < 2; ++t) {
+        const int32_t k0 = r0 + t * 32;
+        if (k0 > w0) break;   // (all masked)
+        f32x16_t s = rows_times<BF16, DC>(lk, t * 32, q);
+        const f32x16_t dp = rows_times<BF16, DC>(lv, t * 32, dO);
 #pragma unroll
-          for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, -lse)) * (dp[r] - delta);
-          if (diag) {
-            keep_branch();
+        for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, -lse)) * (dp[r] - delta);
+        if (k0 == w0) {
+          keep_branch();
 #pragma unroll
-            for (int r = 0; r < 16; ++r)
-              if (r0 + t * 32 + result_row(r, g) > query) s[r] = 0.f;
-          }
-          columns_times<BF16, DC>(lk, t * 32, s, acc);
+          for (int r = 0; r < 16; ++r)
+            if (k0 + result_row(r, g) > query) s[r] = 0.f;
         }
-      };
-      const bool diag = r0 + 63 > w0;
-      step(diag);
-    }
-    if (P::kBuffers == 1 && more) {
-      __syncthreads();
-      ks.fetch(r0 + P::kStep, len, base);
-      vs.fetch(r0 + P::kStep, len, base + P::kStage);
+        columns_times<BF16, DC>(lk, t * 32, s, acc);
+      }
     }
     staged();
-    if (P::kBuffers == 2) buf ^= 1;
+    buf ^= 1;
   }
-  if (query >= len) return;
-  store_rows<BF16, DC>(a.dq, (int64_t)start + query, h, a.D, acc, a.scale);
+  const bool careful = not_all_finite(acc);   // see k_forward
+  if (careful) backward_q_pass<BF16, DC, 1, 1>(true, a, start, len, kh, w0, 0, lds + wv * P::kStage, q, dO, lse, delta, acc);
+  if (query < len) store_rows<BF16, DC>(a.dq, (int64_t)start + query, h, a.D, acc, a.scale);
+  if (careful) {
+    __threadfence_block();
+    add_not_finite<BF16, true, true>(a.k, kh, a.dq, h, start, len, w0, a.D);
+  }
 }
 
 // The same by rows.
@@ -745,15 +903,6 @@ __global__ __launch_bounds__(64 * NS, BF16 ? 2 : 1) void k_backward_q_rows(Args 
   const int lane = threadIdx.x & 63, g = lane >> 5;
   const int split = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int32_t w0 = tile * 32, query = w0 + (lane & 31);
-  const unsigned char* mine = lds + split * P::kBuffers * P::kBuf;
-  const uint32_t base = lds_address(mine);
-  const typename P::Rows ks(a.k, start, kh, a.D), vs(a.v, start, kh, a.D);
-  const auto fetch = [&](int32_t r0, uint32_t to) {
-    ks.fetch(r0, len, to);
-    vs.fetch(r0, len, to + P::kStage);
-  };
-  int32_t k0 = 32 * split;
-  if (k0 <= w0) fetch(k0, base);
   uint4 q[G::kPairs], dO[G::kPairs];
   float delta = 0.f;
   {
@@ -771,61 +920,40 @@ __global__ __launch_bounds__(64 * NS, BF16 ? 2 : 1) void k_backward_q_rows(Args 
     lse = a.lse[at] * kLog2e;
     if (g == 0 && split == 0) *(float2*)(a.pairs + 2 * at) = make_float2(lse, delta);
   }
-  const float c = a.scale * kLog2e;
-  f32x16_t acc[G::kTiles] = {};
-  int buf = 0;
-  for (; k0 <= w0; k0 += 32 * NS) {
-    own_staged();
-    const bool more = k0 + 32 * NS <= w0;
-    if (P::kBuffers == 2 && more) fetch(k0 + 32 * NS, base + (buf ^ 1) * P::kBuf);
-    const unsigned char* lk = mine + buf * P::kBuf;
-    const unsigned char* lv = lk + P::kStage;
-    f32x16_t s = rows_times<BF16, DC>(lk, 0, q);
-    const f32x16_t dp = rows_times<BF16, DC>(lv, 0, dO);
-#pragma unroll
-    for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, -lse)) * (dp[r] - delta);
-    if (k0 == w0) {
-      keep_branch();
-#pragma unroll
-      for (int r = 0; r < 16; ++r)
-        if (k0 + result_row(r, g) > query) s[r] = 0.f;
-    }
-    columns_times<BF16, DC>(lk, 0, s, acc);
-    if (P::kBuffers == 2) {
-      buf ^= 1;
-    } else if (more) {
-      own_staged();   // (the reads of this step are done)
-      fetch(k0 + 32 * NS, base);
-    }
+  f32x16_t acc[G::kTiles];
+  unsigned char* mine = lds + split * P::kBuffers * P::kBuf;
+  bool careful = false;
+#pragma unroll 1
+  for (;;) {
+    backward_q_pass<BF16, DC, NS, P::kBuffers>(careful, a, start, len, kh, w0, 32 * split, mine, q, dO, lse, delta, acc);
+    if (careful || !not_all_finite(acc)) break;
+    careful = true;
   }
+  careful = __syncthreads_or(careful);
   if constexpr (NS > 1) {
     join<NS, G::kTiles>(acc, split, lds);
     if (split > 0) return;
   }
-  if (query >= len) return;
-  store_rows<BF16, DC>(a.dq, (int64_t)start + query, h, a.D, acc, a.scale);
+  if (query < len) store_rows<BF16, DC>(a.dq, (int64_t)start + query, h, a.D, acc, a.scale);
+  if (careful) {
+    __threadfence_block();
+    add_not_finite<BF16, true, true>(a.k, kh, a.dq, h, start, len, w0, a.D);
+  }
 }
 
-// dk and dv by rows: 32 keys of one key head, all query heads of the key head and
-// all queries from the diagonal on.
+// One wave's pass over the queries of the key head's query heads, from the keys w0
+// on, 32 in each 32 NS, for dk and dv. Sets careful where the diagonal held others
+// than finite numbers.
 template <bool BF16, int DC, int NS>
-__global__ __launch_bounds__(64 * NS, BF16 ? 2 : 1) void k_backward_kv(Args a) {
-  using G = Geo<BF16, DC>;
+__device__ __forceinline__ void backward_kv_pass(bool& careful, const Args& a, int32_t start, int32_t len, int32_t kh,
+                                                 int32_t w0, int split, unsigned char* mine, const uint4 (&k)[Geo<BF16, DC>::kPairs],
+                                                 const uint4 (&v)[Geo<BF16, DC>::kPairs],
+                                                 f32x16_t (&dk)[Geo<BF16, DC>::kTiles], f32x16_t (&dv)[Geo<BF16, DC>::kTiles]) {
   using P = OwnRows<BF16, DC, NS, 256>;
-  __shared__ __align__(1024) unsigned char lds[P::kLds];
-  int32_t start, len, tile, tiles;
-  const int32_t kh = blockIdx.x, rep = a.Hq / a.Hkv;
-  if (!find_tile(a, block_slot(a), 32, start, len, tile, tiles)) {
-    clear_rest(a, block_slot(a), tiles, [&](int32_t r) {
-      clear_row(a.dk, r, blockIdx.x, a.D * G::kElem);
-      clear_row(a.dv, r, blockIdx.x, a.D * G::kElem);
-    });
-    return;
-  }
+  using G = Geo<BF16, DC>;
   const int lane = threadIdx.x & 63, g = lane >> 5;
-  const int split = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int32_t w0 = tile * 32, key = w0 + (lane & 31);
-  const unsigned char* mine = lds + split * P::kBuffers * P::kBuf;
+  const int32_t key = w0 + (lane & 31), rep = a.Hq / a.Hkv;
+  const float c = a.scale * kLog2e;
   const uint32_t base = lds_address(mine);
   // 32 queries from q0 on of head h, with their lse and delta: zeros past the
   // end, whose dO and q rows are zero too and so add nothing
@@ -838,28 +966,32 @@ __global__ __launch_bounds__(64 * NS, BF16 ? 2 : 1) void k_backward_kv(Args a) {
     const char* at = (const char*)(a.pairs + 2 * ((int64_t)h * a.N + start + q0));
     dma_words(rows_of(at), q0 + (lane >> 1) < len ? lane * 4 : kOutside, to + 2 * P::kStage);
   };
-  const int32_t first = w0 + 32 * split;
-  const int32_t per = first < len ? (len - first + 32 * NS - 1) / (32 * NS) : 0;   // steps a head
-  const int32_t steps = per * rep;
-  uint4 k[G::kPairs], v[G::kPairs];
-  if (steps > 0) fetch(kh * rep, first, base);
-  load_operand<BF16, DC>(a.k, start, kh, w0, len, a.D, k);
-  load_operand<BF16, DC>(a.v, start, kh, w0, len, a.D, v);
-  const float c = a.scale * kLog2e;
-  f32x16_t dk[G::kTiles] = {}, dv[G::kTiles] = {};
-  int32_t h = kh * rep, q0 = first;
+  // the wave's next 32 queries: each in turn 32 NS apart; where the steps are few (NS
+  // of 8), the first by head and wave, so that the diagonal, whose steps take longer,
+  // falls to every wave (one sequence of 512, 24 heads: 22.6 -> 20.9 us; 4 of 2048: no change)
+  const int32_t hend = kh * rep + rep;
+  const auto first = [&](int32_t h) { return w0 + 32 * (NS == 8 ? (split + h) % NS : split); };
+  const auto settle = [&](int32_t& h, int32_t& q0) {
+    while (q0 >= len && ++h < hend) q0 = first(h);
+  };
+  int32_t h = kh * rep, q0 = first(h);
+  settle(h, q0);
+  if (h < hend) fetch(h, q0, base);
+#pragma unroll
+  for (int t = 0; t < G::kTiles; ++t) dk[t] = f32x16_t{}, dv[t] = f32x16_t{};
   int buf = 0;
-  for (int32_t i = 0; i < steps; ++i) {
+  while (h < hend) {
     int32_t nh = h, nq = q0 + 32 * NS;
-    if (nq >= len) {
-      nq = first;
-      ++nh;
-    }
+    settle(nh, nq);
     own_staged();
-    if (P::kBuffers == 2 && i + 1 < steps) fetch(nh, nq, base + (buf ^ 1) * P::kBuf);
-    const unsigned char* lq = mine + buf * P::kBuf;
-    const unsigned char* lo = lq + P::kStage;
+    if (P::kBuffers == 2 && nh < hend) fetch(nh, nq, base + (buf ^ 1) * P::kBuf);
+    unsigned char* lq = mine + buf * P::kBuf;
+    unsigned char* lo = lq + P::kStage;
     const float* words = (const float*)(lq + 2 * P::kStage);
+    if (q0 == w0) {   // (a query row that is not finite has lse or delta of NaN)
+      careful |= zero_not_finite<BF16, DC>(lo);
+      careful |= zero_not_finite<BF16, DC>(lq);
+    }
     f32x16_t p = rows_times<BF16, DC>(lq, 0, k);
     f32x16_t ds = rows_times<BF16, DC>(lo, 0, v);
 #pragma unroll
@@ -886,19 +1018,57 @@ __global__ __launch_bounds__(64 * NS, BF16 ? 2 : 1) void k_backward_kv(Args a) {
     q0 = nq;
     if (P::kBuffers == 2) {
       buf ^= 1;
-    } else if (i + 1 < steps) {
+    } else if (nh < hend) {
       own_staged();   // (the reads of this step are done)
       fetch(nh, nq, base);
     }
   }
+}
+
+// dk and dv by rows: 32 keys of one key head, all query heads of the key head and
+// all queries from the diagonal on.
+template <bool BF16, int DC, int NS>
+__global__ __launch_bounds__(64 * NS, BF16 || DC == 64 ? 2 : 1) void k_backward_kv(Args a) {
+  using G = Geo<BF16, DC>;
+  using P = OwnRows<BF16, DC, NS, 256>;
+  __shared__ __align__(1024) unsigned char lds[P::kLds];
+  int32_t start, len, tile, tiles;
+  const int32_t kh = blockIdx.x;
+  if (!find_tile(a, block_slot(a), 32, start, len, tile, tiles)) {
+    clear_rest(a, block_slot(a), tiles, [&](int32_t r) {
+      clear_row(a.dk, r, blockIdx.x, a.D * G::kElem);
+      clear_row(a.dv, r, blockIdx.x, a.D * G::kElem);
+    });
+    return;
+  }
+  const int lane = threadIdx.x & 63;
+  const int split = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int32_t w0 = tile * 32, key = w0 + (lane & 31);
+  unsigned char* mine = lds + split * P::kBuffers * P::kBuf;
+  uint4 k[G::kPairs], v[G::kPairs];
+  load_operand<BF16, DC>(a.k, start, kh, w0, len, a.D, k);
+  load_operand<BF16, DC>(a.v, start, kh, w0, len, a.D, v);
+  f32x16_t dk[G::kTiles], dv[G::kTiles];
+  bool careful = false;
+  backward_kv_pass<BF16, DC, NS>(careful, a, start, len, kh, w0, split, mine, k, v, dk, dv);
+  careful = __syncthreads_or(careful);
   if constexpr (NS > 1) {
     join<NS, G::kTiles>(dk, split, lds);
     join<NS, G::kTiles>(dv, split, lds);
     if (split > 0) return;
   }
-  if (key >= len) return;
-  store_rows<BF16, DC>(a.dk, (int64_t)start + key, kh, a.D, dk, a.scale);
-  store_rows<BF16, DC>(a.dv, (int64_t)start + key, kh, a.D, dv, 1.f);
+  if (key < len) {
+    store_rows<BF16, DC>(a.dk, (int64_t)start + key, kh, a.D, dk, a.scale);
+    store_rows<BF16, DC>(a.dv, (int64_t)start + key, kh, a.D, dv, 1.f);
+  }
+  if (careful) {
+    __threadfence_block();
+    const int32_t rep = a.Hq / a.Hkv;
+    for (int32_t h = kh * rep; h < kh * rep + rep; ++h) {
+      add_not_finite<BF16, false, true>(a.q, h, a.dk, kh, start, len, w0, a.D);
+      add_not_finite<BF16, false, true>(a.dO, h, a.dv, kh, start, len, w0, a.D);
+    }
+  }
 }
 
 }  // namespace attn

@@ -246,6 +246,42 @@ def test_rows_of_no_sequence(dtype):
     assert torch.equal(o3[70:201], o2[70:201]) and bool(o3[3:70].isnan().all())
 
 
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("Hq,Hkv", [(2, 1), (64, 64)])
+def test_a_row_that_is_not_finite_leaves_the_rows_before_it(Hq, Hkv, dtype, value):
+    """Causality holds for infinities and NaN: rows before the row that holds one
+    get what they get without it, forward and backward, bit for bit."""
+    import sample_grad_norms_amd as dp
+    N, D = 700 if Hq == 64 else 180, 64
+    q, k, v, do = (x.to(dev()) for x in make(N, Hq, Hkv, D, dtype, 18))
+    o, lse = dp.attention_forward(q, k, v)
+    grads = dp.attention_backward(do, q, k, v, o, lse)
+    for row in (N - 100, N - 1):
+        for name in ("k", "v"):
+            args = {"q": q, "k": k.clone(), "v": v.clone()}
+            args[name][row, :, 5] = value
+            o2, lse2 = dp.attention_forward(**args)
+            assert torch.equal(o2[:row], o[:row]) and torch.equal(lse2[:, :row], lse[:, :row]), (name, row)
+            # every later query sees it: in v as what it is, in k as NaN or as weights of 0 or 1
+            if name == "v":
+                later = o2[row:, :, 5].float()
+                assert bool((later.isnan() if math.isnan(value) else later == value).all())
+                assert bool(o2[row:, :, :5].isfinite().all())
+            # dq of the rows before sees neither (its own do and o are as before)
+            dq, _, _ = dp.attention_backward(do, args["q"], args["k"], args["v"], o, lse)
+            assert torch.equal(dq[:row], grads[0][:row]), (name, row)
+    # dk and dv of later keys see no earlier query
+    for row in (0, 77):
+        for name in ("do", "q"):
+            args = {"do": do.clone(), "q": q.clone()}
+            args[name][row, :, 5] = value
+            _, dk, dv = dp.attention_backward(args["do"], args["q"], k, v, o, lse)
+            assert torch.equal(dk[row + 1:], grads[1][row + 1:]) and torch.equal(dv[row + 1:], grads[2][row + 1:]), (name, row)
+            if name == "do":
+                assert not bool(dv[:row + 1, :, 5].isfinite().any())
+
+
 @pytest.mark.parametrize("cu", [[0, 0, 0], [130, 130], [0, 64, 128], [100, 101, 133]])
 def test_rows_of_no_sequence_are_cleared(cu):
     """No sequence at all, tiles that fill every slot, one row among many."""
