@@ -396,7 +396,8 @@ dpnorm_status dpnorm_attention_forward(const dpnorm_attn_shape* shape, const dpn
  * ds_tu = p_tu (dO_t . v_u - delta_t),
  *   dq_t = scale sum_u ds_tu k_u, dk_u = scale sum_t ds_tu q_t,
  *   dv_u = sum_t p_tu dO_t (dk and dv summed over the key head's query heads).
- * ws holds delta and the scaled lse. */
+ * ws holds delta and the scaled lse, and in small calls the sums of work groups
+ * that share keys. */
 dpnorm_status dpnorm_attention_backward_workspace(const dpnorm_attn_shape* shape, size_t* bytes);
 dpnorm_status dpnorm_attention_backward(const dpnorm_attn_shape* shape, const dpnorm_attn_tensor* dO,
                                         const dpnorm_attn_tensor* q, const dpnorm_attn_tensor* k,

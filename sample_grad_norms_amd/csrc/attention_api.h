@@ -100,11 +100,28 @@ constexpr int64_t kRowsMost = 1536;
 template <bool BF16, int DC>
 constexpr bool kRowsAlways = !BF16 && DC == 64;
 
-// dk and dv: eight waves a work group instead of four while the work groups are
-// few, for chains half as long (T = 2048, 32/4 heads: D = 64 88 us against 132,
-// D = 128 156 against 259; B = 4, 32/8 heads, D = 64, 2080 work groups: 242
-// against 208). float32 rows of eight waves do not fit the LDS.
-constexpr int64_t kKeysMost = 600;
+// dk and dv: the work groups that share the queries of 32 keys of one key head, at
+// most (short ends take fewer, see k_backward_kv): about 1.5 for each place on the CUs,
+// and three where places and keys are nearly as many but the chains are long. Odd, so
+// that those without work do not fall to the same XCDs. us, shared against one work
+// group: T = 2048, 32/4 heads D = 128 126 (3) against 283, 3/1 heads D = 64 of 811 + 443
+// rows 14 (19) against 26; float32 T = 2048, 16/4 heads D = 64 171 (3) against 293, 8/2
+// heads D = 128 of 1500 + 777 rows 176 (3) against 440; B = 2, T = 2048, 32/4 heads
+// D = 64 135 (3) against 168, but 10/5 heads 57 (2) against 47; T = 1024, 16/4 heads
+// 22 (5), 30 (8).
+template <bool BF16, int DC>
+int32_t key_splits(const attn::Args& a) {
+  const int64_t places = 256 * (attn::OwnRows<BF16, DC, 4, 256>::kLds <= 80 * 1024 ? 2 : 1);
+  const int64_t groups = ((int64_t)a.N / 32 + a.S) * a.Hkv;
+  const int64_t splits = 3 * places / (4 * groups) * 2 + 1;
+  if (splits > 1) return (int32_t)splits;
+  const int64_t steps = (int64_t)a.N / a.S / 32 * (a.Hq / a.Hkv);
+  return steps >= 256 && 4 * groups < 5 * places ? 3 : 1;
+}
+int32_t key_splits(const attn::Args& a, bool bf16) {
+  if (bf16) return a.D <= 64 ? key_splits<true, 64>(a) : a.D <= 96 ? key_splits<true, 96>(a) : key_splits<true, 128>(a);
+  return a.D <= 64 ? key_splits<false, 64>(a) : a.D <= 96 ? key_splits<false, 96>(a) : key_splits<false, 128>(a);
+}
 
 // One launch, or more where a grid's z dimension does not hold the slots.
 template <typename F>
@@ -150,15 +167,30 @@ template <bool BF16, int DC>
 hipError_t run_attn_backward(const attn::Args& a, hipStream_t stream) {
   const hipError_t he = run_attn_backward_q<BF16, DC>(a, stream);
   if (he != hipSuccess) return he;
-  if constexpr (BF16) {
-    if (slots_of(a, 32) * a.Hkv <= kKeysMost)
-      return launch_slots(a, 32, 1, [&](const attn::Args& x, dim3 grid) {
-        attn::k_backward_kv<BF16, DC, 8><<<grid, 512, 0, stream>>>(x);
-      });
-  }
+  if (a.splits > 1)
+    return launch_slots(a, 32, a.splits, [&](const attn::Args& x, dim3 grid) {
+      attn::k_backward_kv<BF16, DC, 4, true><<<grid, 256, 0, stream>>>(x);
+    });
   return launch_slots(a, 32, 1, [&](const attn::Args& x, dim3 grid) {
-    attn::k_backward_kv<BF16, DC, 4><<<grid, 256, 0, stream>>>(x);
+    attn::k_backward_kv<BF16, DC, 4, false><<<grid, 256, 0, stream>>>(x);
   });
+}
+
+// The workspace of a backward pass (its bytes; null to ask for them alone): the pairs,
+// and for shared keys the sums and counters.
+size_t backward_layout(attn::Args& a, bool bf16, void* ws) {
+  const size_t pairs = align_up((size_t)a.N * a.Hq * 8);
+  a.pairs = (float*)ws;
+  a.splits = key_splits(a, bf16);
+  if (a.splits < 2) return pairs;
+  a.groups = (int32_t)((slots_of(a, 32) + 1) * a.Hkv);
+  const size_t counts = align_up((size_t)a.groups * 4);
+  const size_t columns = a.D <= 64 ? 64 : a.D <= 96 ? 96 : 128;
+  if (ws) {
+    a.arrived = (uint32_t*)((char*)ws + pairs);
+    a.parts = (float*)((char*)ws + pairs + counts);
+  }
+  return pairs + counts + align_up((size_t)a.groups * a.splits * 2 * 32 * columns * 4);
 }
 
 }  // namespace
@@ -199,7 +231,8 @@ dpnorm_status dpnorm_attention_backward_workspace(const dpnorm_attn_shape* shape
   if (!bytes) return DPNORM_ERR_NULL;
   const dpnorm_status st = check_shape(shape);
   if (st != DPNORM_OK) return st;
-  *bytes = align_up((size_t)shape->N * shape->Hq * 8);
+  attn::Args a = attn_args(shape);
+  *bytes = backward_layout(a, shape->dtype == DPNORM_BF16, nullptr);
   return DPNORM_OK;
 }
 
@@ -238,7 +271,7 @@ dpnorm_status dpnorm_attention_backward(const dpnorm_attn_shape* shape, const dp
   a.dk = tensor_of(dk, e);
   a.dv = tensor_of(dv, e);
   a.lse = const_cast<float*>(lse);
-  a.pairs = (float*)ws;
+  backward_layout(a, shape->dtype == DPNORM_BF16, ws);
   if (shape->dtype == DPNORM_BF16)
     return hip_status(D <= 64 ? run_attn_backward<true, 64>(a, stream) : D <= 96 ? run_attn_backward<true, 96>(a, stream)
                                                                            : run_attn_backward<true, 128>(a, stream));

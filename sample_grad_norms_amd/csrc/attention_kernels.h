@@ -23,7 +23,7 @@
 // 8 (r / 4) + 4 g + r % 4, r = 0 .. 15, of column l % 32.
 //
 // Accumulators, statistics, delta and every sum are fp32. The weights p and ds
-// are rounded to bf16 for bf16 inputs (half a step, 2^-9 relative, as the
+// are rounded to bf16 for bf16 inputs (half a step, up to 2^-8 relative, as the
 // inputs themselves are); the sum of the weights takes them unrounded.
 #pragma once
 #include <type_traits>
@@ -53,6 +53,11 @@ struct Args {
   int32_t slots;      // tile slots per head
   int32_t slot0;      // first slot of the launch
   int32_t clear;      // set rows of no sequence to zero
+  // dk and dv where work groups share their keys' queries:
+  int32_t splits;     // work groups of 32 keys of one key head, and
+  int32_t groups;     // the number of such groups of 32 keys
+  float* parts;       // their sums, [slot][key head][split][dk, dv][tile][1024]
+  uint32_t* arrived;  // [slot][key head] of them have arrived (the launch before sets it to zero)
 };
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -393,30 +398,34 @@ __device__ __forceinline__ float other_half(float x) {
 // Row r (0 .. 15) of a lane's half in a 32 x 32 result.
 __device__ __forceinline__ int result_row(int r, int g) { return 8 * (r >> 2) + 4 * g + (r & 3); }
 
+// Tile i (32 columns) of a row at p, from the transposed result acc, times f.
+template <bool BF16>
+__device__ __forceinline__ void store_tile(char* p, int i, int32_t D, const f32x16_t& acc, float f) {
+  const int g = (threadIdx.x & 63) >> 5;
+#pragma unroll
+  for (int r4 = 0; r4 < 4; ++r4) {
+    const int col = i * 32 + 8 * r4 + 4 * g;
+    if (col >= D) continue;
+    const float x[4] = {acc[4 * r4] * f, acc[4 * r4 + 1] * f, acc[4 * r4 + 2] * f, acc[4 * r4 + 3] * f};
+    if constexpr (BF16) {
+      uint2 y;
+      y.x = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t){x[0], x[1]}, bf16x2_t));
+      y.y = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t){x[2], x[3]}, bf16x2_t));
+      *(uint2*)(p + col * 2) = y;
+    } else {
+      *(float4*)(p + col * 4) = make_float4(x[0], x[1], x[2], x[3]);
+    }
+  }
+}
+
 // Columns of acc (transposed: rows are the D index) to row `row` of t, times f.
 template <bool BF16, int DC>
 __device__ __forceinline__ void store_rows(const Tensor& t, int64_t row, int32_t h, int32_t D,
                                            const f32x16_t (&acc)[Geo<BF16, DC>::kTiles], float f) {
   using G = Geo<BF16, DC>;
   char* p = t.p + row * t.st + h * t.sh;
-  const int g = (threadIdx.x & 63) >> 5;
 #pragma unroll
-  for (int i = 0; i < G::kTiles; ++i) {
-#pragma unroll
-    for (int r4 = 0; r4 < 4; ++r4) {
-      const int col = i * 32 + 8 * r4 + 4 * g;
-      if (col >= D) continue;
-      const float x[4] = {acc[i][4 * r4] * f, acc[i][4 * r4 + 1] * f, acc[i][4 * r4 + 2] * f, acc[i][4 * r4 + 3] * f};
-      if constexpr (BF16) {
-        uint2 y;
-        y.x = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t){x[0], x[1]}, bf16x2_t));
-        y.y = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t){x[2], x[3]}, bf16x2_t));
-        *(uint2*)(p + col * 2) = y;
-      } else {
-        *(float4*)(p + col * 4) = make_float4(x[0], x[1], x[2], x[3]);
-      }
-    }
-  }
+  for (int i = 0; i < G::kTiles; ++i) store_tile<BF16>(p, i, D, acc[i], f);
 }
 
 // Blocks: x is the key head, y the query head of that key head, z the slot
@@ -481,6 +490,14 @@ __device__ __forceinline__ void join(f32x16_t (&acc)[TILES], int split, unsigned
       }
     }
   }
+}
+
+// The counters of a backward pass's second launch, set to zero by its first.
+__device__ __forceinline__ void clear_arrived(const Args& a) {
+  if (a.splits < 2) return;
+  const int64_t block = ((int64_t)blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
+  const int64_t blocks = (int64_t)gridDim.x * gridDim.y * gridDim.z;
+  for (int64_t i = block * blockDim.x + threadIdx.x; i < a.groups; i += blocks * blockDim.x) a.arrived[i] = 0;
 }
 
 // Largest growth of a score, in powers of two, that a wave lets pass without
@@ -806,6 +823,7 @@ __global__ __launch_bounds__(256, !BF16 ? 1 : DC == 64 ? 3 : 2) void k_backward_
   using G = Geo<BF16, DC>;
   using P = Tiles<BF16, DC>;
   __shared__ __align__(1024) unsigned char lds[4 * P::kStage];
+  clear_arrived(a);
   int32_t start, len, tile, tiles;
   if (!find_tile(a, block_slot(a), P::kRows, start, len, tile, tiles)) {
     clear_rest(a, block_slot(a), tiles, [&](int32_t r) {
@@ -891,6 +909,7 @@ __global__ __launch_bounds__(64 * NS, BF16 ? 2 : 1) void k_backward_q_rows(Args 
   using G = Geo<BF16, DC>;
   using P = OwnRows<BF16, DC, NS, 0>;
   __shared__ __align__(1024) unsigned char lds[P::kLds];
+  clear_arrived(a);
   int32_t start, len, tile, tiles;
   if (!find_tile(a, block_slot(a), 32, start, len, tile, tiles)) {
     clear_rest(a, block_slot(a), tiles, [&](int32_t r) {
@@ -941,12 +960,12 @@ __global__ __launch_bounds__(64 * NS, BF16 ? 2 : 1) void k_backward_q_rows(Args 
   }
 }
 
-// One wave's pass over the queries of the key head's query heads, from the keys w0
-// on, 32 in each 32 NS, for dk and dv. Sets careful where the diagonal held others
-// than finite numbers.
+// One wave's pass for dk and dv over the queries of the key head's query heads, from
+// the keys w0 on: one step of 32 of `waves`, from the one `wave` on. Sets careful
+// where the diagonal held others than finite numbers.
 template <bool BF16, int DC, int NS>
 __device__ __forceinline__ void backward_kv_pass(bool& careful, const Args& a, int32_t start, int32_t len, int32_t kh,
-                                                 int32_t w0, int split, unsigned char* mine, const uint4 (&k)[Geo<BF16, DC>::kPairs],
+                                                 int32_t w0, int32_t wave, int32_t waves, unsigned char* mine, const uint4 (&k)[Geo<BF16, DC>::kPairs],
                                                  const uint4 (&v)[Geo<BF16, DC>::kPairs],
                                                  f32x16_t (&dk)[Geo<BF16, DC>::kTiles], f32x16_t (&dv)[Geo<BF16, DC>::kTiles]) {
   using P = OwnRows<BF16, DC, NS, 256>;
@@ -966,22 +985,19 @@ __device__ __forceinline__ void backward_kv_pass(bool& careful, const Args& a, i
     const char* at = (const char*)(a.pairs + 2 * ((int64_t)h * a.N + start + q0));
     dma_words(rows_of(at), q0 + (lane >> 1) < len ? lane * 4 : kOutside, to + 2 * P::kStage);
   };
-  // the wave's next 32 queries: each in turn 32 NS apart; where the steps are few (NS
-  // of 8), the first by head and wave, so that the diagonal, whose steps take longer,
-  // falls to every wave (one sequence of 512, 24 heads: 22.6 -> 20.9 us; 4 of 2048: no change)
-  const int32_t hend = kh * rep + rep;
-  const auto first = [&](int32_t h) { return w0 + 32 * (NS == 8 ? (split + h) % NS : split); };
+  // the steps of one head after another
+  const int32_t hend = kh * rep + rep, end = w0 + (len - w0 + 31) / 32 * 32;
   const auto settle = [&](int32_t& h, int32_t& q0) {
-    while (q0 >= len && ++h < hend) q0 = first(h);
+    while (q0 >= end && h < hend) q0 -= end - w0, ++h;
   };
-  int32_t h = kh * rep, q0 = first(h);
+  int32_t h = kh * rep, q0 = w0 + 32 * wave;
   settle(h, q0);
   if (h < hend) fetch(h, q0, base);
 #pragma unroll
   for (int t = 0; t < G::kTiles; ++t) dk[t] = f32x16_t{}, dv[t] = f32x16_t{};
   int buf = 0;
   while (h < hend) {
-    int32_t nh = h, nq = q0 + 32 * NS;
+    int32_t nh = h, nq = q0 + 32 * waves;
     settle(nh, nq);
     own_staged();
     if (P::kBuffers == 2 && nh < hend) fetch(nh, nq, base + (buf ^ 1) * P::kBuf);
@@ -1026,8 +1042,13 @@ __device__ __forceinline__ void backward_kv_pass(bool& careful, const Args& a, i
 }
 
 // dk and dv by rows: 32 keys of one key head, all query heads of the key head and
-// all queries from the diagonal on.
-template <bool BF16, int DC, int NS>
+// all queries from the diagonal on, by four waves. SPLIT: a few such work groups share
+// the steps, as many as leave each wave kSteps of them, and the last to arrive adds
+// their sums in a fixed order. The sums and the counter go past the L2 caches, which
+// the XCDs do not share: fences, which write back and empty them, cost more than the
+// split won (3/1 heads D = 64, 811 + 443 rows: 34 us with fences, 14 without, 26 unsplit).
+constexpr int kSteps = 2;
+template <bool BF16, int DC, int NS, bool SPLIT>
 __global__ __launch_bounds__(64 * NS, BF16 || DC == 64 ? 2 : 1) void k_backward_kv(Args a) {
   using G = Geo<BF16, DC>;
   using P = OwnRows<BF16, DC, NS, 256>;
@@ -1035,31 +1056,81 @@ __global__ __launch_bounds__(64 * NS, BF16 || DC == 64 ? 2 : 1) void k_backward_
   int32_t start, len, tile, tiles;
   const int32_t kh = blockIdx.x;
   if (!find_tile(a, block_slot(a), 32, start, len, tile, tiles)) {
-    clear_rest(a, block_slot(a), tiles, [&](int32_t r) {
-      clear_row(a.dk, r, blockIdx.x, a.D * G::kElem);
-      clear_row(a.dv, r, blockIdx.x, a.D * G::kElem);
-    });
+    if (blockIdx.y == 0)
+      clear_rest(a, block_slot(a), tiles, [&](int32_t r) {
+        clear_row(a.dk, r, blockIdx.x, a.D * G::kElem);
+        clear_row(a.dv, r, blockIdx.x, a.D * G::kElem);
+      });
     return;
   }
   const int lane = threadIdx.x & 63;
   const int split = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int32_t w0 = tile * 32, key = w0 + (lane & 31);
+  // as many work groups as give each of their waves kSteps steps
+  const int32_t steps = (len - w0 + 31) / 32 * (a.Hq / a.Hkv);
+  const int32_t splits = SPLIT ? min(a.splits, (steps + kSteps * NS - 1) / (kSteps * NS)) : 1;
+  if (SPLIT && (int32_t)blockIdx.y >= splits) return;
   unsigned char* mine = lds + split * P::kBuffers * P::kBuf;
   uint4 k[G::kPairs], v[G::kPairs];
   load_operand<BF16, DC>(a.k, start, kh, w0, len, a.D, k);
   load_operand<BF16, DC>(a.v, start, kh, w0, len, a.D, v);
   f32x16_t dk[G::kTiles], dv[G::kTiles];
   bool careful = false;
-  backward_kv_pass<BF16, DC, NS>(careful, a, start, len, kh, w0, split, mine, k, v, dk, dv);
+  backward_kv_pass<BF16, DC, NS>(careful, a, start, len, kh, w0, SPLIT ? blockIdx.y * NS + split : split, splits * NS,
+                                 mine, k, v, dk, dv);
   careful = __syncthreads_or(careful);
-  if constexpr (NS > 1) {
-    join<NS, G::kTiles>(dk, split, lds);
-    join<NS, G::kTiles>(dv, split, lds);
+  join<NS, G::kTiles>(dk, split, lds);
+  join<NS, G::kTiles>(dv, split, lds);
+  if constexpr (SPLIT) {
+    // the last work group to arrive adds the sums of all, in their order
+    const int64_t group = (int64_t)blockIdx.z * a.Hkv + kh;
+    uint64_t* parts = (uint64_t*)a.parts + group * a.splits * (2 * G::kTiles * 512) + lane;
+    if (split == 0) {
+      uint64_t* p = parts + (int64_t)blockIdx.y * (2 * G::kTiles * 512);
+#pragma unroll
+      for (int t = 0; t < 2 * G::kTiles; ++t) {
+        const f32x16_t& x = t < G::kTiles ? dk[t % G::kTiles] : dv[t % G::kTiles];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          __hip_atomic_store(p + (t * 8 + j) * 64, __builtin_bit_cast(uint64_t, (f32x2_t){x[2 * j], x[2 * j + 1]}),
+                             __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // (all have reached the memory)
+      if (lane == 0) {
+        const uint32_t me = careful ? 0x10001u : 1u;
+        *(uint32_t*)lds = me + __hip_atomic_fetch_add(a.arrived + group, me, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+    }
+    __syncthreads();
+    const uint32_t arrived = *(const uint32_t*)lds;
+    if ((int32_t)(arrived & 0xffff) != splits) return;
+    careful = arrived >> 16;
+#pragma unroll 1
+    for (int t = split; t < 2 * G::kTiles; t += NS) {
+      f32x16_t x = {};
+      for (int32_t z = 0; z < splits; ++z) {
+        const uint64_t* p = parts + (int64_t)(z * 2 * G::kTiles + t) * 512;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const f32x2_t y = __builtin_bit_cast(f32x2_t, __hip_atomic_load(p + 64 * j, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+          x[2 * j] += y[0];
+          x[2 * j + 1] += y[1];
+        }
+      }
+      const bool second = t >= G::kTiles;
+      const Tensor& out = second ? a.dv : a.dk;
+      if (key < len)
+        store_tile<BF16>(row_ptr(out, (int64_t)start + key, kh), second ? t - G::kTiles : t, a.D, x, second ? 1.f : a.scale);
+    }
+    if (!careful) return;
+    __syncthreads();
     if (split > 0) return;
-  }
-  if (key < len) {
-    store_rows<BF16, DC>(a.dk, (int64_t)start + key, kh, a.D, dk, a.scale);
-    store_rows<BF16, DC>(a.dv, (int64_t)start + key, kh, a.D, dv, 1.f);
+  } else {
+    if (split > 0) return;
+    if (key < len) {
+      store_rows<BF16, DC>(a.dk, (int64_t)start + key, kh, a.D, dk, a.scale);
+      store_rows<BF16, DC>(a.dv, (int64_t)start + key, kh, a.D, dv, 1.f);
+    }
   }
   if (careful) {
     __threadfence_block();
