@@ -242,7 +242,7 @@ __global__ __launch_bounds__(kSortThreads) void k_order_scan(const void* tok, in
 }
 
 // Larger batches and tables: radix passes over the mixed ids, `per` positions a block: digit counts of every
-// block first (hist[digit][block]), then the stable scatter. src_keys is null
+// block first (hist[block][digit]), then the stable scatter. src_keys is null
 // in the first pass, which reads the ids.
 __device__ __forceinline__ int32_t load_key(const void* tok, int idx64, const int32_t* src_keys, int64_t q, int32_t V) {
   return src_keys ? src_keys[q] : id_key(tok, idx64, q, V);
@@ -259,7 +259,7 @@ __global__ __launch_bounds__(kSortThreads) void k_order_count(const void* tok, i
   for (int64_t q = lo + threadIdx.x; q < hi; q += kSortThreads)
     atomicAdd(&cnt[(mixed(load_key(tok, idx64, src_keys, q, V), V, id_bits) >> shift) & (digits - 1)], 1u);
   __syncthreads();
-  for (int j = threadIdx.x; j < digits; j += kSortThreads) hist[(int64_t)j * gridDim.x + blockIdx.x] = cnt[j];
+  for (int j = threadIdx.x; j < digits; j += kSortThreads) hist[blockIdx.x * digits + j] = cnt[j];
 }
 
 constexpr int kHeldRounds = 4;   // rounds of a wave whose keys stay in registers between the two walks
@@ -291,7 +291,7 @@ __global__ __launch_bounds__(kSortThreads) void k_order_scatter(const void* tok,
     for (int b0 = 0; b0 < nb; b0 += 16) {   // (16 loads in flight)
       uint32_t h[16];
 #pragma unroll
-      for (int j = 0; j < 16; ++j) h[j] = b0 + j < nb ? hist[(int64_t)threadIdx.x * nb + b0 + j] : 0u;
+      for (int j = 0; j < 16; ++j) h[j] = b0 + j < nb ? hist[(b0 + j) * digits + threadIdx.x] : 0u;
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
         if (b0 + j < (int)blockIdx.x) before += h[j];
