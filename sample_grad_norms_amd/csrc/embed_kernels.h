@@ -386,6 +386,9 @@ __device__ __forceinline__ float wave_sum_f32(float v) {
   return v;
 }
 
+// A wave copies kLookupRows rows at a time, 16 bytes a lane. Bound by HBM, which the
+// distinct rows and the output cross once: 16384 rows of 2048 bf16 out of 131072 take
+// 20 us, 134 MB at 6.6 TB/s; 37 rows of 1000 floats 3 us, the latency of two loads.
 constexpr int kLookupRows = 4;   // rows a wave has in flight
 
 template <bool BF16>
@@ -565,6 +568,15 @@ __device__ __forceinline__ void put_part(const RunArgs& a, int32_t chunk, int sl
 constexpr int kRowsAhead = 8;    // rows a wave loads ahead of adding them
 constexpr int kFillRows = 64;    // table rows a clearing block looks at
 
+// One wave an item: the rows of a chunk's positions in the groups' order, a slice of
+// their columns, 16 bytes a lane and kRowsAhead rows in flight, added in registers
+// until a run ends. Runs inside a chunk are finished here, so most rows of G are read
+// once and leave nothing but a float (norm) or their table row (gradient); chunks of 32
+// instead of 16 positions halve the pieces of cut runs but took longer, as one window of
+// 64 lanes then no longer describes a chunk. The gradient clears the rows without an id
+// in blocks behind the items', with stores that pass the caches. Bound by HBM: norm of
+// 16384 positions of 2048 bf16 18 us (67 MB, 3.7 TB/s, of which 4 us are the latency of
+// keys, positions and first rows), gradient into 131072 rows 110 us (604 MB, 5.5 TB/s).
 template <bool BF16, int MODE>
 __global__ __launch_bounds__(256) void k_run_sums(RunArgs a) {
   using R = Row<BF16>;
@@ -651,7 +663,8 @@ __global__ __launch_bounds__(256) void k_run_sums(RunArgs a) {
 
 // Joins the pieces of each cut run: the block of the chunk that the run starts
 // in adds that chunk's tail and the heads of the chunks after it, four waves
-// in turn, their sums added in wave order.
+// in turn, their sums added in wave order. Bound by latency: 7 us for 4096 items, most
+// of which find no cut run.
 template <bool BF16, int MODE>
 __global__ __launch_bounds__(256) void k_run_join(RunArgs a) {
   using R = Row<BF16>;
@@ -716,7 +729,8 @@ __global__ __launch_bounds__(256) void k_run_join(RunArgs a) {
 }
 
 // n_i (+)= s^2 times the sum of the sample's values, in fp64. Long samples are
-// summed by gridDim.x blocks; the last one to arrive adds their parts in order.
+// summed by gridDim.x blocks; the last one to arrive adds their parts in order. Bound by
+// latency: 4.4 us for 4 samples of 16384 values.
 __global__ __launch_bounds__(1024) void k_norm_sum(const float* val, int64_t N, int32_t T, int32_t slices, double scale2,
                                                    float* n, int accumulate, double* parts, uint32_t* arrived) {
   __shared__ double part[16];
@@ -787,7 +801,8 @@ __device__ __forceinline__ void add_rows(float (&acc)[Row<BF16>::kElems], const 
 }
 
 // Norm of samples of at most kSmallIds positions, a block a sample. The first
-// position of an id stands for its row.
+// position of an id stands for its row. Bound by latency: 3 samples of 61 positions of
+// 256 floats take 6.2 us, against four launches and 31 us with an order.
 template <bool BF16>
 __global__ __launch_bounds__(1024) void k_norm_small(const void* tok, int idx64, const char* G, int32_t T, int32_t V, int32_t d,
                                                      double scale2, float* n, int accumulate) {
@@ -837,7 +852,9 @@ __global__ __launch_bounds__(1024) void k_norm_small(const void* tok, int idx64,
 
 constexpr int kSmallRows = 16;   // table rows of a block, four a wave
 
-// Gradient of the table from at most kSmallIds positions in all.
+// Gradient of the table from at most kSmallIds positions in all: every block looks for
+// its rows among all ids. Bound by latency: 183 positions into 2048 rows of 256 floats
+// take 6.7 us.
 template <bool BF16>
 __global__ __launch_bounds__(256) void k_grad_small(const void* tok, int idx64, RunArgs a) {
   using R = Row<BF16>;
