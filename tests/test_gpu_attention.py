@@ -282,6 +282,36 @@ def test_a_row_that_is_not_finite_leaves_the_rows_before_it(Hq, Hkv, dtype, valu
                 assert not bool(dv[:row + 1, :, 5].isfinite().any())
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("Hq,Hkv,D", [(4, 2, 96), (64, 64, 88), (3, 1, 128), (64, 64, 120)])
+def test_wider_rows_that_are_not_finite_leave_the_others(Hq, Hkv, D, dtype):
+    import sample_grad_norms_amd as dp
+    N = 700 if Hq == 64 else 330
+    q, k, v, do = (x.to(dev()) for x in make(N, Hq, Hkv, D, dtype, 19))
+    o, lse = dp.attention_forward(q, k, v)
+    dq, dk, dv = dp.attention_backward(do, q, k, v, o, lse)
+    at, val = N - 75, torch.tensor([math.nan, math.inf, -math.inf], device=dev()).to(dtype)
+    for name in ("k", "v"):
+        args = {"q": q, "k": k.clone(), "v": v.clone()}
+        args[name][at, :, :3] = val
+        o2, _ = dp.attention_forward(**args)
+        assert torch.equal(o2[:at], o[:at]), name
+        dq2, _, _ = dp.attention_backward(do, args["q"], args["k"], args["v"], o, lse)
+        assert torch.equal(dq2[:at], dq[:at]), name
+    for name in ("do", "q"):
+        args = {"do": do.clone(), "q": q.clone()}
+        args[name][at, :, :3] = val
+        _, dk2, dv2 = dp.attention_backward(args["do"], args["q"], k, v, o, lse)
+        assert torch.equal(dk2[at + 1:], dk[at + 1:]) and torch.equal(dv2[at + 1:], dv[at + 1:]), name
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("lengths", [[400, 397], [31, 1, 0, 801]])
+def test_many_heads_of_88_columns(lengths, dtype):
+    """Work groups of 128 queries, and one for each 32 keys, for rows of 65 to 96 columns."""
+    test_forward_and_backward(lengths, 64, 32, 88, dtype)
+
+
 @pytest.mark.parametrize("cu", [[0, 0, 0], [130, 130], [0, 64, 128], [100, 101, 133]])
 def test_rows_of_no_sequence_are_cleared(cu):
     """No sequence at all, tiles that fill every slot, one row among many."""
