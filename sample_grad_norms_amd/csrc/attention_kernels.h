@@ -255,17 +255,20 @@ __device__ __forceinline__ f32x16_t mfma_chunk(const uint4& a, const uint4& b, f
   }
 }
 
-// 32 rows of LDS (at row r0, a multiple of 8) times the stationary operand: X f^T.
+// 32 rows of LDS (at row r0, a multiple of 8) times the stationary operand: X f^T. A
+// wave here yields to one in its softmax or second products (dq, dk and dv 2 % faster).
 template <bool BF16, int DC>
 __device__ __forceinline__ f32x16_t rows_times(const unsigned char* lds, int r0, const uint4 (&f)[Geo<BF16, DC>::kPairs]) {
   using G = Geo<BF16, DC>;
   const int lane = threadIdx.x & 63, row = lane & 31, g = lane >> 5;
   f32x16_t c = {};
+  __builtin_amdgcn_s_setprio(0);
 #pragma unroll
   for (int i = 0; i < G::kPairs; ++i) {
     const uint4 a = *(const uint4*)(lds + (row * G::kPitch + (swizzle<BF16, DC>(2 * i + g, row) << 4)) + r0 * G::kPitch);
     c = mfma_chunk<BF16>(a, f[i], c);
   }
+  __builtin_amdgcn_s_setprio(1);
   return c;
 }
 
