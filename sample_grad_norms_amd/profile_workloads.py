@@ -18,6 +18,10 @@ NAME is one of:
                       the norm path, backward 2 of sum c_i l_i, noise, Adam
   dpsgd_step_tokens   the same from token ids, with the library's embedding table
                       (32768 rows, trained) and attention
+  embedding           lookup, order, per-sample norm and table gradient, B=4, T=4096,
+                      d=2048, 131072 rows, ids by a vocabulary's frequencies, bf16
+  attention           causal attention and its gradients, B=4, T=2048, 32 heads over
+                      8, head width 64, bf16
 --calib-copy first runs one 1 GiB device-to-device copy, the reference the
 counter summaries scale FETCH_SIZE and WRITE_SIZE by.
 """
@@ -32,7 +36,8 @@ if ROOT not in sys.path:
     sys.path.insert(0, ROOT)
 
 NAMES = ("long_context_hutch", "long_context_exact", "hutchpp", "single_layer", "single_layer_gram", "shared_stack",
-         "sign_stack", "lora_routed", "dpsgd_step", "dpsgd_step_tokens")
+         "sign_stack", "lora_routed", "dpsgd_step", "dpsgd_step_tokens",
+         "embedding", "attention")
 
 
 def main() -> None:
@@ -89,6 +94,27 @@ def main() -> None:
             rc.add_noise()
             opt.step()
             opt.zero_grad(set_to_none=True)
+    elif a.name == "embedding":
+        from workloads import llama_block as lb
+        g = torch.Generator().manual_seed(92)
+        tok, _ = lb.token_batch(93, 4, 4096, 131072, 2, device=dev)
+        W = torch.randn(131072, 2048, generator=g).to(dev, torch.bfloat16)
+        G = torch.randn(4, 4096, 2048, generator=g).to(dev, torch.bfloat16)
+        c = torch.full((4,), 0.5, device=dev)
+
+        def fn():
+            dp.embed_lookup(tok, W)
+            order = dp.embed_order(tok, 131072)
+            dp.embed_norm(order, G)
+            dp.embed_grad(order, G, weights=c)
+    elif a.name == "attention":
+        g = torch.Generator().manual_seed(94)
+        q, do = (torch.randn(8192, 32, 64, generator=g).to(dev, torch.bfloat16) for _ in range(2))
+        k, v = (torch.randn(8192, 8, 64, generator=g).to(dev, torch.bfloat16) for _ in range(2))
+
+        def fn():
+            o, lse = dp.attention_forward(q, k, v, sequences=4)
+            dp.attention_backward(do, q, k, v, o, lse, sequences=4)
     else:
         pr = workloads.config2(device=dev)
         fn = (lambda: dp.exact(pr.A, pr.G, route="gram")) if a.name.endswith("gram") else (lambda: dp.hutch(pr.A, pr.G, pr.P))

@@ -64,7 +64,7 @@ def source_hash(files: Optional[List[str]] = None) -> str:
 def short_name(name: str) -> str:
     if COPY_KERNEL in name:
         return "copyBuffer"
-    m = re.search(r"dpn::(k_\w+)(<[^>]*>)?", name)
+    m = re.search(r"dpn::(?:attn::|embed::)?(k_\w+)(<[^>]*>)?", name)
     if m:
         return m.group(1) + (m.group(2) or "")
     return name.split("(")[0][:60]
