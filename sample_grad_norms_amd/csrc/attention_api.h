@@ -100,6 +100,19 @@ constexpr int64_t kRowsMost = 1536;
 template <bool BF16, int DC>
 constexpr bool kRowsAlways = !BF16 && DC == 64;
 
+// Groups of 32 keys of one key head, at most, and the steps of 32 queries of the first
+// of a sequence of average length (the same with and without offsets).
+int64_t key_groups(const attn::Args& a) { return ((int64_t)a.N / 32 + a.S) * a.Hkv; }
+int64_t key_steps(const attn::Args& a) { return (int64_t)a.N / a.S / 32 * (a.Hq / a.Hkv); }
+
+// dk and dv of bf16 rows of up to 64 columns: eight waves a work group instead of four
+// while work groups that share keys would be too many and those of their own too few
+// (below), if the chains are long. us, eight waves against four: B = 2, T = 2048, 32/4
+// heads 125 against 168, 8/4 heads 38 against 44; 8 x 500 rows, 8/4 heads 28 against 19.
+// Wider rows leave eight waves one work group a CU.
+constexpr int64_t kKeysMost = 600;
+bool keys_eight(const attn::Args& a) { return key_groups(a) <= kKeysMost && key_steps(a) >= 128; }
+
 // dk and dv: the work groups that share the queries of 32 keys of one key head, at
 // most (short ends take fewer, see k_backward_kv): about 1.5 for each place on the CUs,
 // and three where places and keys are nearly as many but the chains are long. Odd, so
@@ -107,16 +120,15 @@ constexpr bool kRowsAlways = !BF16 && DC == 64;
 // group: T = 2048, 32/4 heads D = 128 126 (3) against 283, 3/1 heads D = 64 of 811 + 443
 // rows 14 (19) against 26; float32 T = 2048, 16/4 heads D = 64 171 (3) against 293, 8/2
 // heads D = 128 of 1500 + 777 rows 176 (3) against 440; B = 2, T = 2048, 32/4 heads
-// D = 64 135 (3) against 168, but 10/5 heads 57 (2) against 47; T = 1024, 16/4 heads
-// 22 (5), 30 (8).
+// D = 128 232 (3) against 359, but 10/5 heads D = 64 57 (2) against 47; T = 1024, 16/4
+// heads D = 64 22 (5), 30 (8).
 template <bool BF16, int DC>
 int32_t key_splits(const attn::Args& a) {
   const int64_t places = 256 * (attn::OwnRows<BF16, DC, 4, 256>::kLds <= 80 * 1024 ? 2 : 1);
-  const int64_t groups = ((int64_t)a.N / 32 + a.S) * a.Hkv;
+  const int64_t groups = key_groups(a);
   const int64_t splits = 3 * places / (4 * groups) * 2 + 1;
-  if (splits > 1) return (int32_t)splits;
-  const int64_t steps = (int64_t)a.N / a.S / 32 * (a.Hq / a.Hkv);
-  return steps >= 256 && 4 * groups < 5 * places ? 3 : 1;
+  if (splits > 1 || (BF16 && DC == 64)) return (int32_t)splits;
+  return key_steps(a) >= 256 && 4 * groups < 5 * places ? 3 : 1;
 }
 int32_t key_splits(const attn::Args& a, bool bf16) {
   if (bf16) return a.D <= 64 ? key_splits<true, 64>(a) : a.D <= 96 ? key_splits<true, 96>(a) : key_splits<true, 128>(a);
@@ -171,6 +183,12 @@ hipError_t run_attn_backward(const attn::Args& a, hipStream_t stream) {
     return launch_slots(a, 32, a.splits, [&](const attn::Args& x, dim3 grid) {
       attn::k_backward_kv<BF16, DC, 4, true><<<grid, 256, 0, stream>>>(x);
     });
+  if constexpr (BF16 && DC == 64) {
+    if (keys_eight(a))
+      return launch_slots(a, 32, 1, [&](const attn::Args& x, dim3 grid) {
+        attn::k_backward_kv<BF16, DC, 8, false><<<grid, 512, 0, stream>>>(x);
+      });
+  }
   return launch_slots(a, 32, 1, [&](const attn::Args& x, dim3 grid) {
     attn::k_backward_kv<BF16, DC, 4, false><<<grid, 256, 0, stream>>>(x);
   });

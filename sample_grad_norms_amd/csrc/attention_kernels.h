@@ -1060,11 +1060,13 @@ __device__ __forceinline__ void backward_kv_pass(bool& careful, const Args& a, i
 }
 
 // dk and dv by rows: 32 keys of one key head, all query heads of the key head and
-// all queries from the diagonal on, by four waves with LDS of their own: the keys stay in
+// all queries from the diagonal on, by NS waves with LDS of their own: the keys stay in
 // registers, and four products a step (S, dP, dV, dK) read 32 rows of q and dO. Bound by
-// those reads: a wave uses each for one MFMA, and 128 bytes a clock of LDS feed about half
-// of the MFMA rate. B = 4, T = 2048, 32/8 heads, D = 64: 250 us, 550 TF/s;
-// 16/4 heads, D = 128: 280 us. SPLIT: a few such work groups share
+// the chain of a step, reads, products, exponentials, products, of which the registers
+// allow two waves a SIMD; the LDS is busy half of the time, and a fifth fewer reads (lse
+// and delta as a column of the first products) gained 2 % at D = 64 and lost 5 % at 128.
+// B = 4, T = 2048, 32/8 heads, D = 64: 243 us, 566 TF/s; 16/4 heads, D = 128: 276 us.
+// SPLIT: a few such work groups share
 // the steps, as many as leave each wave kSteps of them, and the last to arrive adds
 // their sums in a fixed order. The sums and the counter go past the L2 caches, which
 // the XCDs do not share: fences, which write back and empty them, cost more than the

@@ -312,6 +312,12 @@ def test_many_heads_of_88_columns(lengths, dtype):
     test_forward_and_backward(lengths, 64, 32, 88, dtype)
 
 
+@pytest.mark.parametrize("D", [40, 64])
+def test_long_chains_of_few_keys(D):
+    """Groups of 32 keys about as many as the places on the CUs, long chains of queries."""
+    test_forward_and_backward([1040], 64, 16, D, torch.bfloat16)
+
+
 @pytest.mark.parametrize("cu", [[0, 0, 0], [130, 130], [0, 64, 128], [100, 101, 133]])
 def test_rows_of_no_sequence_are_cleared(cu):
     """No sequence at all, tiles that fill every slot, one row among many."""
