@@ -692,7 +692,7 @@ def attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seql
     N, Hq, D = q.shape
     device = q.device
     if out is None:
-        out = torch.empty((N, Hq, D), dtype=q.dtype, device=device)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
         lse = torch.empty((Hq, N), dtype=torch.float32, device=device)
     else:
         _need(lse, "lse", 2, torch.float32)
@@ -724,7 +724,7 @@ def attention_backward(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: to
     if tuple(lse.shape) != (Hq, N) or lse.device != device:
         raise ValueError(f"lse must be [Hq={Hq}][N={N}] on q's device")
     if out is None:
-        dq, dk, dv = (torch.empty(t.shape, dtype=dtype, device=device) for t in (q, k, v))
+        dq, dk, dv = (torch.empty_like(t, memory_format=torch.contiguous_format) for t in (q, k, v))
     else:
         dq, dk, dv = out
     tdq, tdk, tdv = (_heads(t, n, dtype, device, x.shape) for t, n, x in ((dq, "dq", q), (dk, "dk", k), (dv, "dv", k)))
