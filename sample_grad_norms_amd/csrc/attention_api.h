@@ -130,9 +130,23 @@ int32_t key_splits(const attn::Args& a) {
   if (splits > 1 || (BF16 && DC == 64)) return (int32_t)splits;
   return key_steps(a) >= 256 && 4 * groups < 5 * places ? 3 : 1;
 }
-int32_t key_splits(const attn::Args& a, bool bf16) {
-  if (bf16) return a.D <= 64 ? key_splits<true, 64>(a) : a.D <= 96 ? key_splits<true, 96>(a) : key_splits<true, 128>(a);
-  return a.D <= 64 ? key_splits<false, 64>(a) : a.D <= 96 ? key_splits<false, 96>(a) : key_splits<false, 128>(a);
+
+// dq: the same for the work groups that share the keys of 32 queries of one head. (Where
+// there are any, there are such of dk and dv too, whose launch adds their sums.)
+template <bool BF16, int DC>
+int32_t query_splits(const attn::Args& a) {
+  const int64_t places = 256 * (attn::OwnRows<BF16, DC, 4, 0>::kLds <= 80 * 1024 ? 2 : 1);
+  return (int32_t)(3 * places / (4 * ((int64_t)a.N / 32 + a.S) * a.Hq) * 2 + 1);
+}
+
+template <bool BF16, int DC>
+void set_splits(attn::Args& a) {
+  a.splits = key_splits<BF16, DC>(a);
+  a.qsplits = a.splits > 1 ? query_splits<BF16, DC>(a) : 1;
+}
+void set_splits(attn::Args& a, bool bf16) {
+  if (bf16) a.D <= 64 ? set_splits<true, 64>(a) : a.D <= 96 ? set_splits<true, 96>(a) : set_splits<true, 128>(a);
+  else a.D <= 64 ? set_splits<false, 64>(a) : a.D <= 96 ? set_splits<false, 96>(a) : set_splits<false, 128>(a);
 }
 
 // One launch, or more where a grid's z dimension does not hold the slots.
@@ -170,8 +184,12 @@ hipError_t run_attn_backward_q(const attn::Args& a, hipStream_t stream) {
         attn::k_backward_q<BF16, DC><<<grid, 256, 0, stream>>>(x);
       });
   }
+  if (a.qsplits > 1)
+    return launch_slots(a, 32, rep * a.qsplits, [&](const attn::Args& x, dim3 grid) {
+      attn::k_backward_q_rows<BF16, DC, 4, true><<<grid, 256, 0, stream>>>(x);
+    });
   return launch_slots(a, 32, rep, [&](const attn::Args& x, dim3 grid) {
-    attn::k_backward_q_rows<BF16, DC, 4><<<grid, 256, 0, stream>>>(x);
+    attn::k_backward_q_rows<BF16, DC, 4, false><<<grid, 256, 0, stream>>>(x);
   });
 }
 
@@ -181,6 +199,7 @@ hipError_t run_attn_backward(const attn::Args& a, hipStream_t stream) {
   if (he != hipSuccess) return he;
   if (a.splits > 1)
     return launch_slots(a, 32, a.splits, [&](const attn::Args& x, dim3 grid) {
+      if (a.qsplits > 1) grid.z += (uint32_t)(((int64_t)x.slots * a.Hq + grid.x * grid.y - 1) / (grid.x * grid.y));
       attn::k_backward_kv<BF16, DC, 4, true><<<grid, 256, 0, stream>>>(x);
     });
   if constexpr (BF16 && DC == 64) {
@@ -195,20 +214,25 @@ hipError_t run_attn_backward(const attn::Args& a, hipStream_t stream) {
 }
 
 // The workspace of a backward pass (its bytes; null to ask for them alone): the pairs,
-// and for shared keys the sums and counters.
+// and where work groups share keys or queries their sums, counters and marks.
 size_t backward_layout(attn::Args& a, bool bf16, void* ws) {
-  const size_t pairs = align_up((size_t)a.N * a.Hq * 8);
-  a.pairs = (float*)ws;
-  a.splits = key_splits(a, bf16);
-  if (a.splits < 2) return pairs;
-  a.groups = (int32_t)((slots_of(a, 32) + 1) * a.Hkv);
-  const size_t counts = align_up((size_t)a.groups * 4);
-  const size_t columns = a.D <= 64 ? 64 : a.D <= 96 ? 96 : 128;
-  if (ws) {
-    a.arrived = (uint32_t*)((char*)ws + pairs);
-    a.parts = (float*)((char*)ws + pairs + counts);
-  }
-  return pairs + counts + align_up((size_t)a.groups * a.splits * 2 * 32 * columns * 4);
+  set_splits(a, bf16);
+  size_t bytes = 0;
+  const auto take = [&](size_t n) {
+    char* p = ws ? (char*)ws + bytes : nullptr;
+    bytes += align_up(n);
+    return p;
+  };
+  a.pairs = (float*)take((size_t)a.N * a.Hq * 8);
+  if (a.splits < 2) return bytes;
+  const size_t slots = (size_t)slots_of(a, 32) + 1, tile = 32 * 4 * (a.D <= 64 ? 64 : a.D <= 96 ? 96 : 128);
+  a.groups = (int32_t)(slots * a.Hkv);
+  a.arrived = (uint32_t*)take(slots * a.Hkv * 4);
+  a.parts = (float*)take(slots * a.Hkv * a.splits * 2 * tile);
+  if (a.qsplits < 2) return bytes;
+  a.qcareful = (uint32_t*)take(slots * a.Hq * a.qsplits * 4);
+  a.qparts = (float*)take(slots * a.Hq * a.qsplits * tile);
+  return bytes;
 }
 
 }  // namespace

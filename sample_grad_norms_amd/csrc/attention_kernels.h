@@ -53,6 +53,11 @@ struct Args {
   int32_t slots;      // tile slots per head
   int32_t slot0;      // first slot of the launch
   int32_t clear;      // set rows of no sequence to zero
+  // Backward pass of small calls. dq where work groups share a tile's keys (the second
+  // launch adds their sums):
+  int32_t qsplits;    // work groups of 32 queries of one head, at most
+  float* qparts;      // their sums, [slot][head][split][tile][1024]
+  uint32_t* qcareful; // [slot][head][split], whether rows were cleaned
   // dk and dv where work groups share their keys' queries:
   int32_t splits;     // work groups of 32 keys of one key head, and
   int32_t groups;     // the number of such groups of 32 keys
@@ -783,10 +788,10 @@ __device__ __forceinline__ float dot_chunk(const uint4& x, const uint4& y, float
   return s;
 }
 
-// One wave's pass over the keys for dq, as forward_pass.
-template <bool BF16, int DC, int NS, int BUFFERS>
+// One wave's pass for dq over the keys k0, k0 + 32 waves, .., as forward_pass.
+template <bool BF16, int DC, int BUFFERS>
 __device__ __forceinline__ void backward_q_pass(bool careful, const Args& a, int32_t start, int32_t len, int32_t kh,
-                                                int32_t w0, int32_t k0, unsigned char* mine, const uint4 (&q)[Geo<BF16, DC>::kPairs],
+                                                int32_t w0, int32_t k0, int32_t waves, unsigned char* mine, const uint4 (&q)[Geo<BF16, DC>::kPairs],
                                                 const uint4 (&dO)[Geo<BF16, DC>::kPairs], float lse, float delta,
                                                 f32x16_t (&acc)[Geo<BF16, DC>::kTiles]) {
   using G = Geo<BF16, DC>;
@@ -805,10 +810,10 @@ __device__ __forceinline__ void backward_q_pass(bool careful, const Args& a, int
 #pragma unroll
   for (int t = 0; t < G::kTiles; ++t) acc[t] = f32x16_t{};
   int buf = 0;
-  for (; k0 <= w0; k0 += 32 * NS) {
+  for (; k0 <= w0; k0 += 32 * waves) {
     own_staged();
-    const bool more = k0 + 32 * NS <= w0;
-    if (BUFFERS == 2 && more) fetch(k0 + 32 * NS, base + (buf ^ 1) * kBuf);
+    const bool more = k0 + 32 * waves <= w0;
+    if (BUFFERS == 2 && more) fetch(k0 + 32 * waves, base + (buf ^ 1) * kBuf);
     unsigned char* lk = mine + buf * kBuf;
     unsigned char* lv = lk + kStage;
     f32x16_t s = rows_times<BF16, DC>(lk, 0, q);
@@ -827,7 +832,7 @@ __device__ __forceinline__ void backward_q_pass(bool careful, const Args& a, int
       buf ^= 1;
     } else if (more) {
       own_staged();   // (the reads of this step are done)
-      fetch(k0 + 32 * NS, base);
+      fetch(k0 + 32 * waves, base);
     }
   }
 }
@@ -912,7 +917,7 @@ __global__ __launch_bounds__(256, !BF16 ? 1 : DC == 64 ? 3 : 2) void k_backward_
     buf ^= 1;
   }
   const bool careful = not_all_finite(acc);   // see k_forward
-  if (careful) backward_q_pass<BF16, DC, 1, 1>(true, a, start, len, kh, w0, 0, lds + wv * P::kStage, q, dO, lse, delta, acc);
+  if (careful) backward_q_pass<BF16, DC, 1>(true, a, start, len, kh, w0, 0, 1, lds + wv * P::kStage, q, dO, lse, delta, acc);
   if (query < len) store_rows<BF16, DC>(a.dq, (int64_t)start + query, h, a.D, acc, a.scale);
   if (careful) {
     __threadfence_block();
@@ -920,26 +925,37 @@ __global__ __launch_bounds__(256, !BF16 ? 1 : DC == 64 ? 3 : 2) void k_backward_
   }
 }
 
-// The same by rows, as k_forward_rows (float32, 515 + 130 + 62 rows, 6/3 heads, D = 80:
-// 37 us, of which a chain of five steps of fp32 MFMAs takes most).
-template <bool BF16, int DC, int NS>
+// Work groups that share the keys of the 32 queries from w0 on, for kSteps steps a wave.
+constexpr int kSteps = 2;
+__device__ __forceinline__ int32_t query_splits(const Args& a, int32_t w0, int ns) {
+  return min(a.qsplits, (w0 / 32 + kSteps * ns) / (kSteps * ns));
+}
+
+// The same by rows, as k_forward_rows. SPLIT: a few work groups share the keys, and the
+// second launch adds their sums in order (join_queries): float32, 515 + 130 + 62 rows,
+// 6/3 heads, D = 80 37 us alone, 22 shared; T = 1024, 8/4 heads, D = 64 39 either way;
+// bf16, T = 1024, 16/4 heads, D = 64 16 alone. Bound by the chain of a wave's steps and,
+// below 12 us, by its first loads.
+template <bool BF16, int DC, int NS, bool SPLIT>
 __global__ __launch_bounds__(64 * NS, BF16 ? 2 : 1) void k_backward_q_rows(Args a) {
   using G = Geo<BF16, DC>;
   using P = OwnRows<BF16, DC, NS, 0>;
   __shared__ __align__(1024) unsigned char lds[P::kLds];
   clear_arrived(a);
+  const int32_t kh = blockIdx.x, rep = a.Hq / a.Hkv;
+  const int32_t h = kh * rep + (SPLIT ? (int32_t)blockIdx.y % rep : (int32_t)blockIdx.y);
+  const int32_t z = SPLIT ? (int32_t)blockIdx.y / rep : 0;
   int32_t start, len, tile, tiles;
   if (!find_tile(a, block_slot(a), 32, start, len, tile, tiles)) {
-    clear_rest(a, block_slot(a), tiles, [&](int32_t r) {
-      clear_row(a.dq, r, blockIdx.x * gridDim.y + blockIdx.y, a.D * G::kElem);
-    });
+    if (z == 0) clear_rest(a, block_slot(a), tiles, [&](int32_t r) { clear_row(a.dq, r, h, a.D * G::kElem); });
     return;
   }
   tile = tiles - 1 - tile;
-  const int32_t kh = blockIdx.x, h = kh * gridDim.y + blockIdx.y;
   const int lane = threadIdx.x & 63, g = lane >> 5;
   const int split = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int32_t w0 = tile * 32, query = w0 + (lane & 31);
+  const int32_t splits = SPLIT ? query_splits(a, w0, NS) : 1;
+  if (SPLIT && z >= splits) return;
   uint4 q[G::kPairs], dO[G::kPairs];
   float delta = 0.f;
   {
@@ -955,27 +971,76 @@ __global__ __launch_bounds__(64 * NS, BF16 ? 2 : 1) void k_backward_q_rows(Args 
   if (query < len) {
     const int64_t at = (int64_t)h * a.N + start + query;
     lse = a.lse[at] * kLog2e;
-    if (g == 0 && split == 0) *(float2*)(a.pairs + 2 * at) = make_float2(lse, delta);
+    if (g == 0 && split == 0 && z == 0) *(float2*)(a.pairs + 2 * at) = make_float2(lse, delta);
   }
   f32x16_t acc[G::kTiles];
   unsigned char* mine = lds + split * P::kBuffers * P::kBuf;
   bool careful = false;
 #pragma unroll 1
   for (;;) {
-    backward_q_pass<BF16, DC, NS, P::kBuffers>(careful, a, start, len, kh, w0, 32 * split, mine, q, dO, lse, delta, acc);
+    backward_q_pass<BF16, DC, P::kBuffers>(careful, a, start, len, kh, w0, 32 * (z * NS + split), splits * NS, mine, q, dO,
+                                           lse, delta, acc);
     if (careful || !not_all_finite(acc)) break;
     careful = true;
   }
   careful = __syncthreads_or(careful);
-  if constexpr (NS > 1) {
-    join<NS, G::kTiles>(acc, split, lds);
-    if (split > 0) return;
+  join<NS, G::kTiles>(acc, split, lds);
+  if (split > 0) return;
+  if (SPLIT && splits > 1) {
+    const int64_t part = ((int64_t)blockIdx.z * a.Hq + h) * a.qsplits + z;
+    f32x4_t* p = (f32x4_t*)a.qparts + part * (G::kTiles * 256) + lane;
+#pragma unroll
+    for (int t = 0; t < G::kTiles; ++t)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        p[t * 256 + 64 * j] = f32x4_t{acc[t][4 * j], acc[t][4 * j + 1], acc[t][4 * j + 2], acc[t][4 * j + 3]};
+    if (lane == 0) a.qcareful[part] = careful;
+    return;
   }
   if (query < len) store_rows<BF16, DC>(a.dq, (int64_t)start + query, h, a.D, acc, a.scale);
   if (careful) {
     __threadfence_block();
     add_not_finite<BF16, true, true>(a.k, kh, a.dq, h, start, len, w0, a.D);
   }
+}
+
+// The sums of k_backward_q_rows' work groups that shared the keys of 32 queries of one
+// head, added in order: work groups behind the keys' own of the second launch.
+template <bool BF16, int DC, int NS>
+__device__ __forceinline__ void join_queries(const Args& a) {
+  using G = Geo<BF16, DC>;
+  const int64_t group = ((int64_t)((int32_t)blockIdx.z - a.slots) * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
+  if (group >= (int64_t)a.slots * a.Hq) return;
+  const int32_t slot = (int32_t)(group / a.Hq), h = (int32_t)(group % a.Hq);
+  int32_t start, len, tile, tiles;
+  if (!find_tile(a, slot, 32, start, len, tile, tiles)) return;
+  const int32_t w0 = (tiles - 1 - tile) * 32;
+  const int32_t splits = query_splits(a, w0, NS);
+  if (splits < 2) return;
+  const int lane = threadIdx.x & 63;
+  const int split = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int32_t query = w0 + (lane & 31);
+  uint32_t careful = 0;
+  for (int32_t z = 0; z < splits; ++z) careful |= a.qcareful[group * a.qsplits + z];
+#pragma unroll 1
+  for (int t = split; t < G::kTiles; t += NS) {
+    f32x16_t x = {};
+    for (int32_t z = 0; z < splits; ++z) {
+      const f32x4_t* p = (const f32x4_t*)a.qparts + ((group * a.qsplits + z) * G::kTiles + t) * 256 + lane;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const f32x4_t y = p[64 * j];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[4 * j + i] += y[i];
+      }
+    }
+    if (query < len) store_tile<BF16>(row_ptr(a.dq, (int64_t)start + query, h), t, a.D, x, a.scale);
+  }
+  if (!careful) return;
+  __syncthreads();
+  if (split > 0) return;
+  __threadfence_block();
+  add_not_finite<BF16, true, true>(a.k, h / (a.Hq / a.Hkv), a.dq, h, start, len, w0, a.D);
 }
 
 // One wave's pass for dk and dv over the queries of the key head's query heads, from
@@ -1071,12 +1136,12 @@ __device__ __forceinline__ void backward_kv_pass(bool& careful, const Args& a, i
 // their sums in a fixed order. The sums and the counter go past the L2 caches, which
 // the XCDs do not share: fences, which write back and empty them, cost more than the
 // split won (3/1 heads D = 64, 811 + 443 rows: 34 us with fences, 14 without, 26 unsplit).
-constexpr int kSteps = 2;
 template <bool BF16, int DC, int NS, bool SPLIT>
 __global__ __launch_bounds__(64 * NS, BF16 || DC == 64 ? 2 : 1) void k_backward_kv(Args a) {
   using G = Geo<BF16, DC>;
   using P = OwnRows<BF16, DC, NS, 256>;
   __shared__ __align__(1024) unsigned char lds[P::kLds];
+  if (SPLIT && (int32_t)blockIdx.z >= a.slots) return join_queries<BF16, DC, NS>(a);
   int32_t start, len, tile, tiles;
   const int32_t kh = blockIdx.x;
   if (!find_tile(a, block_slot(a), 32, start, len, tile, tiles)) {
