@@ -117,7 +117,7 @@ def summarize(trace_dir: str, fetch_dir: str, write_dir: str, out: str, cmds: Li
              "fetch_bytes_per_dispatch": {k: v for k, v in fetch.items() if k.startswith("k_")},
              "write_bytes_per_dispatch": {k: v for k, v in write.items() if k.startswith("k_")},
              "avg_us": {r["name"]: r["avg_us"] for r in stats}}
-    lines = [f"# {title}", "", "Commands (run from the repository root on the GPU box):", ""]
+    lines = [f"# {title}", "", "Commands (run from the repository root):", ""]
     lines += ["```", *cmds, "```", "", "## Kernel statistics (rocprofv3 --kernel-trace --stats)", "",
               "| kernel | calls | avg us | total ms | % |", "|---|---|---|---|---|"]
     shown = stats[:12] + [r for r in stats[12:] if r["name"].startswith("k_")]   # the library's kernels always
@@ -205,7 +205,7 @@ def counters_summary(pmc_dirs: List[str], out: str, cmds: List[str], title: str)
     and the ratios of DERIVED)."""
     means = counter_means(pmc_dirs)
     names = sorted({c for cs in means.values() for c in cs})
-    lines = [f"# {title}", "", "Commands (run from the repository root on the GPU box):", "", "```", *cmds, "```", "",
+    lines = [f"# {title}", "", "Commands (run from the repository root):", "", "```", *cmds, "```", "",
              "## Utilisation", "", "| kernel | " + " | ".join(l for (l, _, _, _) in DERIVED) + " |",
              "|---" * (len(DERIVED) + 1) + "|"]
     for k in sorted(means):
