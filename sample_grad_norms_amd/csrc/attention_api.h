@@ -100,6 +100,11 @@ constexpr int64_t kRowsMost = 1536;
 template <bool BF16, int DC>
 constexpr bool kRowsAlways = !BF16 && DC == 64;
 
+// Never more work groups than leave the waves of the longest possible sequence kSteps steps.
+int64_t most_splits(int64_t splits, int64_t steps) {
+  return std::max<int64_t>(1, std::min(splits, (steps + 4 * attn::kSteps - 1) / (4 * attn::kSteps)));
+}
+
 // Groups of 32 keys of one key head, at most, and the steps of 32 queries of the first
 // of a sequence of average length (the same with and without offsets).
 int64_t key_groups(const attn::Args& a) { return ((int64_t)a.N / 32 + a.S) * a.Hkv; }
@@ -126,7 +131,7 @@ template <bool BF16, int DC>
 int32_t key_splits(const attn::Args& a) {
   const int64_t places = 256 * (attn::OwnRows<BF16, DC, 4, 256>::kLds <= 80 * 1024 ? 2 : 1);
   const int64_t groups = key_groups(a);
-  const int64_t splits = 3 * places / (4 * groups) * 2 + 1;
+  const int64_t splits = most_splits(3 * places / (4 * groups) * 2 + 1, ((int64_t)a.N + 31) / 32 * (a.Hq / a.Hkv));
   if (splits > 1 || (BF16 && DC == 64)) return (int32_t)splits;
   return key_steps(a) >= 256 && 4 * groups < 5 * places ? 3 : 1;
 }
@@ -136,7 +141,7 @@ int32_t key_splits(const attn::Args& a) {
 template <bool BF16, int DC>
 int32_t query_splits(const attn::Args& a) {
   const int64_t places = 256 * (attn::OwnRows<BF16, DC, 4, 0>::kLds <= 80 * 1024 ? 2 : 1);
-  return (int32_t)(3 * places / (4 * ((int64_t)a.N / 32 + a.S) * a.Hq) * 2 + 1);
+  return (int32_t)most_splits(3 * places / (4 * ((int64_t)a.N / 32 + a.S) * a.Hq) * 2 + 1, ((int64_t)a.N + 31) / 32);
 }
 
 template <bool BF16, int DC>
