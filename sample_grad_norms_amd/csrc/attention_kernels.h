@@ -731,7 +731,7 @@ __global__ __launch_bounds__(256, BF16 ? 2 : 1) void k_forward(Args a) {
 #pragma unroll
           for (int r = 0; r < 16; ++r) acc[t][r] *= f;
       }
-      const float mc = m * c;
+      const float mc = m == -INFINITY ? 0.f : m * c;   // (scores of -infinity alone have weights of zero)
       // the next step's scores fill the matrix unit while this step's weights are computed
 #pragma unroll
       for (int t = 0; t < 2; ++t) next[t] = rows_times<BF16, DC>(lds + (buf ^ 1) * P::kStage, t * 32, q);

@@ -318,6 +318,23 @@ def test_long_chains_of_few_keys(D):
     test_forward_and_backward([1040], 64, 16, D, torch.bfloat16)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("Hq,Hkv,D", [(2, 1, 64), (64, 64, 64), (64, 64, 104)])
+def test_scores_of_minus_infinity_have_no_weight(Hq, Hkv, D, dtype):
+    """Keys whose scores are -infinity, for a query's first steps and all through:
+    the later rows are the attention of the other keys, the first have none."""
+    import sample_grad_norms_amd as dp
+    N, first = 700 if Hq == 64 else 330, 190
+    q, k, v, _ = make(N, Hq, Hkv, D, dtype, 21)
+    q = q.abs() + 0.125
+    k[:first, :, 3] = -math.inf
+    o, lse = dp.attention_forward(*(x.to(dev()) for x in (q, k, v)))
+    wo, wl, bo, bl = forward_reference(q[first:], k[first:], v[first:], [0, N - first], 1.0 / math.sqrt(D))
+    inside(o[first:], wo, bo, "o")
+    inside(lse[:, first:], wl, bl, "lse")
+    assert bool(o[:first].isnan().all()) and bool((lse[:, :first] == -math.inf).all())
+
+
 @pytest.mark.parametrize("cu", [[0, 0, 0], [130, 130], [0, 64, 128], [100, 101, 133]])
 def test_rows_of_no_sequence_are_cleared(cu):
     """No sequence at all, tiles that fill every slot, one row among many."""
