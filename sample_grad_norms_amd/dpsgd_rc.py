@@ -37,6 +37,16 @@ holds (a tied embedding). A use of a weight that the hooks cannot see (the
 weight passed to F.linear outside its module) is caught on the first step:
 the clipped gradient autograd accumulates must equal sum_i c_i G_i^T A_i
 from the recordings.
+
+Every row of a recording has to belong to one sample, samples in order: a
+module applied once to rows that all samples use (a learned position table
+looked up as pos(arange(T)) and added to every sample) has output gradients
+that are already summed over the samples, from which no norm of a sample can
+be had. Ids whose first dimension is not the batch are refused, and the first
+step's check finds what the shapes do not show: its first backward pass is of
+sum_i w_i l_i with powers of two w_i in random order, and G_i is what it gives
+divided by w_i, the same bits where a row is sample i's alone and something
+else where it is not.
 """
 from __future__ import annotations
 
@@ -93,9 +103,14 @@ class RandomizedClipping:
     verify_coverage: on the first step, check that each clipped weight's
     gradient from the second backward pass equals sum_i c_i G_i^T A_i from
     the recordings (it does not when the weight has a use the hooks cannot
-    see, such as F.linear called with it outside its module); a mismatch
-    raises RuntimeError. The check assumes nothing else adds to the weights'
-    .grad during that backward pass.
+    see, such as F.linear called with it outside its module, or when rows of
+    a recording are not one sample's); a mismatch raises RuntimeError. The
+    check assumes nothing else adds to the weights' .grad during that backward
+    pass.
+
+    Embedding ids are [B, ...]: one row of ids for each sample. Ids [B], one a
+    sample, look like the positions of B samples of length B, which only the
+    check can tell apart; without it they are refused ([B][1] is not).
     """
 
     def __init__(self, model: nn.Module, C: float, noise_multiplier: float, k: int = 32,
@@ -158,7 +173,8 @@ class RandomizedClipping:
         self._gen: Optional[torch.Generator] = None
         self._noise_gen: Optional[torch.Generator] = None
         self._batch = 0
-        self._verify = bool(verify_coverage)
+        self._verify = bool(verify_coverage)   # on the next step
+        self._verified = False
         self._pending: Optional[List[Tuple[nn.Parameter, torch.Tensor, torch.Tensor]]] = None
         # per table of the last step: (weight, order of its ids, output gradients, scale)
         self._table_recs: List[Tuple[nn.Parameter, dp.EmbedOrder, torch.Tensor, float]] = []
@@ -212,6 +228,9 @@ class RandomizedClipping:
         if not self._rec:
             raise RuntimeError("no forward pass was captured (run the model inside rc.capture())")
         B = losses.shape[0]
+        for m in self.tables:
+            for tok, _ in self._rec.get(m, []):
+                self._check_ids(m, tok, B)
         weights = []   # (weight, [(input, output), ...]) in module order
         for m in self.modules:
             if m in self._rec:
@@ -225,7 +244,18 @@ class RandomizedClipping:
             for r in self._rec.get(m, []):
                 looked.setdefault((id(m.weight), m.scale), (m, []))[1].append(r)
         outputs += [o for _, recs in looked.values() for (_, o) in recs]
-        grads = torch.autograd.grad(losses.sum(), outputs, retain_graph=True, allow_unused=True)
+        # the step that is checked: powers of two, whose product and quotient are exact
+        w, unweighted = None, None
+        if self._verify and B > 1 and all(o.dtype in (torch.bfloat16, torch.float32, torch.float64) for o in outputs):
+            w = self._sample_weights(B, losses.device)
+            unweighted = (1.0 / w).view(B, 1, 1)
+        total = losses.sum() if w is None else (w.to(losses.dtype) * losses).sum()
+        grads = torch.autograd.grad(total, outputs, retain_graph=True, allow_unused=True)
+
+        def by_sample(g):
+            g = g.detach().reshape(B, -1, g.shape[-1])
+            return g if unweighted is None else g * unweighted.to(g.dtype)
+
         layers, at, cast = [], 0, {}
         for w, recs in weights:
             As, Gs = [], []
@@ -233,7 +263,7 @@ class RandomizedClipping:
                 if g is None:  # the output did not reach the loss
                     g = torch.zeros_like(out)
                 As.append(self._cast(a.detach().reshape(B, -1, a.shape[-1]), cast))
-                Gs.append(self._cast(g.detach().reshape(B, -1, g.shape[-1]), cast))
+                Gs.append(self._cast(by_sample(g), cast))
             at += len(recs)
             A = As[0] if len(As) == 1 else torch.cat(As, dim=1)
             G = Gs[0] if len(Gs) == 1 else torch.cat(Gs, dim=1)
@@ -249,7 +279,7 @@ class RandomizedClipping:
                 if g is None:
                     g = torch.zeros_like(out)
                 toks.append(tok.detach().reshape(B, -1))
-                Gs.append(self._cast(g.detach().reshape(B, -1, g.shape[-1]), cast))
+                Gs.append(self._cast(by_sample(g), cast))
             at += len(recs)
             tok = toks[0] if len(toks) == 1 else torch.cat([t.long() for t in toks], dim=1)
             G = Gs[0] if len(Gs) == 1 else torch.cat(Gs, dim=1)
@@ -258,6 +288,23 @@ class RandomizedClipping:
         self._batch = B
         self._rec = {}
         return layers
+
+    def _check_ids(self, table: Embedding, tok: torch.Tensor, B: int) -> None:
+        """The ids of a look-up are [B, ...], so that every row of its output is one sample's."""
+        name = self._names.get(id(table.weight), "")
+        if tok.dim() == 0 or tok.shape[0] != B:
+            raise ValueError(f"table {name} is looked up with ids {list(tok.shape)}: they must be [B={B}, ...], a row for "
+                             f"each sample (a position table: arange(T).expand(B, T))")
+        if tok.dim() == 1 and B > 1 and not (self._verify or self._verified):
+            raise ValueError(f"table {name} is looked up with ids [B={B}], which may as well be positions that all samples "
+                             f"share: give one id a sample as [B][1], or leave verify_coverage on")
+
+    @staticmethod
+    def _sample_weights(B: int, device: torch.device) -> torch.Tensor:
+        """Powers of two in random order, each of eight before one comes again
+        (and no draw from the generators that a program seeds)."""
+        rng = secrets.SystemRandom()
+        return torch.tensor([2.0 ** e for _ in range(0, B, 8) for e in rng.sample(range(8), 8)][:B], device=device)
 
     def clip_factors(self, losses: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
         """Backward pass 1 and the norm path: returns (n, c), float32 [B]."""
@@ -323,7 +370,7 @@ class RandomizedClipping:
             for (w, order, G, scale), g0 in zip(tables, before[len(pending):]):
                 want = dp.embed_grad(order, G, scale=scale, weights=cw).float()
                 self._check_gradient(w, want, g0)
-            self._verify = False
+            self._verify, self._verified = False, True
 
     def _check_coverage(self, pending, before, c: torch.Tensor) -> None:
         """Each weight's gradient from backward pass 2 must be sum_i c_i G_i^T A_i
@@ -347,7 +394,8 @@ class RandomizedClipping:
             raise RuntimeError(
                 f"the gradient of weight {self._names.get(id(w), '')} {list(w.shape)} differs from what its "
                 f"recorded uses give (relative {err / max(scale, 1e-300):.2e}): it has a use the hooks do not "
-                f"see (e.g. F.linear called with it outside its module), which would go unclipped")
+                f"see (e.g. F.linear called with it outside its module), which would go unclipped, or rows of a "
+                f"recording are not one sample's (e.g. a layer applied once to rows that all samples use)")
 
     def add_noise(self) -> None:
         """Adds sigma C N(0, I) to each clipped gradient sum and divides by B."""
