@@ -347,12 +347,13 @@ class RandomizedClipping:
         return n, c
 
     def _cast(self, t: torch.Tensor, cache: dict) -> torch.Tensor:
-        # layers reading one tensor keep sharing one copy (and one pass over it)
+        # layers reading one tensor keep sharing one copy (and one pass over it); the
+        # tensor stays with its copy, so that no other can come to lie at its address
         dt = self.norm_dtype or t.dtype
-        key = (t.data_ptr(), tuple(t.shape), t.dtype)
+        key = (t.data_ptr(), tuple(t.shape), t.stride(), t.dtype)
         if key not in cache:
-            cache[key] = t.to(dt).contiguous()
-        return cache[key]
+            cache[key] = (t.to(dt).contiguous(), t)
+        return cache[key][0]
 
     def clipped_backward(self, losses: torch.Tensor, c: torch.Tensor) -> None:
         """Backward pass 2: accumulates sum_i c_i grad l_i into the weights' .grad

@@ -190,3 +190,58 @@ def test_the_first_step_has_the_gradients_of_the_others():
         res.append((n, [G for _, G, _ in rc.last_layers]))
     assert torch.equal(res[0][0], res[1][0])
     assert all(torch.equal(x, y) for x, y in zip(res[0][1], res[1][1]))
+
+
+class _Transposed(nn.Module):
+    """Two layers that read one square tensor, as it is and transposed."""
+
+    def __init__(self):
+        super().__init__()
+        self.a, self.b = (nn.Linear(6, 6, bias=False) for _ in range(2))
+
+    def forward(self, x):
+        return self.a(x) + self.b(x.transpose(1, 2))
+
+
+def test_a_tensor_and_its_transpose_are_recorded_apart():
+    from sample_grad_norms_amd.dpsgd_rc import RandomizedClipping
+    x = torch.randn(3, 6, 6, generator=torch.Generator().manual_seed(9))
+    model = _Transposed()
+    rc = RandomizedClipping(model, C=1.0, noise_multiplier=0.0)
+    with rc.capture():
+        losses = model(x).sum((1, 2))
+    (A, _), (A2, _) = rc._collect(losses)
+    assert torch.equal(A, x) and torch.equal(A2, x.transpose(1, 2))
+
+
+class _HeadsApart(nn.Module):
+    """Layers whose inputs lie transposed, so that a recording copies them before it casts them."""
+
+    def __init__(self):
+        super().__init__()
+        self.layers = nn.ModuleList(nn.Linear(64, 64, bias=False) for _ in range(6))
+
+    def forward(self, x):
+        return sum(layer((x * (i + 1)).transpose(1, 2)) for i, layer in enumerate(self.layers))
+
+
+def test_casts_of_copies_are_recorded_apart():
+    from sample_grad_norms_amd.dpsgd_rc import RandomizedClipping
+    x = torch.randn(3, 64, 50, 64, generator=torch.Generator().manual_seed(10)).bfloat16()
+    model = _HeadsApart().bfloat16()
+    rc = RandomizedClipping(model, C=1.0, noise_multiplier=0.0, norm_dtype=torch.float32)
+    with rc.capture():
+        losses = model(x).float().sum((1, 2, 3))
+    for i, (A, _) in enumerate(rc._collect(losses)):
+        assert torch.equal(A, (x * (i + 1)).transpose(1, 2).reshape(3, -1, 64).float()), i
+
+
+def test_layers_that_read_one_tensor_share_its_copy():
+    from sample_grad_norms_amd.dpsgd_rc import RandomizedClipping
+    x = torch.randn(3, 5, 6, generator=torch.Generator().manual_seed(11)).bfloat16()
+    model = nn.ModuleList(nn.Linear(6, 6, bias=False) for _ in range(2)).bfloat16()
+    rc = RandomizedClipping(model, C=1.0, noise_multiplier=0.0, norm_dtype=torch.float32)
+    with rc.capture():
+        losses = (model[0](x) + model[1](x)).float().sum((1, 2))
+    (A, _), (A2, _) = rc._collect(losses)
+    assert A.data_ptr() == A2.data_ptr()
