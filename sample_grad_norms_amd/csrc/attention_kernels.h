@@ -1057,8 +1057,8 @@ __device__ __forceinline__ void backward_kv_pass(bool& careful, const Args& a, i
   const int32_t key = w0 + (lane & 31), rep = a.Hq / a.Hkv;
   const float c = a.scale * kLog2e;
   const uint32_t base = lds_address(mine);
-  // 32 queries from q0 on of head h, with their lse and delta: zeros past the
-  // end, whose dO and q rows are zero too and so add nothing
+  // 32 queries from q0 on of head h, with their lse and delta: zeros past the end
+  // (whose weights are set to zero: against an infinity in a key they would be NaN)
   typename P::Rows qs(a.q, start, kh * rep, a.D), os(a.dO, start, kh * rep, a.D);
   const auto fetch = [&](int32_t h, int32_t q0, uint32_t to) {
     qs.head(a.q, start, h);
@@ -1105,11 +1105,13 @@ __device__ __forceinline__ void backward_kv_pass(bool& careful, const Args& a, i
         ds[r + 1] = p[r + 1] * (ds[r + 1] - x[3]);
       }
     }
-    if (q0 == w0) {
+    if (q0 == w0 || q0 + 32 > len) {
       keep_branch();
 #pragma unroll
-      for (int r = 0; r < 16; ++r)
-        if (q0 + result_row(r, g) < key) p[r] = 0.f, ds[r] = 0.f;
+      for (int r = 0; r < 16; ++r) {
+        const int32_t query = q0 + result_row(r, g);
+        if (query < key || query >= len) p[r] = 0.f, ds[r] = 0.f;
+      }
     }
     columns_times<BF16, DC>(lo, 0, p, dv);
     columns_times<BF16, DC>(lq, 0, ds, dk);
