@@ -301,7 +301,8 @@ dpnorm_status dpnorm_clip_factors(const float* n, int64_t B, float C, float* c, 
  *
  * The conventions above hold: device pointers, no allocation, everything
  * enqueued on `stream`, host checks before anything is enqueued, results
- * bitwise reproducible (no floating-point atomics).
+ * bitwise reproducible (no floating-point atomics). The embedding calls take
+ * rows of up to 2^43 elements in all; past that they may return ERR_SIZE.
  * ------------------------------------------------------------------------- */
 typedef enum dpnorm_index {
   DPNORM_I32 = 0,

@@ -103,7 +103,14 @@ void plan_runs(EmbedPlan& pl, dpnorm_dtype dt, int64_t d, bool ordered) {
   pl.grad_ws = align_up(g.off);
 }
 
-// Blocks of one launch fit the 2^31 - 1 of a grid's x dimension.
+// A grid of `blocks` blocks (below 2^31), at most 2^20 along x: HIP takes fewer than
+// 2^32 threads along a dimension, and 2^16 blocks along y.
+dim3 grid_of(int64_t blocks) {
+  const int64_t y = (blocks + (1 << 20) - 1) >> 20;
+  return dim3((uint32_t)((blocks + y - 1) / y), (uint32_t)y);
+}
+
+// Blocks of one launch are numbered in 31 bits.
 dpnorm_status check_grid(const EmbedPlan& pl) {
   const int64_t lim = 0x7fffffff;
   if (pl.chunks * pl.slices > lim) return DPNORM_ERR_SIZE;
@@ -163,8 +170,7 @@ embed::RunArgs run_args(const EmbedPlan& pl, const void* order, const void* G) {
 
 template <int MODE>
 hipError_t launch_runs(const embed::RunArgs& a, bool bf16, hipStream_t stream) {
-  const uint32_t blocks = (uint32_t)((a.items + 3) / 4 + a.fill_blocks);
-  const uint32_t joins = (uint32_t)((int64_t)a.runs.chunks * a.slices);
+  const dim3 blocks = grid_of((a.items + 3) / 4 + a.fill_blocks), joins = grid_of(a.items);
   if (bf16) {
     embed::k_run_sums<true, MODE><<<blocks, 256, 0, stream>>>(a);
     embed::k_run_join<true, MODE><<<joins, 256, 0, stream>>>(a);
@@ -197,10 +203,10 @@ dpnorm_status dpnorm_embed_lookup(const void* tok, dpnorm_index it, const void* 
   const int64_t blocks = ((N + embed::kLookupRows - 1) / embed::kLookupRows * slices + 3) / 4;
   if (blocks > 0x7fffffff) return DPNORM_ERR_SIZE;
   if (bf16)
-    embed::k_lookup<true><<<(uint32_t)blocks, 256, 0, stream>>>(tok, it == DPNORM_I64, (const char*)W, (char*)out, N, (int32_t)V,
+    embed::k_lookup<true><<<grid_of(blocks), 256, 0, stream>>>(tok, it == DPNORM_I64, (const char*)W, (char*)out, N, (int32_t)V,
                                                                 (int32_t)d, (int32_t)slices, scale);
   else
-    embed::k_lookup<false><<<(uint32_t)blocks, 256, 0, stream>>>(tok, it == DPNORM_I64, (const char*)W, (char*)out, N, (int32_t)V,
+    embed::k_lookup<false><<<grid_of(blocks), 256, 0, stream>>>(tok, it == DPNORM_I64, (const char*)W, (char*)out, N, (int32_t)V,
                                                                  (int32_t)d, (int32_t)slices, scale);
   return hip_status(hipGetLastError());
 }
@@ -282,11 +288,11 @@ dpnorm_status dpnorm_embed_norm(const void* tok, dpnorm_index it, const void* or
   const double scale2 = (double)scale * (double)scale;
   if (pl.small_norm) {
     if (bf16)
-      embed::k_norm_small<true><<<(uint32_t)B, 1024, 0, stream>>>(tok, it == DPNORM_I64, (const char*)G, pl.T, pl.V, pl.d, scale2,
-                                                                  n, accumulate);
+      embed::k_norm_small<true><<<grid_of(B), 1024, 0, stream>>>(tok, it == DPNORM_I64, (const char*)G, (int32_t)B, pl.T, pl.V, pl.d,
+                                                                 scale2, n, accumulate);
     else
-      embed::k_norm_small<false><<<(uint32_t)B, 1024, 0, stream>>>(tok, it == DPNORM_I64, (const char*)G, pl.T, pl.V, pl.d, scale2,
-                                                                   n, accumulate);
+      embed::k_norm_small<false><<<grid_of(B), 1024, 0, stream>>>(tok, it == DPNORM_I64, (const char*)G, (int32_t)B, pl.T, pl.V, pl.d,
+                                                                  scale2, n, accumulate);
     return hip_status(hipGetLastError());
   }
   hipError_t he = hipSuccess;
@@ -347,7 +353,7 @@ dpnorm_status dpnorm_embed_grad(const void* tok, dpnorm_index it, const void* or
   a.out = (char*)dW;
   a.accumulate = accumulate;
   if (pl.small_grad) {
-    const uint32_t blocks = (uint32_t)((pl.V + embed::kSmallRows - 1) / embed::kSmallRows);
+    const dim3 blocks = grid_of((pl.V + embed::kSmallRows - 1) / embed::kSmallRows);
     if (bf16) embed::k_grad_small<true><<<blocks, 256, 0, stream>>>(tok, it == DPNORM_I64, a);
     else embed::k_grad_small<false><<<blocks, 256, 0, stream>>>(tok, it == DPNORM_I64, a);
     return hip_status(hipGetLastError());

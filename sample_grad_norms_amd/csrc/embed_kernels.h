@@ -18,6 +18,11 @@
 namespace dpn {
 namespace embed {
 
+// Block of a launch by its number: a dimension of a grid holds fewer than 2^32
+// threads, so that many blocks lie along two (grid_of; the last ones may be past
+// the end).
+__device__ __forceinline__ uint32_t block_number() { return blockIdx.x + blockIdx.y * gridDim.x; }
+
 // ---------------------------------------------------------------------------
 // Order: the positions grouped by id, each group in position order. The groups
 // are sorted by a mixed id, which spreads neighbouring ids (the frequent ones of
@@ -398,7 +403,7 @@ __global__ __launch_bounds__(256) void k_lookup(const void* tok, int idx64, cons
                                                 int32_t d, int32_t slices, float scale) {
   using R = Row<BF16>;
   const int lane = threadIdx.x & 63;
-  const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int64_t item = (int64_t)block_number() * 4 + (threadIdx.x >> 6);
   const int64_t q0 = item / slices * kLookupRows;
   const int col = (int)(item % slices) * R::kSlice + lane * R::kElems;
   if (q0 >= N || col >= d) return;
@@ -583,10 +588,10 @@ template <bool BF16, int MODE>
 __global__ __launch_bounds__(256) void k_run_sums(RunArgs a) {
   using R = Row<BF16>;
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  const int64_t item_blocks = (a.items + 3) / 4;
-  if (MODE == RUN_GRAD && (int64_t)blockIdx.x >= item_blocks) {
+  const int64_t item_blocks = (a.items + 3) / 4, block = block_number();
+  if (MODE == RUN_GRAD && block >= item_blocks) {
     // clear the rows of ids that do not occur: lane r looks for row v0 + r
-    const int64_t v0 = ((int64_t)blockIdx.x - item_blocks) * kFillRows;
+    const int64_t v0 = (block - item_blocks) * kFillRows;
     const int64_t v = v0 + lane;
     const bool absent = v < a.runs.V && !occurs(a.runs, (int32_t)v);
     uint64_t m = __ballot(absent);
@@ -599,7 +604,7 @@ __global__ __launch_bounds__(256) void k_run_sums(RunArgs a) {
     }
     return;
   }
-  const int64_t item = (int64_t)blockIdx.x * 4 + wv;
+  const int64_t item = block * 4 + wv;
   if (item >= a.items) return;
   const int32_t chunk = (int32_t)(item / a.slices);
   const int slice = (int)(item % a.slices);
@@ -672,8 +677,10 @@ __global__ __launch_bounds__(256) void k_run_join(RunArgs a) {
   using R = Row<BF16>;
   __shared__ float sums[3][R::kElems][kWave];
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  const int32_t chunk = (int32_t)(blockIdx.x / a.slices);
-  const int slice = (int)(blockIdx.x % a.slices);
+  const uint32_t block = block_number();
+  const int32_t chunk = (int32_t)(block / (uint32_t)a.slices);
+  const int slice = (int)(block % (uint32_t)a.slices);
+  if (chunk >= a.runs.chunks) return;
   const Chunk w = look_at<MODE>(a.runs, chunk);
   if (!w.cut1) return;
   // the run at x1 started in this chunk unless the chunk holds it whole, cut on both sides
@@ -806,13 +813,15 @@ __device__ __forceinline__ void add_rows(float (&acc)[Row<BF16>::kElems], const 
 // position of an id stands for its row. Bound by latency: 3 samples of 61 positions of
 // 256 floats take 6.2 us, against four launches and 31 us with an order.
 template <bool BF16>
-__global__ __launch_bounds__(1024) void k_norm_small(const void* tok, int idx64, const char* G, int32_t T, int32_t V, int32_t d,
-                                                     double scale2, float* n, int accumulate) {
+__global__ __launch_bounds__(1024) void k_norm_small(const void* tok, int idx64, const char* G, int32_t B, int32_t T, int32_t V,
+                                                     int32_t d, double scale2, float* n, int accumulate) {
   using R = Row<BF16>;
   __shared__ int32_t keys[kSmallIds];
   __shared__ double part[16];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t q0 = (int64_t)blockIdx.x * T;
+  const uint32_t i = block_number();
+  if (i >= (uint32_t)B) return;
+  const int64_t q0 = (int64_t)i * T;
   if (threadIdx.x < kSmallIds) keys[threadIdx.x] = (int)threadIdx.x < T ? id_key(tok, idx64, q0 + threadIdx.x, V) : V;
   __syncthreads();
   int32_t mine[kSmallIds / 64];
@@ -848,7 +857,7 @@ __global__ __launch_bounds__(1024) void k_norm_small(const void* tok, int idx64,
 #pragma unroll
     for (int w = 0; w < 16; ++w) t += part[w];
     t *= scale2;
-    n[blockIdx.x] = (float)(accumulate ? (double)n[blockIdx.x] + t : t);
+    n[i] = (float)(accumulate ? (double)n[i] + t : t);
   }
 }
 
@@ -863,7 +872,7 @@ __global__ __launch_bounds__(256) void k_grad_small(const void* tok, int idx64, 
   __shared__ int32_t keys[kSmallIds];
   __shared__ float wgt[kSmallIds];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int32_t v0 = blockIdx.x * kSmallRows;
+  const int32_t v0 = (int32_t)block_number() * kSmallRows;
   {
     const int q = threadIdx.x;
     keys[q] = q < a.runs.N ? id_key(tok, idx64, q, a.runs.V) : a.runs.V;

@@ -29,6 +29,8 @@ static hipError_t g_last = hipSuccess;
 long long dpnorm_fake_launches = 0;
 long long dpnorm_fake_bad_launches = 0;
 unsigned long long dpnorm_fake_max_grid = 0;
+// launches with 2^32 threads or more along a dimension, which HIP does not take
+long long dpnorm_fake_wide_launches = 0;
 
 void** __hipRegisterFatBinary(const void*) {
   static void* handle[1] = {nullptr};
@@ -66,6 +68,8 @@ hipError_t hipLaunchKernel(const void*, dim3 grid, dim3 block, void**, size_t sh
     g_last = hipErrorInvalidConfiguration;
     return g_last;
   }
+  const auto wide = [](unsigned int blocks, unsigned int size) { return (unsigned long long)blocks * size >> 32 != 0; };
+  if (wide(grid.x, block.x) || wide(grid.y, block.y) || wide(grid.z, block.z)) ++dpnorm_fake_wide_launches;
   const unsigned long long g = (unsigned long long)grid.x * grid.y * grid.z;
   if (g > dpnorm_fake_max_grid) dpnorm_fake_max_grid = g;
   return hipSuccess;

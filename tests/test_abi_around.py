@@ -214,3 +214,43 @@ def test_valid_calls_launch_valid_grids(lib, seed):
     assert lib.dpnorm_attention_forward(C.byref(sh), q, k, v, o, p[8], None) == _lib.OK
     assert lib.dpnorm_attention_backward_workspace(C.byref(sh), C.byref(nb)) == _lib.OK
     assert lib.dpnorm_attention_backward(C.byref(sh), do, q, k, v, o, p[8], dq, dk, dv, p[10], nb.value, None) == _lib.OK
+
+
+FAR = [(1 << 56) + (j << 50) for j in range(8)]
+
+
+@pytest.mark.skipif("DPNORM_TEST_LIB" not in os.environ, reason="launches are only checked by the sanitized library's stand-in")
+@pytest.mark.parametrize("dt", [_lib.BF16, _lib.F32])
+@pytest.mark.parametrize("B,T,V,d", [
+    (2 ** 22 - 1, 1, 50, 8), (2 ** 22, 1, 50, 8), (2 ** 24, 1, 50, 8), (2 ** 30, 1, 50, 8), (2 ** 22, 256, 50, 8),   # a block a sample
+    (1, 1, 2 ** 28 - 16, 8), (1, 256, 2 ** 28, 8), (256, 1, 2 ** 30, 8),             # few positions, many rows
+    (1, 257, 2 ** 30, 8), (1, 2 ** 24, 2 ** 30, 8), (2 ** 15, 2 ** 15, 2 ** 30, 8),  # many rows to clear
+    (1, 2 ** 28 - 16, 50, 8), (1, 2 ** 28, 50, 8), (1, 2 ** 30, 50, 8), (2 ** 20, 2 ** 10, 7, 8),
+    (1, 2 ** 24, 50, 4096), (3, 2 ** 20, 50, 2 ** 17), (1, 300, 2 ** 20, 2 ** 24), (1, 2 ** 20, 50, 2 ** 24), (5, 2 ** 26, 11, 2 ** 13)])
+def test_largest_calls_launch_valid_grids(lib, B, T, V, d, dt):
+    """Sizes around and far past 2^32 threads: every call either fails its query, and
+    then launches nothing, or succeeds, with fewer than 2^32 threads along each dimension."""
+    tok, order, g, out, ws, w, n, c = FAR
+    launches = C.c_longlong.in_dll(lib, "dpnorm_fake_launches")
+    wide = C.c_longlong.in_dll(lib, "dpnorm_fake_wide_launches")
+    before = wide.value
+    nb = C.c_size_t(0)
+    for ordered in (0, 1):
+        ids = (None, 0, order) if ordered else (tok, _lib.I32, None)
+        for which in ("norm", "grad"):
+            st = getattr(lib, f"dpnorm_embed_{which}_workspace")(dt, B, T, V, d, ordered, C.byref(nb))
+            assert st in (_lib.OK, _lib.ERR_SIZE)
+            at = launches.value
+            if which == "norm":
+                got = lib.dpnorm_embed_norm(*ids, g, dt, B, T, V, d, 1.0, n, 0, ws, nb.value, None)
+                assert got == st
+            else:
+                for acc in (0, 1):
+                    got = lib.dpnorm_embed_grad(*ids, g, dt, B, T, V, d, 1.0, c, out, acc, ws, nb.value, None)
+                    assert got == st
+            assert (launches.value > at) == (st == _lib.OK)
+    at = launches.value
+    got = lib.dpnorm_embed_lookup(tok, _lib.I64, w, dt, B * T, V, d, 1.0, out, None)
+    assert got in (_lib.OK, _lib.ERR_SIZE) and (launches.value > at) == (got == _lib.OK)
+    assert got == _lib.OK or B * T * d > 2 ** 38
+    assert wide.value == before

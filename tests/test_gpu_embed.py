@@ -259,3 +259,44 @@ def test_refusals():
                  lambda: dp.embed_grad(order, G, weights=torch.ones(2, dtype=torch.float64, device=dev()))):
         with pytest.raises(TypeError):
             call()
+
+
+def test_more_blocks_than_one_grid_dimension_holds():
+    """Calls whose blocks have 2^32 threads and more along one dimension: a block a
+    sample (2^22 of 1024 threads), and a block for every 16 of 2^28 and more rows."""
+    import sample_grad_norms_amd as dp
+    B, d = 2 ** 22 + 3, 8
+    tok = torch.zeros(B, 1, dtype=torch.int32, device=dev())
+    tok[::5] = -1
+    G = (torch.arange(B, device=dev()) % 251).to(torch.bfloat16).view(B, 1, 1).expand(B, 1, d).contiguous()
+    n = dp.embed_norm(tok, G, V=1)
+    want = d * (torch.arange(B, device=dev()) % 251).double() ** 2     # whole numbers below 2^24
+    want[::5] = 0
+    same = bool((n.double() == want).all())
+    assert same
+    V, d = 2 ** 28 + 5, 4
+    rows = torch.tensor([[0, 17, 2 ** 28 - 1, 2 ** 28, V - 1, 17]], device=dev())
+    dW = dp.embed_grad(rows, torch.ones(1, 6, d, device=dev()), V)
+    touched = dW[rows[0, :5]]
+    assert bool((touched == torch.tensor([1, 2, 1, 1, 1], device=dev())[:, None]).all())
+    assert float(dW.double().sum()) == 6 * d and int(torch.count_nonzero(dW)) == 5 * d
+    out = dp.embed_lookup(rows, dW, scale=2.0)
+    assert bool((out[0] == 2 * dW[rows[0]]).all())
+
+
+def test_more_chunks_than_one_grid_dimension_holds():
+    """2^24 chunks of 16 positions for the join of cut runs, and 2^30 rows to clear."""
+    import sample_grad_norms_amd as dp
+    T, d = 2 ** 27 + 40, 8
+    tok = torch.arange(2 * T, device=dev(), dtype=torch.int32).view(2, T) // 40     # runs of 40: cut at most chunk ends
+    tok = tok.remainder_(1 << 20)
+    G = torch.ones(2, T, d, dtype=torch.bfloat16, device=dev())
+    n = dp.embed_norm(tok, G, V=1 << 20)
+    for i in range(2):
+        c = torch.bincount(tok[i].long(), minlength=1 << 20).double()
+        assert float(n[i]) == pytest.approx(d * float((c * c).sum()), rel=2.0 ** -24)
+    del tok, G
+    V, d = 1 << 30, 4
+    tok = torch.arange(0, 600, device=dev()).view(1, 600) * 1789569
+    dW = dp.embed_grad(tok, torch.ones(1, 600, d, device=dev()), V)
+    assert bool((dW[tok[0]] == 1).all()) and int(torch.count_nonzero(dW.view(torch.int32))) == 600 * d
