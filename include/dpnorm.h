@@ -379,7 +379,8 @@ typedef struct dpnorm_attn_shape {
 /* A [N][H][D] tensor: row t of head h starts at data + t stride_token +
  * h stride_head (elements; not negative, multiples of 16 bytes; the D
  * elements of a row are contiguous), data 16-byte aligned, stride_token below
- * 2^22 elements. Inputs may overlap each other (views of one q, k, v buffer)
+ * 2^22 elements. The stride of a lone row (N = 1) or head (H = 1) is not used
+ * and may be anything. Inputs may overlap each other (views of one q, k, v buffer)
  * and repeat rows (a stride of 0); the rows of an output must be apart, and an
  * output's span must not overlap an input's or another output's. */
 typedef struct dpnorm_attn_tensor {

@@ -678,8 +678,8 @@ def attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seql
                       lse: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Causal attention of packed sequences (dpnorm_attention_forward).
 
-    q [N][Hq][D], k and v [N][Hkv][D], bfloat16 or float32, any token and head
-    strides; Hq a multiple of Hkv. cu_seqlens: int32 [S + 1] row offsets on
+    q [N][Hq][D], k and v [N][Hkv][D], bfloat16 or float32, token and head
+    strides of any multiples of 16 bytes; Hq a multiple of Hkv. cu_seqlens: int32 [S + 1] row offsets on
     the GPU; without it the N rows are ``sequences`` (default 1) sequences of
     equal length. scale defaults to 1 / sqrt(D). Returns (o [N][Hq][D],
     lse float32 [Hq][N]). Rows that belong to no sequence are left as they

@@ -10,8 +10,14 @@ struct AttnCheck {
   bool bf16 = true;
 };
 
+// The strides that are ever multiplied: 0 for a lone row or head, whatever the caller gives.
+dpnorm_attn_tensor used_strides(const dpnorm_attn_tensor& t, int64_t N, int64_t H) {
+  return {t.data, N > 1 ? t.stride_token : 0, H > 1 ? t.stride_head : 0};
+}
+
 // Bytes that a [N][H][D] tensor with the given element strides spans.
-size_t span(const dpnorm_attn_tensor& t, int64_t N, int64_t H, int64_t D, size_t e) {
+size_t span(const dpnorm_attn_tensor& x, int64_t N, int64_t H, int64_t D, size_t e) {
+  const dpnorm_attn_tensor t = used_strides(x, N, H);
   return (size_t)((N - 1) * t.stride_token + (H - 1) * t.stride_head + D) * e;
 }
 
@@ -37,21 +43,23 @@ dpnorm_status check_shape(const dpnorm_attn_shape* s) {
   return DPNORM_OK;
 }
 
-dpnorm_status check_tensor(const dpnorm_attn_tensor* t, const dpnorm_attn_shape* s, int64_t H, bool output) {
-  if (!t || !t->data) return DPNORM_ERR_NULL;
-  if (!aligned(t->data, 16)) return DPNORM_ERR_ALIGN;
+dpnorm_status check_tensor(const dpnorm_attn_tensor* x, const dpnorm_attn_shape* s, int64_t H, bool output) {
+  if (!x || !x->data) return DPNORM_ERR_NULL;
+  if (!aligned(x->data, 16)) return DPNORM_ERR_ALIGN;
+  const dpnorm_attn_tensor t = used_strides(*x, s->N, H);
   const int64_t g = s->dtype == DPNORM_BF16 ? 8 : 4;
-  // 128 rows of a tile are addressed with 31-bit byte offsets
-  const int64_t lim = ((int64_t)1 << 31) / 128 / 4 - 256;
-  if (t->stride_token < 0 || t->stride_head < 0 || t->stride_token > lim || t->stride_head > ((int64_t)1 << 40) / H)
+  // the 64 rows of a step are addressed with 31-bit byte offsets
+  const int64_t lim = (int64_t)1 << 22;
+  if (t.stride_token < 0 || t.stride_head < 0 || t.stride_token >= lim || t.stride_head > ((int64_t)1 << 40) / H)
     return DPNORM_ERR_SIZE;
-  if (t->stride_token % g != 0 || t->stride_head % g != 0) return DPNORM_ERR_ALIGN;
-  if (output && !rows_apart(*t, s->N, H, s->D)) return DPNORM_ERR_VALUE;
+  if (t.stride_token % g != 0 || t.stride_head % g != 0) return DPNORM_ERR_ALIGN;
+  if (output && !rows_apart(t, s->N, H, s->D)) return DPNORM_ERR_VALUE;
   return DPNORM_OK;
 }
 
-attn::Tensor tensor_of(const dpnorm_attn_tensor* t, size_t e) {
-  return attn::Tensor{(char*)t->data, t->stride_token * (int64_t)e, t->stride_head * (int64_t)e};
+attn::Tensor tensor_of(const dpnorm_attn_tensor* x, int64_t N, int64_t H, size_t e) {
+  const dpnorm_attn_tensor t = used_strides(*x, N, H);
+  return attn::Tensor{(char*)t.data, t.stride_token * (int64_t)e, t.stride_head * (int64_t)e};
 }
 
 attn::Args attn_args(const dpnorm_attn_shape* s) {
@@ -262,10 +270,10 @@ dpnorm_status dpnorm_attention_forward(const dpnorm_attn_shape* shape, const dpn
                       {{o->data, span(*o, N, Hq, D, e)}, {lse, (size_t)N * Hq * 4}}))
     return DPNORM_ERR_VALUE;
   attn::Args a = attn_args(shape);
-  a.q = tensor_of(q, e);
-  a.k = tensor_of(k, e);
-  a.v = tensor_of(v, e);
-  a.o = tensor_of(o, e);
+  a.q = tensor_of(q, N, Hq, e);
+  a.k = tensor_of(k, N, Hkv, e);
+  a.v = tensor_of(v, N, Hkv, e);
+  a.o = tensor_of(o, N, Hq, e);
   a.lse = lse;
   if (shape->dtype == DPNORM_BF16)
     return hip_status(D <= 64 ? run_attn_forward<true, 64>(a, stream) : D <= 96 ? run_attn_forward<true, 96>(a, stream)
@@ -309,14 +317,14 @@ dpnorm_status dpnorm_attention_backward(const dpnorm_attn_shape* shape, const dp
                        {ws, bytes}}))
     return DPNORM_ERR_VALUE;
   attn::Args a = attn_args(shape);
-  a.dO = tensor_of(dO, e);
-  a.q = tensor_of(q, e);
-  a.k = tensor_of(k, e);
-  a.v = tensor_of(v, e);
-  a.o = tensor_of(o, e);
-  a.dq = tensor_of(dq, e);
-  a.dk = tensor_of(dk, e);
-  a.dv = tensor_of(dv, e);
+  a.dO = tensor_of(dO, N, Hq, e);
+  a.q = tensor_of(q, N, Hq, e);
+  a.k = tensor_of(k, N, Hkv, e);
+  a.v = tensor_of(v, N, Hkv, e);
+  a.o = tensor_of(o, N, Hq, e);
+  a.dq = tensor_of(dq, N, Hq, e);
+  a.dk = tensor_of(dk, N, Hkv, e);
+  a.dv = tensor_of(dv, N, Hkv, e);
   a.lse = const_cast<float*>(lse);
   backward_layout(a, shape->dtype == DPNORM_BF16, ws);
   if (shape->dtype == DPNORM_BF16)

@@ -254,3 +254,18 @@ def test_largest_calls_launch_valid_grids(lib, B, T, V, d, dt):
     assert got in (_lib.OK, _lib.ERR_SIZE) and (launches.value > at) == (got == _lib.OK)
     assert got == _lib.OK or B * T * d > 2 ** 38
     assert wide.value == before
+
+
+@pytest.mark.skipif("DPNORM_TEST_LIB" not in os.environ, reason="valid calls launch: only on the sanitized library's stand-in")
+def test_strides_of_a_lone_row_are_not_read(lib):
+    one = shape(n=1, s=1, hq=1, hkv=1, cu=None)
+    for st, sh in ((3, 5), (-7, -64), (1 << 60, 1 << 61), (0, 0)):
+        ts = [C.byref(tensor(p, 1, st=st, sh=sh)) for p in (Q, K, V_, O)]
+        assert lib.dpnorm_attention_forward(C.byref(one), *ts, LSE, None) == _lib.OK
+        nb = C.c_size_t(0)
+        assert lib.dpnorm_attention_backward_workspace(C.byref(one), C.byref(nb)) == _lib.OK
+        ts = [C.byref(tensor(p, 1, st=st, sh=sh)) for p in (DO, Q, K, V_, O)]
+        outs = [C.byref(tensor(p, 1, st=st, sh=sh)) for p in (DQ, DK, DV)]
+        assert lib.dpnorm_attention_backward(C.byref(one), *ts, LSE, *outs, WS, nb.value, None) == _lib.OK
+    # the last token stride that 31 bits of a step's rows reach
+    assert forward(lib, k=tensor(K, 2, st=(1 << 22) - 8)) == _lib.OK and forward(lib, k=tensor(K, 2, st=1 << 22)) == _lib.ERR_SIZE

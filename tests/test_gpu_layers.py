@@ -259,3 +259,24 @@ def test_a_table_looked_up_twice_is_one_gradient():
         loss = F.cross_entropy(((W[t] * 0.5 + W[t.flip(1)]) @ H.t())[0], y[i], reduction="sum")
         want.append(sum(float((g ** 2).sum()) for g in torch.autograd.grad(loss, [W, H])))
     np.testing.assert_allclose(n.cpu().double().numpy(), np.array(want), rtol=1e-4)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_a_lone_row_may_have_any_stride(dtype):
+    """One token, or one head, of a wider buffer: its stride is never used."""
+    import sample_grad_norms_amd as dp
+    from sample_grad_norms_amd.layers import attention
+    g = torch.Generator().manual_seed(23)
+    for N, Hq, Hkv in ((1, 4, 2), (9, 1, 1), (1, 1, 1)):
+        D = 64
+        x = [torch.randn(N, h, D, generator=g).to(dtype).to(dev()) for h in (Hq, Hkv, Hkv)]
+        want, lse = dp.attention_forward(*x)
+        strides = [(3 if N == 1 else h * D, 5 if h == 1 else D) for h in (Hq, Hkv, Hkv)]
+        odd = [t.as_strided(t.shape, (st, sh, 1)) for t, (st, sh) in zip(x, strides)]
+        far = [t.as_strided(t.shape, (1 << 40 if N == 1 else t.stride(0), 1 << 50 if t.shape[1] == 1 else t.stride(1), 1)) for t in x]
+        for y in (odd, far):
+            o, lse2 = dp.attention_forward(*y)
+            assert torch.equal(o, want) and torch.equal(lse, lse2)
+            grads = dp.attention_backward(o, *y, o, lse)
+            assert all(torch.equal(i, j) for i, j in zip(grads, dp.attention_backward(want, *x, want, lse)))
+            assert torch.equal(attention(*y), want)
