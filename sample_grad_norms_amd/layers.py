@@ -33,8 +33,10 @@ class _Lookup(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, grad):
         (tokens,) = ctx.saved_tensors
-        return dp.embed_grad(tokens.reshape(1, -1), grad.reshape(1, -1, grad.shape[-1]).contiguous(), ctx.rows,
-                             scale=ctx.scale), None, None
+        grad = grad.reshape(1, -1, grad.shape[-1])
+        if not grad.is_contiguous() or grad.data_ptr() % 16 != 0:
+            grad = grad.clone(memory_format=torch.contiguous_format)
+        return dp.embed_grad(tokens.reshape(1, -1), grad, ctx.rows, scale=ctx.scale), None, None
 
 
 class Embedding(nn.Module):
@@ -71,10 +73,11 @@ class _Attention(torch.autograd.Function):
 
 
 def _rows(t: torch.Tensor) -> torch.Tensor:
-    """t as the library reads it: rows contiguous, on 16-byte boundaries."""
+    """t as the library reads it: rows contiguous, on 16-byte boundaries, tokens less than 2^22 elements apart."""
     step = 16 // t.element_size()
-    ok = t.stride(2) == 1 and t.stride(0) % step == 0 and t.stride(1) % step == 0 and t.data_ptr() % 16 == 0
-    return t if ok else t.contiguous()
+    st, sh, sd = t.stride()
+    ok = sd == 1 and st % step == 0 and sh % step == 0 and st < 1 << 22 and t.data_ptr() % 16 == 0
+    return t if ok else t.clone(memory_format=torch.contiguous_format)
 
 
 def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None,

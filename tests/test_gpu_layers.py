@@ -280,3 +280,29 @@ def test_a_lone_row_may_have_any_stride(dtype):
             grads = dp.attention_backward(o, *y, o, lse)
             assert all(torch.equal(i, j) for i, j in zip(grads, dp.attention_backward(want, *x, want, lse)))
             assert torch.equal(attention(*y), want)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_inputs_and_gradients_off_a_boundary(dtype):
+    """q, k, v and the output's gradient as contiguous views that start one element into a
+    buffer: the results and gradients of the same values on a boundary, bit for bit."""
+    from sample_grad_norms_amd.layers import Embedding, attention
+    g = torch.Generator().manual_seed(21)
+    N, Hq, Hkv, D = 37, 4, 2, 64
+
+    def off(t):
+        return torch.cat([torch.zeros(1, dtype=dtype, device=dev()), t.flatten()])[1:].view(t.shape)
+
+    x = [torch.randn(N, h, D, generator=g).to(dtype).to(dev()).requires_grad_(True) for h in (Hq, Hkv, Hkv)]
+    w = torch.randn(N, Hq, D, generator=g).to(dtype).to(dev())
+    a = attention(*x)
+    want = torch.autograd.grad(a, x, grad_outputs=w)
+    b = attention(*(off(t) for t in x))
+    got = torch.autograd.grad(b, x, grad_outputs=off(w))
+    assert torch.equal(a, b) and all(torch.equal(i, j) for i, j in zip(want, got))
+    e = Embedding(30, 48, device=dev(), dtype=dtype)
+    tok = torch.randint(0, 30, (3, 20), generator=g).to(dev())
+    w = torch.randn(3, 20, 48, generator=g).to(dtype).to(dev())
+    (want,) = torch.autograd.grad(e(tok), [e.weight], grad_outputs=w)
+    (got,) = torch.autograd.grad(e(tok), [e.weight], grad_outputs=off(w))
+    assert torch.equal(want, got)

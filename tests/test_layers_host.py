@@ -63,3 +63,22 @@ def test_layers_refuse_cpu_tensors_and_wrong_shapes():
         attention(q, q[:1], q)
     with pytest.raises(ValueError, match="must be"):
         attention(q[0, 0], q[0, 0], q[0, 0])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rows_that_the_library_cannot_read_are_copied(dtype):
+    """Views off a 16-byte boundary, rows whose strides are, a lone row of any stride, and
+    tokens too far apart; what can be read stays where it is."""
+    from sample_grad_norms_amd.layers import _rows
+    buf = torch.arange(4096, dtype=torch.float32).to(dtype)
+    views = [buf[1:1 + 96].view(4, 3, 8), buf.as_strided((1, 2, 8), (9, 8, 1)), buf.as_strided((5, 1, 8), (16, 3, 1)),
+             buf.as_strided((4, 2, 8), (24, 8, 1), 4 if dtype == torch.bfloat16 else 2), buf[:96].view(8, 4, 3).transpose(0, 2)[:, :, :8],
+             buf[0].expand(2, 2, 8), torch.empty((1 << 22) + 8, dtype=dtype).as_strided((2, 1, 8), (1 << 22, 8, 1))]
+    for t in views:
+        r = _rows(t)
+        assert r.is_contiguous() and r.data_ptr() % 16 == 0 and r.data_ptr() != t.data_ptr()
+        assert all(s % (16 // r.element_size()) == 0 for s in r.stride()[:2]) and r.stride(2) == 1
+        if t.numel() < 1000:
+            assert torch.equal(r, t)
+    for t in (buf[:96].view(4, 3, 8), buf[:192].view(4, 3, 16)[:, :, 8:], buf[:96].view(3, 4, 8).transpose(0, 1), buf[:8].expand(4, 3, 8)):
+        assert _rows(t) is t
