@@ -42,7 +42,7 @@ class _Lookup(torch.autograd.Function):
 class Embedding(nn.Module):
     """A table [rows][dim] looked up as scale * weight[tokens].
 
-    tokens: int32 or int64 of any shape, contiguous, on the GPU. An id outside
+    tokens: int32 or int64 of any shape, on the GPU. An id outside
     [0, rows) (a padded position) gives a zero row and adds nothing to the
     gradient. dim: a multiple of 8 (bfloat16) or 4 (float32).
     """
@@ -53,7 +53,7 @@ class Embedding(nn.Module):
         self.weight = nn.Parameter(torch.randn(rows, dim, device=device, dtype=dtype))
 
     def forward(self, tokens: torch.Tensor) -> torch.Tensor:
-        return _Lookup.apply(self.weight, tokens, self.scale)
+        return _Lookup.apply(self.weight, tokens.contiguous(), self.scale)
 
 
 class _Attention(torch.autograd.Function):

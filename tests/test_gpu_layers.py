@@ -306,3 +306,14 @@ def test_inputs_and_gradients_off_a_boundary(dtype):
     (want,) = torch.autograd.grad(e(tok), [e.weight], grad_outputs=w)
     (got,) = torch.autograd.grad(e(tok), [e.weight], grad_outputs=off(w))
     assert torch.equal(want, got)
+
+
+def test_ids_need_not_be_contiguous():
+    from sample_grad_norms_amd.layers import Embedding
+    e = Embedding(30, 48, device=dev())
+    tok = torch.randint(0, 30, (4, 21), generator=torch.Generator().manual_seed(22)).to(dev())
+    for ids in (tok[:, :-1], tok[:, 1:], tok.t(), tok[0].expand(4, 21), tok[::2, ::3]):
+        out = e(ids)
+        assert torch.equal(out, e(ids.contiguous())) and torch.equal(out, e.weight[ids])
+        (got,) = torch.autograd.grad(out.sum(), [e.weight])
+        assert torch.equal(got, torch.bincount(ids.flatten(), minlength=30)[:, None].expand(30, 48).float())
