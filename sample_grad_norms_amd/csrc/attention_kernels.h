@@ -657,6 +657,91 @@ __global__ __launch_bounds__(64 * NS, BF16 ? 2 : 1) void k_forward_rows(Args a) 
   }
 }
 
+// A step of 64 keys from r0 on by tiles, before its weights: masks the scores, raises
+// the running maximum and rescales the sums. Returns the maximum in powers of two.
+template <bool BF16, int DC>
+__device__ __forceinline__ float raise_maximum(f32x16_t (&s)[2], int32_t r0, int32_t w0, int32_t query, float c, float& m, float& l,
+                                               f32x16_t (&acc)[Geo<BF16, DC>::kTiles]) {
+  using G = Geo<BF16, DC>;
+  const int g = (threadIdx.x & 63) >> 5;
+  if (r0 + 63 > w0) {
+    keep_branch();
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        if (r0 + t * 32 + result_row(r, g) > query) s[t][r] = -INFINITY;
+  }
+  float x[4] = {s[0][0], s[0][1], s[0][2], s[0][3]};
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) x[r & 3] = fmaxf(x[r & 3], s[t][r]);
+  float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+  top = fmaxf(top, other_half(top));
+  const bool grown = (top - m) * c > kGrowth;
+  if (__any(grown)) {   // (each query by its own scores alone)
+    keep_branch();
+    const float f = grown ? __builtin_amdgcn_exp2f((m - top) * c) : 1.f;
+    m = grown ? top : m;
+    l *= f;
+#pragma unroll
+    for (int t = 0; t < G::kTiles; ++t)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[t][r] *= f;
+  }
+  return m == -INFINITY ? 0.f : m * c;   // (scores of -infinity alone have weights of zero)
+}
+
+// The step's scores become its weights, and join the sum.
+__device__ __forceinline__ void weigh(f32x16_t (&s)[2], float c, float mc, float& l) {
+  float sum[2] = {0.f, 0.f};
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      s[t][r] = __builtin_amdgcn_exp2f(fmaf(s[t][r], c, -mc));
+      sum[r & 1] += s[t][r];
+    }
+  l += sum[0] + sum[1];
+}
+
+// A wave's queries of k_forward once more, without the infinities and NaN of values that
+// some of them do not see. The same steps and operations, so that queries whose sums were
+// finite keep their bits; keys and values in turn in the wave's quarter of the LDS.
+template <bool BF16, int DC>
+__device__ __forceinline__ void tile_again(const Args& a, int32_t start, int32_t len, int32_t kh, int32_t w0, unsigned char* mine,
+                                           const uint4 (&q)[Geo<BF16, DC>::kPairs], float& m, float& l,
+                                           f32x16_t (&acc)[Geo<BF16, DC>::kTiles]) {
+  using G = Geo<BF16, DC>;
+  const float c = a.scale * kLog2e;
+  const int32_t query = w0 + (threadIdx.x & 31);
+  const Stream<BF16, DC, 64, 1> ks(a.k, start, kh, a.D), vs(a.v, start, kh, a.D);
+  m = -INFINITY;
+  l = 0.f;
+#pragma unroll
+  for (int t = 0; t < G::kTiles; ++t) acc[t] = f32x16_t{};
+#pragma unroll 1
+  for (int32_t r0 = 0; r0 <= w0; r0 += 64) {
+    own_staged();   // (the reads of the step before are done)
+    ks.fetch(r0, len, lds_address(mine));
+    own_staged();
+    f32x16_t s[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) s[t] = rows_times<BF16, DC>(mine, t * 32, q);
+    own_staged();
+    vs.fetch(r0, len, lds_address(mine));
+    const float mc = raise_maximum<BF16, DC>(s, r0, w0, query, c, m, l, acc);
+    weigh(s, c, mc, l);
+    own_staged();
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      if (r0 + t * 32 >= w0) zero_not_finite<BF16, DC>(mine + t * 32 * G::kPitch);
+      columns_times<BF16, DC>(mine, t * 32, s[t], acc);
+    }
+  }
+}
+
 // The output by tiles: 128 queries of one head, 32 a wave, which share steps of 64 keys
 // in two LDS buffers. Longest tiles first, so that the short ones fill the end. The scores
 // of the next step are computed beside the weights of this one: what bounds it is a
@@ -705,45 +790,11 @@ __global__ __launch_bounds__(256, BF16 ? 2 : 1) void k_forward(Args a) {
     if (r0 + P::kStep < end) vs.fetch(r0 + P::kStep, len, base + (2 + (buf ^ 1)) * P::kStage);
     if (r0 + 2 * P::kStep < end) ks.fetch(r0 + 2 * P::kStep, len, base + buf * P::kStage);
     if (r0 <= w0 + 31) {
-      if (r0 + 63 > w0) {
-        keep_branch();
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int r = 0; r < 16; ++r)
-            if (r0 + t * 32 + result_row(r, g) > query) s[t][r] = -INFINITY;
-      }
-      float x[4] = {s[0][0], s[0][1], s[0][2], s[0][3]};
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) x[r & 3] = fmaxf(x[r & 3], s[t][r]);
-      float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-      top = fmaxf(top, other_half(top));
-      const bool grown = (top - m) * c > kGrowth;
-      if (__any(grown)) {   // (each query by its own scores alone)
-        keep_branch();
-        const float f = grown ? __builtin_amdgcn_exp2f((m - top) * c) : 1.f;
-        m = grown ? top : m;
-        l *= f;
-#pragma unroll
-        for (int t = 0; t < G::kTiles; ++t)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) acc[t][r] *= f;
-      }
-      const float mc = m == -INFINITY ? 0.f : m * c;   // (scores of -infinity alone have weights of zero)
+      const float mc = raise_maximum<BF16, DC>(s, r0, w0, query, c, m, l, acc);
       // the next step's scores fill the matrix unit while this step's weights are computed
 #pragma unroll
       for (int t = 0; t < 2; ++t) next[t] = rows_times<BF16, DC>(lds + (buf ^ 1) * P::kStage, t * 32, q);
-      float sum[2] = {0.f, 0.f};
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          s[t][r] = __builtin_amdgcn_exp2f(fmaf(s[t][r], c, -mc));
-          sum[r & 1] += s[t][r];
-        }
-      l += sum[0] + sum[1];
+      weigh(s, c, mc, l);
       const unsigned char* lv = lds + (2 + buf) * P::kStage;
 #pragma unroll
       for (int t = 0; t < 2; ++t) columns_times<BF16, DC>(lv, t * 32, s[t], acc);
@@ -757,10 +808,10 @@ __global__ __launch_bounds__(256, BF16 ? 2 : 1) void k_forward(Args a) {
     step(r0, odd, even, std::integral_constant<int, 1>{});
     r0 += P::kStep;
   }
-  // Masked values may have added NaN: the wave takes its queries once more, by rows,
-  // from its quarter of the LDS (every wave is past the last step).
+  // Masked values may have added NaN: the wave takes its queries once more, from its
+  // quarter of the LDS (every wave is past the last step).
   const bool careful = not_all_finite(acc);
-  if (careful) forward_pass<BF16, DC, 1, 1>(true, a, start, len, kh, w0, 0, lds + wv * P::kStage, q, m, l, acc);
+  if (careful) tile_again<BF16, DC>(a, start, len, kh, w0, lds + wv * P::kStage, q, m, l, acc);
   l += other_half(l);
   if (query < len) {
     store_rows<BF16, DC>(a.o, (int64_t)start + query, h, a.D, acc, 1.f / l);

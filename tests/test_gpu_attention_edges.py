@@ -11,10 +11,12 @@ import math
 import pytest
 import torch
 
+import attention_forms
 from test_gpu_attention import dev, make
 
 pytestmark = pytest.mark.gpu
 
+EVERY = [(torch.bfloat16, *s) for s in attention_forms.BF16] + [(torch.float32, *s) for s in attention_forms.F32]
 FORMS = [   # N, Hq, Hkv, D, by way of
     (330, 2, 1, 64),       # shared keys and queries
     (320, 2, 1, 64),
@@ -47,3 +49,53 @@ def test_keys_without_weight_get_no_gradient(N, Hq, Hkv, D, dtype):
     assert bool((dk[gone] == 0).all()) and bool((dv[gone] == 0).all())
     same = torch.equal(dk, dk2) and torch.equal(dv, dv2)
     assert same
+
+
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("dtype,N,Hq,Hkv,D", EVERY)
+def test_a_row_that_is_not_finite_leaves_the_others(N, Hq, Hkv, D, dtype, value):
+    """Rows that do not see a row with an infinity or NaN get what they get without it, bit
+    for bit, in the last rows of a step, of a wave and of a tile and in the middle of each."""
+    import sample_grad_norms_amd as dp
+    q, k, v, do = (x.to(dev()) for x in make(N, Hq, Hkv, D, dtype, 32))
+    o, lse = dp.attention_forward(q, k, v)
+    dq, dk, dv = dp.attention_backward(do, q, k, v, o, lse)
+    for row in (5, 63, 64, N // 2, N - 33, N - 1):
+        for name in ("k", "v"):
+            args = {"q": q, "k": k.clone(), "v": v.clone()}
+            args[name][row, :, 3] = value
+            o2, lse2 = dp.attention_forward(**args)
+            same = torch.equal(o2[:row], o[:row]) and torch.equal(lse2[:, :row], lse[:, :row])
+            assert same, (name, row)
+            if name == "v":   # every later query sees it, in its column alone
+                later = o2[row:, :, 3].float()
+                seen = bool((later.isnan() if math.isnan(value) else later == value).all())
+                same = torch.equal(o2[:, :, :3], o[:, :, :3]) and torch.equal(o2[:, :, 4:], o[:, :, 4:]) and torch.equal(lse2, lse)
+                assert seen and same, row
+            dq2, _, _ = dp.attention_backward(do, args["q"], args["k"], args["v"], o, lse)
+            same = torch.equal(dq2[:row], dq[:row])
+            assert same, (name, row)
+        for name in ("do", "q"):
+            args = {"do": do.clone(), "q": q.clone()}
+            args[name][row, :, 3] = value
+            _, dk2, dv2 = dp.attention_backward(args["do"], args["q"], k, v, o, lse)
+            same = torch.equal(dk2[row + 1:], dk[row + 1:]) and torch.equal(dv2[row + 1:], dv[row + 1:])
+            assert same, (name, row)
+
+
+@pytest.mark.parametrize("dtype,N,Hq,Hkv,D", EVERY)
+def test_keys_of_minus_infinity_leave_the_forward_pass(N, Hq, Hkv, D, dtype):
+    """Scores of -infinity, against scores so low that exp gives 0: the same output, bit for
+    bit, also in the waves whose rows past the end meet those keys."""
+    import sample_grad_norms_amd as dp
+    q, k, v, _ = make(N, Hq, Hkv, D, dtype, 33)
+    q = q.abs() + 0.125
+    gone = torch.tensor([9, 10, 33, 64, N // 2, N - 33, N - 12, N - 1])
+    low = k.clone()
+    low[gone, :, 3] = -1e5
+    k[gone, :, 3] = -math.inf
+    qd, kd, ld, vd = (x.to(dev()) for x in (q, k, low, v))
+    o, lse = dp.attention_forward(qd, kd, vd)
+    o2, lse2 = dp.attention_forward(qd, ld, vd)
+    same = torch.equal(o, o2) and torch.equal(lse, lse2)
+    assert same and bool(o.isfinite().all())
