@@ -14,6 +14,17 @@
 #include <cstdint>
 #include <cstdio>
 #include <cstdlib>
+#include <map>
+#include <string>
+#include <vector>
+
+namespace {
+std::map<const void*, std::string>& kernel_names() {
+  static std::map<const void*, std::string> names;
+  return names;
+}
+std::vector<const void*> g_launched;   // since the last dpnorm_fake_launched
+}  // namespace
 
 extern "C" {
 
@@ -36,7 +47,9 @@ void** __hipRegisterFatBinary(const void*) {
   static void* handle[1] = {nullptr};
   return handle;
 }
-void __hipRegisterFunction(void**, const void*, char*, const char*, unsigned int, void*, void*, void*, void*, int*) {}
+void __hipRegisterFunction(void**, const void* host, char*, const char* name, unsigned int, void*, void*, void*, void*, int*) {
+  kernel_names()[host] = name;
+}
 void __hipRegisterVar(void**, void*, char*, char*, int, size_t, int, int) {}
 void __hipUnregisterFatBinary(void**) {}
 
@@ -56,8 +69,18 @@ hipError_t __hipPopCallConfiguration(dim3* grid, dim3* block, size_t* shmem, hip
   return hipSuccess;
 }
 
-hipError_t hipLaunchKernel(const void*, dim3 grid, dim3 block, void**, size_t shmem, hipStream_t) {
+// The (mangled) names of the kernels launched since the last call, one a line.
+const char* dpnorm_fake_launched(void) {
+  static std::string res;
+  res.clear();
+  for (const void* k : g_launched) res += kernel_names()[k] + "\n";
+  g_launched.clear();
+  return res.c_str();
+}
+
+hipError_t hipLaunchKernel(const void* kernel, dim3 grid, dim3 block, void**, size_t shmem, hipStream_t) {
   ++dpnorm_fake_launches;
+  if (g_launched.size() < 1000) g_launched.push_back(kernel);
   const unsigned long long threads = (unsigned long long)block.x * block.y * block.z;
   const bool ok = grid.x >= 1 && grid.y >= 1 && grid.z >= 1 && grid.x <= 0x7fffffffu && grid.y <= 65535u &&
                   grid.z <= 65535u && threads >= 1 && threads <= 1024 && shmem <= 160 * 1024;

@@ -12,7 +12,7 @@ import pytest
 import torch
 
 import attention_forms
-from test_gpu_attention import dev, make
+from test_gpu_attention import dev, make, test_forward_and_backward as forward_and_backward
 
 pytestmark = pytest.mark.gpu
 
@@ -49,6 +49,11 @@ def test_keys_without_weight_get_no_gradient(N, Hq, Hkv, D, dtype):
     assert bool((dk[gone] == 0).all()) and bool((dv[gone] == 0).all())
     same = torch.equal(dk, dk2) and torch.equal(dv, dv2)
     assert same
+
+
+@pytest.mark.parametrize("dtype,N,Hq,Hkv,D", EVERY)
+def test_every_form_against_its_definition(N, Hq, Hkv, D, dtype):
+    forward_and_backward([N], Hq, Hkv, D, dtype)
 
 
 @pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
