@@ -354,7 +354,9 @@ __device__ __forceinline__ bool not_all_finite(const f32x16_t (&acc)[TILES]) {
 // that see them. The output and dq do so in a second pass of a wave whose sums come
 // out not finite. dk and dv take each step on the diagonal so: a second pass would
 // cost them registers (D 128, 4 x 1024: 257 us without the guard, 282 with it, 307
-// with a second pass; D 64, 4 x 2048: 239, 252, 262).
+// with a second pass; D 64, 4 x 2048: 239, 252, 262). Before the first products, so
+// that an infinity of dO there reaches dk through delta alone, as an infinity or NaN
+// (after them 303; D 64 248).
 
 // 32 rows in LDS, the wave's own: infinities and NaN become zero. Returns whether any were.
 template <bool BF16, int DC>
@@ -1279,7 +1281,7 @@ __global__ __launch_bounds__(64 * NS, BF16 || DC == 64 ? 2 : 1) void k_backward_
     const int32_t rep = a.Hq / a.Hkv;
     for (int32_t h = kh * rep; h < kh * rep + rep; ++h) {
       add_not_finite<BF16, false, true>(a.q, h, a.dk, kh, start, len, w0, a.D);
-      add_not_finite<BF16, false, true>(a.dO, h, a.dv, kh, start, len, w0, a.D);
+      add_not_finite<BF16, false, false>(a.dO, h, a.dv, kh, start, len, w0, a.D);   // (weights are not negative)
     }
   }
 }

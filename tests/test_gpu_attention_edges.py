@@ -104,3 +104,24 @@ def test_keys_of_minus_infinity_leave_the_forward_pass(N, Hq, Hkv, D, dtype):
     o2, lse2 = dp.attention_forward(qd, ld, vd)
     same = torch.equal(o, o2) and torch.equal(lse, lse2)
     assert same and bool(o.isfinite().all())
+
+
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("dtype,N,Hq,Hkv,D", EVERY)
+def test_an_output_gradient_that_is_not_finite_reaches_dv_as_it_is(N, Hq, Hkv, D, dtype, value):
+    """dv_u = sum_t p_tu dO_t with weights above zero: the keys that a row of dO with an
+    infinity or NaN sees get that value in its column, wherever the row lies in its tile
+    (weights of scores of a few units, far from where exp gives 0)."""
+    import sample_grad_norms_amd as dp
+    q, k, v, do = (x.to(dev()) for x in make(N, Hq, Hkv, D, dtype, 34))
+    o, lse = dp.attention_forward(q, k, v)
+    _, dk0, dv0 = dp.attention_backward(do, q, k, v, o, lse)
+    for row in (5, 63, N // 2, N - 1):
+        do2 = do.clone()
+        do2[row, :, 3] = value
+        _, dk, dv = dp.attention_backward(do2, q, k, v, o, lse)
+        seen = dv[:row + 1, :, 3].float()
+        right = bool((seen.isnan() if math.isnan(value) else seen == value).all())
+        others = torch.cat([dv[:, :, :3], dv[:, :, 4:]], dim=2), torch.cat([dv0[:, :, :3], dv0[:, :, 4:]], dim=2)
+        assert right and torch.equal(*others) and torch.equal(dv[row + 1:], dv0[row + 1:]), row
+        assert not bool(dk[:row + 1].isfinite().any()) and torch.equal(dk[row + 1:], dk0[row + 1:]), row
