@@ -841,6 +841,10 @@ __device__ __forceinline__ float dot_chunk(const uint4& x, const uint4& y, float
   return s;
 }
 
+// lse in units of log 2. A query all of whose scores are -infinity has no weights: NaN,
+// also against scores that are computed without the row's infinities.
+__device__ __forceinline__ float scaled_lse(float lse) { return lse == -INFINITY ? NAN : lse * kLog2e; }
+
 // One wave's pass for dq over the keys k0, k0 + 32 waves, .., as forward_pass.
 template <bool BF16, int DC, int BUFFERS>
 __device__ __forceinline__ void backward_q_pass(bool careful, const Args& a, int32_t start, int32_t len, int32_t kh,
@@ -931,7 +935,7 @@ __global__ __launch_bounds__(256, !BF16 ? 1 : DC == 64 ? 3 : 2) void k_backward_
   float lse = 0.f;
   if (query < len) {
     const int64_t at = (int64_t)h * a.N + start + query;
-    lse = a.lse[at] * kLog2e;
+    lse = scaled_lse(a.lse[at]);
     if (g == 0) {
       *(float2*)(a.pairs + 2 * at) = make_float2(lse, delta);
     }
@@ -1023,7 +1027,7 @@ __global__ __launch_bounds__(64 * NS, BF16 ? 2 : 1) void k_backward_q_rows(Args 
   float lse = 0.f;
   if (query < len) {
     const int64_t at = (int64_t)h * a.N + start + query;
-    lse = a.lse[at] * kLog2e;
+    lse = scaled_lse(a.lse[at]);
     if (g == 0 && split == 0 && z == 0) *(float2*)(a.pairs + 2 * at) = make_float2(lse, delta);
   }
   f32x16_t acc[G::kTiles];

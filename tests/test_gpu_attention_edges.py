@@ -125,3 +125,23 @@ def test_an_output_gradient_that_is_not_finite_reaches_dv_as_it_is(N, Hq, Hkv, D
         others = torch.cat([dv[:, :, :3], dv[:, :, 4:]], dim=2), torch.cat([dv0[:, :, :3], dv0[:, :, 4:]], dim=2)
         assert right and torch.equal(*others) and torch.equal(dv[row + 1:], dv0[row + 1:]), row
         assert not bool(dk[:row + 1].isfinite().any()) and torch.equal(dk[row + 1:], dk0[row + 1:]), row
+
+
+@pytest.mark.parametrize("dtype,N,Hq,Hkv,D", EVERY)
+def test_a_query_without_weights_gives_nan(N, Hq, Hkv, D, dtype):
+    """A query all of whose scores are -infinity: exp(-inf - -inf) is NaN for every key
+    that it sees, and so are those keys' gradients, in the query's own tile as elsewhere."""
+    import sample_grad_norms_amd as dp
+    q, k, v, do = make(N, Hq, Hkv, D, dtype, 35)
+    k[:, :, 3] = k[:, :, 3].abs() + 0.125
+    q, k, v, do = (x.to(dev()) for x in (q, k, v, do))
+    o, lse = dp.attention_forward(q, k, v)
+    _, dk0, dv0 = dp.attention_backward(do, q, k, v, o, lse)
+    for row in (5, 63, N // 2, N - 1):
+        q2 = q.clone()
+        q2[row, :, 3] = -math.inf
+        o, lse = dp.attention_forward(q2, k, v)
+        assert bool(o[row].isnan().all()) and bool((lse[:, row] == -math.inf).all())
+        dq, dk, dv = dp.attention_backward(do, q2, k, v, o, lse)
+        gone = bool(dv[:row + 1].isnan().all()) and bool(dk[:row + 1].isnan().all()) and bool(dq[row].isnan().all())
+        assert gone and torch.equal(dk[row + 1:], dk0[row + 1:]) and torch.equal(dv[row + 1:], dv0[row + 1:]), row
