@@ -342,6 +342,8 @@ class RandomizedClipping:
                     used.append((A, G, (S, P)))
         for (_, order, G, scale) in self._table_recs:
             dp.embed_norm(order, G, scale=scale, out=n, accumulate=True)
+        if self._pending is None:   # (no check will read them)
+            self._table_recs = []
         c = dp.clip_factors(n, self.C)
         self.last_layers = used if self.keep_layers else []
         return n, c

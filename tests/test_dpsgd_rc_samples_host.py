@@ -245,3 +245,33 @@ def test_layers_that_read_one_tensor_share_its_copy():
         losses = (model[0](x) + model[1](x)).float().sum((1, 2))
     (A, _), (A2, _) = rc._collect(losses)
     assert A.data_ptr() == A2.data_ptr()
+
+
+def test_a_tables_gradients_are_let_go_after_the_norm(monkeypatch):
+    """Only the step that is checked keeps the order and output gradients of a table for
+    the second backward pass."""
+    import gc
+    import weakref
+
+    import sample_grad_norms_amd as dp
+    from sample_grad_norms_amd.dpsgd_rc import RandomizedClipping
+    plain, held = dp.embed_norm, []
+
+    def norm(order, G, **kw):
+        held.append(weakref.ref(G))
+        return plain(order, G, **kw)
+
+    monkeypatch.setattr(dp, "embed_norm", norm)
+    torch.manual_seed(12)
+    model = _Flattened(True)
+    rc = RandomizedClipping(model, C=1.0, noise_multiplier=0.0, estimator="exact")
+    for j in range(3):
+        held.clear()
+        with rc.capture():
+            losses = losses_of(model, tokens())
+        _, c = rc.clip_factors(losses)
+        gc.collect()
+        assert len(held) == 2 and all((g() is not None) == (j == 0) for g in held)
+        rc.clipped_backward(losses, c)
+        gc.collect()
+        assert all(g() is None for g in held)
