@@ -1,7 +1,7 @@
 """Runs one named workload a few times, for profiling with rocprofv3 (the
 112-projection stack with independent inputs is profiled through bench.py).
 
-    python sample_grad_norms_amd/profile_workloads.py NAME [--reps R] [--calib-copy]
+    python sample_grad_norms_amd/profile_workloads.py NAME [--reps R] [--calib-copy] [--time]
 
 NAME is one of:
   long_context_hutch  Hutchinson, B=1, T=32768, d=2048, p=8192, k=32
@@ -16,6 +16,7 @@ NAME is one of:
   dpsgd_step          DP-SGD-RC training steps on a random-init Llama-width stack
                       (2 decoder layers, B=4, T=2048, bf16): forward, backward 1,
                       the norm path, backward 2 of sum c_i l_i, noise, Adam
+  dpsgd_step_library  the same with the library's attention
   dpsgd_step_tokens   the same from token ids, with the library's embedding table
                       (32768 rows, trained) and attention
   embedding           lookup, order, per-sample norm and table gradient, B=4, T=4096,
@@ -23,20 +24,23 @@ NAME is one of:
   attention           causal attention and its gradients, B=4, T=2048, 32 heads over
                       8, head width 64, bf16
 --calib-copy first runs one 1 GiB device-to-device copy, the reference the
-counter summaries scale FETCH_SIZE and WRITE_SIZE by.
+counter summaries scale FETCH_SIZE and WRITE_SIZE by. --time (for runs without
+the profiler) prints the wall time of a call, after three that are not timed, and
+the largest amount of memory allocated in them.
 """
 from __future__ import annotations
 
 import argparse
 import os
 import sys
+import time
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 if ROOT not in sys.path:
     sys.path.insert(0, ROOT)
 
 NAMES = ("long_context_hutch", "long_context_exact", "hutchpp", "single_layer", "single_layer_gram", "shared_stack",
-         "sign_stack", "lora_routed", "dpsgd_step", "dpsgd_step_tokens",
+         "sign_stack", "lora_routed", "dpsgd_step", "dpsgd_step_library", "dpsgd_step_tokens",
          "embedding", "attention")
 
 
@@ -45,6 +49,7 @@ def main() -> None:
     ap.add_argument("name", choices=NAMES)
     ap.add_argument("--reps", type=int, default=5)
     ap.add_argument("--calib-copy", action="store_true")
+    ap.add_argument("--time", action="store_true")
     a = ap.parse_args()
     import torch
     import sample_grad_norms_amd as dp
@@ -73,12 +78,14 @@ def main() -> None:
     elif a.name == "lora_routed":
         routed = [(A, G, None) for (A, G, _) in workloads.lora_stack(device=dev)]
         fn = lambda: dp.norms_routed(routed, 32)
-    elif a.name in ("dpsgd_step", "dpsgd_step_tokens"):
+    elif a.name.startswith("dpsgd_step"):
         from sample_grad_norms_amd.dpsgd_rc import RandomizedClipping
         from workloads import llama_block as lb
         shape = dict(layers=2, dim=2048, heads=32, kv_heads=8, hidden=8192, vocab=2048)
-        if a.name == "dpsgd_step_tokens":   # from token ids, with the library's table and attention
-            shape.update(vocab_in=32768, embed_scale=45.0, ops="library")
+        if a.name == "dpsgd_step_tokens":   # from token ids, with the library's table
+            shape.update(vocab_in=32768, embed_scale=45.0)
+        if a.name != "dpsgd_step":
+            shape.update(ops="library")
         model = lb.build(90, device=dev, dtype=torch.bfloat16, **shape)
         x, y = lb.batch(91, 4, 2048, shape["dim"], shape["vocab"], device=dev, dtype=torch.bfloat16)
         if a.name == "dpsgd_step_tokens":
@@ -118,9 +125,18 @@ def main() -> None:
     else:
         pr = workloads.config2(device=dev)
         fn = (lambda: dp.exact(pr.A, pr.G, route="gram")) if a.name.endswith("gram") else (lambda: dp.hutch(pr.A, pr.G, pr.P))
+    if a.time:
+        for _ in range(3):
+            fn()
+        torch.cuda.synchronize()
+        torch.cuda.reset_peak_memory_stats()
+    start = time.perf_counter()
     for _ in range(a.reps):
         fn()
     torch.cuda.synchronize()
+    if a.time:
+        print(f"{a.name}: {(time.perf_counter() - start) / a.reps * 1e3:.2f} ms a call, "
+              f"{torch.cuda.max_memory_allocated() / 1e9:.2f} GB at most", flush=True)
     print(f"{a.name}: {a.reps} calls done", flush=True)
 
 
