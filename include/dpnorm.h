@@ -367,6 +367,10 @@ dpnorm_status dpnorm_embed_grad(const void* tok, dpnorm_index it, const void* or
  * memory outside the tensors is touched, and give undefined values. Rows that
  * belong to no sequence (before the first and behind the last) are not read;
  * they are left as they are in the outputs, or set to zero with clear_rest = 1.
+ * Sums, softmax statistics and delta are fp32. For bf16 inputs the weights (p,
+ * and ds of the gradients) are rounded to bf16, half a step or 2^-8 relative
+ * each, before they multiply rows; lse has the unrounded weights' sum. A row
+ * with an infinity or NaN changes no bit of the rows that do not see it.
  * D: a multiple of 8 (bf16) or 4 (fp32), at most 128. scale finite and > 0. */
 typedef struct dpnorm_attn_shape {
   dpnorm_dtype dtype;

@@ -682,7 +682,8 @@ def attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seql
     strides of any multiples of 16 bytes; Hq a multiple of Hkv. cu_seqlens: int32 [S + 1] row offsets on
     the GPU; without it the N rows are ``sequences`` (default 1) sequences of
     equal length. scale defaults to 1 / sqrt(D). Returns (o [N][Hq][D],
-    lse float32 [Hq][N]). Rows that belong to no sequence are left as they
+    lse float32 [Hq][N]). Sums are float32; bfloat16 calls round the softmax
+    weights to bfloat16 before they multiply v. Rows that belong to no sequence are left as they
     are in a given ``out`` and ``lse`` (give both or neither), and are zero
     where the call makes them.
     """
@@ -712,7 +713,8 @@ def attention_backward(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: to
                        workspace: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """(dq, dk, dv) of attention_forward for the output gradient ``do``
     (dpnorm_attention_backward). q, k, v, cu_seqlens, sequences and scale are
-    the forward call's, o and lse its results. ``out``: three tensors to write
+    the forward call's, o and lse its results. Sums are float32; bfloat16 calls
+    round p and ds to bfloat16 before they multiply rows. ``out``: three tensors to write
     to. Rows that belong to no sequence are left as they are in ``out``, and
     are zero where the call makes it.
     """

@@ -102,8 +102,8 @@ int64_t slots_of(const attn::Args& a, int rows) {
 // work groups are few (us, rows against tiles: forward T = 1024, 16/4 heads,
 // D = 64 11.6 against 18.7; T = 2048, 16 heads 26 against 33; T = 2048, 32 heads
 // 48 against 37); float32 rows of up to 64 columns, where two of their work groups
-// fit a CU, always (B = 2, T = 2048, 16/4 heads 182 against 275; 128 columns 410
-// against 367).
+// fit a CU, always (B = 2, T = 2048, 16/4 heads 190 against 275; 128 columns 410
+// against 366).
 constexpr int64_t kRowsMost = 1536;
 template <bool BF16, int DC>
 constexpr bool kRowsAlways = !BF16 && DC == 64;

@@ -749,8 +749,8 @@ __device__ __forceinline__ void tile_again(const Args& a, int32_t start, int32_t
 // of the next step are computed beside the weights of this one: what bounds it is a
 // wave's exponentials, maxima and sums, about as long as its MFMAs, and two or three
 // work groups a CU so that one wave's run beside another's. B = 4, T = 2048, 32/8 heads,
-// D = 64: 102 us, 674 TF/s of the pairs u <= t; 12289 + 777 + 4100 rows, 16/2 heads,
-// D = 128: 750 us, 920 TF/s. A large bf16 matrix product reaches 1241 TF/s.
+// D = 64: 104 us, 661 TF/s of the pairs u <= t; 12289 + 777 + 4100 rows, 16/2 heads,
+// D = 128: 713 us, 968 TF/s. A large bf16 matrix product reaches 1241 TF/s.
 template <bool BF16, int DC>
 __global__ __launch_bounds__(256, BF16 ? 2 : 1) void k_forward(Args a) {
   using G = Geo<BF16, DC>;
@@ -896,7 +896,7 @@ __device__ __forceinline__ void backward_q_pass(bool careful, const Args& a, int
 
 // dq, and the pairs for the second launch, by tiles as k_forward's. Three products a
 // step (S, dP, dQ); bound by the MFMAs and the reads of K and V from LDS, each used by
-// 32 queries a wave. B = 4, T = 2048, 32/8 heads, D = 64: 140 us, 736 TF/s.
+// 32 queries a wave. B = 4, T = 2048, 32/8 heads, D = 64: 131 us, 787 TF/s.
 template <bool BF16, int DC>
 __global__ __launch_bounds__(256, !BF16 ? 1 : DC == 64 ? 3 : 2) void k_backward_q(Args a) {
   using G = Geo<BF16, DC>;
@@ -1189,7 +1189,8 @@ __device__ __forceinline__ void backward_kv_pass(bool& careful, const Args& a, i
 // the chain of a step, reads, products, exponentials, products, of which the registers
 // allow two waves a SIMD; the LDS is busy half of the time, and a fifth fewer reads (lse
 // and delta as a column of the first products) gained 2 % at D = 64 and lost 5 % at 128.
-// B = 4, T = 2048, 32/8 heads, D = 64: 243 us, 566 TF/s; 16/4 heads, D = 128: 276 us.
+// B = 4, T = 2048, 32/8 heads, D = 64: 229 us, 600 TF/s; 16/4 heads, D = 128: 285 us
+// (where 12 registers spill).
 // SPLIT: a few such work groups share
 // the steps, as many as leave each wave kSteps of them, and the last to arrive adds
 // their sums in a fixed order. The sums and the counter go past the L2 caches, which

@@ -90,6 +90,8 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: Opt
     sequence without them). Hq is a multiple of Hkv, D a multiple of 8
     (bfloat16) or 4 (float32) up to 128; scale defaults to 1 / sqrt(D). Rows of
     a packed call that belong to no sequence give zeros and get zero gradients.
+    Sums are float32; in bfloat16 the softmax weights are rounded to bfloat16
+    before they multiply rows.
     """
     if q.dim() == 4:
         if cu_seqlens is not None:
