@@ -25,9 +25,9 @@ import sample_grad_norms_amd as dp
 class _Lookup(torch.autograd.Function):
     @staticmethod
     def forward(ctx, weight, tokens, scale):
-        ctx.save_for_backward(tokens)
+        ctx.save_for_backward(tokens)   # (the caller's own, so that autograd sees a write to them)
         ctx.rows, ctx.scale = weight.shape[0], scale
-        return dp.embed_lookup(tokens, weight, scale=scale)
+        return dp.embed_lookup(tokens.contiguous(), weight, scale=scale)
 
     @staticmethod
     @once_differentiable
@@ -36,7 +36,7 @@ class _Lookup(torch.autograd.Function):
         grad = grad.reshape(1, -1, grad.shape[-1])
         if not grad.is_contiguous() or grad.data_ptr() % 16 != 0:
             grad = grad.clone(memory_format=torch.contiguous_format)
-        return dp.embed_grad(tokens.reshape(1, -1), grad, ctx.rows, scale=ctx.scale), None, None
+        return dp.embed_grad(tokens.reshape(1, -1).contiguous(), grad, ctx.rows, scale=ctx.scale), None, None
 
 
 class Embedding(nn.Module):
@@ -53,7 +53,7 @@ class Embedding(nn.Module):
         self.weight = nn.Parameter(torch.randn(rows, dim, device=device, dtype=dtype))
 
     def forward(self, tokens: torch.Tensor) -> torch.Tensor:
-        return _Lookup.apply(self.weight, tokens.contiguous(), self.scale)
+        return _Lookup.apply(self.weight, tokens, self.scale)
 
 
 class _Attention(torch.autograd.Function):

@@ -317,3 +317,18 @@ def test_ids_need_not_be_contiguous():
         assert torch.equal(out, e(ids.contiguous())) and torch.equal(out, e.weight[ids])
         (got,) = torch.autograd.grad(out.sum(), [e.weight])
         assert torch.equal(got, torch.bincount(ids.flatten(), minlength=30)[:, None].expand(30, 48).float())
+
+
+def test_a_write_to_the_ids_before_the_backward_pass_is_an_error():
+    """Contiguous or not: the gradient would be that of other rows."""
+    from sample_grad_norms_amd.layers import Embedding
+    e = Embedding(30, 48, device=dev())
+    for cut in (slice(None), slice(0, 20), slice(3, 4)):
+        tok = torch.randint(0, 30, (4, 21), generator=torch.Generator().manual_seed(24)).to(dev())
+        ids = tok[:, cut]
+        out = e(ids)
+        (got,) = torch.autograd.grad(out.sum(), [e.weight], retain_graph=True)
+        assert torch.equal(got, torch.bincount(ids.flatten(), minlength=30)[:, None].expand(30, 48).float())
+        tok += 1
+        with pytest.raises(RuntimeError, match="modified by an inplace"):
+            out.sum().backward()
