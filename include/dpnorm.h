@@ -411,6 +411,58 @@ dpnorm_status dpnorm_attention_backward(const dpnorm_attn_shape* shape, const dp
                                         const dpnorm_attn_tensor* dq, const dpnorm_attn_tensor* dk,
                                         const dpnorm_attn_tensor* dv, void* ws, size_t ws_bytes, hipStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Layer norm and RMS norm: forward, gradients, and the per-sample norm of the
+ * gradient of their gain w and bias b [d]. With N rows of d columns (or the
+ * rows of B samples of T) and
+ *   h = (x - mu) r,   r = (mean((x - mu)^2) + eps)^-1/2,
+ *   mu = mean(x) for DPNORM_LN_LAYER, 0 for DPNORM_LN_RMS,
+ * all sums are fp32 (a sample's sum of squares over the columns fp64), and each
+ * result is rounded once. x, dy, G, y, dx [N][d] and w, b, dw, db [d] are of
+ * type dt, contiguous and 16-byte aligned; mean, rstd float [N]. d: a multiple
+ * of 8 (bf16) or 4 (fp32), at most 32768; N (B T) at most 2^30. RMS norm has no
+ * mean and no bias: pass NULL. A row that is not finite gives what the formulas
+ * give; it changes no other row of y and dx. Outputs must not overlap inputs or
+ * each other. The conventions at the top hold.
+ * ------------------------------------------------------------------------- */
+typedef enum dpnorm_ln_kind {
+  DPNORM_LN_LAYER = 0,
+  DPNORM_LN_RMS = 1,
+  DPNORM_LN_KIND_RANGE_MIN_ = -2147483647 - 1,
+  DPNORM_LN_KIND_RANGE_MAX_ = 2147483647
+} dpnorm_ln_kind;
+
+/* y = h w + b. b may be NULL (no bias), and so may mean and rstd (the row's mu
+ * and r, which the backward call reads). eps finite and not negative. */
+dpnorm_status dpnorm_layernorm_forward(const void* x, const void* w, const void* b, dpnorm_dtype dt, dpnorm_ln_kind kind,
+                                       int64_t N, int64_t d, float eps, void* y, float* mean, float* rstd,
+                                       hipStream_t stream);
+
+/* Gradients for the output's gradient dy, from the forward call's mean and rstd:
+ *   dx = r (g - mean(g) - h mean(g h)),  g = dy w   (RMS norm: without mean(g))
+ *   dw = sum_i c[i] sum_{t in i} dy_t h_t,   db = sum_i c[i] sum_{t in i} dy_t
+ * c float [B], or NULL for 1; it does not change dx. dx, dw and db may each be
+ * NULL (not wanted), but not all. ws may be NULL when its size is 0 or neither
+ * dw nor db is wanted. */
+dpnorm_status dpnorm_layernorm_backward_workspace(dpnorm_dtype dt, dpnorm_ln_kind kind, int64_t B, int64_t T, int64_t d,
+                                                  size_t* bytes);
+dpnorm_status dpnorm_layernorm_backward(const void* dy, const void* x, const void* w, const float* mean, const float* rstd,
+                                        dpnorm_dtype dt, dpnorm_ln_kind kind, int64_t B, int64_t T, int64_t d,
+                                        const float* c, void* dx, void* dw, void* db, void* ws, size_t ws_bytes,
+                                        hipStream_t stream);
+
+/* Exact squared per-sample norm of the gradients of gain (parts DPNORM_LN_GAIN),
+ * bias (DPNORM_LN_BIAS) or both (their sum of the two values):
+ *   n[i] (+)= || sum_{t in i} G_t h_t ||^2 + || sum_{t in i} G_t ||^2
+ * with G the gradient of the output and h taken again from x. */
+#define DPNORM_LN_GAIN 1
+#define DPNORM_LN_BIAS 2
+dpnorm_status dpnorm_layernorm_norm_workspace(dpnorm_dtype dt, dpnorm_ln_kind kind, int64_t B, int64_t T, int64_t d,
+                                              size_t* bytes);
+dpnorm_status dpnorm_layernorm_norm(const void* x, const void* G, dpnorm_dtype dt, dpnorm_ln_kind kind, int64_t B, int64_t T,
+                                    int64_t d, float eps, int parts, float* n, int accumulate, void* ws, size_t ws_bytes,
+                                    hipStream_t stream);
+
 /* Thin event helpers for profiling (wrap hipEventCreate / Destroy /
  * ElapsedTime / Synchronize); provided so bindings need only this library. */
 dpnorm_status dpnorm_event_create(hipEvent_t* ev);

@@ -25,6 +25,7 @@ from . import _lib
 
 __all__ = ["DpnormError", "hutch", "hutch_grouped", "hutchpp", "exact", "clip_factors", "hutchpp_split", "KernelTimer",
            "embed_lookup", "EmbedOrder", "embed_order", "embed_norm", "embed_grad", "attention_forward", "attention_backward",
+           "layernorm_forward", "layernorm_backward", "layernorm_norm",
            "lib", "hutch_workspace", "hutch_grouped_workspace", "hutchpp_workspace", "exact_workspace"]
 
 
@@ -458,7 +459,7 @@ def hutchpp_split(k: int) -> Tuple[int, int]:
 
 
 # ---------------------------------------------------------------------------
-# Around the linear layers: the embedding table and causal attention. The calls
+# Around the linear layers: the embedding table, causal attention and norm layers. The calls
 # run on the current stream of the tensors' device; temporaries come from
 # torch's allocator on that stream.
 # ---------------------------------------------------------------------------
@@ -738,6 +739,142 @@ def attention_backward(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: to
     elif shape.clear_rest:
         dq.zero_(), dk.zero_(), dv.zero_()
     return dq, dk, dv
+
+
+def _normed(x: torch.Tensor, w: Optional[torch.Tensor], b: Optional[torch.Tensor], d: int) -> int:
+    """Checks gain and bias against rows x of d columns; the type's code."""
+    code = _code(x.dtype)
+    for t, name in ((w, "weight"), (b, "bias")):
+        if t is not None:
+            _need(t, name, 1, x.dtype)
+            if t.shape[0] != d:
+                raise ValueError(f"{name} must have the {d} entries of a row")
+    _one_device(x.device, w, b)
+    return code
+
+
+def _rows_of(t: torch.Tensor, name: str, like: Optional[torch.Tensor] = None) -> None:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dim() < 1:
+        raise ValueError(f"{name} must have rows: [..., d]")
+    _need(t, name, t.dim(), like.dtype if like is not None else None)
+    if like is not None and t.shape != like.shape:
+        raise ValueError(f"{name} must be {list(like.shape)}, got {list(t.shape)}")
+
+
+def layernorm_forward(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None, eps: float = 1e-5,
+                      rms: bool = False, out: Optional[torch.Tensor] = None
+                      ) -> Tuple[torch.Tensor, Optional[torch.Tensor], torch.Tensor]:
+    """Layer norm (or, with rms=True, RMS norm) of the rows of x
+    (dpnorm_layernorm_forward): (x - mean) rstd weight + bias.
+
+    x [..., d], weight and bias [d], bfloat16 or float32, contiguous; d a
+    multiple of 8 (bfloat16) or 4 (float32) up to 32768. Returns (y, mean, rstd), the
+    statistics float32 [...], which layernorm_backward reads; RMS norm has
+    no bias and its mean is None. Sums are float32; y is rounded once.
+    """
+    _rows_of(x, "x")
+    d = x.shape[-1]
+    if rms and bias is not None:
+        raise ValueError("RMS norm has no bias")
+    _need(weight, "weight", 1, x.dtype)
+    code = _normed(x, weight, bias, d)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _rows_of(out, "out", x)
+        _one_device(x.device, out)
+    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    mean = None if rms else torch.empty_like(rstd)
+    n = rstd.numel()
+    if n * d > 0:
+        _run(x.device, "dpnorm_layernorm_forward", x.data_ptr(), weight.data_ptr(), bias.data_ptr() if bias is not None else None, code,
+             int(rms), n, d, eps, out.data_ptr(), mean.data_ptr() if mean is not None else None, rstd.data_ptr())
+    return out, mean, rstd
+
+
+def layernorm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, mean: Optional[torch.Tensor], rstd: torch.Tensor,
+                       bias: bool = True, weights: Optional[torch.Tensor] = None, need_dx: bool = True, need_dw: bool = True,
+                       workspace: Optional[torch.Tensor] = None
+                       ) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor], Optional[torch.Tensor]]:
+    """(dx, dweight, dbias) of layernorm_forward for the output's gradient dy
+    (dpnorm_layernorm_backward); mean (None: RMS norm) and rstd are the forward
+    call's. dbias is None for RMS norm and with bias=False; need_dx=False and
+    need_dw=False leave out the others.
+
+    weights: float32 [B] factors of the samples (clip factors) for dweight and
+    dbias, x then being [B, ..., d]; they do not change dx. Sums are float32,
+    each result is rounded once, and results are reproducible bit for bit.
+    """
+    _rows_of(x, "x")
+    _rows_of(dy, "dy", x)
+    d, device = x.shape[-1], x.device
+    _need(weight, "weight", 1, x.dtype)
+    code = _normed(x, weight, None, d)
+    rms = mean is None
+    bias = bias and not rms
+    for t, name in ((mean, "mean"), (rstd, "rstd")):
+        if t is not None:
+            _need(t, name, x.dim() - 1, torch.float32)
+            if t.shape != x.shape[:-1]:
+                raise ValueError(f"{name} must be {list(x.shape[:-1])}, got {list(t.shape)}")
+    N, B = rstd.numel(), 1
+    if weights is not None:
+        _need(weights, "weights", 1, torch.float32)
+        B = weights.shape[0]
+        if x.dim() < 2 or x.shape[0] != B:
+            raise ValueError(f"weights are of {B} samples, x must be [{B}, ..., d]")
+    if not (need_dx or need_dw or bias):
+        raise ValueError("no gradient is wanted")
+    _one_device(device, dy, mean, rstd, weights)
+    dx = torch.empty_like(x) if need_dx else None
+    dw = torch.empty_like(weight) if need_dw else None
+    db = torch.empty_like(weight) if bias else None
+    if N * d == 0:
+        for t in (dw, db):
+            if t is not None:
+                t.zero_()
+        return dx, dw, db
+    nbytes = C.c_size_t(0)
+    _check(lib().dpnorm_layernorm_backward_workspace(code, int(rms), B, N // B, d, C.byref(nbytes)), "dpnorm_layernorm_backward_workspace")
+    need = nbytes.value if need_dw or bias else 0
+    ws, wsp = _given_workspace(workspace, need, device)
+    ptr = lambda t: t.data_ptr() if t is not None else None
+    _run(device, "dpnorm_layernorm_backward", dy.data_ptr(), x.data_ptr(), weight.data_ptr(), ptr(mean), rstd.data_ptr(), code, int(rms),
+         B, N // B, d, ptr(weights), ptr(dx), ptr(dw), ptr(db), wsp, need)
+    return dx, dw, db
+
+
+def layernorm_norm(x: torch.Tensor, G: torch.Tensor, eps: float = 1e-5, rms: bool = False, gain: bool = True, bias: bool = True,
+                   out: Optional[torch.Tensor] = None, accumulate: bool = False,
+                   workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Exact squared per-sample gradient norm of a layer norm's gain and bias
+    (dpnorm_layernorm_norm): n_i = ||sum_t G[i, t] h[i, t]||^2 + ||sum_t G[i, t]||^2
+    with h the normalised rows of x.
+
+    x [B][T][d] the norm's input, G [B][T][d] the gradient of its output.
+    gain, bias: whose gradients count (RMS norm has no bias). Returns
+    float32 [B]; with accumulate=True the norms are added to ``out``.
+    """
+    _need(x, "x", 3)
+    _need(G, "G", 3, x.dtype)
+    if G.shape != x.shape:
+        raise ValueError(f"G must be {list(x.shape)}, got {list(G.shape)}")
+    parts = (_lib.LN_GAIN if gain else 0) | (_lib.LN_BIAS if bias and not rms else 0)
+    if parts == 0:
+        raise ValueError("neither the gain's gradient nor a bias's is wanted")
+    code, (B, T, d), device = _code(x.dtype), x.shape, x.device
+    n = _out(out, B, device, accumulate)
+    _one_device(device, G, n)
+    if B * T * d == 0:
+        return n if accumulate else n.zero_()
+    nbytes = C.c_size_t(0)
+    _check(lib().dpnorm_layernorm_norm_workspace(code, int(rms), B, T, d, C.byref(nbytes)), "dpnorm_layernorm_norm_workspace")
+    ws, wsp = _given_workspace(workspace, nbytes.value, device)
+    _run(device, "dpnorm_layernorm_norm", x.data_ptr(), G.data_ptr(), code, int(rms), B, T, d, eps, parts, n.data_ptr(), int(accumulate),
+         wsp, nbytes.value)
+    return n
 
 
 class KernelTimer:

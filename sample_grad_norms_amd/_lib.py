@@ -23,6 +23,9 @@ F32, BF16 = 0, 1
 I32, I64 = 0, 1
 # dpnorm_route
 EXACT_AUTO, EXACT_EXPLICIT, EXACT_GRAM = 0, 1, 2
+# dpnorm_ln_kind, and the parts of dpnorm_layernorm_norm
+LN_LAYER, LN_RMS = 0, 1
+LN_GAIN, LN_BIAS = 1, 2
 # dpnorm_kernel_kind
 KERNEL_PREPARE, KERNEL_ROWPROJ, KERNEL_TCONTRACT, KERNEL_YSUM, KERNEL_FINISH = 1, 2, 3, 4, 5
 KERNEL_NAMES = {1: "prepare", 2: "rowproj", 3: "tcontract", 4: "ysum", 5: "finish"}
@@ -94,6 +97,13 @@ SIGNATURES = {
     "dpnorm_attention_forward": ([_shp, _tp, _tp, _tp, _tp, _vp, _vp], C.c_int),
     "dpnorm_attention_backward_workspace": ([_shp, _szp], C.c_int),
     "dpnorm_attention_backward": ([_shp, _tp, _tp, _tp, _tp, _tp, _vp, _tp, _tp, _tp, _vp, _sz, _vp], C.c_int),
+    "dpnorm_layernorm_forward": ([_vp, _vp, _vp, C.c_int, C.c_int, _i64, _i64, _f32, _vp, _vp, _vp, _vp], C.c_int),
+    "dpnorm_layernorm_backward_workspace": ([C.c_int, C.c_int, _i64, _i64, _i64, _szp], C.c_int),
+    "dpnorm_layernorm_backward": ([_vp, _vp, _vp, _vp, _vp, C.c_int, C.c_int, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _sz,
+                                   _vp], C.c_int),
+    "dpnorm_layernorm_norm_workspace": ([C.c_int, C.c_int, _i64, _i64, _i64, _szp], C.c_int),
+    "dpnorm_layernorm_norm": ([_vp, _vp, C.c_int, C.c_int, _i64, _i64, _i64, _f32, C.c_int, _vp, C.c_int, _vp, _sz, _vp],
+                              C.c_int),
     "dpnorm_event_create": ([C.POINTER(_vp)], C.c_int),
     "dpnorm_event_destroy": ([_vp], C.c_int),
     "dpnorm_event_elapsed_ms": ([_vp, _vp, _fp], C.c_int),

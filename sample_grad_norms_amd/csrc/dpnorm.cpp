@@ -1145,3 +1145,4 @@ dpnorm_status dpnorm_event_synchronize(hipEvent_t ev) {
 // one unit, so that a build of the library's host side alone has them too.
 #include "embed_api.h"
 #include "attention_api.h"
+#include "layernorm_api.h"
