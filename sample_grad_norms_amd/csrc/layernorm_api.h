@@ -48,19 +48,25 @@ hipError_t with_ln(dpnorm_dtype dt, dpnorm_ln_kind kind, int64_t d, F f) {
   return dt == DPNORM_BF16 ? kinds(std::true_type{}) : kinds(std::false_type{});
 }
 
-// Rows that a work group of the summing kernels takes in one round.
-int64_t ln_round(dpnorm_dtype dt, int64_t d) {
+// Work groups of the summing kernels that share `rows` rows (among `others` such sets of
+// rows): as many as the GPU holds at once, since each leaves 2 d sums for the second
+// launch. One wave a row: a work group a CU (two gain nothing: 4 x 4096 rows of 2048
+// bf16, 46 us with 256, 50 with 512), with two rounds of rows for each wave at least;
+// four waves: two (2 x 4096 rows of 4096: 54 us with 512, 66 with 256); four rows at
+// least (1024 rows of 16384: 49 us with four, 73 with two).
+int64_t ln_blocks(dpnorm_dtype dt, int64_t d, int64_t rows, int64_t others) {
   const int64_t chunks = d / (dt == DPNORM_BF16 ? 8 : 4);
-  return chunks <= 64 ? 32 : chunks <= 128 ? 16 : chunks <= 256 ? 8 : 1;
+  const int64_t least = chunks <= 64 ? 64 : chunks <= 128 ? 32 : chunks <= 256 ? 16 : 4;
+  const int64_t places = chunks > 256 && chunks <= 1024 ? 512 : 256;
+  return std::max<int64_t>(1, std::min(places / others, rows / least));
 }
 
-// Work groups of `places` on the whole GPU that share `rows` rows, with at least two
-// rounds each.
-int64_t ln_blocks(dpnorm_dtype dt, int64_t d, int64_t rows, int64_t places) {
-  const int64_t round = ln_round(dt, d);
-  return std::max<int64_t>(1, std::min(places, rows / (2 * round)));
+// Threads that share `rows` partial sums of a column (see add_rows): about four each.
+int32_t ln_slots(int64_t rows) {
+  int32_t s = 1;
+  while (s < 64 && 4 * s < rows) s *= 2;
+  return s;
 }
-constexpr int64_t kLnPlaces = 512;
 
 ln::Args ln_args(int64_t B, int64_t T, int64_t d) {
   ln::Args a{};
@@ -77,9 +83,10 @@ struct LnNormPlan {
 };
 LnNormPlan plan_ln_norm(dpnorm_dtype dt, int64_t B, int64_t T, int64_t d, int32_t columns) {
   LnNormPlan p;
-  p.shares = ln_blocks(dt, d, T, std::max<int64_t>(1, kLnPlaces / B));
+  p.shares = ln_blocks(dt, d, T, B);
   if (p.shares < 2) return p;
-  p.groups = (columns + 63) / 64;
+  const int64_t at_once = 4096 / ln_slots(p.shares);
+  p.groups = (columns + at_once - 1) / at_once;
   Bump w;
   w.take((size_t)(B * p.shares) * 2 * d * 4);
   p.off_arrived = w.take((size_t)B * 4);
@@ -126,7 +133,7 @@ dpnorm_status dpnorm_layernorm_backward_workspace(dpnorm_dtype dt, dpnorm_ln_kin
   if (!bytes) return DPNORM_ERR_NULL;
   const dpnorm_status st = check_ln(dt, kind, B, T, d);
   if (st != DPNORM_OK) return st;
-  const int64_t blocks = ln_blocks(dt, d, B * T, kLnPlaces);
+  const int64_t blocks = ln_blocks(dt, d, B * T, 1);
   *bytes = blocks > 1 ? align_up((size_t)blocks * 2 * d * 4) : 0;
   return DPNORM_OK;
 }
@@ -159,7 +166,7 @@ dpnorm_status dpnorm_layernorm_backward(const void* dy, const void* x, const voi
   a.dx = (char*)dx;
   a.dw = (char*)dw;
   a.db = (char*)db;
-  a.blocks = (int32_t)ln_blocks(dt, d, B * T, kLnPlaces);
+  a.blocks = (int32_t)ln_blocks(dt, d, B * T, 1);
   a.part = a.blocks > 1 ? (float*)ws : nullptr;
   hipError_t he = with_ln(dt, kind, d, [&](auto bf16, auto rms, auto nc, auto wv, auto r) {
     constexpr int W = decltype(wv)::value;
@@ -168,9 +175,10 @@ dpnorm_status dpnorm_layernorm_backward(const void* dy, const void* x, const voi
     return hipGetLastError();
   });
   if (he == hipSuccess && a.part && (dw || db)) {
-    const dim3 grid((uint32_t)((d + 63) / 64), layer ? 2 : 1);
-    if (dt == DPNORM_BF16) ln::k_backward_columns<true><<<grid, 1024, 0, stream>>>(a);
-    else ln::k_backward_columns<false><<<grid, 1024, 0, stream>>>(a);
+    const int32_t slots = ln_slots(a.blocks), at_once = 4096 / slots;
+    const dim3 grid((uint32_t)((d + at_once - 1) / at_once), layer ? 2 : 1);
+    if (dt == DPNORM_BF16) ln::k_backward_columns<true><<<grid, 1024, 0, stream>>>(a, slots);
+    else ln::k_backward_columns<false><<<grid, 1024, 0, stream>>>(a, slots);
     he = hipGetLastError();
   }
   return hip_status(he);
@@ -216,7 +224,7 @@ dpnorm_status dpnorm_layernorm_norm(const void* x, const void* G, dpnorm_dtype d
     return hipGetLastError();
   });
   if (he == hipSuccess && p.shares > 1) {
-    ln::k_norm_columns<><<<grid_of(B * p.groups), 1024, 0, stream>>>(a, B, (int32_t)p.groups);
+    ln::k_norm_columns<><<<grid_of(B * p.groups), 1024, 0, stream>>>(a, B, (int32_t)p.groups, ln_slots(p.shares));
     he = hipGetLastError();
   }
   return hip_status(he);
