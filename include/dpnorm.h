@@ -411,6 +411,34 @@ dpnorm_status dpnorm_attention_backward(const dpnorm_attn_shape* shape, const dp
                                         const dpnorm_attn_tensor* dq, const dpnorm_attn_tensor* dk,
                                         const dpnorm_attn_tensor* dv, void* ws, size_t ws_bytes, hipStream_t stream);
 
+/* Attention whose scores are changed before the softmax:
+ *   s_tu = cap tanh(scale q_t . k_u / cap) - slopes[h] |t - u|
+ * (cap = 0: scale q_t . k_u itself; slopes NULL: no bias), where row t of sequence s sees
+ * the rows u <= t and, with prefix, the rows u < prefix[s] of its sequence (clamped to
+ * its length). slopes: device float [Hq], of either sign, finite (not checked); prefix:
+ * device int32 [S]. cap is 0 or in 1/1024 .. 1024, with slopes scale is at least 2^-64,
+ * else ERR_VALUE. The gradients are those of q, k and v: the backward call is given what
+ * the forward call was, and ds has the factor 1 - tanh^2. slopes and prefix must not
+ * overlap outputs or ws. scores may be NULL, and all its fields 0: then the calls are
+ * dpnorm_attention_forward and _backward, bit for bit, whose definitions, checks and
+ * workspace hold for the rest. */
+typedef struct dpnorm_attn_scores {
+  float cap;
+  const float* slopes;
+  const int32_t* prefix;
+} dpnorm_attn_scores;
+
+dpnorm_status dpnorm_attention_scores_forward(const dpnorm_attn_shape* shape, const dpnorm_attn_scores* scores,
+                                              const dpnorm_attn_tensor* q, const dpnorm_attn_tensor* k,
+                                              const dpnorm_attn_tensor* v, const dpnorm_attn_tensor* o, float* lse,
+                                              hipStream_t stream);
+dpnorm_status dpnorm_attention_scores_backward(const dpnorm_attn_shape* shape, const dpnorm_attn_scores* scores,
+                                               const dpnorm_attn_tensor* dO, const dpnorm_attn_tensor* q,
+                                               const dpnorm_attn_tensor* k, const dpnorm_attn_tensor* v,
+                                               const dpnorm_attn_tensor* o, const float* lse, const dpnorm_attn_tensor* dq,
+                                               const dpnorm_attn_tensor* dk, const dpnorm_attn_tensor* dv, void* ws,
+                                               size_t ws_bytes, hipStream_t stream);
+
 /* ---------------------------------------------------------------------------
  * Layer norm and RMS norm: forward, gradients, and the per-sample norm of the
  * gradient of their gain w and bias b [d]. With N rows of d columns (or the

@@ -674,9 +674,30 @@ def _attn_shape(q, k, v, cu_seqlens, sequences, scale, clear):
     return _lib.AttnShape(code, N, S, Hq, Hkv, D, cup, scale, int(clear)), tq, tk, tv
 
 
+def _attn_scores(cap: Optional[float], slopes: Optional[torch.Tensor], prefix: Optional[torch.Tensor],
+                 shape: _lib.AttnShape, device: torch.device) -> Optional[_lib.AttnScores]:
+    """The record of changed scores; None where they are not."""
+    if slopes is None and prefix is None and not cap:
+        return None
+    sp = pp = None
+    if slopes is not None:
+        _need(slopes, "slopes", 1, torch.float32)
+        if slopes.shape[0] != shape.Hq:
+            raise ValueError(f"slopes must have an entry for each of the {shape.Hq} query heads")
+        sp = slopes.data_ptr()
+    if prefix is not None:
+        _need(prefix, "prefix", 1, torch.int32)
+        if prefix.shape[0] != shape.S:
+            raise ValueError(f"prefix must have an entry for each of the {shape.S} sequences")
+        pp = prefix.data_ptr()
+    _one_device(device, slopes, prefix)
+    return _lib.AttnScores(cap or 0.0, sp, pp)
+
+
 def attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None,
                       sequences: Optional[int] = None, scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
-                      lse: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+                      lse: Optional[torch.Tensor] = None, cap: Optional[float] = None, slopes: Optional[torch.Tensor] = None,
+                      prefix: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Causal attention of packed sequences (dpnorm_attention_forward).
 
     q [N][Hq][D], k and v [N][Hkv][D], bfloat16 or float32, token and head
@@ -687,6 +708,11 @@ def attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seql
     weights to bfloat16 before they multiply v. Rows that belong to no sequence are left as they
     are in a given ``out`` and ``lse`` (give both or neither), and are zero
     where the call makes them.
+
+    Scores may be changed before the softmax (dpnorm_attention_scores_forward):
+    cap, in 1/1024 .. 1024, makes a score s cap * tanh(s / cap); slopes, float32
+    [Hq] on the GPU, adds -slopes[h] * |t - u| for row t and key u; prefix, int32 [S]
+    on the GPU, lets every row of a sequence see its first prefix[s] rows.
     """
     if (out is None) != (lse is None):
         raise ValueError("give out and lse both, or neither")
@@ -701,8 +727,12 @@ def attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seql
         if tuple(lse.shape) != (Hq, N) or lse.device != device:
             raise ValueError(f"lse must be [Hq={Hq}][N={N}] on q's device")
     to = _heads(out, "out", q.dtype, device, q.shape)
+    scores = _attn_scores(cap, slopes, prefix, shape, device)
     if N > 0 and shape.S > 0:
-        _run(device, "dpnorm_attention_forward", shape, tq, tk, tv, to, lse.data_ptr())
+        if scores is None:
+            _run(device, "dpnorm_attention_forward", shape, tq, tk, tv, to, lse.data_ptr())
+        else:
+            _run(device, "dpnorm_attention_scores_forward", shape, scores, tq, tk, tv, to, lse.data_ptr())
     elif shape.clear_rest:
         out.zero_(), lse.zero_()
     return out, lse
@@ -711,10 +741,12 @@ def attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seql
 def attention_backward(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
                        lse: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None, sequences: Optional[int] = None,
                        scale: Optional[float] = None, out: Optional[Sequence[torch.Tensor]] = None,
-                       workspace: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+                       workspace: Optional[torch.Tensor] = None, cap: Optional[float] = None,
+                       slopes: Optional[torch.Tensor] = None,
+                       prefix: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """(dq, dk, dv) of attention_forward for the output gradient ``do``
-    (dpnorm_attention_backward). q, k, v, cu_seqlens, sequences and scale are
-    the forward call's, o and lse its results. Sums are float32; bfloat16 calls
+    (dpnorm_attention_backward, dpnorm_attention_scores_backward). q, k, v,
+    cu_seqlens, sequences, scale, cap, slopes and prefix are the forward call's, o and lse its results. Sums are float32; bfloat16 calls
     round p and ds to bfloat16 before they multiply rows. ``out``: three tensors to write
     to. Rows that belong to no sequence are left as they are in ``out``, and
     are zero where the call makes it.
@@ -731,11 +763,16 @@ def attention_backward(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: to
     else:
         dq, dk, dv = out
     tdq, tdk, tdv = (_heads(t, n, dtype, device, x.shape) for t, n, x in ((dq, "dq", q), (dk, "dk", k), (dv, "dv", k)))
+    scores = _attn_scores(cap, slopes, prefix, shape, device)
     if N > 0 and shape.S > 0:
         nbytes = C.c_size_t(0)
         _check(lib().dpnorm_attention_backward_workspace(shape, C.byref(nbytes)), "dpnorm_attention_backward_workspace")
         ws, wsp = _given_workspace(workspace, nbytes.value, device)
-        _run(device, "dpnorm_attention_backward", shape, tdo, tq, tk, tv, to, lse.data_ptr(), tdq, tdk, tdv, wsp, nbytes.value)
+        rest = (tdo, tq, tk, tv, to, lse.data_ptr(), tdq, tdk, tdv, wsp, nbytes.value)
+        if scores is None:
+            _run(device, "dpnorm_attention_backward", shape, *rest)
+        else:
+            _run(device, "dpnorm_attention_scores_backward", shape, scores, *rest)
     elif shape.clear_rest:
         dq.zero_(), dk.zero_(), dv.zero_()
     return dq, dk, dv

@@ -53,9 +53,15 @@ class AttnTensor(C.Structure):
     _fields_ = [("data", C.c_void_p), ("stride_token", C.c_int64), ("stride_head", C.c_int64)]
 
 
+class AttnScores(C.Structure):
+    """struct dpnorm_attn_scores: how attention's scores are changed before the softmax."""
+    _fields_ = [("cap", C.c_float), ("slopes", C.c_void_p), ("prefix", C.c_void_p)]
+
+
 _vp, _i64, _i32, _f32, _sz = C.c_void_p, C.c_int64, C.c_int, C.c_float, C.c_size_t
 _fp = C.POINTER(C.c_float)
 _szp, _shp, _tp = C.POINTER(C.c_size_t), C.POINTER(AttnShape), C.POINTER(AttnTensor)
+_scp = C.POINTER(AttnScores)
 
 SIGNATURES = {
     "dpnorm_version": ([], C.c_int),
@@ -97,6 +103,8 @@ SIGNATURES = {
     "dpnorm_attention_forward": ([_shp, _tp, _tp, _tp, _tp, _vp, _vp], C.c_int),
     "dpnorm_attention_backward_workspace": ([_shp, _szp], C.c_int),
     "dpnorm_attention_backward": ([_shp, _tp, _tp, _tp, _tp, _tp, _vp, _tp, _tp, _tp, _vp, _sz, _vp], C.c_int),
+    "dpnorm_attention_scores_forward": ([_shp, _scp, _tp, _tp, _tp, _tp, _vp, _vp], C.c_int),
+    "dpnorm_attention_scores_backward": ([_shp, _scp, _tp, _tp, _tp, _tp, _tp, _vp, _tp, _tp, _tp, _vp, _sz, _vp], C.c_int),
     "dpnorm_layernorm_forward": ([_vp, _vp, _vp, C.c_int, C.c_int, _i64, _i64, _f32, _vp, _vp, _vp, _vp], C.c_int),
     "dpnorm_layernorm_backward_workspace": ([C.c_int, C.c_int, _i64, _i64, _i64, _szp], C.c_int),
     "dpnorm_layernorm_backward": ([_vp, _vp, _vp, _vp, _vp, C.c_int, C.c_int, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _sz,

@@ -10,6 +10,7 @@ import shutil
 import subprocess
 import sys
 import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -29,7 +30,7 @@ SOURCES = [
 # Packed-fp32 VALU forms are disabled for all device code (-packed-fp32-ops);
 # the host pass warns that it does not know the feature, which is harmless.
 HIP_FLAGS = [
-    "-O3", "-std=c++17", "--offload-arch=gfx950", "-fPIC", "-shared",
+    "-O3", "-std=c++17", "--offload-arch=gfx950", "-fPIC",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wno-unused-command-line-argument",
 ]
@@ -44,18 +45,23 @@ def hipcc() -> str:
 
 def build_library(verbose: bool = False) -> str:
     """Compile every HIP source into LIB_PATH (always recompiles)."""
-    srcs = [os.path.join(CSRC, s) for s in SOURCES]
-    fd, tmp = tempfile.mkstemp(suffix=".so", dir=HERE, prefix=".libdpnorm.")
-    os.close(fd)
-    cmd = [hipcc(), *HIP_FLAGS, "-I", INCLUDE, "-I", CSRC, "-x", "hip", *srcs, "-o", tmp]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        os.unlink(tmp)
-        sys.stderr.write(res.stdout + res.stderr)
-        raise RuntimeError(f"hipcc failed building {LIB_NAME} (exit {res.returncode})")
-    os.replace(tmp, LIB_PATH)
+    def run(cmd):
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            sys.stderr.write(res.stdout + res.stderr)
+            raise RuntimeError(f"hipcc failed building {LIB_NAME} (exit {res.returncode})")
+
+    with tempfile.TemporaryDirectory(prefix=".libdpnorm.", dir=HERE) as tmp:
+        objs = [os.path.join(tmp, s + ".o") for s in SOURCES]
+        # the sources one beside the other: attention's kernels take as long as all the rest
+        with ThreadPoolExecutor(max_workers=len(SOURCES)) as pool:
+            list(pool.map(run, [[hipcc(), *HIP_FLAGS, "-I", INCLUDE, "-I", CSRC, "-x", "hip", "-c", os.path.join(CSRC, s), "-o", o]
+                                for s, o in zip(SOURCES, objs)]))
+        so = os.path.join(tmp, LIB_NAME)
+        run([hipcc(), *HIP_FLAGS, "-shared", *objs, "-o", so])
+        os.replace(so, LIB_PATH)
     return LIB_PATH
 
 

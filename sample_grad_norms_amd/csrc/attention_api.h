@@ -174,56 +174,96 @@ hipError_t launch_slots(attn::Args a, int rows, int rep, F launch) {
   return hipGetLastError();
 }
 
-template <bool BF16, int DC>
+template <bool BF16, int DC, int MOD>
 hipError_t run_attn_forward(const attn::Args& a, hipStream_t stream) {
   const int rep = a.Hq / a.Hkv;
   if constexpr (!kRowsAlways<BF16, DC>) {
     if (slots_of(a, 32) * a.Hq > kRowsMost)
       return launch_slots(a, 128, rep, [&](const attn::Args& x, dim3 grid) {
-        attn::k_forward<BF16, DC><<<grid, 256, 0, stream>>>(x);
+        attn::k_forward<BF16, DC, MOD><<<grid, 256, 0, stream>>>(x);
       });
   }
   return launch_slots(a, 32, rep, [&](const attn::Args& x, dim3 grid) {
-    attn::k_forward_rows<BF16, DC, 4><<<grid, 256, 0, stream>>>(x);
+    attn::k_forward_rows<BF16, DC, 4, MOD><<<grid, 256, 0, stream>>>(x);
   });
 }
 
-template <bool BF16, int DC>
+template <bool BF16, int DC, int MOD>
 hipError_t run_attn_backward_q(const attn::Args& a, hipStream_t stream) {
   const int rep = a.Hq / a.Hkv;
   if constexpr (!kRowsAlways<BF16, DC>) {
     if (slots_of(a, 32) * a.Hq > kRowsMost)
       return launch_slots(a, 128, rep, [&](const attn::Args& x, dim3 grid) {
-        attn::k_backward_q<BF16, DC><<<grid, 256, 0, stream>>>(x);
+        attn::k_backward_q<BF16, DC, MOD><<<grid, 256, 0, stream>>>(x);
       });
   }
   if (a.qsplits > 1)
     return launch_slots(a, 32, rep * a.qsplits, [&](const attn::Args& x, dim3 grid) {
-      attn::k_backward_q_rows<BF16, DC, 4, true><<<grid, 256, 0, stream>>>(x);
+      attn::k_backward_q_rows<BF16, DC, 4, true, MOD><<<grid, 256, 0, stream>>>(x);
     });
   return launch_slots(a, 32, rep, [&](const attn::Args& x, dim3 grid) {
-    attn::k_backward_q_rows<BF16, DC, 4, false><<<grid, 256, 0, stream>>>(x);
+    attn::k_backward_q_rows<BF16, DC, 4, false, MOD><<<grid, 256, 0, stream>>>(x);
   });
 }
 
-template <bool BF16, int DC>
+template <bool BF16, int DC, int MOD>
 hipError_t run_attn_backward(const attn::Args& a, hipStream_t stream) {
-  const hipError_t he = run_attn_backward_q<BF16, DC>(a, stream);
+  const hipError_t he = run_attn_backward_q<BF16, DC, MOD>(a, stream);
   if (he != hipSuccess) return he;
   if (a.splits > 1)
     return launch_slots(a, 32, a.splits, [&](const attn::Args& x, dim3 grid) {
       if (a.qsplits > 1) grid.z += (uint32_t)(((int64_t)x.slots * a.Hq + grid.x * grid.y - 1) / (grid.x * grid.y));
-      attn::k_backward_kv<BF16, DC, 4, true><<<grid, 256, 0, stream>>>(x);
+      attn::k_backward_kv<BF16, DC, 4, true, MOD><<<grid, 256, 0, stream>>>(x);
     });
   if constexpr (BF16 && DC == 64) {
     if (keys_eight(a))
       return launch_slots(a, 32, 1, [&](const attn::Args& x, dim3 grid) {
-        attn::k_backward_kv<BF16, DC, 8, false><<<grid, 512, 0, stream>>>(x);
+        attn::k_backward_kv<BF16, DC, 8, false, MOD><<<grid, 512, 0, stream>>>(x);
       });
   }
   return launch_slots(a, 32, 1, [&](const attn::Args& x, dim3 grid) {
-    attn::k_backward_kv<BF16, DC, 4, false><<<grid, 256, 0, stream>>>(x);
+    attn::k_backward_kv<BF16, DC, 4, false, MOD><<<grid, 256, 0, stream>>>(x);
   });
+}
+
+// f with the kernels' type, columns and set as constants.
+template <int MOD, typename F>
+hipError_t with_columns(bool bf16, int32_t D, F f) {
+  using std::integral_constant;
+  const auto go = [&](auto b) {
+    constexpr bool B = decltype(b)::value;
+    if (D <= 64) return f(b, integral_constant<int, 64>{}, integral_constant<int, MOD>{});
+    if (D <= 96) return f(b, integral_constant<int, 96>{}, integral_constant<int, MOD>{});
+    return f(integral_constant<bool, B>{}, integral_constant<int, 128>{}, integral_constant<int, MOD>{});
+  };
+  return bf16 ? go(integral_constant<bool, true>{}) : go(integral_constant<bool, false>{});
+}
+template <typename F>
+hipError_t with_kernels(const attn::Args& a, bool bf16, F f) {
+  if (a.cap > 0.f) return with_columns<attn::kCapped>(bf16, a.D, f);
+  if (a.slopes || a.prefix) return with_columns<attn::kBiased>(bf16, a.D, f);
+  return with_columns<attn::kPlain>(bf16, a.D, f);
+}
+
+// Caps: a score's tanh has an absolute error of a few 2^-24, times the cap; past 1024 that
+// would come near the rounding of bf16 weights. Slopes are added in units of the scale.
+dpnorm_status check_scores(const dpnorm_attn_shape* shape, const dpnorm_attn_scores* s) {
+  if (!s) return DPNORM_OK;
+  if (!(s->cap == 0.f || (s->cap >= 1.f / 1024 && s->cap <= 1024.f))) return DPNORM_ERR_VALUE;
+  if (s->slopes && shape->scale < 0x1p-64f) return DPNORM_ERR_VALUE;
+  if (!aligned(s->slopes, 4) || !aligned(s->prefix, 4)) return DPNORM_ERR_ALIGN;
+  return DPNORM_OK;
+}
+void set_scores(attn::Args& a, const dpnorm_attn_scores* s) {
+  if (!s) return;
+  a.cap = s->cap;
+  a.slopes = s->slopes;
+  a.prefix = s->prefix;
+}
+// What the scores read, as inputs.
+std::vector<Region> score_inputs(const dpnorm_attn_shape* shape, const dpnorm_attn_scores* s) {
+  if (!s) return {};
+  return {{s->slopes, (size_t)shape->Hq * 4}, {s->prefix, (size_t)shape->S * 4}};
 }
 
 // The workspace of a backward pass (its bytes; null to ask for them alone): the pairs,
@@ -252,10 +292,12 @@ size_t backward_layout(attn::Args& a, bool bf16, void* ws) {
 
 extern "C" {
 
-dpnorm_status dpnorm_attention_forward(const dpnorm_attn_shape* shape, const dpnorm_attn_tensor* q, const dpnorm_attn_tensor* k,
-                                       const dpnorm_attn_tensor* v, const dpnorm_attn_tensor* o, float* lse,
-                                       hipStream_t stream) {
+dpnorm_status dpnorm_attention_scores_forward(const dpnorm_attn_shape* shape, const dpnorm_attn_scores* scores,
+                                              const dpnorm_attn_tensor* q, const dpnorm_attn_tensor* k,
+                                              const dpnorm_attn_tensor* v, const dpnorm_attn_tensor* o, float* lse,
+                                              hipStream_t stream) {
   dpnorm_status st = check_shape(shape);
+  if (st == DPNORM_OK) st = check_scores(shape, scores);
   if (st == DPNORM_OK) st = check_tensor(q, shape, shape->Hq, false);
   if (st == DPNORM_OK) st = check_tensor(k, shape, shape->Hkv, false);
   if (st == DPNORM_OK) st = check_tensor(v, shape, shape->Hkv, false);
@@ -265,21 +307,26 @@ dpnorm_status dpnorm_attention_forward(const dpnorm_attn_shape* shape, const dpn
   if (!aligned(lse, 4)) return DPNORM_ERR_ALIGN;
   const size_t e = esize(shape->dtype);
   const int64_t N = shape->N, Hq = shape->Hq, Hkv = shape->Hkv, D = shape->D;
-  if (outputs_overlap({{q->data, span(*q, N, Hq, D, e)}, {k->data, span(*k, N, Hkv, D, e)}, {v->data, span(*v, N, Hkv, D, e)},
-                       {shape->cu_seqlens, (size_t)(shape->S + 1) * 4}},
-                      {{o->data, span(*o, N, Hq, D, e)}, {lse, (size_t)N * Hq * 4}}))
-    return DPNORM_ERR_VALUE;
+  std::vector<Region> in = score_inputs(shape, scores);
+  in.insert(in.end(), {{q->data, span(*q, N, Hq, D, e)}, {k->data, span(*k, N, Hkv, D, e)}, {v->data, span(*v, N, Hkv, D, e)},
+                       {shape->cu_seqlens, (size_t)(shape->S + 1) * 4}});
+  if (outputs_overlap(in, {{o->data, span(*o, N, Hq, D, e)}, {lse, (size_t)N * Hq * 4}})) return DPNORM_ERR_VALUE;
   attn::Args a = attn_args(shape);
   a.q = tensor_of(q, N, Hq, e);
   a.k = tensor_of(k, N, Hkv, e);
   a.v = tensor_of(v, N, Hkv, e);
   a.o = tensor_of(o, N, Hq, e);
   a.lse = lse;
-  if (shape->dtype == DPNORM_BF16)
-    return hip_status(D <= 64 ? run_attn_forward<true, 64>(a, stream) : D <= 96 ? run_attn_forward<true, 96>(a, stream)
-                                                                           : run_attn_forward<true, 128>(a, stream));
-  return hip_status(D <= 64 ? run_attn_forward<false, 64>(a, stream) : D <= 96 ? run_attn_forward<false, 96>(a, stream)
-                                                                          : run_attn_forward<false, 128>(a, stream));
+  set_scores(a, scores);
+  return hip_status(with_kernels(a, shape->dtype == DPNORM_BF16, [&](auto bf16, auto columns, auto mod) {
+    return run_attn_forward<decltype(bf16)::value, decltype(columns)::value, decltype(mod)::value>(a, stream);
+  }));
+}
+
+dpnorm_status dpnorm_attention_forward(const dpnorm_attn_shape* shape, const dpnorm_attn_tensor* q, const dpnorm_attn_tensor* k,
+                                       const dpnorm_attn_tensor* v, const dpnorm_attn_tensor* o, float* lse,
+                                       hipStream_t stream) {
+  return dpnorm_attention_scores_forward(shape, nullptr, q, k, v, o, lse, stream);
 }
 
 dpnorm_status dpnorm_attention_backward_workspace(const dpnorm_attn_shape* shape, size_t* bytes) {
@@ -291,12 +338,15 @@ dpnorm_status dpnorm_attention_backward_workspace(const dpnorm_attn_shape* shape
   return DPNORM_OK;
 }
 
-dpnorm_status dpnorm_attention_backward(const dpnorm_attn_shape* shape, const dpnorm_attn_tensor* dO, const dpnorm_attn_tensor* q,
-                                        const dpnorm_attn_tensor* k, const dpnorm_attn_tensor* v, const dpnorm_attn_tensor* o,
-                                        const float* lse, const dpnorm_attn_tensor* dq, const dpnorm_attn_tensor* dk,
-                                        const dpnorm_attn_tensor* dv, void* ws, size_t ws_bytes, hipStream_t stream) {
+dpnorm_status dpnorm_attention_scores_backward(const dpnorm_attn_shape* shape, const dpnorm_attn_scores* scores,
+                                               const dpnorm_attn_tensor* dO, const dpnorm_attn_tensor* q,
+                                               const dpnorm_attn_tensor* k, const dpnorm_attn_tensor* v,
+                                               const dpnorm_attn_tensor* o, const float* lse, const dpnorm_attn_tensor* dq,
+                                               const dpnorm_attn_tensor* dk, const dpnorm_attn_tensor* dv, void* ws,
+                                               size_t ws_bytes, hipStream_t stream) {
   size_t bytes = 0;
   dpnorm_status st = dpnorm_attention_backward_workspace(shape, &bytes);
+  if (st == DPNORM_OK) st = check_scores(shape, scores);
   for (const dpnorm_attn_tensor* t : {dO, q, o})
     if (st == DPNORM_OK) st = check_tensor(t, shape, shape->Hq, false);
   for (const dpnorm_attn_tensor* t : {k, v})
@@ -310,9 +360,11 @@ dpnorm_status dpnorm_attention_backward(const dpnorm_attn_shape* shape, const dp
   if (ws_bytes < bytes) return DPNORM_ERR_WORKSPACE;
   const size_t e = esize(shape->dtype);
   const int64_t N = shape->N, Hq = shape->Hq, Hkv = shape->Hkv, D = shape->D;
-  if (outputs_overlap({{dO->data, span(*dO, N, Hq, D, e)}, {q->data, span(*q, N, Hq, D, e)}, {o->data, span(*o, N, Hq, D, e)},
+  std::vector<Region> in = score_inputs(shape, scores);
+  in.insert(in.end(), {{dO->data, span(*dO, N, Hq, D, e)}, {q->data, span(*q, N, Hq, D, e)}, {o->data, span(*o, N, Hq, D, e)},
                        {k->data, span(*k, N, Hkv, D, e)}, {v->data, span(*v, N, Hkv, D, e)}, {lse, (size_t)N * Hq * 4},
-                       {shape->cu_seqlens, (size_t)(shape->S + 1) * 4}},
+                       {shape->cu_seqlens, (size_t)(shape->S + 1) * 4}});
+  if (outputs_overlap(in,
                       {{dq->data, span(*dq, N, Hq, D, e)}, {dk->data, span(*dk, N, Hkv, D, e)}, {dv->data, span(*dv, N, Hkv, D, e)},
                        {ws, bytes}}))
     return DPNORM_ERR_VALUE;
@@ -327,11 +379,17 @@ dpnorm_status dpnorm_attention_backward(const dpnorm_attn_shape* shape, const dp
   a.dv = tensor_of(dv, N, Hkv, e);
   a.lse = const_cast<float*>(lse);
   backward_layout(a, shape->dtype == DPNORM_BF16, ws);
-  if (shape->dtype == DPNORM_BF16)
-    return hip_status(D <= 64 ? run_attn_backward<true, 64>(a, stream) : D <= 96 ? run_attn_backward<true, 96>(a, stream)
-                                                                           : run_attn_backward<true, 128>(a, stream));
-  return hip_status(D <= 64 ? run_attn_backward<false, 64>(a, stream) : D <= 96 ? run_attn_backward<false, 96>(a, stream)
-                                                                          : run_attn_backward<false, 128>(a, stream));
+  set_scores(a, scores);
+  return hip_status(with_kernels(a, shape->dtype == DPNORM_BF16, [&](auto bf16, auto columns, auto mod) {
+    return run_attn_backward<decltype(bf16)::value, decltype(columns)::value, decltype(mod)::value>(a, stream);
+  }));
+}
+
+dpnorm_status dpnorm_attention_backward(const dpnorm_attn_shape* shape, const dpnorm_attn_tensor* dO, const dpnorm_attn_tensor* q,
+                                        const dpnorm_attn_tensor* k, const dpnorm_attn_tensor* v, const dpnorm_attn_tensor* o,
+                                        const float* lse, const dpnorm_attn_tensor* dq, const dpnorm_attn_tensor* dk,
+                                        const dpnorm_attn_tensor* dv, void* ws, size_t ws_bytes, hipStream_t stream) {
+  return dpnorm_attention_scores_backward(shape, nullptr, dO, q, k, v, o, lse, dq, dk, dv, ws, ws_bytes, stream);
 }
 
 }  // extern "C"

@@ -7,6 +7,9 @@
 //   dv_u = sum_t p_tu do_t,   dk_u = a sum_t ds_tu q_t,   dq_t = a sum_u ds_tu k_u
 //   (dk and dv sum over the query heads that share the key head).
 //
+// Scores may be changed before the softmax (MOD below): capped, s = C tanh(a q.k / C);
+// biased by distance, - m_h |t - u|; and a sequence's first rows seen by all of its rows.
+//
 // Nothing of size T x T is stored. Every product is an MFMA of 32 x 32 tiles
 // whose result keeps the free index of the next product in its columns:
 //   forward and dq:  S^T = K Q^T      (rows: keys, columns: queries)
@@ -63,7 +66,15 @@ struct Args {
   int32_t groups;     // the number of such groups of 32 keys
   float* parts;       // their sums, [slot][key head][split][dk, dv][tile][1024]
   uint32_t* arrived;  // [slot][key head] of them have arrived (the launch before sets it to zero)
+  // Changed scores:
+  float cap;              // C
+  const float* slopes;    // [Hq] m, or null
+  const int32_t* prefix;  // [S] rows of a sequence that all of its rows see, or null
 };
+
+// Scores as they are; biased or with a prefix; capped, and those where given. Three sets
+// of kernels, so that a set holds no more in registers, and does no more, than it needs.
+enum : int { kPlain = 0, kBiased = 1, kCapped = 2 };
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint32_t kOutside = 0x80000000u;   // an offset past every buffer's range: reads as zero
@@ -73,10 +84,11 @@ constexpr uint32_t kOutside = 0x80000000u;   // an offset past every buffer's ra
 // all). Offsets outside [0, N] or out of order are clamped, so no row outside the
 // tensors is ever touched.
 __device__ __forceinline__ bool find_tile(const Args& a, int32_t slot, int rows, int32_t& start, int32_t& len, int32_t& tile,
-                                          int32_t& tiles) {
+                                          int32_t& tiles, int32_t& seq) {
   if (!a.cu) {
     tiles = (a.T + rows - 1) / rows;
     const int32_t s = slot / tiles;
+    seq = s;
     start = s * a.T;
     len = a.T;
     tile = slot - s * tiles;
@@ -101,6 +113,7 @@ __device__ __forceinline__ bool find_tile(const Args& a, int32_t slot, int rows,
     const int32_t total = __builtin_amdgcn_readlane(inc, 63);
     if (slot < before + total) {
       const int l = __builtin_ctzll(__ballot(before + inc > slot));
+      seq = s0 + l;
       start = __builtin_amdgcn_readlane(lo, l);
       len = __builtin_amdgcn_readlane(n, l);
       tiles = __builtin_amdgcn_readlane(nt, l);
@@ -111,6 +124,29 @@ __device__ __forceinline__ bool find_tile(const Args& a, int32_t slot, int rows,
   }
   tiles = before;
   return false;
+}
+
+// What changes the scores of a work group's queries (all wave-uniform): rows of the
+// sequence that all of its rows see, and the bias of the head, in the unit that the
+// scores are in when it is added (see change_scores and weight).
+struct Change {
+  int32_t pre;
+  float slope;
+  bool biased;
+};
+template <int MOD>
+__device__ __forceinline__ int32_t prefix_of(const Args& a, int32_t seq, int32_t len) {
+  return MOD != kPlain && a.prefix ? min(max(__builtin_amdgcn_readfirstlane(a.prefix[seq]), 0), len) : 0;
+}
+// The head's slope times f.
+template <int MOD>
+__device__ __forceinline__ float slope_of(const Args& a, int32_t h, float f) {
+  return MOD != kPlain && a.slopes ? a.slopes[h] * f : 0.f;
+}
+// Scores times this are in powers of two: capped ones are so already.
+template <int MOD>
+__device__ __forceinline__ float unit_of(const Args& a) {
+  return MOD == kCapped ? 1.f : a.scale * kLog2e;
 }
 
 // The slots without a tile share the rows of no sequence (before the first and
@@ -378,23 +414,33 @@ __device__ __forceinline__ bool zero_not_finite(unsigned char* lds) {
 
 // Adds the infinities and NaN of rows w0 .. w0 + 31 of head hs of src to the results
 // of head ho that see them: those of the same and later rows (UP) or of the same and
-// earlier ones; as they are, or as NaN (weights of either sign). By one wave.
+// earlier ones; as they are, or as NaN (weights of either sign). By one wave. pre: keys
+// before it are seen by all rows; UP then adds theirs to all results, and the results of
+// such keys get what rows 0 .. w0 + 31 hold (pre <= w0 + 31 here: the steps of keys that
+// all rows see leave nothing out).
 template <bool BF16, bool UP, bool AS_NAN>
 __device__ __forceinline__ void add_not_finite(const Tensor& src, int32_t hs, const Tensor& out, int32_t ho, int64_t start,
-                                               int32_t len, int32_t w0, int32_t D) {
+                                               int32_t len, int32_t w0, int32_t D, int32_t pre = 0) {
   constexpr int e = BF16 ? 2 : 4;
   for (int32_t d = threadIdx.x & 63; d < D; d += 64) {
-    float bad = 0.f;
+    const auto held = [&](int32_t row) {
+      if (row >= len) return 0.f;
+      const char* p = row_ptr(src, start + row, hs) + d * e;
+      const uint32_t x = BF16 ? (uint32_t)*(const uint16_t*)p << 16 : *(const uint32_t*)p;
+      return (x & 0x7f800000u) == 0x7f800000u ? AS_NAN ? NAN : __uint_as_float(x) : 0.f;
+    };
+    float bad = 0.f, all = 0.f;
+    if (pre > w0)
+      for (int32_t row = UP ? w0 : 0; row < (UP ? pre : w0 + 32); ++row) all += held(row);
     for (int i = 0; i < 32; ++i) {
       const int32_t row = w0 + (UP ? i : 31 - i);
       if (row >= len) continue;
-      const char* p = row_ptr(src, start + row, hs) + d * e;
-      const uint32_t x = BF16 ? (uint32_t)*(const uint16_t*)p << 16 : *(const uint32_t*)p;
-      if ((x & 0x7f800000u) == 0x7f800000u) bad += AS_NAN ? NAN : __uint_as_float(x);
-      if (bad == 0.f) continue;
+      if (!UP || row >= pre) bad += held(row);
+      const float more = UP ? bad + all : row < pre ? all : bad;
+      if (more == 0.f) continue;
       char* q = row_ptr(out, start + row, ho) + d * e;
-      if constexpr (BF16) *(uint16_t*)q = (uint16_t)f32_to_bf16_bits(bf16_bits_to_f32(*(const uint16_t*)q) + bad);
-      else *(float*)q += bad;
+      if constexpr (BF16) *(uint16_t*)q = (uint16_t)f32_to_bf16_bits(bf16_bits_to_f32(*(const uint16_t*)q) + more);
+      else *(float*)q += more;
     }
   }
 }
@@ -407,6 +453,99 @@ __device__ __forceinline__ float other_half(float x) {
 
 // Row r (0 .. 15) of a lane's half in a 32 x 32 result.
 __device__ __forceinline__ int result_row(int r, int g) { return 8 * (r >> 2) + 4 * g + (r & 3); }
+
+// A product's tanh(a s / C) as u: with E = exp(2 a s / C) it is 1 - 2 / (1 + E). For bf16
+// u = 1 / (1 + E), whose absolute error of a step near 1 is one of 2^-23 C in a capped
+// score, far below the weights' rounding; for fp32 u is the tanh itself, near zero by the
+// first terms of its series, so that small scores keep their relative accuracy.
+// capped: C tanh in powers of two; steep: tanh's derivative, 1 - tanh^2 (bf16: a quarter of it).
+template <bool BF16>
+__device__ __forceinline__ float squash(float s, float k) {   // k: 2 a log2(e) / C
+  const float x = s * k;
+  const float r = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(x));
+  if constexpr (BF16) return r;
+  const float z = x * (0.5f / kLog2e), z2 = z * z;
+  const float p = fmaf(z2, fmaf(z2, fmaf(z2, fmaf(z2, 62.f / 2835.f, -17.f / 315.f), 2.f / 15.f), -1.f / 3.f), 1.f);
+  return fabsf(z) < 0.3f ? z * p : fmaf(-2.f, r, 1.f);
+}
+template <bool BF16>
+__device__ __forceinline__ float capped(float u, float cap2, float more) {   // cap2: C log2(e)
+  if constexpr (BF16) return fmaf(u, -2.f * cap2, cap2 + more);
+  return fmaf(u, cap2, more);
+}
+template <bool BF16>
+__device__ __forceinline__ float steep(float u) {
+  return BF16 ? fmaf(-u, u, u) : fmaf(-u, u, 1.f);
+}
+// dq and dk are sums of ds, in which bf16's quarter is, times this.
+template <bool BF16, int MOD>
+__device__ __forceinline__ float grad_scale(const Args& a) {
+  return BF16 && MOD == kCapped ? 4.f * a.scale : a.scale;
+}
+
+// Changed scores of the lane's column for the softmax, from products: capped, in powers of
+// two; biased, in the products' unit. apart: the column's position less that of row 0 of
+// the lane's half (a slope of the opposite sign of distance needs no case of its own).
+template <bool BF16, int MOD>
+__device__ __forceinline__ void change_scores(f32x16_t& s, const Args& a, const Change& ch, int32_t apart) {
+  if constexpr (MOD == kCapped) {
+    const float k = 2.f * kLog2e * a.scale / a.cap, cap2 = a.cap * kLog2e;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) s[r] = capped<BF16>(squash<BF16>(s[r], k), cap2, 0.f);
+  }
+  if (MOD != kPlain && ch.biased) {
+    keep_branch();
+    const float d = (float)apart;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) s[r] = fmaf(-ch.slope, fabsf(d - (float)result_row(r, 0)), s[r]);
+  }
+}
+// The factor of a head's slope for change_scores.
+template <int MOD>
+__device__ __forceinline__ float bias_unit(const Args& a) {
+  return MOD == kCapped ? kLog2e : 1.f / a.scale;
+}
+
+// In the backward pass: the products s of a column become the weights p = exp2(score - lse),
+// and ds their gradients p (dp - delta) times the derivative of the change. lse and
+// delta of row r from at(r): those of the lane's query, or of each row's.
+template <bool BF16, int MOD, typename F>
+__device__ __forceinline__ void weights_and_gradients(f32x16_t& s, f32x16_t& dp, const Args& a, const Change& ch, int32_t apart, F at) {
+  if constexpr (MOD == kPlain) {
+    const float c = a.scale * kLog2e;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const f32x2_t x = at(r);
+      s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, -x[0]));
+      dp[r] = s[r] * (dp[r] - x[1]);
+    }
+  } else {
+    const float c = a.scale * kLog2e;
+    const float k = MOD == kCapped ? 2.f * c / a.cap : 0.f, cap2 = a.cap * kLog2e;
+    const auto all = [&](auto bias) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const f32x2_t x = at(r);
+        const float more = bias(r) - x[0];
+        if constexpr (MOD == kCapped) {
+          const float u = squash<BF16>(s[r], k);
+          s[r] = __builtin_amdgcn_exp2f(capped<BF16>(u, cap2, more));
+          dp[r] = s[r] * (dp[r] - x[1]) * steep<BF16>(u);
+        } else {
+          s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, more));
+          dp[r] = s[r] * (dp[r] - x[1]);
+        }
+      }
+    };
+    if (ch.biased) {
+      keep_branch();
+      const float d = (float)apart;
+      all([&](int r) { return -ch.slope * fabsf(d - (float)result_row(r, 0)); });
+    } else {
+      all([&](int) { return 0.f; });
+    }
+  }
+}
 
 // Tile i (32 columns) of a row at p, from the transposed result acc, times f.
 template <bool BF16>
@@ -516,8 +655,8 @@ constexpr float kGrowth = 8.f;
 
 // One wave's pass over the keys k0, k0 + 32 NS, .. up to its 32 queries from w0 on,
 // from LDS of its own. careful: without the infinities and NaN on the diagonal.
-template <bool BF16, int DC, int NS, int BUFFERS>
-__device__ __forceinline__ void forward_pass(bool careful, const Args& a, int32_t start, int32_t len, int32_t kh,
+template <bool BF16, int DC, int NS, int BUFFERS, int MOD>
+__device__ __forceinline__ void forward_pass(bool careful, const Args& a, const Change& ch, int32_t start, int32_t len, int32_t kh,
                                              int32_t w0, int32_t k0, unsigned char* mine, const uint4 (&q)[Geo<BF16, DC>::kPairs], float& m, float& l,
                                              f32x16_t (&acc)[Geo<BF16, DC>::kTiles]) {
   using G = Geo<BF16, DC>;
@@ -525,31 +664,35 @@ __device__ __forceinline__ void forward_pass(bool careful, const Args& a, int32_
   constexpr int kStage = 32 * G::kPitch, kBuf = 2 * kStage;
   const int lane = threadIdx.x & 63, g = lane >> 5;
   const int32_t query = w0 + (lane & 31);
-  const float c = a.scale * kLog2e;
+  const float c = unit_of<MOD>(a);
+  // keys that some query sees; where all see the same ones, rows behind them read as zeros
+  const int32_t end = max(w0 + 32, ch.pre);
+  if (ch.pre >= w0 + 32) len = ch.pre;
   const uint32_t base = lds_address(mine);
   const Rows ks(a.k, start, kh, a.D), vs(a.v, start, kh, a.D);
   const auto fetch = [&](int32_t r0, uint32_t to) {
     ks.fetch(r0, len, to);
     vs.fetch(r0, len, to + kStage);
   };
-  if (k0 <= w0) fetch(k0, base);
+  if (k0 < end) fetch(k0, base);
   m = -INFINITY;
   l = 0.f;
 #pragma unroll
   for (int t = 0; t < G::kTiles; ++t) acc[t] = f32x16_t{};
   int buf = 0;
-  for (; k0 <= w0; k0 += 32 * NS) {
+  for (; k0 < end; k0 += 32 * NS) {
     own_staged();
-    const bool more = k0 + 32 * NS <= w0;
+    const bool more = k0 + 32 * NS < end;
     if (BUFFERS == 2 && more) fetch(k0 + 32 * NS, base + (buf ^ 1) * kBuf);
     unsigned char* lk = mine + buf * kBuf;
     unsigned char* lv = lk + kStage;
     f32x16_t s = rows_times<BF16, DC>(lk, 0, q);
-    if (k0 == w0) {
+    change_scores<BF16, MOD>(s, a, ch, query - k0 - 4 * g);
+    if (MOD == kPlain ? k0 == w0 : k0 >= w0 && k0 + 32 > ch.pre) {
       keep_branch();
 #pragma unroll
       for (int r = 0; r < 16; ++r)
-        if (k0 + result_row(r, g) > query) s[r] = -INFINITY;
+        if (k0 + result_row(r, g) > query && (MOD == kPlain || k0 + result_row(r, g) >= ch.pre)) s[r] = -INFINITY;
     }
     float x[2] = {s[0], s[1]};
 #pragma unroll
@@ -576,7 +719,7 @@ __device__ __forceinline__ void forward_pass(bool careful, const Args& a, int32_
       sum[r & 1] += s[r];
     }
     l += sum[0] + sum[1];
-    if (careful && k0 == w0) zero_not_finite<BF16, DC>(lv);
+    if (careful && k0 == w0 && ch.pre < w0 + 32) zero_not_finite<BF16, DC>(lv);
     columns_times<BF16, DC>(lv, 0, s, acc);
     if (BUFFERS == 2) {
       buf ^= 1;
@@ -592,13 +735,13 @@ __device__ __forceinline__ void forward_pass(bool careful, const Args& a, int32_
 // chain of a work group is a quarter of the tiles' and its loads are used by 32 queries
 // instead of 128: for few work groups, bound by the latency of a chain's steps (T = 1024,
 // 16/4 heads, D = 64: 11.6 us against 18.7 by tiles; 4 sequences of 107 rows: 6 us).
-template <bool BF16, int DC, int NS>
+template <bool BF16, int DC, int NS, int MOD>
 __global__ __launch_bounds__(64 * NS, BF16 ? 2 : 1) void k_forward_rows(Args a) {
   using G = Geo<BF16, DC>;
   using P = OwnRows<BF16, DC, NS, 0>;
   __shared__ __align__(1024) unsigned char lds[P::kLds];
-  int32_t start, len, tile, tiles;
-  if (!find_tile(a, block_slot(a), 32, start, len, tile, tiles)) {
+  int32_t start, len, tile, tiles, seq;
+  if (!find_tile(a, block_slot(a), 32, start, len, tile, tiles, seq)) {
     clear_rest(a, block_slot(a), tiles, [&](int32_t r) {
       clear_row(a.o, r, blockIdx.x * gridDim.y + blockIdx.y, a.D * G::kElem);
       if (threadIdx.x == 0) a.lse[(int64_t)(blockIdx.x * gridDim.y + blockIdx.y) * a.N + r] = 0.f;
@@ -612,14 +755,15 @@ __global__ __launch_bounds__(64 * NS, BF16 ? 2 : 1) void k_forward_rows(Args a) 
   const int32_t w0 = tile * 32, query = w0 + (lane & 31);
   uint4 q[G::kPairs];
   load_operand<BF16, DC>(a.q, start, h, w0, len, a.D, q);
-  const float c = a.scale * kLog2e;
+  const float c = unit_of<MOD>(a);
+  const Change ch{prefix_of<MOD>(a, seq, len), slope_of<MOD>(a, h, bias_unit<MOD>(a)), MOD != kPlain && a.slopes};
   float m, l;
   f32x16_t acc[G::kTiles];
   unsigned char* mine = lds + split * P::kBuffers * P::kBuf;
   bool careful = false;
 #pragma unroll 1
   for (;;) {
-    forward_pass<BF16, DC, NS, P::kBuffers>(careful, a, start, len, kh, w0, 32 * split, mine, q, m, l, acc);
+    forward_pass<BF16, DC, NS, P::kBuffers, MOD>(careful, a, ch, start, len, kh, w0, 32 * split, mine, q, m, l, acc);
     if (careful || !not_all_finite(acc)) break;
     careful = true;
   }
@@ -651,28 +795,32 @@ __global__ __launch_bounds__(64 * NS, BF16 ? 2 : 1) void k_forward_rows(Args a) 
   }
   if (query < len) {
     store_rows<BF16, DC>(a.o, (int64_t)start + query, h, a.D, acc, 1.f / l);
-    if (g == 0) a.lse[(int64_t)h * a.N + start + query] = fmaf(m, a.scale, logf(l));
+    if (g == 0) a.lse[(int64_t)h * a.N + start + query] = fmaf(m, MOD == kCapped ? 1.f / kLog2e : a.scale, logf(l));
   }
-  if (careful) {
+  if (careful && ch.pre < w0 + 32) {
     __threadfence_block();
-    add_not_finite<BF16, true, false>(a.v, kh, a.o, h, start, len, w0, a.D);
+    add_not_finite<BF16, true, false>(a.v, kh, a.o, h, start, len, w0, a.D, ch.pre);
   }
 }
 
 // A step of 64 keys from r0 on by tiles, before its weights: masks the scores, raises
 // the running maximum and rescales the sums. Returns the maximum in powers of two.
-template <bool BF16, int DC>
-__device__ __forceinline__ float raise_maximum(f32x16_t (&s)[2], int32_t r0, int32_t w0, int32_t query, float c, float& m, float& l,
+template <bool BF16, int DC, int MOD>
+__device__ __forceinline__ float raise_maximum(f32x16_t (&s)[2], const Args& a, const Change& ch, int32_t r0, int32_t w0, int32_t query, float c, float& m, float& l,
                                                f32x16_t (&acc)[Geo<BF16, DC>::kTiles]) {
   using G = Geo<BF16, DC>;
   const int g = (threadIdx.x & 63) >> 5;
-  if (r0 + 63 > w0) {
+#pragma unroll
+  for (int t = 0; t < 2; ++t) change_scores<BF16, MOD>(s[t], a, ch, query - r0 - t * 32 - 4 * g);
+  if (r0 + 63 > w0 && (MOD == kPlain || r0 + 64 > ch.pre)) {
     keep_branch();
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int r = 0; r < 16; ++r)
-        if (r0 + t * 32 + result_row(r, g) > query) s[t][r] = -INFINITY;
+      for (int r = 0; r < 16; ++r) {
+        const int32_t key = r0 + t * 32 + result_row(r, g);
+        if (key > query && (MOD == kPlain || key >= ch.pre)) s[t][r] = -INFINITY;
+      }
   }
   float x[4] = {s[0][0], s[0][1], s[0][2], s[0][3]};
 #pragma unroll
@@ -711,12 +859,14 @@ __device__ __forceinline__ void weigh(f32x16_t (&s)[2], float c, float mc, float
 // A wave's queries of k_forward once more, without the infinities and NaN of values that
 // some of them do not see. The same steps and operations, so that queries whose sums were
 // finite keep their bits; keys and values in turn in the wave's quarter of the LDS.
-template <bool BF16, int DC>
-__device__ __forceinline__ void tile_again(const Args& a, int32_t start, int32_t len, int32_t kh, int32_t w0, unsigned char* mine,
+template <bool BF16, int DC, int MOD>
+__device__ __forceinline__ void tile_again(const Args& a, const Change& ch, int32_t start, int32_t len, int32_t kh, int32_t w0, unsigned char* mine,
                                            const uint4 (&q)[Geo<BF16, DC>::kPairs], float& m, float& l,
                                            f32x16_t (&acc)[Geo<BF16, DC>::kTiles]) {
   using G = Geo<BF16, DC>;
-  const float c = a.scale * kLog2e;
+  const float c = unit_of<MOD>(a);
+  const int32_t end = max(w0 + 32, ch.pre);
+  if (ch.pre >= w0 + 32) len = ch.pre;   // (as in forward_pass)
   const int32_t query = w0 + (threadIdx.x & 31);
   const Stream<BF16, DC, 64, 1> ks(a.k, start, kh, a.D), vs(a.v, start, kh, a.D);
   m = -INFINITY;
@@ -724,7 +874,7 @@ __device__ __forceinline__ void tile_again(const Args& a, int32_t start, int32_t
 #pragma unroll
   for (int t = 0; t < G::kTiles; ++t) acc[t] = f32x16_t{};
 #pragma unroll 1
-  for (int32_t r0 = 0; r0 <= w0; r0 += 64) {
+  for (int32_t r0 = 0; r0 < end; r0 += 64) {
     own_staged();   // (the reads of the step before are done)
     ks.fetch(r0, len, lds_address(mine));
     own_staged();
@@ -733,12 +883,12 @@ __device__ __forceinline__ void tile_again(const Args& a, int32_t start, int32_t
     for (int t = 0; t < 2; ++t) s[t] = rows_times<BF16, DC>(mine, t * 32, q);
     own_staged();
     vs.fetch(r0, len, lds_address(mine));
-    const float mc = raise_maximum<BF16, DC>(s, r0, w0, query, c, m, l, acc);
+    const float mc = raise_maximum<BF16, DC, MOD>(s, a, ch, r0, w0, query, c, m, l, acc);
     weigh(s, c, mc, l);
     own_staged();
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      if (r0 + t * 32 >= w0) zero_not_finite<BF16, DC>(mine + t * 32 * G::kPitch);
+      if (r0 + t * 32 >= w0 && ch.pre < w0 + 32) zero_not_finite<BF16, DC>(mine + t * 32 * G::kPitch);
       columns_times<BF16, DC>(mine, t * 32, s[t], acc);
     }
   }
@@ -751,14 +901,14 @@ __device__ __forceinline__ void tile_again(const Args& a, int32_t start, int32_t
 // work groups a CU so that one wave's run beside another's. B = 4, T = 2048, 32/8 heads,
 // D = 64: 104 us, 661 TF/s of the pairs u <= t; 12289 + 777 + 4100 rows, 16/2 heads,
 // D = 128: 713 us, 968 TF/s. A large bf16 matrix product reaches 1241 TF/s.
-template <bool BF16, int DC>
+template <bool BF16, int DC, int MOD>
 __global__ __launch_bounds__(256, BF16 ? 2 : 1) void k_forward(Args a) {
   using G = Geo<BF16, DC>;
   using P = Tiles<BF16, DC>;
   // keys are needed a step ahead of their values, whose scores they give
   __shared__ __align__(1024) unsigned char lds[4 * P::kStage];
-  int32_t start, len, tile, tiles;
-  if (!find_tile(a, block_slot(a), P::kRows, start, len, tile, tiles)) {
+  int32_t start, len, tile, tiles, seq;
+  if (!find_tile(a, block_slot(a), P::kRows, start, len, tile, tiles, seq)) {
     clear_rest(a, block_slot(a), tiles, [&](int32_t r) {
       clear_row(a.o, r, blockIdx.x * gridDim.y + blockIdx.y, a.D * G::kElem);
       if (threadIdx.x == 0) a.lse[(int64_t)(blockIdx.x * gridDim.y + blockIdx.y) * a.N + r] = 0.f;
@@ -772,14 +922,16 @@ __global__ __launch_bounds__(256, BF16 ? 2 : 1) void k_forward(Args a) {
   const int32_t w0 = tile * P::kRows + wv * 32;   // the wave's first query
   const int32_t query = w0 + (lane & 31);
   const uint32_t base = lds_address(lds);
-  const int32_t end = min(tile * P::kRows + P::kRows, len);   // keys that some query of the block sees
+  const Change ch{prefix_of<MOD>(a, seq, len), slope_of<MOD>(a, h, bias_unit<MOD>(a)), MOD != kPlain && a.slopes};
+  const int32_t end = max(min(tile * P::kRows + P::kRows, len), ch.pre);   // keys that some query of the block sees
+  const int32_t last = max(w0 + 32, ch.pre);                               // and of the wave
   const typename P::Rows ks(a.k, start, kh, a.D), vs(a.v, start, kh, a.D);
   ks.fetch(0, len, base);
   vs.fetch(0, len, base + 2 * P::kStage);
   if (P::kStep < end) ks.fetch(P::kStep, len, base + P::kStage);
   uint4 q[G::kPairs];
   load_operand<BF16, DC>(a.q, start, h, w0, len, a.D, q);
-  const float c = a.scale * kLog2e;
+  const float c = unit_of<MOD>(a);
   float m = -INFINITY, l = 0.f;
   f32x16_t acc[G::kTiles] = {};
   f32x16_t even[2], odd[2];   // scores of the even and the odd steps
@@ -791,8 +943,8 @@ __global__ __launch_bounds__(256, BF16 ? 2 : 1) void k_forward(Args a) {
     constexpr int buf = buffer.value;
     if (r0 + P::kStep < end) vs.fetch(r0 + P::kStep, len, base + (2 + (buf ^ 1)) * P::kStage);
     if (r0 + 2 * P::kStep < end) ks.fetch(r0 + 2 * P::kStep, len, base + buf * P::kStage);
-    if (r0 <= w0 + 31) {
-      const float mc = raise_maximum<BF16, DC>(s, r0, w0, query, c, m, l, acc);
+    if (r0 < last) {
+      const float mc = raise_maximum<BF16, DC, MOD>(s, a, ch, r0, w0, query, c, m, l, acc);
       // the next step's scores fill the matrix unit while this step's weights are computed
 #pragma unroll
       for (int t = 0; t < 2; ++t) next[t] = rows_times<BF16, DC>(lds + (buf ^ 1) * P::kStage, t * 32, q);
@@ -813,15 +965,15 @@ __global__ __launch_bounds__(256, BF16 ? 2 : 1) void k_forward(Args a) {
   // Masked values may have added NaN: the wave takes its queries once more, from its
   // quarter of the LDS (every wave is past the last step).
   const bool careful = not_all_finite(acc);
-  if (careful) tile_again<BF16, DC>(a, start, len, kh, w0, lds + wv * P::kStage, q, m, l, acc);
+  if (careful) tile_again<BF16, DC, MOD>(a, ch, start, len, kh, w0, lds + wv * P::kStage, q, m, l, acc);
   l += other_half(l);
   if (query < len) {
     store_rows<BF16, DC>(a.o, (int64_t)start + query, h, a.D, acc, 1.f / l);
-    if (g == 0) a.lse[(int64_t)h * a.N + start + query] = fmaf(m, a.scale, logf(l));
+    if (g == 0) a.lse[(int64_t)h * a.N + start + query] = fmaf(m, MOD == kCapped ? 1.f / kLog2e : a.scale, logf(l));
   }
-  if (careful) {
+  if (careful && ch.pre < w0 + 32) {
     __threadfence_block();
-    add_not_finite<BF16, true, false>(a.v, kh, a.o, h, start, len, w0, a.D);
+    add_not_finite<BF16, true, false>(a.v, kh, a.o, h, start, len, w0, a.D, ch.pre);
   }
 }
 
@@ -846,8 +998,8 @@ __device__ __forceinline__ float dot_chunk(const uint4& x, const uint4& y, float
 __device__ __forceinline__ float scaled_lse(float lse) { return lse == -INFINITY ? NAN : lse * kLog2e; }
 
 // One wave's pass for dq over the keys k0, k0 + 32 waves, .., as forward_pass.
-template <bool BF16, int DC, int BUFFERS>
-__device__ __forceinline__ void backward_q_pass(bool careful, const Args& a, int32_t start, int32_t len, int32_t kh,
+template <bool BF16, int DC, int BUFFERS, int MOD>
+__device__ __forceinline__ void backward_q_pass(bool careful, const Args& a, const Change& ch, int32_t start, int32_t len, int32_t kh,
                                                 int32_t w0, int32_t k0, int32_t waves, unsigned char* mine, const uint4 (&q)[Geo<BF16, DC>::kPairs],
                                                 const uint4 (&dO)[Geo<BF16, DC>::kPairs], float lse, float delta,
                                                 f32x16_t (&acc)[Geo<BF16, DC>::kTiles]) {
@@ -856,35 +1008,35 @@ __device__ __forceinline__ void backward_q_pass(bool careful, const Args& a, int
   constexpr int kStage = 32 * G::kPitch, kBuf = 2 * kStage;
   const int lane = threadIdx.x & 63, g = lane >> 5;
   const int32_t query = w0 + (lane & 31);
-  const float c = a.scale * kLog2e;
+  const int32_t end = max(w0 + 32, ch.pre);
+  if (ch.pre >= w0 + 32) len = ch.pre;   // (as in forward_pass)
   const uint32_t base = lds_address(mine);
   const Rows ks(a.k, start, kh, a.D), vs(a.v, start, kh, a.D);
   const auto fetch = [&](int32_t r0, uint32_t to) {
     ks.fetch(r0, len, to);
     vs.fetch(r0, len, to + kStage);
   };
-  if (k0 <= w0) fetch(k0, base);
+  if (k0 < end) fetch(k0, base);
 #pragma unroll
   for (int t = 0; t < G::kTiles; ++t) acc[t] = f32x16_t{};
   int buf = 0;
-  for (; k0 <= w0; k0 += 32 * waves) {
+  for (; k0 < end; k0 += 32 * waves) {
     own_staged();
-    const bool more = k0 + 32 * waves <= w0;
+    const bool more = k0 + 32 * waves < end;
     if (BUFFERS == 2 && more) fetch(k0 + 32 * waves, base + (buf ^ 1) * kBuf);
     unsigned char* lk = mine + buf * kBuf;
     unsigned char* lv = lk + kStage;
     f32x16_t s = rows_times<BF16, DC>(lk, 0, q);
-    const f32x16_t dp = rows_times<BF16, DC>(lv, 0, dO);
-#pragma unroll
-    for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, -lse)) * (dp[r] - delta);
-    if (k0 == w0) {
+    f32x16_t ds = rows_times<BF16, DC>(lv, 0, dO);
+    weights_and_gradients<BF16, MOD>(s, ds, a, ch, query - k0 - 4 * g, [&](int) { return f32x2_t{lse, delta}; });
+    if (MOD == kPlain ? k0 == w0 : k0 >= w0 && k0 + 32 > ch.pre) {
       keep_branch();
 #pragma unroll
       for (int r = 0; r < 16; ++r)
-        if (k0 + result_row(r, g) > query) s[r] = 0.f;
-      if (careful) zero_not_finite<BF16, DC>(lk);
+        if (k0 + result_row(r, g) > query && (MOD == kPlain || k0 + result_row(r, g) >= ch.pre)) ds[r] = 0.f;
+      if (careful && ch.pre < w0 + 32) zero_not_finite<BF16, DC>(lk);
     }
-    columns_times<BF16, DC>(lk, 0, s, acc);
+    columns_times<BF16, DC>(lk, 0, ds, acc);
     if (BUFFERS == 2) {
       buf ^= 1;
     } else if (more) {
@@ -897,14 +1049,14 @@ __device__ __forceinline__ void backward_q_pass(bool careful, const Args& a, int
 // dq, and the pairs for the second launch, by tiles as k_forward's. Three products a
 // step (S, dP, dQ); bound by the MFMAs and the reads of K and V from LDS, each used by
 // 32 queries a wave. B = 4, T = 2048, 32/8 heads, D = 64: 131 us, 787 TF/s.
-template <bool BF16, int DC>
+template <bool BF16, int DC, int MOD>
 __global__ __launch_bounds__(256, !BF16 ? 1 : DC == 64 ? 3 : 2) void k_backward_q(Args a) {
   using G = Geo<BF16, DC>;
   using P = Tiles<BF16, DC>;
   __shared__ __align__(1024) unsigned char lds[4 * P::kStage];
   clear_arrived(a);
-  int32_t start, len, tile, tiles;
-  if (!find_tile(a, block_slot(a), P::kRows, start, len, tile, tiles)) {
+  int32_t start, len, tile, tiles, seq;
+  if (!find_tile(a, block_slot(a), P::kRows, start, len, tile, tiles, seq)) {
     clear_rest(a, block_slot(a), tiles, [&](int32_t r) {
       clear_row(a.dq, r, blockIdx.x * gridDim.y + blockIdx.y, a.D * G::kElem);
     });
@@ -917,7 +1069,8 @@ __global__ __launch_bounds__(256, !BF16 ? 1 : DC == 64 ? 3 : 2) void k_backward_
   const int32_t w0 = tile * P::kRows + wv * 32;
   const int32_t query = w0 + (lane & 31);
   const uint32_t base = lds_address(lds);
-  const int32_t end = min(tile * P::kRows + P::kRows, len);
+  const Change ch{prefix_of<MOD>(a, seq, len), slope_of<MOD>(a, h, kLog2e), MOD != kPlain && a.slopes};
+  const int32_t end = max(min(tile * P::kRows + P::kRows, len), ch.pre), last = max(w0 + 32, ch.pre);
   const typename P::Rows ks(a.k, start, kh, a.D), vs(a.v, start, kh, a.D);
   ks.fetch(0, len, base);
   vs.fetch(0, len, base + P::kStage);
@@ -940,7 +1093,6 @@ __global__ __launch_bounds__(256, !BF16 ? 1 : DC == 64 ? 3 : 2) void k_backward_
       *(float2*)(a.pairs + 2 * at) = make_float2(lse, delta);
     }
   }
-  const float c = a.scale * kLog2e;
   f32x16_t acc[G::kTiles] = {};
   staged();
   int buf = 0;
@@ -950,42 +1102,41 @@ __global__ __launch_bounds__(256, !BF16 ? 1 : DC == 64 ? 3 : 2) void k_backward_
       ks.fetch(r0 + P::kStep, len, to);
       vs.fetch(r0 + P::kStep, len, to + P::kStage);
     }
-    if (r0 <= w0 + 31) {
+    if (r0 < last) {
       const unsigned char* lk = lds + buf * 2 * P::kStage;
       const unsigned char* lv = lk + P::kStage;
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         const int32_t k0 = r0 + t * 32;
-        if (k0 > w0) break;   // (all masked)
+        if (k0 >= last) break;   // (all masked)
         f32x16_t s = rows_times<BF16, DC>(lk, t * 32, q);
-        const f32x16_t dp = rows_times<BF16, DC>(lv, t * 32, dO);
-#pragma unroll
-        for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, -lse)) * (dp[r] - delta);
-        if (k0 == w0) {
+        f32x16_t ds = rows_times<BF16, DC>(lv, t * 32, dO);
+        weights_and_gradients<BF16, MOD>(s, ds, a, ch, query - k0 - 4 * g, [&](int) { return f32x2_t{lse, delta}; });
+        if (MOD == kPlain ? k0 == w0 : k0 >= w0 && k0 + 32 > ch.pre) {
           keep_branch();
 #pragma unroll
           for (int r = 0; r < 16; ++r)
-            if (k0 + result_row(r, g) > query) s[r] = 0.f;
+            if (k0 + result_row(r, g) > query && (MOD == kPlain || k0 + result_row(r, g) >= ch.pre)) ds[r] = 0.f;
         }
-        columns_times<BF16, DC>(lk, t * 32, s, acc);
+        columns_times<BF16, DC>(lk, t * 32, ds, acc);
       }
     }
     staged();
     buf ^= 1;
   }
   const bool careful = not_all_finite(acc);   // see k_forward
-  if (careful) backward_q_pass<BF16, DC, 1>(true, a, start, len, kh, w0, 0, 1, lds + wv * P::kStage, q, dO, lse, delta, acc);
-  if (query < len) store_rows<BF16, DC>(a.dq, (int64_t)start + query, h, a.D, acc, a.scale);
-  if (careful) {
+  if (careful) backward_q_pass<BF16, DC, 1, MOD>(true, a, ch, start, len, kh, w0, 0, 1, lds + wv * P::kStage, q, dO, lse, delta, acc);
+  if (query < len) store_rows<BF16, DC>(a.dq, (int64_t)start + query, h, a.D, acc, grad_scale<BF16, MOD>(a));
+  if (careful && ch.pre < w0 + 32) {
     __threadfence_block();
-    add_not_finite<BF16, true, true>(a.k, kh, a.dq, h, start, len, w0, a.D);
+    add_not_finite<BF16, true, true>(a.k, kh, a.dq, h, start, len, w0, a.D, ch.pre);
   }
 }
 
 // Work groups that share the keys of the 32 queries from w0 on, for kSteps steps a wave.
 constexpr int kSteps = 2;
-__device__ __forceinline__ int32_t query_splits(const Args& a, int32_t w0, int ns) {
-  return min(a.qsplits, (w0 / 32 + kSteps * ns) / (kSteps * ns));
+__device__ __forceinline__ int32_t query_splits(const Args& a, int32_t w0, int32_t pre, int ns) {
+  return min(a.qsplits, ((max(w0 + 32, pre) + 31) / 32 - 1 + kSteps * ns) / (kSteps * ns));
 }
 
 // The same by rows, as k_forward_rows. SPLIT: a few work groups share the keys, and the
@@ -993,7 +1144,7 @@ __device__ __forceinline__ int32_t query_splits(const Args& a, int32_t w0, int n
 // 6/3 heads, D = 80 37 us alone, 22 shared; T = 1024, 8/4 heads, D = 64 39 either way;
 // bf16, T = 1024, 16/4 heads, D = 64 16 alone. Bound by the chain of a wave's steps and,
 // below 12 us, by its first loads.
-template <bool BF16, int DC, int NS, bool SPLIT>
+template <bool BF16, int DC, int NS, bool SPLIT, int MOD>
 __global__ __launch_bounds__(64 * NS, BF16 ? 2 : 1) void k_backward_q_rows(Args a) {
   using G = Geo<BF16, DC>;
   using P = OwnRows<BF16, DC, NS, 0>;
@@ -1002,8 +1153,8 @@ __global__ __launch_bounds__(64 * NS, BF16 ? 2 : 1) void k_backward_q_rows(Args 
   const int32_t kh = blockIdx.x, rep = a.Hq / a.Hkv;
   const int32_t h = kh * rep + (SPLIT ? (int32_t)blockIdx.y % rep : (int32_t)blockIdx.y);
   const int32_t z = SPLIT ? (int32_t)blockIdx.y / rep : 0;
-  int32_t start, len, tile, tiles;
-  if (!find_tile(a, block_slot(a), 32, start, len, tile, tiles)) {
+  int32_t start, len, tile, tiles, seq;
+  if (!find_tile(a, block_slot(a), 32, start, len, tile, tiles, seq)) {
     if (z == 0) clear_rest(a, block_slot(a), tiles, [&](int32_t r) { clear_row(a.dq, r, h, a.D * G::kElem); });
     return;
   }
@@ -1011,7 +1162,8 @@ __global__ __launch_bounds__(64 * NS, BF16 ? 2 : 1) void k_backward_q_rows(Args 
   const int lane = threadIdx.x & 63, g = lane >> 5;
   const int split = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int32_t w0 = tile * 32, query = w0 + (lane & 31);
-  const int32_t splits = SPLIT ? query_splits(a, w0, NS) : 1;
+  const Change ch{prefix_of<MOD>(a, seq, len), slope_of<MOD>(a, h, kLog2e), MOD != kPlain && a.slopes};
+  const int32_t splits = SPLIT ? query_splits(a, w0, ch.pre, NS) : 1;
   if (SPLIT && z >= splits) return;
   uint4 q[G::kPairs], dO[G::kPairs];
   float delta = 0.f;
@@ -1035,7 +1187,7 @@ __global__ __launch_bounds__(64 * NS, BF16 ? 2 : 1) void k_backward_q_rows(Args 
   bool careful = false;
 #pragma unroll 1
   for (;;) {
-    backward_q_pass<BF16, DC, P::kBuffers>(careful, a, start, len, kh, w0, 32 * (z * NS + split), splits * NS, mine, q, dO,
+    backward_q_pass<BF16, DC, P::kBuffers, MOD>(careful, a, ch, start, len, kh, w0, 32 * (z * NS + split), splits * NS, mine, q, dO,
                                            lse, delta, acc);
     if (careful || !not_all_finite(acc)) break;
     careful = true;
@@ -1054,25 +1206,26 @@ __global__ __launch_bounds__(64 * NS, BF16 ? 2 : 1) void k_backward_q_rows(Args 
     if (lane == 0) a.qcareful[part] = careful;
     return;
   }
-  if (query < len) store_rows<BF16, DC>(a.dq, (int64_t)start + query, h, a.D, acc, a.scale);
-  if (careful) {
+  if (query < len) store_rows<BF16, DC>(a.dq, (int64_t)start + query, h, a.D, acc, grad_scale<BF16, MOD>(a));
+  if (careful && ch.pre < w0 + 32) {
     __threadfence_block();
-    add_not_finite<BF16, true, true>(a.k, kh, a.dq, h, start, len, w0, a.D);
+    add_not_finite<BF16, true, true>(a.k, kh, a.dq, h, start, len, w0, a.D, ch.pre);
   }
 }
 
 // The sums of k_backward_q_rows' work groups that shared the keys of 32 queries of one
 // head, added in order: work groups behind the keys' own of the second launch.
-template <bool BF16, int DC, int NS>
+template <bool BF16, int DC, int NS, int MOD>
 __device__ __forceinline__ void join_queries(const Args& a) {
   using G = Geo<BF16, DC>;
   const int64_t group = ((int64_t)((int32_t)blockIdx.z - a.slots) * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
   if (group >= (int64_t)a.slots * a.Hq) return;
   const int32_t slot = (int32_t)(group / a.Hq), h = (int32_t)(group % a.Hq);
-  int32_t start, len, tile, tiles;
-  if (!find_tile(a, slot, 32, start, len, tile, tiles)) return;
+  int32_t start, len, tile, tiles, seq;
+  if (!find_tile(a, slot, 32, start, len, tile, tiles, seq)) return;
   const int32_t w0 = (tiles - 1 - tile) * 32;
-  const int32_t splits = query_splits(a, w0, NS);
+  const int32_t pre = prefix_of<MOD>(a, seq, len);
+  const int32_t splits = query_splits(a, w0, pre, NS);
   if (splits < 2) return;
   const int lane = threadIdx.x & 63;
   const int split = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -1091,20 +1244,20 @@ __device__ __forceinline__ void join_queries(const Args& a) {
         for (int i = 0; i < 4; ++i) x[4 * j + i] += y[i];
       }
     }
-    if (query < len) store_tile<BF16>(row_ptr(a.dq, (int64_t)start + query, h), t, a.D, x, a.scale);
+    if (query < len) store_tile<BF16>(row_ptr(a.dq, (int64_t)start + query, h), t, a.D, x, grad_scale<BF16, MOD>(a));
   }
-  if (!careful) return;
+  if (!careful || pre >= w0 + 32) return;
   __syncthreads();
   if (split > 0) return;
   __threadfence_block();
-  add_not_finite<BF16, true, true>(a.k, h / (a.Hq / a.Hkv), a.dq, h, start, len, w0, a.D);
+  add_not_finite<BF16, true, true>(a.k, h / (a.Hq / a.Hkv), a.dq, h, start, len, w0, a.D, pre);
 }
 
 // One wave's pass for dk and dv over the queries of the key head's query heads, from
 // the keys w0 on: one step of 32 of `waves`, from the one `wave` on. Sets careful
 // where the diagonal held others than finite numbers.
-template <bool BF16, int DC, int NS>
-__device__ __forceinline__ void backward_kv_pass(bool& careful, const Args& a, int32_t start, int32_t len, int32_t kh,
+template <bool BF16, int DC, int NS, int MOD>
+__device__ __forceinline__ void backward_kv_pass(bool& careful, const Args& a, int32_t pre, int32_t start, int32_t len, int32_t kh,
                                                  int32_t w0, int32_t wave, int32_t waves, unsigned char* mine, const uint4 (&k)[Geo<BF16, DC>::kPairs],
                                                  const uint4 (&v)[Geo<BF16, DC>::kPairs],
                                                  f32x16_t (&dk)[Geo<BF16, DC>::kTiles], f32x16_t (&dv)[Geo<BF16, DC>::kTiles]) {
@@ -1112,7 +1265,6 @@ __device__ __forceinline__ void backward_kv_pass(bool& careful, const Args& a, i
   using G = Geo<BF16, DC>;
   const int lane = threadIdx.x & 63, g = lane >> 5;
   const int32_t key = w0 + (lane & 31), rep = a.Hq / a.Hkv;
-  const float c = a.scale * kLog2e;
   const uint32_t base = lds_address(mine);
   // 32 queries from q0 on of head h, with their lse and delta: zeros past the end
   // (whose weights are set to zero: against an infinity in a key they would be NaN)
@@ -1125,12 +1277,13 @@ __device__ __forceinline__ void backward_kv_pass(bool& careful, const Args& a, i
     const char* at = (const char*)(a.pairs + 2 * ((int64_t)h * a.N + start + q0));
     dma_words(rows_of(at), q0 + (lane >> 1) < len ? lane * 4 : kOutside, to + 2 * P::kStage);
   };
-  // the steps of one head after another
+  // the steps of one head after another, from the first query that sees a key
+  const int32_t first = pre > w0 ? 0 : w0;
   const int32_t hend = kh * rep + rep, end = w0 + (len - w0 + 31) / 32 * 32;
   const auto settle = [&](int32_t& h, int32_t& q0) {
-    while (q0 >= end && h < hend) q0 -= end - w0, ++h;
+    while (q0 >= end && h < hend) q0 -= end - first, ++h;
   };
-  int32_t h = kh * rep, q0 = w0 + 32 * wave;
+  int32_t h = kh * rep, q0 = first + 32 * wave;
   settle(h, q0);
   if (h < hend) fetch(h, q0, base);
 #pragma unroll
@@ -1144,30 +1297,40 @@ __device__ __forceinline__ void backward_kv_pass(bool& careful, const Args& a, i
     unsigned char* lq = mine + buf * P::kBuf;
     unsigned char* lo = lq + P::kStage;
     const float* words = (const float*)(lq + 2 * P::kStage);
-    if (q0 == w0) {   // (a query row that is not finite has lse or delta of NaN)
+    f32x16_t p;
+    // (capped scores of a query row that is not finite may be finite, and so its lse)
+    if constexpr (MOD == kCapped) p = rows_times<BF16, DC>(lq, 0, k);
+    if (MOD == kPlain ? q0 == w0 : q0 <= w0 && pre < w0 + 32) {   // (a query row that is not finite has lse or delta of NaN)
       careful |= zero_not_finite<BF16, DC>(lo);
       careful |= zero_not_finite<BF16, DC>(lq);
     }
-    f32x16_t p = rows_times<BF16, DC>(lq, 0, k);
+    if constexpr (MOD != kCapped) p = rows_times<BF16, DC>(lq, 0, k);
     f32x16_t ds = rows_times<BF16, DC>(lo, 0, v);
+    if constexpr (MOD == kPlain) {
+      const float c = a.scale * kLog2e;
 #pragma unroll
-    for (int r4 = 0; r4 < 4; ++r4) {
+      for (int r4 = 0; r4 < 4; ++r4) {
 #pragma unroll
-      for (int i = 0; i < 4; i += 2) {
-        const f32x4_t x = *(const f32x4_t*)(words + 2 * (8 * r4 + 4 * g + i));   // lse, delta of two queries
-        const int r = 4 * r4 + i;
-        p[r] = __builtin_amdgcn_exp2f(fmaf(p[r], c, -x[0]));
-        ds[r] = p[r] * (ds[r] - x[1]);
-        p[r + 1] = __builtin_amdgcn_exp2f(fmaf(p[r + 1], c, -x[2]));
-        ds[r + 1] = p[r + 1] * (ds[r + 1] - x[3]);
+        for (int i = 0; i < 4; i += 2) {
+          const f32x4_t x = *(const f32x4_t*)(words + 2 * (8 * r4 + 4 * g + i));   // lse, delta of two queries
+          const int r = 4 * r4 + i;
+          p[r] = __builtin_amdgcn_exp2f(fmaf(p[r], c, -x[0]));
+          ds[r] = p[r] * (ds[r] - x[1]);
+          p[r + 1] = __builtin_amdgcn_exp2f(fmaf(p[r + 1], c, -x[2]));
+          ds[r + 1] = p[r + 1] * (ds[r + 1] - x[3]);
+        }
       }
+    } else {
+      const Change ch{pre, slope_of<MOD>(a, h, kLog2e), a.slopes != nullptr};
+      weights_and_gradients<BF16, MOD>(p, ds, a, ch, key - q0 - 4 * g,
+                                       [&](int r) { return *(const f32x2_t*)(words + 2 * result_row(r, g)); });
     }
-    if (q0 == w0 || q0 + 32 > len) {
+    if ((MOD == kPlain ? q0 == w0 : q0 <= w0 && pre < w0 + 32) || q0 + 32 > len) {
       keep_branch();
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
         const int32_t query = q0 + result_row(r, g);
-        if (query < key || query >= len) p[r] = 0.f, ds[r] = 0.f;
+        if ((query < key && (MOD == kPlain || key >= pre)) || query >= len) p[r] = 0.f, ds[r] = 0.f;
       }
     }
     columns_times<BF16, DC>(lo, 0, p, dv);
@@ -1196,15 +1359,15 @@ __device__ __forceinline__ void backward_kv_pass(bool& careful, const Args& a, i
 // their sums in a fixed order. The sums and the counter go past the L2 caches, which
 // the XCDs do not share: fences, which write back and empty them, cost more than the
 // split won (3/1 heads D = 64, 811 + 443 rows: 34 us with fences, 14 without, 26 unsplit).
-template <bool BF16, int DC, int NS, bool SPLIT>
+template <bool BF16, int DC, int NS, bool SPLIT, int MOD>
 __global__ __launch_bounds__(64 * NS, BF16 || DC == 64 ? 2 : 1) void k_backward_kv(Args a) {
   using G = Geo<BF16, DC>;
   using P = OwnRows<BF16, DC, NS, 256>;
   __shared__ __align__(1024) unsigned char lds[P::kLds];
-  if (SPLIT && (int32_t)blockIdx.z >= a.slots) return join_queries<BF16, DC, NS>(a);
-  int32_t start, len, tile, tiles;
+  if (SPLIT && (int32_t)blockIdx.z >= a.slots) return join_queries<BF16, DC, NS, MOD>(a);
+  int32_t start, len, tile, tiles, seq;
   const int32_t kh = blockIdx.x;
-  if (!find_tile(a, block_slot(a), 32, start, len, tile, tiles)) {
+  if (!find_tile(a, block_slot(a), 32, start, len, tile, tiles, seq)) {
     if (blockIdx.y == 0)
       clear_rest(a, block_slot(a), tiles, [&](int32_t r) {
         clear_row(a.dk, r, blockIdx.x, a.D * G::kElem);
@@ -1216,7 +1379,8 @@ __global__ __launch_bounds__(64 * NS, BF16 || DC == 64 ? 2 : 1) void k_backward_
   const int split = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int32_t w0 = tile * 32, key = w0 + (lane & 31);
   // as many work groups as give each of their waves kSteps steps
-  const int32_t steps = (len - w0 + 31) / 32 * (a.Hq / a.Hkv);
+  const int32_t pre = prefix_of<MOD>(a, seq, len), first = pre > w0 ? 0 : w0;
+  const int32_t steps = ((len - w0 + 31) / 32 + (w0 - first) / 32) * (a.Hq / a.Hkv);
   const int32_t splits = SPLIT ? min(a.splits, (steps + kSteps * NS - 1) / (kSteps * NS)) : 1;
   if (SPLIT && (int32_t)blockIdx.y >= splits) return;
   unsigned char* mine = lds + split * P::kBuffers * P::kBuf;
@@ -1225,7 +1389,7 @@ __global__ __launch_bounds__(64 * NS, BF16 || DC == 64 ? 2 : 1) void k_backward_
   load_operand<BF16, DC>(a.v, start, kh, w0, len, a.D, v);
   f32x16_t dk[G::kTiles], dv[G::kTiles];
   bool careful = false;
-  backward_kv_pass<BF16, DC, NS>(careful, a, start, len, kh, w0, SPLIT ? blockIdx.y * NS + split : split, splits * NS,
+  backward_kv_pass<BF16, DC, NS, MOD>(careful, a, pre, start, len, kh, w0, SPLIT ? blockIdx.y * NS + split : split, splits * NS,
                                  mine, k, v, dk, dv);
   careful = __syncthreads_or(careful);
   join<NS, G::kTiles>(dk, split, lds);
@@ -1269,7 +1433,7 @@ __global__ __launch_bounds__(64 * NS, BF16 || DC == 64 ? 2 : 1) void k_backward_
       const bool second = t >= G::kTiles;
       const Tensor& out = second ? a.dv : a.dk;
       if (key < len)
-        store_tile<BF16>(row_ptr(out, (int64_t)start + key, kh), second ? t - G::kTiles : t, a.D, x, second ? 1.f : a.scale);
+        store_tile<BF16>(row_ptr(out, (int64_t)start + key, kh), second ? t - G::kTiles : t, a.D, x, second ? 1.f : grad_scale<BF16, MOD>(a));
     }
     if (!careful) return;
     __syncthreads();
@@ -1277,7 +1441,7 @@ __global__ __launch_bounds__(64 * NS, BF16 || DC == 64 ? 2 : 1) void k_backward_
   } else {
     if (split > 0) return;
     if (key < len) {
-      store_rows<BF16, DC>(a.dk, (int64_t)start + key, kh, a.D, dk, a.scale);
+      store_rows<BF16, DC>(a.dk, (int64_t)start + key, kh, a.D, dk, grad_scale<BF16, MOD>(a));
       store_rows<BF16, DC>(a.dv, (int64_t)start + key, kh, a.D, dv, 1.f);
     }
   }
@@ -1285,8 +1449,8 @@ __global__ __launch_bounds__(64 * NS, BF16 || DC == 64 ? 2 : 1) void k_backward_
     __threadfence_block();
     const int32_t rep = a.Hq / a.Hkv;
     for (int32_t h = kh * rep; h < kh * rep + rep; ++h) {
-      add_not_finite<BF16, false, true>(a.q, h, a.dk, kh, start, len, w0, a.D);
-      add_not_finite<BF16, false, false>(a.dO, h, a.dv, kh, start, len, w0, a.D);   // (weights are not negative)
+      add_not_finite<BF16, false, true>(a.q, h, a.dk, kh, start, len, w0, a.D, pre);
+      add_not_finite<BF16, false, false>(a.dO, h, a.dv, kh, start, len, w0, a.D, pre);   // (weights are not negative)
     }
   }
 }
