@@ -240,6 +240,7 @@ hipError_t with_columns(bool bf16, int32_t D, F f) {
 }
 template <typename F>
 hipError_t with_kernels(const attn::Args& a, bool bf16, F f) {
+  if (a.cap > 0.f && a.slopes) return with_columns<attn::kCapped | attn::kBiased>(bf16, a.D, f);
   if (a.cap > 0.f) return with_columns<attn::kCapped>(bf16, a.D, f);
   if (a.slopes || a.prefix) return with_columns<attn::kBiased>(bf16, a.D, f);
   return with_columns<attn::kPlain>(bf16, a.D, f);

@@ -72,8 +72,10 @@ struct Args {
   const int32_t* prefix;  // [S] rows of a sequence that all of its rows see, or null
 };
 
-// Scores as they are; biased or with a prefix; capped, and those where given. Three sets
-// of kernels, so that a set holds no more in registers, and does no more, than it needs.
+// How a set of kernels changes scores: not at all; by a bias; by a cap; by both. A prefix
+// goes with any but the first (alone: a bias with slopes of 0). Sets of their own rather
+// than branches, across which the compiler would hold the loads of both sides (dk and dv,
+// D 64: 36 registers).
 enum : int { kPlain = 0, kBiased = 1, kCapped = 2 };
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -132,7 +134,6 @@ __device__ __forceinline__ bool find_tile(const Args& a, int32_t slot, int rows,
 struct Change {
   int32_t pre;
   float slope;
-  bool biased;
 };
 template <int MOD>
 __device__ __forceinline__ int32_t prefix_of(const Args& a, int32_t seq, int32_t len) {
@@ -141,12 +142,19 @@ __device__ __forceinline__ int32_t prefix_of(const Args& a, int32_t seq, int32_t
 // The head's slope times f.
 template <int MOD>
 __device__ __forceinline__ float slope_of(const Args& a, int32_t h, float f) {
-  return MOD != kPlain && a.slopes ? a.slopes[h] * f : 0.f;
+  return (MOD & kBiased) && a.slopes ? a.slopes[h] * f : 0.f;
 }
-// Scores times this are in powers of two: capped ones are so already.
-template <int MOD>
+// What the softmax works on, times this, is in powers of two: products, or of capped
+// scores u (see squash), of which bf16's u is tanh / 2 up to a constant.
+template <bool BF16, int MOD>
 __device__ __forceinline__ float unit_of(const Args& a) {
-  return MOD == kCapped ? 1.f : a.scale * kLog2e;
+  return ((MOD & kCapped) ? (BF16 ? 2.f : 1.f) * a.cap : a.scale) * kLog2e;
+}
+// The log-sum-exp from the softmax's maximum and sum.
+template <bool BF16, int MOD>
+__device__ __forceinline__ float lse_of(const Args& a, float m, float l) {
+  if constexpr ((MOD & kCapped) && BF16) return fmaf(m, 2.f * a.cap, a.cap) + logf(l);
+  return fmaf(m, (MOD & kCapped) ? a.cap : a.scale, logf(l));
 }
 
 // The slots without a tile share the rows of no sequence (before the first and
@@ -455,94 +463,72 @@ __device__ __forceinline__ float other_half(float x) {
 __device__ __forceinline__ int result_row(int r, int g) { return 8 * (r >> 2) + 4 * g + (r & 3); }
 
 // A product's tanh(a s / C) as u: with E = exp(2 a s / C) it is 1 - 2 / (1 + E). For bf16
-// u = 1 / (1 + E), whose absolute error of a step near 1 is one of 2^-23 C in a capped
-// score, far below the weights' rounding; for fp32 u is the tanh itself, near zero by the
-// first terms of its series, so that small scores keep their relative accuracy.
-// capped: C tanh in powers of two; steep: tanh's derivative, 1 - tanh^2 (bf16: a quarter of it).
+// u = -1 / (1 + E), so that tanh = 1 + 2 u; its absolute error of a step near 1 is one of
+// 2^-23 C in a capped score, far below the weights' rounding. For fp32 u is the tanh itself,
+// near zero by the first terms of its series, so that small scores keep their relative accuracy.
 template <bool BF16>
 __device__ __forceinline__ float squash(float s, float k) {   // k: 2 a log2(e) / C
   const float x = s * k;
-  const float r = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(x));
+  const float r = __builtin_amdgcn_rcpf(-1.f - __builtin_amdgcn_exp2f(x));
   if constexpr (BF16) return r;
   const float z = x * (0.5f / kLog2e), z2 = z * z;
   const float p = fmaf(z2, fmaf(z2, fmaf(z2, fmaf(z2, 62.f / 2835.f, -17.f / 315.f), 2.f / 15.f), -1.f / 3.f), 1.f);
-  return fabsf(z) < 0.3f ? z * p : fmaf(-2.f, r, 1.f);
+  return fabsf(z) < 0.3f ? z * p : fmaf(2.f, r, 1.f);
 }
-template <bool BF16>
-__device__ __forceinline__ float capped(float u, float cap2, float more) {   // cap2: C log2(e)
-  if constexpr (BF16) return fmaf(u, -2.f * cap2, cap2 + more);
-  return fmaf(u, cap2, more);
-}
+// tanh's derivative 1 - tanh^2; of bf16's u a quarter of it, -u - u^2.
 template <bool BF16>
 __device__ __forceinline__ float steep(float u) {
-  return BF16 ? fmaf(-u, u, u) : fmaf(-u, u, 1.f);
+  return BF16 ? fmaf(-u, u, -u) : fmaf(-u, u, 1.f);
 }
 // dq and dk are sums of ds, in which bf16's quarter is, times this.
 template <bool BF16, int MOD>
 __device__ __forceinline__ float grad_scale(const Args& a) {
-  return BF16 && MOD == kCapped ? 4.f * a.scale : a.scale;
+  return BF16 && (MOD & kCapped) ? 4.f * a.scale : a.scale;
 }
 
-// Changed scores of the lane's column for the softmax, from products: capped, in powers of
-// two; biased, in the products' unit. apart: the column's position less that of row 0 of
+// Changed scores of the lane's column for the softmax, from products: in unit_of. apart: the column's position less that of row 0 of
 // the lane's half (a slope of the opposite sign of distance needs no case of its own).
 template <bool BF16, int MOD>
 __device__ __forceinline__ void change_scores(f32x16_t& s, const Args& a, const Change& ch, int32_t apart) {
-  if constexpr (MOD == kCapped) {
-    const float k = 2.f * kLog2e * a.scale / a.cap, cap2 = a.cap * kLog2e;
+  if constexpr (MOD & kCapped) {
+    const float k = 2.f * kLog2e * a.scale / a.cap;
 #pragma unroll
-    for (int r = 0; r < 16; ++r) s[r] = capped<BF16>(squash<BF16>(s[r], k), cap2, 0.f);
+    for (int r = 0; r < 16; ++r) s[r] = squash<BF16>(s[r], k);
   }
-  if (MOD != kPlain && ch.biased) {
-    keep_branch();
+  if constexpr (MOD & kBiased) {
     const float d = (float)apart;
 #pragma unroll
     for (int r = 0; r < 16; ++r) s[r] = fmaf(-ch.slope, fabsf(d - (float)result_row(r, 0)), s[r]);
   }
 }
 // The factor of a head's slope for change_scores.
-template <int MOD>
+template <bool BF16, int MOD>
 __device__ __forceinline__ float bias_unit(const Args& a) {
-  return MOD == kCapped ? kLog2e : 1.f / a.scale;
+  return 1.f / ((MOD & kCapped) ? (BF16 ? 2.f : 1.f) * a.cap : a.scale);
 }
 
 // In the backward pass: the products s of a column become the weights p = exp2(score - lse),
-// and ds their gradients p (dp - delta) times the derivative of the change. lse and
-// delta of row r from at(r): those of the lane's query, or of each row's.
+// and dp their gradients p (dp - delta) times the derivative of the change. at(r): lse and
+// delta of rows r and r + 1, which are those of the lane's query, or of each row's.
 template <bool BF16, int MOD, typename F>
 __device__ __forceinline__ void weights_and_gradients(f32x16_t& s, f32x16_t& dp, const Args& a, const Change& ch, int32_t apart, F at) {
-  if constexpr (MOD == kPlain) {
-    const float c = a.scale * kLog2e;
+  const float c = unit_of<BF16, MOD>(a), k = (MOD & kCapped) ? 2.f * kLog2e * a.scale / a.cap : 0.f;
+  const float d = (float)apart;
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const f32x2_t x = at(r);
-      s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, -x[0]));
-      dp[r] = s[r] * (dp[r] - x[1]);
-    }
-  } else {
-    const float c = a.scale * kLog2e;
-    const float k = MOD == kCapped ? 2.f * c / a.cap : 0.f, cap2 = a.cap * kLog2e;
-    const auto all = [&](auto bias) {
+  for (int r0 = 0; r0 < 16; r0 += 2) {
+    const f32x4_t x = at(r0);
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const f32x2_t x = at(r);
-        const float more = bias(r) - x[0];
-        if constexpr (MOD == kCapped) {
-          const float u = squash<BF16>(s[r], k);
-          s[r] = __builtin_amdgcn_exp2f(capped<BF16>(u, cap2, more));
-          dp[r] = s[r] * (dp[r] - x[1]) * steep<BF16>(u);
-        } else {
-          s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, more));
-          dp[r] = s[r] * (dp[r] - x[1]);
-        }
+    for (int i = 0; i < 2; ++i) {
+      const int r = r0 + i;
+      const float more = MOD & kBiased ? fmaf(-ch.slope, fabsf(d - (float)result_row(r, 0)), -x[2 * i]) : -x[2 * i];
+      if constexpr (MOD & kCapped) {
+        const float u = squash<BF16>(s[r], k);
+        s[r] = __builtin_amdgcn_exp2f(fmaf(u, c, more));
+        dp[r] = s[r] * (dp[r] - x[2 * i + 1]) * steep<BF16>(u);
+      } else {
+        s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, more));
+        dp[r] = s[r] * (dp[r] - x[2 * i + 1]);
       }
-    };
-    if (ch.biased) {
-      keep_branch();
-      const float d = (float)apart;
-      all([&](int r) { return -ch.slope * fabsf(d - (float)result_row(r, 0)); });
-    } else {
-      all([&](int) { return 0.f; });
     }
   }
 }
@@ -664,7 +650,7 @@ __device__ __forceinline__ void forward_pass(bool careful, const Args& a, const 
   constexpr int kStage = 32 * G::kPitch, kBuf = 2 * kStage;
   const int lane = threadIdx.x & 63, g = lane >> 5;
   const int32_t query = w0 + (lane & 31);
-  const float c = unit_of<MOD>(a);
+  const float c = unit_of<BF16, MOD>(a);
   // keys that some query sees; where all see the same ones, rows behind them read as zeros
   const int32_t end = max(w0 + 32, ch.pre);
   if (ch.pre >= w0 + 32) len = ch.pre;
@@ -755,8 +741,8 @@ __global__ __launch_bounds__(64 * NS, BF16 ? 2 : 1) void k_forward_rows(Args a) 
   const int32_t w0 = tile * 32, query = w0 + (lane & 31);
   uint4 q[G::kPairs];
   load_operand<BF16, DC>(a.q, start, h, w0, len, a.D, q);
-  const float c = unit_of<MOD>(a);
-  const Change ch{prefix_of<MOD>(a, seq, len), slope_of<MOD>(a, h, bias_unit<MOD>(a)), MOD != kPlain && a.slopes};
+  const float c = unit_of<BF16, MOD>(a);
+  const Change ch{prefix_of<MOD>(a, seq, len), slope_of<MOD>(a, h, bias_unit<BF16, MOD>(a))};
   float m, l;
   f32x16_t acc[G::kTiles];
   unsigned char* mine = lds + split * P::kBuffers * P::kBuf;
@@ -795,7 +781,7 @@ __global__ __launch_bounds__(64 * NS, BF16 ? 2 : 1) void k_forward_rows(Args a) 
   }
   if (query < len) {
     store_rows<BF16, DC>(a.o, (int64_t)start + query, h, a.D, acc, 1.f / l);
-    if (g == 0) a.lse[(int64_t)h * a.N + start + query] = fmaf(m, MOD == kCapped ? 1.f / kLog2e : a.scale, logf(l));
+    if (g == 0) a.lse[(int64_t)h * a.N + start + query] = lse_of<BF16, MOD>(a, m, l);
   }
   if (careful && ch.pre < w0 + 32) {
     __threadfence_block();
@@ -864,7 +850,7 @@ __device__ __forceinline__ void tile_again(const Args& a, const Change& ch, int3
                                            const uint4 (&q)[Geo<BF16, DC>::kPairs], float& m, float& l,
                                            f32x16_t (&acc)[Geo<BF16, DC>::kTiles]) {
   using G = Geo<BF16, DC>;
-  const float c = unit_of<MOD>(a);
+  const float c = unit_of<BF16, MOD>(a);
   const int32_t end = max(w0 + 32, ch.pre);
   if (ch.pre >= w0 + 32) len = ch.pre;   // (as in forward_pass)
   const int32_t query = w0 + (threadIdx.x & 31);
@@ -902,7 +888,7 @@ __device__ __forceinline__ void tile_again(const Args& a, const Change& ch, int3
 // D = 64: 104 us, 661 TF/s of the pairs u <= t; 12289 + 777 + 4100 rows, 16/2 heads,
 // D = 128: 713 us, 968 TF/s. A large bf16 matrix product reaches 1241 TF/s.
 template <bool BF16, int DC, int MOD>
-__global__ __launch_bounds__(256, BF16 ? 2 : 1) void k_forward(Args a) {
+__global__ __launch_bounds__(256, !BF16 ? 1 : MOD != kPlain && DC == 64 ? 3 : 2) void k_forward(Args a) {
   using G = Geo<BF16, DC>;
   using P = Tiles<BF16, DC>;
   // keys are needed a step ahead of their values, whose scores they give
@@ -922,7 +908,7 @@ __global__ __launch_bounds__(256, BF16 ? 2 : 1) void k_forward(Args a) {
   const int32_t w0 = tile * P::kRows + wv * 32;   // the wave's first query
   const int32_t query = w0 + (lane & 31);
   const uint32_t base = lds_address(lds);
-  const Change ch{prefix_of<MOD>(a, seq, len), slope_of<MOD>(a, h, bias_unit<MOD>(a)), MOD != kPlain && a.slopes};
+  const Change ch{prefix_of<MOD>(a, seq, len), slope_of<MOD>(a, h, bias_unit<BF16, MOD>(a))};
   const int32_t end = max(min(tile * P::kRows + P::kRows, len), ch.pre);   // keys that some query of the block sees
   const int32_t last = max(w0 + 32, ch.pre);                               // and of the wave
   const typename P::Rows ks(a.k, start, kh, a.D), vs(a.v, start, kh, a.D);
@@ -931,7 +917,7 @@ __global__ __launch_bounds__(256, BF16 ? 2 : 1) void k_forward(Args a) {
   if (P::kStep < end) ks.fetch(P::kStep, len, base + P::kStage);
   uint4 q[G::kPairs];
   load_operand<BF16, DC>(a.q, start, h, w0, len, a.D, q);
-  const float c = unit_of<MOD>(a);
+  const float c = unit_of<BF16, MOD>(a);
   float m = -INFINITY, l = 0.f;
   f32x16_t acc[G::kTiles] = {};
   f32x16_t even[2], odd[2];   // scores of the even and the odd steps
@@ -969,7 +955,7 @@ __global__ __launch_bounds__(256, BF16 ? 2 : 1) void k_forward(Args a) {
   l += other_half(l);
   if (query < len) {
     store_rows<BF16, DC>(a.o, (int64_t)start + query, h, a.D, acc, 1.f / l);
-    if (g == 0) a.lse[(int64_t)h * a.N + start + query] = fmaf(m, MOD == kCapped ? 1.f / kLog2e : a.scale, logf(l));
+    if (g == 0) a.lse[(int64_t)h * a.N + start + query] = lse_of<BF16, MOD>(a, m, l);
   }
   if (careful && ch.pre < w0 + 32) {
     __threadfence_block();
@@ -993,9 +979,13 @@ __device__ __forceinline__ float dot_chunk(const uint4& x, const uint4& y, float
   return s;
 }
 
-// lse in units of log 2. A query all of whose scores are -infinity has no weights: NaN,
+// lse in units of log 2, less the constant of bf16's capped scores. A query all of whose scores are -infinity has no weights: NaN,
 // also against scores that are computed without the row's infinities.
-__device__ __forceinline__ float scaled_lse(float lse) { return lse == -INFINITY ? NAN : lse * kLog2e; }
+template <bool BF16, int MOD>
+__device__ __forceinline__ float scaled_lse(const Args& a, float lse) {
+  if constexpr (BF16 && (MOD & kCapped)) return lse == -INFINITY ? NAN : (lse - a.cap) * kLog2e;
+  return lse == -INFINITY ? NAN : lse * kLog2e;
+}
 
 // One wave's pass for dq over the keys k0, k0 + 32 waves, .., as forward_pass.
 template <bool BF16, int DC, int BUFFERS, int MOD>
@@ -1028,7 +1018,7 @@ __device__ __forceinline__ void backward_q_pass(bool careful, const Args& a, con
     unsigned char* lv = lk + kStage;
     f32x16_t s = rows_times<BF16, DC>(lk, 0, q);
     f32x16_t ds = rows_times<BF16, DC>(lv, 0, dO);
-    weights_and_gradients<BF16, MOD>(s, ds, a, ch, query - k0 - 4 * g, [&](int) { return f32x2_t{lse, delta}; });
+    weights_and_gradients<BF16, MOD>(s, ds, a, ch, query - k0 - 4 * g, [&](int) { return f32x4_t{lse, delta, lse, delta}; });
     if (MOD == kPlain ? k0 == w0 : k0 >= w0 && k0 + 32 > ch.pre) {
       keep_branch();
 #pragma unroll
@@ -1069,7 +1059,7 @@ __global__ __launch_bounds__(256, !BF16 ? 1 : DC == 64 ? 3 : 2) void k_backward_
   const int32_t w0 = tile * P::kRows + wv * 32;
   const int32_t query = w0 + (lane & 31);
   const uint32_t base = lds_address(lds);
-  const Change ch{prefix_of<MOD>(a, seq, len), slope_of<MOD>(a, h, kLog2e), MOD != kPlain && a.slopes};
+  const Change ch{prefix_of<MOD>(a, seq, len), slope_of<MOD>(a, h, kLog2e)};
   const int32_t end = max(min(tile * P::kRows + P::kRows, len), ch.pre), last = max(w0 + 32, ch.pre);
   const typename P::Rows ks(a.k, start, kh, a.D), vs(a.v, start, kh, a.D);
   ks.fetch(0, len, base);
@@ -1088,7 +1078,7 @@ __global__ __launch_bounds__(256, !BF16 ? 1 : DC == 64 ? 3 : 2) void k_backward_
   float lse = 0.f;
   if (query < len) {
     const int64_t at = (int64_t)h * a.N + start + query;
-    lse = scaled_lse(a.lse[at]);
+    lse = scaled_lse<BF16, MOD>(a, a.lse[at]);
     if (g == 0) {
       *(float2*)(a.pairs + 2 * at) = make_float2(lse, delta);
     }
@@ -1111,7 +1101,7 @@ __global__ __launch_bounds__(256, !BF16 ? 1 : DC == 64 ? 3 : 2) void k_backward_
         if (k0 >= last) break;   // (all masked)
         f32x16_t s = rows_times<BF16, DC>(lk, t * 32, q);
         f32x16_t ds = rows_times<BF16, DC>(lv, t * 32, dO);
-        weights_and_gradients<BF16, MOD>(s, ds, a, ch, query - k0 - 4 * g, [&](int) { return f32x2_t{lse, delta}; });
+        weights_and_gradients<BF16, MOD>(s, ds, a, ch, query - k0 - 4 * g, [&](int) { return f32x4_t{lse, delta, lse, delta}; });
         if (MOD == kPlain ? k0 == w0 : k0 >= w0 && k0 + 32 > ch.pre) {
           keep_branch();
 #pragma unroll
@@ -1162,7 +1152,7 @@ __global__ __launch_bounds__(64 * NS, BF16 ? 2 : 1) void k_backward_q_rows(Args 
   const int lane = threadIdx.x & 63, g = lane >> 5;
   const int split = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int32_t w0 = tile * 32, query = w0 + (lane & 31);
-  const Change ch{prefix_of<MOD>(a, seq, len), slope_of<MOD>(a, h, kLog2e), MOD != kPlain && a.slopes};
+  const Change ch{prefix_of<MOD>(a, seq, len), slope_of<MOD>(a, h, kLog2e)};
   const int32_t splits = SPLIT ? query_splits(a, w0, ch.pre, NS) : 1;
   if (SPLIT && z >= splits) return;
   uint4 q[G::kPairs], dO[G::kPairs];
@@ -1179,7 +1169,7 @@ __global__ __launch_bounds__(64 * NS, BF16 ? 2 : 1) void k_backward_q_rows(Args 
   float lse = 0.f;
   if (query < len) {
     const int64_t at = (int64_t)h * a.N + start + query;
-    lse = scaled_lse(a.lse[at]);
+    lse = scaled_lse<BF16, MOD>(a, a.lse[at]);
     if (g == 0 && split == 0 && z == 0) *(float2*)(a.pairs + 2 * at) = make_float2(lse, delta);
   }
   f32x16_t acc[G::kTiles];
@@ -1299,12 +1289,12 @@ __device__ __forceinline__ void backward_kv_pass(bool& careful, const Args& a, i
     const float* words = (const float*)(lq + 2 * P::kStage);
     f32x16_t p;
     // (capped scores of a query row that is not finite may be finite, and so its lse)
-    if constexpr (MOD == kCapped) p = rows_times<BF16, DC>(lq, 0, k);
+    if constexpr (MOD & kCapped) p = rows_times<BF16, DC>(lq, 0, k);
     if (MOD == kPlain ? q0 == w0 : q0 <= w0 && pre < w0 + 32) {   // (a query row that is not finite has lse or delta of NaN)
       careful |= zero_not_finite<BF16, DC>(lo);
       careful |= zero_not_finite<BF16, DC>(lq);
     }
-    if constexpr (MOD != kCapped) p = rows_times<BF16, DC>(lq, 0, k);
+    if constexpr (!(MOD & kCapped)) p = rows_times<BF16, DC>(lq, 0, k);
     f32x16_t ds = rows_times<BF16, DC>(lo, 0, v);
     if constexpr (MOD == kPlain) {
       const float c = a.scale * kLog2e;
@@ -1321,9 +1311,9 @@ __device__ __forceinline__ void backward_kv_pass(bool& careful, const Args& a, i
         }
       }
     } else {
-      const Change ch{pre, slope_of<MOD>(a, h, kLog2e), a.slopes != nullptr};
+      const Change ch{pre, slope_of<MOD>(a, h, kLog2e)};
       weights_and_gradients<BF16, MOD>(p, ds, a, ch, key - q0 - 4 * g,
-                                       [&](int r) { return *(const f32x2_t*)(words + 2 * result_row(r, g)); });
+                                       [&](int r) { return *(const f32x4_t*)(words + 2 * result_row(r, g)); });
     }
     if ((MOD == kPlain ? q0 == w0 : q0 <= w0 && pre < w0 + 32) || q0 + 32 > len) {
       keep_branch();
