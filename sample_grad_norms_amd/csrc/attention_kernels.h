@@ -135,14 +135,22 @@ struct Change {
   int32_t pre;
   float slope;
 };
+// Read as constants, by the scalar unit: a vector load in the loop over a key head's query
+// heads would wait for the rows that are under way (dk and dv of biased scores).
+template <typename T>
+__device__ __forceinline__ T uniform_load(const T* p, int32_t i) {
+  return *((const __attribute__((address_space(4))) T*)p + __builtin_amdgcn_readfirstlane(i));
+}
 template <int MOD>
 __device__ __forceinline__ int32_t prefix_of(const Args& a, int32_t seq, int32_t len) {
-  return MOD != kPlain && a.prefix ? min(max(__builtin_amdgcn_readfirstlane(a.prefix[seq]), 0), len) : 0;
+  return MOD != kPlain && a.prefix ? min(max(uniform_load(a.prefix, seq), 0), len) : 0;
 }
 // The head's slope times f.
 template <int MOD>
 __device__ __forceinline__ float slope_of(const Args& a, int32_t h, float f) {
-  return (MOD & kBiased) && a.slopes ? a.slopes[h] * f : 0.f;
+  if constexpr (!(MOD & kBiased)) return 0.f;
+  const float m = uniform_load(a.slopes ? a.slopes : (const float*)a.k.p, a.slopes ? h : 0);   // (no branch in the loop)
+  return a.slopes ? m * f : 0.f;
 }
 // What the softmax works on, times this, is in powers of two: products, or of capped
 // scores u (see squash), of which bf16's u is tanh / 2 up to a constant.

@@ -28,10 +28,12 @@ Readings where the pages leave a step open:
 
 Every norm estimate runs in libdpnorm on the GPU; torch runs the model and its
 two backward passes. The weights that are clipped are those of bias-free
-nn.Linear modules (Llama has no biases) and of layers.Embedding tables, whose
-per-sample norm is exact whatever the estimator is: row v of sample i's
-gradient is the sum of its output gradients at the positions of id v, so the
-norm costs one pass over the output gradients. Refused, since part of a gradient would go unclipped: any other
+nn.Linear modules (Llama has no biases), of layers.Embedding tables and of
+layers.LayerNorm and layers.RMSNorm, gain and bias. The norms of the last three
+are exact whatever the estimator is: row v of sample i's gradient of a table
+is the sum of its output gradients at the positions of id v, and its gradient of
+a gain the sum of output gradients times normalised rows, so the
+norm costs one pass over the output gradients (and a norm layer's inputs). Refused, since part of a gradient would go unclipped: any other
 trainable parameter, and a weight that a module of another kind also
 holds (a tied embedding). A use of a weight that the hooks cannot see (the
 weight passed to F.linear outside its module) is caught on the first step:
@@ -57,7 +59,7 @@ import torch
 from torch import nn
 
 import sample_grad_norms_amd as dp
-from sample_grad_norms_amd.layers import Embedding
+from sample_grad_norms_amd.layers import Embedding, LayerNorm, _aligned
 
 ProjectionFn = Callable[[int, int, torch.dtype, torch.device, torch.Generator], torch.Tensor]
 
@@ -71,8 +73,9 @@ def gaussian_projection(p: int, k: int, dtype: torch.dtype, device: torch.device
 
 
 class RandomizedClipping:
-    """Hooks a model's bias-free linear layers and embedding tables
-    (layers.Embedding) and runs the DP-SGD-RC step.
+    """Hooks a model's bias-free linear layers, embedding tables
+    (layers.Embedding) and norm layers (layers.LayerNorm, layers.RMSNorm) and
+    runs the DP-SGD-RC step.
 
     Usage::
 
@@ -110,7 +113,9 @@ class RandomizedClipping:
 
     Embedding ids are [B, ...]: one row of ids for each sample. Ids [B], one a
     sample, look like the positions of B samples of length B, which only the
-    check can tell apart; without it they are refused ([B][1] is not).
+    check can tell apart; without it they are refused ([B][1] is not). A norm
+    layer's input is [B, ..., d]. Norm layers that share a gain or a bias share
+    both, and their eps and kind.
     """
 
     def __init__(self, model: nn.Module, C: float, noise_multiplier: float, k: int = 32,
@@ -150,10 +155,25 @@ class RandomizedClipping:
             raise ValueError(f"embedding tables shared with modules that are not layers.Embedding would go partly "
                              f"unclipped: {shared}")
         covered |= covered_tables
+        self.norms: List[LayerNorm] = [m for m in model.modules() if isinstance(m, LayerNorm)]
+        covered_norms = {id(p) for m in self.norms for p in m.parameters(recurse=False)}
+        shared = [f"{name}.{pname}" if name else pname for name, mod in model.named_modules()
+                  if not isinstance(mod, LayerNorm)
+                  for pname, p in mod.named_parameters(recurse=False) if id(p) in covered_norms]
+        if shared:
+            raise ValueError(f"weights of norm layers shared with modules that are not norm layers would go partly "
+                             f"unclipped: {shared}")
+        held: Dict[int, Tuple] = {}
+        for m in self.norms:
+            for p in m.parameters(recurse=False):
+                if held.setdefault(id(p), self._norm_key(m)) != self._norm_key(m):
+                    raise ValueError("norm layers that share a gain or a bias must share both, and their eps and kind")
+        covered |= covered_norms
         loose = [name for name, p in model.named_parameters(remove_duplicate=False)
                  if p.requires_grad and id(p) not in covered]
         if loose:
-            raise ValueError(f"trainable parameters outside bias-free linear layers would go unclipped: {loose}")
+            raise ValueError(f"trainable parameters outside bias-free linear layers, layers.Embedding and norm layers "
+                             f"of the library would go unclipped: {loose}")
         # one entry per distinct weight, in module order (modules holding the
         # same weight contribute to one per-sample gradient)
         self.params: List[nn.Parameter] = []
@@ -167,6 +187,8 @@ class RandomizedClipping:
         for t in self.tables:
             if t.weight.requires_grad and all(p is not t.weight for p in self.params):
                 self.params.append(t.weight)
+        for m in self.norms:
+            self.params += [p for p in m.parameters(recurse=False) if p.requires_grad and all(p is not q for q in self.params)]
         self._names = {id(p): name for name, p in model.named_parameters()}
         self._capturing = False
         self._rec: Dict[nn.Module, List[Tuple[torch.Tensor, torch.Tensor]]] = {}
@@ -178,11 +200,17 @@ class RandomizedClipping:
         self._pending: Optional[List[Tuple[nn.Parameter, torch.Tensor, torch.Tensor]]] = None
         # per table of the last step: (weight, order of its ids, output gradients, scale)
         self._table_recs: List[Tuple[nn.Parameter, dp.EmbedOrder, torch.Tensor, float]] = []
-        self._handles = [m.register_forward_hook(self._hook) for m in [*self.modules, *self.tables]]
+        # per norm layer of the last step: (module, inputs, output gradients)
+        self._norm_recs: List[Tuple[LayerNorm, torch.Tensor, torch.Tensor]] = []
+        self._handles = [m.register_forward_hook(self._hook) for m in [*self.modules, *self.tables, *self.norms]]
+
+    @staticmethod
+    def _norm_key(m: LayerNorm) -> Tuple:
+        return id(m.weight), id(m.bias), m.eps, m.rms
 
     # -- capture ---------------------------------------------------------
     def _hook(self, module, inputs, output):
-        if self._capturing and module.weight.requires_grad:
+        if self._capturing and any(p.requires_grad for p in module.parameters(recurse=False)):
             self._rec.setdefault(module, []).append((inputs[0], output))
 
     class _Capture:
@@ -244,6 +272,15 @@ class RandomizedClipping:
             for r in self._rec.get(m, []):
                 looked.setdefault((id(m.weight), m.scale), (m, []))[1].append(r)
         outputs += [o for _, recs in looked.values() for (_, o) in recs]
+        # the uses of every norm layer's weights
+        normed: Dict[Tuple, Tuple[LayerNorm, List]] = {}
+        for m in self.norms:
+            for x, o in self._rec.get(m, []):
+                if x.dim() < 2 or x.shape[0] != B:
+                    raise ValueError(f"norm layer {self._names.get(id(m.weight), '')} is applied to {list(x.shape)}: it must be "
+                                     f"[B={B}, ..., d], rows of one sample each")
+                normed.setdefault(self._norm_key(m), (m, []))[1].append((x, o))
+        outputs += [o for _, recs in normed.values() for (_, o) in recs]
         # the step that is checked: powers of two, whose product and quotient are exact
         w, unweighted = None, None
         if self._verify and B > 1 and all(o.dtype in (torch.bfloat16, torch.float32, torch.float64) for o in outputs):
@@ -284,6 +321,17 @@ class RandomizedClipping:
             tok = toks[0] if len(toks) == 1 else torch.cat([t.long() for t in toks], dim=1)
             G = Gs[0] if len(Gs) == 1 else torch.cat(Gs, dim=1)
             self._table_recs.append((m.weight, dp.embed_order(tok.contiguous(), m.weight.shape[0]), G, m.scale))
+        self._norm_recs = []
+        for m, recs in normed.values():
+            xs, Gs = [], []
+            for (x, out), g in zip(recs, grads[at:at + len(recs)]):
+                if g is None:
+                    g = torch.zeros_like(out)
+                xs.append(x.detach().reshape(B, -1, x.shape[-1]))
+                Gs.append(by_sample(g))
+            at += len(recs)
+            x, G = (t[0] if len(t) == 1 else torch.cat(t, dim=1) for t in (xs, Gs))
+            self._norm_recs.append((m, _aligned(x), _aligned(G)))
         self._pending = [(w, A, G) for (w, _), (A, G) in zip(weights, layers)] if self._verify else None
         self._batch = B
         self._rec = {}
@@ -310,7 +358,7 @@ class RandomizedClipping:
         """Backward pass 1 and the norm path: returns (n, c), float32 [B]."""
         layers = self._collect(losses)
         B = losses.shape[0]
-        device = layers[0][0].device if layers else self._table_recs[0][2].device
+        device = (layers[0][0] if layers else (self._table_recs or self._norm_recs)[0][2]).device
         gen = self._generator(device)
         n = torch.zeros(B, dtype=torch.float32, device=device)
         used = []
@@ -342,8 +390,11 @@ class RandomizedClipping:
                     used.append((A, G, (S, P)))
         for (_, order, G, scale) in self._table_recs:
             dp.embed_norm(order, G, scale=scale, out=n, accumulate=True)
+        for (m, x, G) in self._norm_recs:
+            dp.layernorm_norm(x, G, eps=m.eps, rms=m.rms, gain=m.weight.requires_grad,
+                              bias=m.bias is not None and m.bias.requires_grad, out=n, accumulate=True)
         if self._pending is None:   # (no check will read them)
-            self._table_recs = []
+            self._table_recs, self._norm_recs = [], []
         c = dp.clip_factors(n, self.C)
         self.last_layers = used if self.keep_layers else []
         return n, c
@@ -362,10 +413,12 @@ class RandomizedClipping:
         (on the first step, then checked against the recordings)."""
         pending, self._pending = self._pending, None
         tables, self._table_recs = self._table_recs, []
+        norms, self._norm_recs = self._norm_recs, []
         before = None
         if pending is not None:
             before = [w.grad.detach().float().clone() if w.grad is not None else None
-                      for w in [w for w, _, _ in pending] + [w for w, _, _, _ in tables]]
+                      for w in [w for w, _, _ in pending] + [w for w, _, _, _ in tables]
+                      + [p for m, _, _ in norms for p in m.parameters(recurse=False)]]
         (c.detach().to(losses.dtype) * losses).sum().backward()
         if pending is not None:
             self._check_coverage(pending, before, c)
@@ -373,6 +426,15 @@ class RandomizedClipping:
             for (w, order, G, scale), g0 in zip(tables, before[len(pending):]):
                 want = dp.embed_grad(order, G, scale=scale, weights=cw).float()
                 self._check_gradient(w, want, g0)
+            held = iter(before[len(pending) + len(tables):])
+            for m, x, G in norms:
+                _, mean, rstd = dp.layernorm_forward(x, _aligned(m.weight.detach()), eps=m.eps, rms=m.rms)
+                _, *wants = dp.layernorm_backward(G, x, _aligned(m.weight.detach()), mean, rstd, bias=m.bias is not None, weights=cw,
+                                                  need_dx=False)
+                for w, want in zip(m.parameters(recurse=False), wants):
+                    g0 = next(held)
+                    if w.requires_grad:
+                        self._check_gradient(w, want.float(), g0)
             self._verify, self._verified = False, True
 
     def _check_coverage(self, pending, before, c: torch.Tensor) -> None:
