@@ -114,7 +114,7 @@ class RandomizedClipping:
     Embedding ids are [B, ...]: one row of ids for each sample. Ids [B], one a
     sample, look like the positions of B samples of length B, which only the
     check can tell apart; without it they are refused ([B][1] is not). A norm
-    layer's input is [B, ..., d]. Norm layers that share a gain or a bias share
+    layer's input is [B, ..., d], and [B, d] is taken with the check alone. Norm layers that share a gain or a bias share
     both, and their eps and kind.
     """
 
@@ -279,6 +279,10 @@ class RandomizedClipping:
                 if x.dim() < 2 or x.shape[0] != B:
                     raise ValueError(f"norm layer {self._names.get(id(m.weight), '')} is applied to {list(x.shape)}: it must be "
                                      f"[B={B}, ..., d], rows of one sample each")
+                if x.dim() == 2 and B > 1 and not (self._verify or self._verified):
+                    raise ValueError(f"norm layer {self._names.get(id(m.weight), '')} is applied to [B={B}, d], which may as well "
+                                     f"be rows that all samples share: give one row a sample as [B][1][d], or leave "
+                                     f"verify_coverage on")
                 normed.setdefault(self._norm_key(m), (m, []))[1].append((x, o))
         outputs += [o for _, recs in normed.values() for (_, o) in recs]
         # the step that is checked: powers of two, whose product and quotient are exact
