@@ -247,17 +247,20 @@ hipError_t with_kernels(const attn::Args& a, bool bf16, F f) {
 }
 
 // Caps: a score's tanh has an absolute error of a few 2^-24, times the cap; past 1024 that
-// would come near the rounding of bf16 weights. Slopes are added in units of the scale.
+// would come near the rounding of bf16 weights. Slopes are added in units of the scale, and
+// products squeezed by scale / cap.
 dpnorm_status check_scores(const dpnorm_attn_shape* shape, const dpnorm_attn_scores* s) {
   if (!s) return DPNORM_OK;
   if (!(s->cap == 0.f || (s->cap >= 1.f / 1024 && s->cap <= 1024.f))) return DPNORM_ERR_VALUE;
   if (s->slopes && shape->scale < 0x1p-64f) return DPNORM_ERR_VALUE;
+  if (s->cap > 0.f && shape->scale > 0x1p64f) return DPNORM_ERR_VALUE;
   if (!aligned(s->slopes, 4) || !aligned(s->prefix, 4)) return DPNORM_ERR_ALIGN;
   return DPNORM_OK;
 }
 void set_scores(attn::Args& a, const dpnorm_attn_scores* s) {
   if (!s) return;
   a.cap = s->cap;
+  a.squeeze = s->cap > 0.f ? (float)(2.0 * 1.4426950408889634 * a.scale / s->cap) : 0.f;
   a.slopes = s->slopes;
   a.prefix = s->prefix;
 }

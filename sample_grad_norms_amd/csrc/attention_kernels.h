@@ -67,7 +67,7 @@ struct Args {
   float* parts;       // their sums, [slot][key head][split][dk, dv][tile][1024]
   uint32_t* arrived;  // [slot][key head] of them have arrived (the launch before sets it to zero)
   // Changed scores:
-  float cap;              // C
+  float cap, squeeze;     // C and 2 a log2(e) / C
   const float* slopes;    // [Hq] m, or null
   const int32_t* prefix;  // [S] rows of a sequence that all of its rows see, or null
 };
@@ -472,16 +472,19 @@ __device__ __forceinline__ int result_row(int r, int g) { return 8 * (r >> 2) + 
 
 // A product's tanh(a s / C) as u: with E = exp(2 a s / C) it is 1 - 2 / (1 + E). For bf16
 // u = -1 / (1 + E), so that tanh = 1 + 2 u; its absolute error of a step near 1 is one of
-// 2^-23 C in a capped score, far below the weights' rounding. For fp32 u is the tanh itself,
-// near zero by the first terms of its series, so that small scores keep their relative accuracy.
+// 2^-23 C in a capped score, far below the weights' rounding. For fp32 u is the tanh itself, from
+// |s| (where the reciprocal is small), its reciprocal once refined, and near zero by the first
+// terms of its series, so that it is off by little more than its own rounding.
 template <bool BF16>
 __device__ __forceinline__ float squash(float s, float k) {   // k: 2 a log2(e) / C
   const float x = s * k;
-  const float r = __builtin_amdgcn_rcpf(-1.f - __builtin_amdgcn_exp2f(x));
-  if constexpr (BF16) return r;
+  if constexpr (BF16) return __builtin_amdgcn_rcpf(-1.f - __builtin_amdgcn_exp2f(x));
+  const float e = 1.f + __builtin_amdgcn_exp2f(fabsf(x));
+  const float r = __builtin_amdgcn_rcpf(e);
+  const float fine = e < INFINITY ? fmaf(r, fmaf(-e, r, 1.f), r) : r;
   const float z = x * (0.5f / kLog2e), z2 = z * z;
   const float p = fmaf(z2, fmaf(z2, fmaf(z2, fmaf(z2, 62.f / 2835.f, -17.f / 315.f), 2.f / 15.f), -1.f / 3.f), 1.f);
-  return fabsf(z) < 0.3f ? z * p : fmaf(2.f, r, 1.f);
+  return fabsf(z) < 0.3f ? z * p : copysignf(fmaf(-2.f, fine, 1.f), s);
 }
 // tanh's derivative 1 - tanh^2; of bf16's u a quarter of it, -u - u^2.
 template <bool BF16>
@@ -499,9 +502,8 @@ __device__ __forceinline__ float grad_scale(const Args& a) {
 template <bool BF16, int MOD>
 __device__ __forceinline__ void change_scores(f32x16_t& s, const Args& a, const Change& ch, int32_t apart) {
   if constexpr (MOD & kCapped) {
-    const float k = 2.f * kLog2e * a.scale / a.cap;
 #pragma unroll
-    for (int r = 0; r < 16; ++r) s[r] = squash<BF16>(s[r], k);
+    for (int r = 0; r < 16; ++r) s[r] = squash<BF16>(s[r], a.squeeze);
   }
   if constexpr (MOD & kBiased) {
     const float d = (float)apart;
@@ -515,12 +517,19 @@ __device__ __forceinline__ float bias_unit(const Args& a) {
   return 1.f / ((MOD & kCapped) ? (BF16 ? 2.f : 1.f) * a.cap : a.scale);
 }
 
+// Capped scores in fp32 are differences from lse before they are in powers of two: a factor
+// on an lse of some tens, the cap's size, would round by more than the rest of the weight.
+template <bool BF16, int MOD>
+__device__ __forceinline__ constexpr bool natural() {
+  return !BF16 && (MOD & kCapped);
+}
+
 // In the backward pass: the products s of a column become the weights p = exp2(score - lse),
 // and dp their gradients p (dp - delta) times the derivative of the change. at(r): lse and
 // delta of rows r and r + 1, which are those of the lane's query, or of each row's.
 template <bool BF16, int MOD, typename F>
 __device__ __forceinline__ void weights_and_gradients(f32x16_t& s, f32x16_t& dp, const Args& a, const Change& ch, int32_t apart, F at) {
-  const float c = unit_of<BF16, MOD>(a), k = (MOD & kCapped) ? 2.f * kLog2e * a.scale / a.cap : 0.f;
+  const float c = natural<BF16, MOD>() ? a.cap : unit_of<BF16, MOD>(a), last = natural<BF16, MOD>() ? kLog2e : 1.f;
   const float d = (float)apart;
 #pragma unroll
   for (int r0 = 0; r0 < 16; r0 += 2) {
@@ -530,11 +539,11 @@ __device__ __forceinline__ void weights_and_gradients(f32x16_t& s, f32x16_t& dp,
       const int r = r0 + i;
       const float more = MOD & kBiased ? fmaf(-ch.slope, fabsf(d - (float)result_row(r, 0)), -x[2 * i]) : -x[2 * i];
       if constexpr (MOD & kCapped) {
-        const float u = squash<BF16>(s[r], k);
-        s[r] = __builtin_amdgcn_exp2f(fmaf(u, c, more));
+        const float u = squash<BF16>(s[r], a.squeeze);
+        s[r] = __builtin_amdgcn_exp2f(fmaf(u, c, more) * last);
         dp[r] = s[r] * (dp[r] - x[2 * i + 1]) * steep<BF16>(u);
       } else {
-        s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, more));
+        s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, more) * last);
         dp[r] = s[r] * (dp[r] - x[2 * i + 1]);
       }
     }
@@ -987,10 +996,12 @@ __device__ __forceinline__ float dot_chunk(const uint4& x, const uint4& y, float
   return s;
 }
 
-// lse in units of log 2, less the constant of bf16's capped scores. A query all of whose scores are -infinity has no weights: NaN,
+// lse in units of log 2, less the constant of bf16's capped scores; as it is for fp32's
+// (see natural). A query all of whose scores are -infinity has no weights: NaN,
 // also against scores that are computed without the row's infinities.
 template <bool BF16, int MOD>
 __device__ __forceinline__ float scaled_lse(const Args& a, float lse) {
+  if constexpr (natural<BF16, MOD>()) return lse == -INFINITY ? NAN : lse;
   if constexpr (BF16 && (MOD & kCapped)) return lse == -INFINITY ? NAN : (lse - a.cap) * kLog2e;
   return lse == -INFINITY ? NAN : lse * kLog2e;
 }
@@ -1067,7 +1078,7 @@ __global__ __launch_bounds__(256, !BF16 ? 1 : DC == 64 ? 3 : 2) void k_backward_
   const int32_t w0 = tile * P::kRows + wv * 32;
   const int32_t query = w0 + (lane & 31);
   const uint32_t base = lds_address(lds);
-  const Change ch{prefix_of<MOD>(a, seq, len), slope_of<MOD>(a, h, kLog2e)};
+  const Change ch{prefix_of<MOD>(a, seq, len), slope_of<MOD>(a, h, natural<BF16, MOD>() ? 1.f : kLog2e)};
   const int32_t end = max(min(tile * P::kRows + P::kRows, len), ch.pre), last = max(w0 + 32, ch.pre);
   const typename P::Rows ks(a.k, start, kh, a.D), vs(a.v, start, kh, a.D);
   ks.fetch(0, len, base);
@@ -1160,7 +1171,7 @@ __global__ __launch_bounds__(64 * NS, BF16 ? 2 : 1) void k_backward_q_rows(Args 
   const int lane = threadIdx.x & 63, g = lane >> 5;
   const int split = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int32_t w0 = tile * 32, query = w0 + (lane & 31);
-  const Change ch{prefix_of<MOD>(a, seq, len), slope_of<MOD>(a, h, kLog2e)};
+  const Change ch{prefix_of<MOD>(a, seq, len), slope_of<MOD>(a, h, natural<BF16, MOD>() ? 1.f : kLog2e)};
   const int32_t splits = SPLIT ? query_splits(a, w0, ch.pre, NS) : 1;
   if (SPLIT && z >= splits) return;
   uint4 q[G::kPairs], dO[G::kPairs];
@@ -1319,7 +1330,7 @@ __device__ __forceinline__ void backward_kv_pass(bool& careful, const Args& a, i
         }
       }
     } else {
-      const Change ch{pre, slope_of<MOD>(a, h, kLog2e)};
+      const Change ch{pre, slope_of<MOD>(a, h, natural<BF16, MOD>() ? 1.f : kLog2e)};
       weights_and_gradients<BF16, MOD>(p, ds, a, ch, key - q0 - 4 * g,
                                        [&](int r) { return *(const f32x4_t*)(words + 2 * result_row(r, g)); });
     }

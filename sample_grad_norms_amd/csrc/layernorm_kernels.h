@@ -217,7 +217,7 @@ __device__ __forceinline__ void statistics(uint4 (&x)[R][NC], int32_t d, float e
   Row<BF16, NC, W>::sums(s, lds, turn);
   if constexpr (BF16) keep_packed(x);
 #pragma unroll
-  for (int r = 0; r < R; ++r) rs[r] = rsqrtf(fmaf(s[r], inv, eps));
+  for (int r = 0; r < R; ++r) rs[r] = 1.f / sqrtf(fmaf(s[r], inv, eps));
 }
 
 // W = 1: four rows' waves a work group; else one row's.

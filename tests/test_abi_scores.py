@@ -45,7 +45,7 @@ def test_checks(lib, call):
     for cap in (-1.0, -0.0001, NAN, INF, -INF, 1e-4, 1025.0, 1e30):
         assert call(lib, scores(cap=cap)) == _lib.ERR_VALUE, cap
     assert call(lib, scores(slopes=SL + 2)) == call(lib, scores(prefix=PRE + 1)) == _lib.ERR_ALIGN
-    assert call(lib, scores(), shape(scale=1e-30)) == _lib.ERR_VALUE
+    assert call(lib, scores(), shape(scale=1e-30)) == call(lib, scores(slopes=None), shape(scale=1e30)) == _lib.ERR_VALUE
     for bad in (dict(n=0), dict(d=136), dict(hkv=3), dict(s=0)):
         assert call(lib, scores(), shape(**bad)) == _lib.ERR_SIZE
     assert call(lib, scores(), shape(dtype=3)) == _lib.ERR_DTYPE
