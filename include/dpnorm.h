@@ -420,8 +420,8 @@ dpnorm_status dpnorm_attention_backward(const dpnorm_attn_shape* shape, const dp
  * and at most 2^64 with a cap; else ERR_VALUE. The gradients are those of q, k and v: the
  * backward call is given what the forward call was, and ds has the factor 1 - tanh^2. slopes and prefix must not
  * overlap outputs or ws. scores may be NULL, and all its fields 0: then the calls are
- * dpnorm_attention_forward and _backward, bit for bit, whose definitions, checks and
- * workspace hold for the rest. */
+ * dpnorm_attention_forward and _backward, bit for bit, whose definitions and checks hold
+ * for the rest. */
 typedef struct dpnorm_attn_scores {
   float cap;
   const float* slopes;
@@ -432,6 +432,8 @@ dpnorm_status dpnorm_attention_scores_forward(const dpnorm_attn_shape* shape, co
                                               const dpnorm_attn_tensor* q, const dpnorm_attn_tensor* k,
                                               const dpnorm_attn_tensor* v, const dpnorm_attn_tensor* o, float* lse,
                                               hipStream_t stream);
+dpnorm_status dpnorm_attention_scores_backward_workspace(const dpnorm_attn_shape* shape, const dpnorm_attn_scores* scores,
+                                                         size_t* bytes);
 dpnorm_status dpnorm_attention_scores_backward(const dpnorm_attn_shape* shape, const dpnorm_attn_scores* scores,
                                                const dpnorm_attn_tensor* dO, const dpnorm_attn_tensor* q,
                                                const dpnorm_attn_tensor* k, const dpnorm_attn_tensor* v,

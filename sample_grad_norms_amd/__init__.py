@@ -766,7 +766,8 @@ def attention_backward(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: to
     scores = _attn_scores(cap, slopes, prefix, shape, device)
     if N > 0 and shape.S > 0:
         nbytes = C.c_size_t(0)
-        _check(lib().dpnorm_attention_backward_workspace(shape, C.byref(nbytes)), "dpnorm_attention_backward_workspace")
+        _check(lib().dpnorm_attention_scores_backward_workspace(shape, scores, C.byref(nbytes)),
+               "dpnorm_attention_scores_backward_workspace")
         ws, wsp = _given_workspace(workspace, nbytes.value, device)
         rest = (tdo, tq, tk, tv, to, lse.data_ptr(), tdq, tdk, tdv, wsp, nbytes.value)
         if scores is None:

@@ -104,6 +104,7 @@ SIGNATURES = {
     "dpnorm_attention_backward_workspace": ([_shp, _szp], C.c_int),
     "dpnorm_attention_backward": ([_shp, _tp, _tp, _tp, _tp, _tp, _vp, _tp, _tp, _tp, _vp, _sz, _vp], C.c_int),
     "dpnorm_attention_scores_forward": ([_shp, _scp, _tp, _tp, _tp, _tp, _vp, _vp], C.c_int),
+    "dpnorm_attention_scores_backward_workspace": ([_shp, _scp, _szp], C.c_int),
     "dpnorm_attention_scores_backward": ([_shp, _scp, _tp, _tp, _tp, _tp, _tp, _vp, _tp, _tp, _tp, _vp, _sz, _vp], C.c_int),
     "dpnorm_layernorm_forward": ([_vp, _vp, _vp, C.c_int, C.c_int, _i64, _i64, _f32, _vp, _vp, _vp, _vp], C.c_int),
     "dpnorm_layernorm_backward_workspace": ([C.c_int, C.c_int, _i64, _i64, _i64, _szp], C.c_int),

@@ -140,7 +140,15 @@ int32_t key_splits(const attn::Args& a) {
   const int64_t places = 256 * (attn::OwnRows<BF16, DC, 4, 256>::kLds <= 80 * 1024 ? 2 : 1);
   const int64_t groups = key_groups(a);
   const int64_t splits = most_splits(3 * places / (4 * groups) * 2 + 1, ((int64_t)a.N + 31) / 32 * (a.Hq / a.Hkv));
-  if (splits > 1 || (BF16 && DC == 64)) return (int32_t)splits;
+  if (splits > 1) return (int32_t)splits;
+  // With a prefix every key in it has the whole sequence's queries, and those chains last
+  // longest: three work groups share them where there are up to two for each place and the
+  // chains are long (us, three against one: 4 x 2048, 16/4 heads D = 64 239 against 280,
+  // D = 128 465 against 534; 1501 + 900 + 33 + 1200 rows 174 against 223; 8 x 1024 316
+  // against 317; but 5 x 800, of 100 steps, 142 against 120, and twice as many keys 917
+  // against 904).
+  if (a.prefix && key_steps(a) > 104 && groups <= 1100) return 3;
+  if (BF16 && DC == 64) return (int32_t)splits;
   return key_steps(a) >= 256 && 4 * groups < 5 * places ? 3 : 1;
 }
 
@@ -333,13 +341,20 @@ dpnorm_status dpnorm_attention_forward(const dpnorm_attn_shape* shape, const dpn
   return dpnorm_attention_scores_forward(shape, nullptr, q, k, v, o, lse, stream);
 }
 
-dpnorm_status dpnorm_attention_backward_workspace(const dpnorm_attn_shape* shape, size_t* bytes) {
+dpnorm_status dpnorm_attention_scores_backward_workspace(const dpnorm_attn_shape* shape, const dpnorm_attn_scores* scores,
+                                                         size_t* bytes) {
   if (!bytes) return DPNORM_ERR_NULL;
-  const dpnorm_status st = check_shape(shape);
+  dpnorm_status st = check_shape(shape);
+  if (st == DPNORM_OK) st = check_scores(shape, scores);
   if (st != DPNORM_OK) return st;
   attn::Args a = attn_args(shape);
+  set_scores(a, scores);
   *bytes = backward_layout(a, shape->dtype == DPNORM_BF16, nullptr);
   return DPNORM_OK;
+}
+
+dpnorm_status dpnorm_attention_backward_workspace(const dpnorm_attn_shape* shape, size_t* bytes) {
+  return dpnorm_attention_scores_backward_workspace(shape, nullptr, bytes);
 }
 
 dpnorm_status dpnorm_attention_scores_backward(const dpnorm_attn_shape* shape, const dpnorm_attn_scores* scores,
@@ -349,8 +364,7 @@ dpnorm_status dpnorm_attention_scores_backward(const dpnorm_attn_shape* shape, c
                                                const dpnorm_attn_tensor* dk, const dpnorm_attn_tensor* dv, void* ws,
                                                size_t ws_bytes, hipStream_t stream) {
   size_t bytes = 0;
-  dpnorm_status st = dpnorm_attention_backward_workspace(shape, &bytes);
-  if (st == DPNORM_OK) st = check_scores(shape, scores);
+  dpnorm_status st = dpnorm_attention_scores_backward_workspace(shape, scores, &bytes);
   for (const dpnorm_attn_tensor* t : {dO, q, o})
     if (st == DPNORM_OK) st = check_tensor(t, shape, shape->Hq, false);
   for (const dpnorm_attn_tensor* t : {k, v})
@@ -382,8 +396,8 @@ dpnorm_status dpnorm_attention_scores_backward(const dpnorm_attn_shape* shape, c
   a.dk = tensor_of(dk, N, Hkv, e);
   a.dv = tensor_of(dv, N, Hkv, e);
   a.lse = const_cast<float*>(lse);
-  backward_layout(a, shape->dtype == DPNORM_BF16, ws);
   set_scores(a, scores);
+  backward_layout(a, shape->dtype == DPNORM_BF16, ws);
   return hip_status(with_kernels(a, shape->dtype == DPNORM_BF16, [&](auto bf16, auto columns, auto mod) {
     return run_attn_backward<decltype(bf16)::value, decltype(columns)::value, decltype(mod)::value>(a, stream);
   }));

@@ -52,6 +52,18 @@ def test_checks(lib, call):
     assert call(lib, scores(), shape(scale=-1.0)) == _lib.ERR_VALUE
 
 
+def test_workspace(lib):
+    nb, plain = C.c_size_t(0), C.c_size_t(0)
+    query = lib.dpnorm_attention_scores_backward_workspace
+    for sh in (shape(), shape(n=4096, s=2, hq=16, hkv=4), shape(dtype=_lib.F32, d=80)):
+        assert lib.dpnorm_attention_backward_workspace(C.byref(sh), C.byref(plain)) == _lib.OK
+        for sc in (None, scores(), scores(cap=0.0, slopes=None, prefix=None)):
+            assert query(C.byref(sh), C.byref(sc) if sc else None, C.byref(nb)) == _lib.OK and nb.value >= plain.value
+            assert nb.value % 256 == 0 and (nb.value == plain.value or sc.prefix)
+    assert query(C.byref(shape()), C.byref(scores()), None) == query(None, None, C.byref(nb)) == _lib.ERR_NULL
+    assert query(C.byref(shape()), C.byref(scores(cap=-1.0)), C.byref(nb)) == _lib.ERR_VALUE
+
+
 def test_outputs_on_slopes_or_prefixes(lib):
     assert forward(lib, scores(), o=SL) == forward(lib, scores(), o=PRE) == forward(lib, scores(), lse=SL) == _lib.ERR_VALUE
     assert forward(lib, scores(), lse=PRE + 4) == forward(lib, scores(), lse=Q) == _lib.ERR_VALUE
@@ -81,7 +93,8 @@ SETS = [(None, 0), ((0.0, None, None), 0), ((0.0, SL, None), 1), ((0.0, None, PR
 @standin
 @pytest.mark.parametrize("change,kernels", SETS)
 def test_the_kernels_of_a_change(lib, change, kernels):
-    """The forms are those of plain attention; the set of kernels goes by the change."""
+    """The set of kernels goes by the change; the forms are those of plain attention, but that
+    with a prefix three work groups share keys with long chains."""
     names = lib.dpnorm_fake_launched
     names.restype = C.c_char_p
     sc = None if change is None else _lib.AttnScores(*change)
@@ -91,7 +104,12 @@ def test_the_kernels_of_a_change(lib, change, kernels):
             q, k, v, o, do, dq, dk, dv = (C.byref(_lib.AttnTensor((j + 1) << 44, h * d, d))
                                           for j, h in enumerate((hq, hkv, hkv, hq, hq, hq, hkv, hkv)))
             lse, ws, nb = 10 << 44, 11 << 44, C.c_size_t(0)
-            assert lib.dpnorm_attention_backward_workspace(sh, C.byref(nb)) == _lib.OK
+            rec = C.byref(sc) if sc else None
+            assert lib.dpnorm_attention_scores_backward_workspace(sh, rec, C.byref(nb)) == _lib.OK
+            plain_bytes = C.c_size_t(0)
+            assert lib.dpnorm_attention_backward_workspace(sh, C.byref(plain_bytes)) == _lib.OK
+            groups, steps = (n // 32 + 1) * hkv, n // 32 * (hq // hkv)
+            shared = bool(sc and sc.prefix) and groups <= 1100 and steps > 104
             launched = []
             for plain in (True, False):
                 names()
@@ -99,12 +117,15 @@ def test_the_kernels_of_a_change(lib, change, kernels):
                     assert lib.dpnorm_attention_forward(sh, q, k, v, o, lse, None) == _lib.OK
                     assert lib.dpnorm_attention_backward(sh, do, q, k, v, o, lse, dq, dk, dv, ws, nb.value, None) == _lib.OK
                 else:
-                    rec = C.byref(sc) if sc else None
                     assert lib.dpnorm_attention_scores_forward(sh, rec, q, k, v, o, lse, None) == _lib.OK
                     assert lib.dpnorm_attention_scores_backward(sh, rec, do, q, k, v, o, lse, dq, dk, dv, ws, nb.value, None) == _lib.OK
                 launched.append([re.match(r"(.*)Li(\d)(EEEvNS0_4ArgsE)$", x).groups() for x in names().decode().split()])
             assert all(m == "0" for _, m, _ in launched[0]) and all(m == str(kernels) for _, m, _ in launched[1])
-            assert [a for a, _, _ in launched[0]] == [a for a, _, _ in launched[1]]
+            forms = [[a for a, _, _ in x] for x in launched]
+            if shared and "Lb1E" not in forms[0][2][-5:]:
+                assert forms[0][:2] == forms[1][:2] and forms[1][2].endswith("Li4ELb1E") and nb.value > plain_bytes.value
+            else:
+                assert forms[0] == forms[1] and nb.value == plain_bytes.value
 
 
 @standin
