@@ -779,16 +779,19 @@ def attention_backward(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: to
     return dq, dk, dv
 
 
-def _normed(x: torch.Tensor, w: Optional[torch.Tensor], b: Optional[torch.Tensor], d: int) -> int:
-    """Checks gain and bias against rows x of d columns; the type's code."""
-    code = _code(x.dtype)
+def _normed(x: torch.Tensor, w: torch.Tensor, b: Optional[torch.Tensor]) -> int:
+    """Checks rows x [..., d] and their gain and bias; the type's code."""
+    _rows_of(x, "x")
+    d, dtype = x.shape[-1], x.dtype
     for t, name in ((w, "weight"), (b, "bias")):
-        if t is not None:
-            _need(t, name, 1, x.dtype)
-            if t.shape[0] != d:
-                raise ValueError(f"{name} must have the {d} entries of a row")
-    _one_device(x.device, w, b)
-    return code
+        if t is b is None:
+            break
+        _need(t, name, 1, dtype)
+        if t.shape[0] != d:
+            raise ValueError(f"{name} must have the {d} entries of a row")
+        if t.device != x.device:
+            raise ValueError("all tensors of a call must be on one device")
+    return _code(dtype)
 
 
 def _rows_of(t: torch.Tensor, name: str, like: Optional[torch.Tensor] = None) -> None:
@@ -812,12 +815,10 @@ def layernorm_forward(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torc
     statistics float32 [...], which layernorm_backward reads; RMS norm has
     no bias and its mean is None. Sums are float32; y is rounded once.
     """
-    _rows_of(x, "x")
-    d = x.shape[-1]
     if rms and bias is not None:
         raise ValueError("RMS norm has no bias")
-    _need(weight, "weight", 1, x.dtype)
-    code = _normed(x, weight, bias, d)
+    code = _normed(x, weight, bias)
+    d = x.shape[-1]
     if out is None:
         out = torch.empty_like(x)
     else:
@@ -845,11 +846,9 @@ def layernorm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, 
     dbias, x then being [B, ..., d]; they do not change dx. Sums are float32,
     each result is rounded once, and results are reproducible bit for bit.
     """
-    _rows_of(x, "x")
+    code = _normed(x, weight, None)
     _rows_of(dy, "dy", x)
     d, device = x.shape[-1], x.device
-    _need(weight, "weight", 1, x.dtype)
-    code = _normed(x, weight, None, d)
     rms = mean is None
     bias = bias and not rms
     for t, name in ((mean, "mean"), (rstd, "rstd")):

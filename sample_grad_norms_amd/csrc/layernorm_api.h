@@ -53,12 +53,15 @@ hipError_t with_ln(dpnorm_dtype dt, dpnorm_ln_kind kind, int64_t d, F f) {
 // launch. One wave a row: a work group a CU (two gain nothing: 4 x 4096 rows of 2048
 // bf16, 46 us with 256, 50 with 512), with two rounds of rows for each wave at least;
 // four waves: two (2 x 4096 rows of 4096: 54 us with 512, 66 with 256); four rows at
-// least (1024 rows of 16384: 49 us with four, 73 with two).
+// least (1024 rows of 16384: 49 us with four, 73 with two). One work group, and one
+// launch, for up to six rounds (gradients of 183 rows of 256 fp32, six rounds: 14 us, and
+// 19 in two launches; 64 rows of 2048 bf16, eight: 22 and 19).
 int64_t ln_blocks(dpnorm_dtype dt, int64_t d, int64_t rows, int64_t others) {
   const int64_t chunks = d / (dt == DPNORM_BF16 ? 8 : 4);
-  const int64_t least = chunks <= 64 ? 64 : chunks <= 128 ? 32 : chunks <= 256 ? 16 : 4;
+  const int64_t round = chunks <= 64 ? 32 : chunks <= 128 ? 16 : chunks <= 256 ? 8 : 1;
+  if (rows <= 6 * round) return 1;
   const int64_t places = chunks > 256 && chunks <= 1024 ? 512 : 256;
-  return std::max<int64_t>(1, std::min(places / others, rows / least));
+  return std::max<int64_t>(1, std::min(places / others, rows / (chunks <= 256 ? 2 * round : 4)));
 }
 
 // Threads that share `rows` partial sums of a column (see add_rows): about four each.
