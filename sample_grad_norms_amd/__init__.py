@@ -827,7 +827,7 @@ def layernorm_forward(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torc
     rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
     mean = None if rms else torch.empty_like(rstd)
     n = rstd.numel()
-    if n * d > 0:
+    if n > 0:
         _run(x.device, "dpnorm_layernorm_forward", x.data_ptr(), weight.data_ptr(), bias.data_ptr() if bias is not None else None, code,
              int(rms), n, d, eps, out.data_ptr(), mean.data_ptr() if mean is not None else None, rstd.data_ptr())
     return out, mean, rstd

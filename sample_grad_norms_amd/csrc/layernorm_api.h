@@ -26,7 +26,7 @@ hipError_t with_row(int64_t d, F f) {
   if (chunks <= 64) return go(integral_constant<int, 1>{}, integral_constant<int, 1>{}, integral_constant<int, 4>{});
   if (chunks <= 128) return go(integral_constant<int, 2>{}, integral_constant<int, 1>{}, integral_constant<int, 2>{});
   if (chunks <= 256) return go(integral_constant<int, 4>{}, integral_constant<int, 1>{}, integral_constant<int, 1>{});
-  if (chunks <= 512) return go(integral_constant<int, 2>{}, integral_constant<int, 4>{}, integral_constant<int, 1>{});
+  if (chunks <= 512) return go(integral_constant<int, 2>{}, integral_constant<int, 4>{}, integral_constant<int, BF16 ? 2 : 1>{});
   if (chunks <= 1024) return go(integral_constant<int, 4>{}, integral_constant<int, 4>{}, integral_constant<int, 1>{});
   if (chunks <= 2048) return go(integral_constant<int, 2>{}, integral_constant<int, 16>{}, integral_constant<int, 1>{});
   if constexpr (BF16) {
@@ -49,19 +49,20 @@ hipError_t with_ln(dpnorm_dtype dt, dpnorm_ln_kind kind, int64_t d, F f) {
 }
 
 // Work groups of the summing kernels that share `rows` rows (among `others` such sets of
-// rows): as many as the GPU holds at once, since each leaves 2 d sums for the second
-// launch. One wave a row: a work group a CU (two gain nothing: 4 x 4096 rows of 2048
-// bf16, 46 us with 256, 50 with 512), with two rounds of rows for each wave at least;
-// four waves: two (2 x 4096 rows of 4096: 54 us with 512, 66 with 256); four rows at
-// least (1024 rows of 16384: 49 us with four, 73 with two). One work group, and one
-// launch, for up to six rounds (gradients of 183 rows of 256 fp32, six rounds: 14 us, and
-// 19 in two launches; 64 rows of 2048 bf16, eight: 22 and 19).
-int64_t ln_blocks(dpnorm_dtype dt, int64_t d, int64_t rows, int64_t others) {
-  const int64_t chunks = d / (dt == DPNORM_BF16 ? 8 : 4);
-  const int64_t round = chunks <= 64 ? 32 : chunks <= 128 ? 16 : chunks <= 256 ? 8 : 1;
+// rows). One a CU, since each leaves 2 d sums for the second launch (4 x 4096 rows of 2048
+// bf16: gradients 46 us with 256, 50 with 512); rows of four waves and two chunks, whose
+// registers leave room, two a CU for the gradients (2 x 4096 rows of 4096 bf16: 46 us with
+// 512, 51 with 256; norms 37 with 256, 41 with 512) and for fp32. Two rounds of rows each
+// at least (four of rows of sixteen waves: 1024 rows of 16384 49 us, 73 with two). One work
+// group, and one launch, for up to six rounds (gradients of 183 rows of 256 fp32, six
+// rounds: 14 us, and 19 in two launches; 64 rows of 2048 bf16, eight: 22 and 19).
+int64_t ln_blocks(dpnorm_dtype dt, int64_t d, int64_t rows, int64_t others, bool gradients) {
+  const bool bf16 = dt == DPNORM_BF16;
+  const int64_t chunks = d / (bf16 ? 8 : 4);
+  const int64_t round = chunks <= 64 ? 32 : chunks <= 128 ? 16 : chunks <= 256 ? 8 : chunks <= 512 ? (bf16 ? 4 : 1) : chunks <= 1024 ? 2 : 1;
   if (rows <= 6 * round) return 1;
-  const int64_t places = chunks > 256 && chunks <= 1024 ? 512 : 256;
-  return std::max<int64_t>(1, std::min(places / others, rows / (chunks <= 256 ? 2 * round : 4)));
+  const int64_t places = chunks > 256 && chunks <= 512 && (gradients || !bf16) ? 512 : 256;
+  return std::max<int64_t>(1, std::min(places / others, rows / std::max<int64_t>(2 * round, 4)));
 }
 
 // Threads that share `rows` partial sums of a column (see add_rows): about four each.
@@ -86,7 +87,7 @@ struct LnNormPlan {
 };
 LnNormPlan plan_ln_norm(dpnorm_dtype dt, int64_t B, int64_t T, int64_t d, int32_t columns) {
   LnNormPlan p;
-  p.shares = ln_blocks(dt, d, T, B);
+  p.shares = ln_blocks(dt, d, T, B, false);
   if (p.shares < 2) return p;
   const int64_t at_once = 4096 / ln_slots(p.shares);
   p.groups = (columns + at_once - 1) / at_once;
@@ -136,7 +137,7 @@ dpnorm_status dpnorm_layernorm_backward_workspace(dpnorm_dtype dt, dpnorm_ln_kin
   if (!bytes) return DPNORM_ERR_NULL;
   const dpnorm_status st = check_ln(dt, kind, B, T, d);
   if (st != DPNORM_OK) return st;
-  const int64_t blocks = ln_blocks(dt, d, B * T, 1);
+  const int64_t blocks = ln_blocks(dt, d, B * T, 1, true);
   *bytes = blocks > 1 ? align_up((size_t)blocks * 2 * d * 4) : 0;
   return DPNORM_OK;
 }
@@ -169,12 +170,13 @@ dpnorm_status dpnorm_layernorm_backward(const void* dy, const void* x, const voi
   a.dx = (char*)dx;
   a.dw = (char*)dw;
   a.db = (char*)db;
-  a.blocks = (int32_t)ln_blocks(dt, d, B * T, 1);
+  a.blocks = (int32_t)ln_blocks(dt, d, B * T, 1, true);
   a.part = a.blocks > 1 ? (float*)ws : nullptr;
   hipError_t he = with_ln(dt, kind, d, [&](auto bf16, auto rms, auto nc, auto wv, auto r) {
-    constexpr int W = decltype(wv)::value;
-    ln::k_backward<decltype(bf16)::value, decltype(rms)::value, decltype(nc)::value, W, decltype(r)::value>
-        <<<(uint32_t)a.blocks, 64 * ln::kSumWaves<W>, 0, stream>>>(a);
+    constexpr bool BF16 = decltype(bf16)::value;
+    constexpr int NC = decltype(nc)::value, W = decltype(wv)::value;
+    ln::k_backward<BF16, decltype(rms)::value, NC, W, decltype(r)::value>
+        <<<(uint32_t)a.blocks, 64 * ln::kSumWaves<BF16, NC, W>, 0, stream>>>(a);
     return hipGetLastError();
   });
   if (he == hipSuccess && a.part && (dw || db)) {
@@ -221,9 +223,10 @@ dpnorm_status dpnorm_layernorm_norm(const void* x, const void* G, dpnorm_dtype d
   a.arrived = (uint32_t*)((char*)ws + p.off_arrived);
   a.parts = (double*)((char*)ws + p.off_parts);
   hipError_t he = with_ln(dt, kind, d, [&](auto bf16, auto rms, auto nc, auto wv, auto r) {
-    constexpr int W = decltype(wv)::value;
-    ln::k_norm<decltype(bf16)::value, decltype(rms)::value, decltype(nc)::value, W, decltype(r)::value>
-        <<<grid_of(B * p.shares), 64 * ln::kSumWaves<W>, 0, stream>>>(a);
+    constexpr bool BF16 = decltype(bf16)::value;
+    constexpr int NC = decltype(nc)::value, W = decltype(wv)::value;
+    ln::k_norm<BF16, decltype(rms)::value, NC, W, decltype(r)::value>
+        <<<grid_of(B * p.shares), 64 * ln::kSumWaves<BF16, NC, W>, 0, stream>>>(a);
     return hipGetLastError();
   });
   if (he == hipSuccess && p.shares > 1) {

@@ -118,8 +118,8 @@ template <bool BF16, int NC, int W>
 struct Row {
   static constexpr int kN = Chunk<BF16>::kN, kLanes = 64 * W;
   static constexpr int kColumns = kLanes * NC * kN;   // at most
-  // Sums over the W waves of a row. `turn` alternates, so that one barrier is enough:
-  // what a call reads is written again two calls later.
+  // Sums over the W waves of a row (lds: 4 W R floats of these waves). `turn` alternates, so
+  // that one barrier is enough: what a call reads is written again two calls later.
   template <int M>
   static __device__ __forceinline__ void sums(float (&v)[M], float* lds, int& turn) {
     wave_sums(v);
@@ -128,7 +128,7 @@ struct Row {
       turn ^= 1;
       if ((threadIdx.x & 63) == 0)
 #pragma unroll
-        for (int m = 0; m < M; ++m) at[(threadIdx.x >> 6) * M + m] = v[m];
+        for (int m = 0; m < M; ++m) at[(threadIdx.x >> 6) % W * M + m] = v[m];
       __syncthreads();
 #pragma unroll
       for (int m = 0; m < M; ++m) {
@@ -270,30 +270,44 @@ __global__ __launch_bounds__(kForwardThreads<W>) void k_forward(Args a) {
   }
 }
 
-// Column sums of a block: out(column, sum) for every column below d.
-template <bool BF16, int NC, int W, int WAVES, typename F>
+// Rows of a round of a work group of the summing kernels, whose column sums it leaves as
+// one: 8 of one wave, 2 of four (one of up to 2048 fp32 columns: gradients of 4 x 2048
+// rows 39 us, 41 with two; but 8192 bf16 columns 60 us with one, 49 with two), one of sixteen.
+template <bool BF16, int NC, int W>
+constexpr int kSumRows = W == 1 ? 8 : W == 4 && (BF16 || NC > 2) ? 2 : 1;
+template <bool BF16, int NC, int W>
+constexpr int kSumWaves = W * kSumRows<BF16, NC, W>;
+template <bool BF16, int NC, int W, int R>
+constexpr int kSumLds = kSumRows<BF16, NC, W> > 1 && kSumRows<BF16, NC, W> * Row<BF16, NC, W>::kColumns > 4 * kSumWaves<BF16, NC, W> * R
+                            ? kSumRows<BF16, NC, W> * Row<BF16, NC, W>::kColumns
+                            : 4 * kSumWaves<BF16, NC, W> * R;
+
+// Column sums of a work group: out(column, sum) for every column below d.
+template <bool BF16, int NC, int W, typename F>
 __device__ __forceinline__ void block_columns(const float (&acc)[NC][Chunk<BF16>::kN], int32_t d, float* lds, F out) {
   using C = Chunk<BF16>;
-  if constexpr (W == 1) {
-    constexpr int kColumns = Row<BF16, NC, 1>::kColumns;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  constexpr int kRows = kSumRows<BF16, NC, W>;
+  const int lane = threadIdx.x % (64 * W), mine = threadIdx.x / (64 * W);
+  if constexpr (kRows > 1) {
+    constexpr int kColumns = Row<BF16, NC, W>::kColumns;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < NC; ++i)
 #pragma unroll
       for (int e = 0; e < C::kN; e += 4)
-        *(f32x4_t*)(lds + wave * kColumns + (lane + 64 * i) * C::kN + e) = f32x4_t{acc[i][e], acc[i][e + 1], acc[i][e + 2], acc[i][e + 3]};
+        *(f32x4_t*)(lds + mine * kColumns + (lane + 64 * W * i) * C::kN + e) =
+            f32x4_t{acc[i][e], acc[i][e + 1], acc[i][e + 2], acc[i][e + 3]};
     __syncthreads();
-    for (int32_t j = threadIdx.x; j < d; j += 64 * WAVES) {
+    for (int32_t j = threadIdx.x; j < d; j += 64 * kSumWaves<BF16, NC, W>) {
       float s = lds[j];
 #pragma unroll
-      for (int v = 1; v < WAVES; ++v) s += lds[v * kColumns + j];
+      for (int v = 1; v < kRows; ++v) s += lds[v * kColumns + j];
       out(j, s);
     }
   } else {
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      const int32_t j = (threadIdx.x + 64 * W * i) * C::kN;
+      const int32_t j = (lane + 64 * W * i) * C::kN;
       if (j >= d) continue;
 #pragma unroll
       for (int e = 0; e < C::kN; ++e) out(j + e, acc[i][e]);
@@ -301,31 +315,26 @@ __device__ __forceinline__ void block_columns(const float (&acc)[NC][Chunk<BF16>
   }
 }
 
-// Waves of a work group that sums columns: 8 rows' waves, or those of one row.
-template <int W>
-constexpr int kSumWaves = W == 1 ? 8 : W;
-template <bool BF16, int NC, int W, int R>
-constexpr int kSumLds = W == 1 ? kSumWaves<W> * Row<BF16, NC, W>::kColumns : 4 * W * R;
-
 template <bool BF16, bool RMS, int NC, int W, int R>
-__global__ __launch_bounds__(64 * kSumWaves<W>) void k_backward(Args a) {
+__global__ __launch_bounds__((64 * kSumWaves<BF16, NC, W>)) void k_backward(Args a) {
   using C = Chunk<BF16>;
   __shared__ __align__(16) float lds[kSumLds<BF16, NC, W, R>];
   int turn = 0;
-  const int lane = W == 1 ? threadIdx.x & 63 : threadIdx.x;
-  const int32_t wave = W == 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
-  constexpr int32_t kStep = (W == 1 ? kSumWaves<W> : 1) * R;
-  // the wave's rows: the blocks' rounds in turn, so that those of one time lie together
-  const int64_t first = (int64_t)blockIdx.x * kStep + wave * R, step = (int64_t)a.blocks * kStep;
+  const int lane = threadIdx.x % (64 * W);
+  const int32_t mine = __builtin_amdgcn_readfirstlane(threadIdx.x / (64 * W));
+  constexpr int32_t kStep = kSumRows<BF16, NC, W> * R;
+  float* own = lds + mine * 4 * W * R;
+  // the blocks' rounds in turn, so that rows of one time lie together
+  const int64_t first = (int64_t)blockIdx.x * kStep, step = (int64_t)a.blocks * kStep;
   const int32_t end = a.N;
   uint4 w[1][NC];
   float aw[NC][C::kN] = {}, ab[NC][C::kN] = {};
   load_rows<BF16, NC, W, 1>(a.w, 0, 1, a.d, lane, w);
-  for (int64_t at = first; at < end; at += step) {
+  for (int64_t at = first; at < end; at += step) {   // (all waves: they meet at the sums)
+    const int64_t row = at + mine * R;
     uint4 x[R][NC], dy[R][NC];
-    load_rows<BF16, NC, W, R>(a.dy, at, end, a.d, lane, dy);
-    load_rows<BF16, NC, W, R>(a.x, at, end, a.d, lane, x);
-    const int32_t row = (int32_t)at;
+    load_rows<BF16, NC, W, R>(a.dy, row, end, a.d, lane, dy);
+    load_rows<BF16, NC, W, R>(a.x, row, end, a.d, lane, x);
     if constexpr (BF16) keep_packed(w);
     float mu[R], rs[R], cf[R], s[2 * R];
 #pragma unroll
@@ -362,7 +371,7 @@ __global__ __launch_bounds__(64 * kSumWaves<W>) void k_backward(Args a) {
         if constexpr (!RMS) asm volatile("" : "+v"(ab[i][e]));
       }
     }
-    Row<BF16, NC, W>::sums(s, lds, turn);
+    Row<BF16, NC, W>::sums(s, own, turn);
     if constexpr (BF16) {
       keep_packed(x);
       keep_packed(dy);
@@ -388,14 +397,14 @@ __global__ __launch_bounds__(64 * kSumWaves<W>) void k_backward(Args a) {
     }
   }
   if (!a.dw && !a.db) return;
-  float* mine = a.part ? a.part + (int64_t)blockIdx.x * 2 * a.d : nullptr;
-  block_columns<BF16, NC, W, kSumWaves<W>>(aw, a.d, lds, [&](int32_t j, float v) {
-    if (mine) mine[j] = v;
+  float* part = a.part ? a.part + (int64_t)blockIdx.x * 2 * a.d : nullptr;
+  block_columns<BF16, NC, W>(aw, a.d, lds, [&](int32_t j, float v) {
+    if (part) part[j] = v;
     else if (a.dw) store_one<BF16>(a.dw, j, v);
   });
   if constexpr (!RMS)
-    block_columns<BF16, NC, W, kSumWaves<W>>(ab, a.d, lds, [&](int32_t j, float v) {
-      if (mine) mine[a.d + j] = v;
+    block_columns<BF16, NC, W>(ab, a.d, lds, [&](int32_t j, float v) {
+      if (part) part[a.d + j] = v;
       else if (a.db) store_one<BF16>(a.db, j, v);
     });
 }
@@ -444,27 +453,28 @@ __device__ __forceinline__ void store_norm(const Args& a, int64_t i, double t) {
 // them), and where a work group has them all the norm. The statistics are taken again
 // from the rows, which are read anyway.
 template <bool BF16, bool RMS, int NC, int W, int R>
-__global__ __launch_bounds__(64 * kSumWaves<W>) void k_norm(Args a) {
+__global__ __launch_bounds__((64 * kSumWaves<BF16, NC, W>)) void k_norm(Args a) {
   using C = Chunk<BF16>;
   __shared__ __align__(16) float lds[kSumLds<BF16, NC, W, R>];
-  __shared__ double total[kSumWaves<W>];
+  __shared__ double total[kSumWaves<BF16, NC, W>];
   int turn = 0;
-  const int lane = W == 1 ? threadIdx.x & 63 : threadIdx.x;
-  const int32_t wave = W == 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
-  constexpr int32_t kStep = (W == 1 ? kSumWaves<W> : 1) * R;
+  const int lane = threadIdx.x % (64 * W);
+  const int32_t mine = __builtin_amdgcn_readfirstlane(threadIdx.x / (64 * W));
+  constexpr int32_t kStep = kSumRows<BF16, NC, W> * R;
+  float* own = lds + mine * 4 * W * R;
   const int64_t item = blockIdx.x + (int64_t)blockIdx.y * gridDim.x, i = item / a.blocks;
   const int32_t share = (int32_t)(item - i * a.blocks);
   if (i * a.T >= a.N) return;
-  const int64_t first = i * a.T + (int64_t)share * kStep + wave * R, step = (int64_t)a.blocks * kStep;
+  const int64_t first = i * a.T + (int64_t)share * kStep, step = (int64_t)a.blocks * kStep;
   const int32_t end = (int32_t)((i + 1) * a.T);
   float aw[NC][C::kN] = {}, ab[NC][C::kN] = {};
   for (int64_t at = first; at < end; at += step) {
+    const int64_t row = at + mine * R;
     uint4 x[R][NC], dy[R][NC];
-    load_rows<BF16, NC, W, R>(a.x, at, end, a.d, lane, x);
-    load_rows<BF16, NC, W, R>(a.dy, at, end, a.d, lane, dy);
-    const int32_t row = (int32_t)at;
+    load_rows<BF16, NC, W, R>(a.x, row, end, a.d, lane, x);
+    load_rows<BF16, NC, W, R>(a.dy, row, end, a.d, lane, dy);
     float mu[R], rs[R];
-    statistics<BF16, RMS, NC, W, R>(x, a.d, a.eps, a.inv, lane, lds, turn, mu, rs);
+    statistics<BF16, RMS, NC, W, R>(x, a.d, a.eps, a.inv, lane, own, turn, mu, rs);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       if (row + r >= end) break;
@@ -482,23 +492,23 @@ __global__ __launch_bounds__(64 * kSumWaves<W>) void k_norm(Args a) {
     }
   }
   if (a.blocks > 1) {
-    float* mine = a.part + item * 2 * a.d;
+    float* part = a.part + item * 2 * a.d;
     if (share == 0 && threadIdx.x == 0) a.arrived[i] = 0;   // (of the second launch)
-    block_columns<BF16, NC, W, kSumWaves<W>>(aw, a.d, lds, [&](int32_t j, float v) { mine[j] = v; });
-    if constexpr (!RMS) block_columns<BF16, NC, W, kSumWaves<W>>(ab, a.d, lds, [&](int32_t j, float v) { mine[a.d + j] = v; });
+    block_columns<BF16, NC, W>(aw, a.d, lds, [&](int32_t j, float v) { part[j] = v; });
+    if constexpr (!RMS) block_columns<BF16, NC, W>(ab, a.d, lds, [&](int32_t j, float v) { part[a.d + j] = v; });
     return;
   }
   double s = 0.0;
-  if (a.first == 0) block_columns<BF16, NC, W, kSumWaves<W>>(aw, a.d, lds, [&](int32_t, float v) { s += (double)v * v; });
+  if (a.first == 0) block_columns<BF16, NC, W>(aw, a.d, lds, [&](int32_t, float v) { s += (double)v * v; });
   if constexpr (!RMS)
-    if (a.first + a.columns > a.d) block_columns<BF16, NC, W, kSumWaves<W>>(ab, a.d, lds, [&](int32_t, float v) { s += (double)v * v; });
+    if (a.first + a.columns > a.d) block_columns<BF16, NC, W>(ab, a.d, lds, [&](int32_t, float v) { s += (double)v * v; });
   s = wave_sum(s);
   if ((threadIdx.x & 63) == 0) total[threadIdx.x >> 6] = s;
   __syncthreads();
   if (threadIdx.x != 0) return;
   double t = 0.0;
 #pragma unroll
-  for (int v = 0; v < kSumWaves<W>; ++v) t += total[v];
+  for (int v = 0; v < kSumWaves<BF16, NC, W>; ++v) t += total[v];
   store_norm(a, i, t);
 }
 

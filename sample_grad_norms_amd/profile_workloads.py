@@ -19,10 +19,17 @@ NAME is one of:
   dpsgd_step_library  the same with the library's attention
   dpsgd_step_tokens   the same from token ids, with the library's embedding table
                       (32768 rows, trained) and attention
+  dpsgd_step_norms    dpsgd_step_library with the library's layer norms, trained, and
+                      attention scores capped by a tanh and biased by distance
   embedding           lookup, order, per-sample norm and table gradient, B=4, T=4096,
                       d=2048, 131072 rows, ids by a vocabulary's frequencies, bf16
   attention           causal attention and its gradients, B=4, T=2048, 32 heads over
                       8, head width 64, bf16
+  attention_capped, attention_biased, attention_prefix
+                      the same with scores capped at 50, with a bias by distance, and
+                      with a prefix of two fifths of each sample
+  layernorm           layer norm's forward pass, gradients and per-sample norms, B=4,
+                      T=4096, d=2048, bf16
 --calib-copy first runs one 1 GiB device-to-device copy, the reference the
 counter summaries scale FETCH_SIZE and WRITE_SIZE by. --time (for runs without
 the profiler) prints the wall time of a call, after three that are not timed, and
@@ -40,8 +47,8 @@ if ROOT not in sys.path:
     sys.path.insert(0, ROOT)
 
 NAMES = ("long_context_hutch", "long_context_exact", "hutchpp", "single_layer", "single_layer_gram", "shared_stack",
-         "sign_stack", "lora_routed", "dpsgd_step", "dpsgd_step_library", "dpsgd_step_tokens",
-         "embedding", "attention")
+         "sign_stack", "lora_routed", "dpsgd_step", "dpsgd_step_library", "dpsgd_step_tokens", "dpsgd_step_norms",
+         "embedding", "attention", "attention_capped", "attention_biased", "attention_prefix", "layernorm")
 
 
 def main() -> None:
@@ -86,6 +93,8 @@ def main() -> None:
             shape.update(vocab_in=32768, embed_scale=45.0)
         if a.name != "dpsgd_step":
             shape.update(ops="library")
+        if a.name == "dpsgd_step_norms":
+            shape.update(norm="layer", cap=50.0, distance=True)
         model = lb.build(90, device=dev, dtype=torch.bfloat16, **shape)
         x, y = lb.batch(91, 4, 2048, shape["dim"], shape["vocab"], device=dev, dtype=torch.bfloat16)
         if a.name == "dpsgd_step_tokens":
@@ -114,14 +123,28 @@ def main() -> None:
             order = dp.embed_order(tok, 131072)
             dp.embed_norm(order, G)
             dp.embed_grad(order, G, weights=c)
-    elif a.name == "attention":
+    elif a.name == "layernorm":
+        g = torch.Generator().manual_seed(95)
+        x, G = (torch.randn(4, 4096, 2048, generator=g).to(dev, torch.bfloat16) for _ in range(2))
+        w, b = (torch.randn(2048, generator=g).to(dev, torch.bfloat16) for _ in range(2))
+        c = torch.full((4,), 0.5, device=dev)
+
+        def fn():
+            _, mean, rstd = dp.layernorm_forward(x, w, b)
+            dp.layernorm_backward(G, x, w, mean, rstd, weights=c)
+            dp.layernorm_norm(x, G)
+    elif a.name.startswith("attention"):
         g = torch.Generator().manual_seed(94)
         q, do = (torch.randn(8192, 32, 64, generator=g).to(dev, torch.bfloat16) for _ in range(2))
         k, v = (torch.randn(8192, 8, 64, generator=g).to(dev, torch.bfloat16) for _ in range(2))
 
+        how = {"attention": {}, "attention_capped": dict(cap=50.0),
+               "attention_biased": dict(slopes=torch.exp2(-8.0 * torch.arange(1, 33) / 32).to(dev)),
+               "attention_prefix": dict(prefix=torch.full((4,), 819, dtype=torch.int32, device=dev))}[a.name]
+
         def fn():
-            o, lse = dp.attention_forward(q, k, v, sequences=4)
-            dp.attention_backward(do, q, k, v, o, lse, sequences=4)
+            o, lse = dp.attention_forward(q, k, v, sequences=4, **how)
+            dp.attention_backward(do, q, k, v, o, lse, sequences=4, **how)
     else:
         pr = workloads.config2(device=dev)
         fn = (lambda: dp.exact(pr.A, pr.G, route="gram")) if a.name.endswith("gram") else (lambda: dp.hutch(pr.A, pr.G, pr.P))
