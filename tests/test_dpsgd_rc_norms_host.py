@@ -208,3 +208,18 @@ def test_the_stack_with_norms_that_train(norm):
     assert all(torch.equal(p, plain[n]) for n, p in model.named_parameters() if n in plain)
     with pytest.raises(ValueError, match="norm"):
         lb.LlamaStack(layers=1, dim=32, heads=2, kv_heads=1, hidden=64, vocab=16, norm="other")
+
+
+@pytest.mark.parametrize("C", [1e9, 1.0])
+def test_a_bias_whose_gradient_cancels(C):
+    """What a sample's rows have in common is taken off behind the norm (as a softmax takes it
+    off its keys): the bias's gradient is zero up to rounding, which is no error."""
+    def centred(m, x):
+        h = m.norms[0](x)
+        return m.linears[0](h - h.mean(1, keepdim=True))
+    model, x = _Model(centred, ("layer",)), inputs()
+    params, grads = true_grads(model, x)
+    at = [j for j, p in enumerate(params) if p is model.norms[0].bias]
+    assert all(float(gs[at[0]].abs().max()) < 1e-12 for gs in grads)
+    n, c = step(model, x, C)
+    assert torch.allclose(n.double(), torch.stack([sum((g ** 2).sum() for g in gs) for gs in grads]), rtol=1e-6)
