@@ -220,7 +220,11 @@ __device__ __forceinline__ void statistics(uint4 (&x)[R][NC], int32_t d, float e
   for (int r = 0; r < R; ++r) rs[r] = 1.f / sqrtf(fmaf(s[r], inv, eps));
 }
 
-// W = 1: four rows' waves a work group; else one row's.
+// Forward. Gain and bias stay packed in registers over the rows of a work group; loads of
+// eight work groups a CU hide each other. Bound by HBM: 4 x 4096 rows of 2048 bf16 in
+// 22 us (RMS norm 21), 6.1 TB/s of what is read and written (a copy reaches 5.1: part comes
+// from the last-level cache). W = 1: four
+// rows' waves a work group; else one row's.
 template <int W>
 constexpr int kForwardThreads = W == 1 ? 256 : 64 * W;
 
@@ -315,6 +319,10 @@ __device__ __forceinline__ void block_columns(const float (&acc)[NC][Chunk<BF16>
   }
 }
 
+// Gradients. A row's two sums (g and g h) are ready together, so dx costs one reduction; dw
+// and db are summed in the registers of the lanes that hold their columns, 2 NC chunks of
+// floats, which leaves two or three waves a SIMD. Bound by HBM: 4 x 4096 rows of 2048 bf16
+// 35 to 36 us, 5.7 TB/s, and the columns 4 to 4.6 us.
 template <bool BF16, bool RMS, int NC, int W, int R>
 __global__ __launch_bounds__((64 * kSumWaves<BF16, NC, W>)) void k_backward(Args a) {
   using C = Chunk<BF16>;
@@ -451,7 +459,10 @@ __device__ __forceinline__ void store_norm(const Args& a, int64_t i, double t) {
 
 // Column sums of G h and of G over a sample's rows (the y-th of a.blocks shares of
 // them), and where a work group has them all the norm. The statistics are taken again
-// from the rows, which are read anyway.
+// from the rows, which are read anyway: two reductions, one behind the other, between the
+// loads and the sums. Bound by HBM and that latency: 4 x 4096 rows of 2048 bf16 23 to 26 us,
+// 5.2 to 5.7 TB/s, and the columns 5 to 5.6 us; 256 samples of 64 rows 27 us a call. (The
+// next rows loaded ahead: 34.1 us a call against 33.7.)
 template <bool BF16, bool RMS, int NC, int W, int R>
 __global__ __launch_bounds__((64 * kSumWaves<BF16, NC, W>)) void k_norm(Args a) {
   using C = Chunk<BF16>;
