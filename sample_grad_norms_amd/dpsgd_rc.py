@@ -156,16 +156,16 @@ class RandomizedClipping:
                              f"unclipped: {shared}")
         covered |= covered_tables
         self.norms: List[LayerNorm] = [m for m in model.modules() if isinstance(m, LayerNorm)]
-        covered_norms = {id(p) for m in self.norms for p in m.parameters(recurse=False)}
+        covered_norms = {id(p) for m in self.norms for p in self._gain_and_bias(m)}
         shared = [f"{name}.{pname}" if name else pname for name, mod in model.named_modules()
-                  if not isinstance(mod, LayerNorm)
-                  for pname, p in mod.named_parameters(recurse=False) if id(p) in covered_norms]
+                  for pname, p in mod.named_parameters(recurse=False, remove_duplicate=False)
+                  if id(p) in covered_norms and not (isinstance(mod, LayerNorm) and pname in ("weight", "bias"))]
         if shared:
             raise ValueError(f"weights of norm layers shared with modules that are not norm layers would go partly "
                              f"unclipped: {shared}")
         held: Dict[int, Tuple] = {}
         for m in self.norms:
-            for p in m.parameters(recurse=False):
+            for p in self._gain_and_bias(m):
                 if held.setdefault(id(p), self._norm_key(m)) != self._norm_key(m):
                     raise ValueError("norm layers that share a gain or a bias must share both, and their eps and kind")
         covered |= covered_norms
@@ -188,7 +188,7 @@ class RandomizedClipping:
             if t.weight.requires_grad and all(p is not t.weight for p in self.params):
                 self.params.append(t.weight)
         for m in self.norms:
-            self.params += [p for p in m.parameters(recurse=False) if p.requires_grad and all(p is not q for q in self.params)]
+            self.params += [p for p in self._gain_and_bias(m) if p.requires_grad and all(p is not q for q in self.params)]
         self._names = {id(p): name for name, p in model.named_parameters()}
         self._capturing = False
         self._rec: Dict[nn.Module, List[Tuple[torch.Tensor, torch.Tensor]]] = {}
@@ -203,6 +203,11 @@ class RandomizedClipping:
         # per norm layer of the last step: (module, inputs, output gradients)
         self._norm_recs: List[Tuple[LayerNorm, torch.Tensor, torch.Tensor]] = []
         self._handles = [m.register_forward_hook(self._hook) for m in [*self.modules, *self.tables, *self.norms]]
+
+    @staticmethod
+    def _gain_and_bias(m: LayerNorm) -> List[nn.Parameter]:
+        """What of a norm layer has a norm here (a subclass may hold more)."""
+        return [p for p in (m.weight, m.bias) if p is not None]
 
     @staticmethod
     def _norm_key(m: LayerNorm) -> Tuple:
@@ -422,7 +427,7 @@ class RandomizedClipping:
         if pending is not None:
             before = [w.grad.detach().float().clone() if w.grad is not None else None
                       for w in [w for w, _, _ in pending] + [w for w, _, _, _ in tables]
-                      + [p for m, _, _ in norms for p in m.parameters(recurse=False)]]
+                      + [p for m, _, _ in norms for p in self._gain_and_bias(m)]]
         (c.detach().to(losses.dtype) * losses).sum().backward()
         if pending is not None:
             self._check_coverage(pending, before, c)
@@ -439,7 +444,7 @@ class RandomizedClipping:
                 # of a norm of keys): a few half steps of the type, of terms of any sign
                 dy = G.float() * cw.view(-1, 1, 1)
                 h = (x.float() if mean is None else x.float() - mean[..., None]) * rstd[..., None]
-                for w, want, terms in zip(m.parameters(recurse=False), wants, (dy * h, dy)):
+                for w, want, terms in zip(self._gain_and_bias(m), wants, (dy * h, dy)):
                     g0 = next(held)
                     if w.requires_grad:
                         self._check_gradient(w, want.float(), g0, 4 * torch.finfo(G.dtype).eps * float(torch.linalg.vector_norm(terms)))

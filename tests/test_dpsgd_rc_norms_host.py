@@ -223,3 +223,28 @@ def test_a_bias_whose_gradient_cancels(C):
     assert all(float(gs[at[0]].abs().max()) < 1e-12 for gs in grads)
     n, c = step(model, x, C)
     assert torch.allclose(n.double(), torch.stack([sum((g ** 2).sum() for g in gs) for gs in grads]), rtol=1e-6)
+
+
+def test_a_parameter_that_a_subclass_adds_is_refused():
+    """Only gain and bias have a norm here; anything else a norm layer holds would go unclipped."""
+    from sample_grad_norms_amd.dpsgd_rc import RandomizedClipping
+    from sample_grad_norms_amd.layers import RMSNorm
+
+    class Gated(RMSNorm):
+        def __init__(self, dim, **kw):
+            super().__init__(dim, **kw)
+            self.gate = nn.Parameter(torch.ones(dim, dtype=torch.float64))
+
+        def forward(self, x):
+            return super().forward(x) * self.gate
+
+    model = nn.Sequential(Gated(D, dtype=torch.float64))
+    with pytest.raises(ValueError, match="gate"):
+        RandomizedClipping(model, C=1.0, noise_multiplier=0.0)
+    model[0].gate.requires_grad_(False)
+    assert [p is model[0].weight for p in RandomizedClipping(model, C=1.0, noise_multiplier=0.0).params] == [True]
+    for held in (0, 1):   # its own gain, or another layer's, in the added place
+        model = nn.Sequential(Gated(D, dtype=torch.float64), RMSNorm(D, dtype=torch.float64))
+        model[0].gate = model[held].weight
+        with pytest.raises(ValueError, match="gate"):
+            RandomizedClipping(model, C=1.0, noise_multiplier=0.0)
