@@ -216,7 +216,12 @@ class RandomizedClipping:
     # -- capture ---------------------------------------------------------
     def _hook(self, module, inputs, output):
         if self._capturing and any(p.requires_grad for p in module.parameters(recurse=False)):
-            self._rec.setdefault(module, []).append((inputs[0], output))
+            x = inputs[0]
+            if isinstance(module, LayerNorm):
+                # rows that the layer has to copy may be changed behind it without autograd's
+                # objection: recorded as they are now
+                x = _aligned(x.detach())
+            self._rec.setdefault(module, []).append((x, output))
 
     class _Capture:
         def __init__(self, rc):

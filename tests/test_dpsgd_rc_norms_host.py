@@ -248,3 +248,19 @@ def test_a_parameter_that_a_subclass_adds_is_refused():
         model[0].gate = model[held].weight
         with pytest.raises(ValueError, match="gate"):
             RandomizedClipping(model, C=1.0, noise_multiplier=0.0)
+
+
+def test_an_input_changed_in_place_later_is_recorded_as_it_was():
+    """A layer copies rows that it cannot read as they lie, so autograd lets them be changed
+    behind it; the recording is of what the layer saw."""
+    def use(m, x):
+        h = (x * 1.0).transpose(0, 1).contiguous().transpose(0, 1)   # [B][T][D], not contiguous
+        y = m.norms[0](h)
+        h.add_(inputs(seed=9))
+        return y
+
+    model, x = _Model(use, kinds=("layer",)), inputs()
+    params, per = true_grads(model, x)
+    n, _ = step(model, x, verify_coverage=False)
+    want = torch.stack([sum((g ** 2).sum() for g in gs) for gs in per])
+    assert torch.allclose(n.double(), want, rtol=1e-6, atol=0)   # (n is kept in float32: a few halves of 2^-23)
