@@ -784,7 +784,7 @@ def _normed(x: torch.Tensor, w: torch.Tensor, b: Optional[torch.Tensor]) -> int:
     _rows_of(x, "x")
     d, dtype = x.shape[-1], x.dtype
     for t, name in ((w, "weight"), (b, "bias")):
-        if t is b is None:
+        if t is None and name == "bias":
             break
         _need(t, name, 1, dtype)
         if t.shape[0] != d:

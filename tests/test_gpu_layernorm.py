@@ -332,3 +332,13 @@ def test_refusals():
         dp.layernorm_norm(x, x, rms=True, gain=False)
     with pytest.raises(ValueError):
         dp.layernorm_norm(x, x, accumulate=True)
+
+
+def test_a_missing_weight_is_refused():
+    import sample_grad_norms_amd as dp
+    x = torch.zeros(2, 5, 64, device=dev(), dtype=BF16)
+    rstd = torch.ones(2, 5, device=dev())
+    with pytest.raises(TypeError, match="weight"):
+        dp.layernorm_forward(x, None)
+    with pytest.raises(TypeError, match="weight"):
+        dp.layernorm_backward(x, x, None, None, rstd)
