@@ -524,6 +524,17 @@ __device__ __forceinline__ constexpr bool natural() {
   return !BF16 && (MOD & kCapped);
 }
 
+// The running maximum in powers of two. Scores of -infinity alone (of a split, of the steps so
+// far) have weights of zero. A steep bias may lower a step's maximum so far that its product's
+// rounding, half a step of 2^8 from 2^31 on, is an infinite weight, which no later maximum
+// takes away: held at -2^31 there, where weights are zeros or right (a row's own key, without
+// bias, comes later or is in another split).
+template <int MOD>
+__device__ __forceinline__ float in_powers(float m, float c) {
+  if (m == -INFINITY) return 0.f;
+  return MOD & kBiased ? fmaxf(m * c, -0x1p31f) : m * c;
+}
+
 // In the backward pass: the products s of a column become the weights p = exp2(score - lse),
 // and dp their gradients p (dp - delta) times the derivative of the change. at(r): lse and
 // delta of rows r and r + 1, which are those of the lane's query, or of each row's.
@@ -713,8 +724,7 @@ __device__ __forceinline__ void forward_pass(bool careful, const Args& a, const 
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[t][r] *= f;
     }
-    // (queries that see none of a split's keys so far: every weight 0)
-    const float mc = m == -INFINITY ? 0.f : m * c;
+    const float mc = in_powers<MOD>(m, c);
     float sum[2] = {0.f, 0.f};
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
@@ -843,7 +853,7 @@ __device__ __forceinline__ float raise_maximum(f32x16_t (&s)[2], const Args& a, 
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[t][r] *= f;
   }
-  return m == -INFINITY ? 0.f : m * c;   // (scores of -infinity alone have weights of zero)
+  return in_powers<MOD>(m, c);
 }
 
 // The step's scores become its weights, and join the sum.

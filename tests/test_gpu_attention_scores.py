@@ -354,3 +354,53 @@ def test_refusals():
     for bad in (dict(slopes=slopes.double()), dict(prefix=prefix.long())):
         with pytest.raises(TypeError):
             dp.attention_backward(do, q, k, v, o, lse, **bad)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("kw", [{}, dict(cap=5.0), dict(prefix=True), dict(cap=5.0, prefix=True)])
+@pytest.mark.parametrize("Hq,lengths", [(4, [1, 70, 33]), (64, [1, 1500, 1333])])   # by rows, by tiles
+def test_the_steepest_slopes(dtype, kw, Hq, lengths):
+    """Slopes of 2^32: every row has itself alone, since the next weight is exp(-2^32) = 0. So
+    o = v, and lse is the row's own score; dp - delta is 0 but for roundings.
+
+    Bounds (h the type's half step): in the forward pass the weight is exp(s - m) of one s, off by
+    4 (|s| + 2) u, and o by 2 h more (the weight's rounding, the result's). The backward pass's
+    weight exp(s - lse) is off by what its s and the forward pass's are off besides: each by
+    (D + 8) u of sum |q k| scale and by 8 u of the cap, |s| and 1. dp and delta are
+    sums of D products of the same numbers but for o's rounding error, so their difference
+    is at most (2 D + 8) u + 4 (20 + 2) u + 2 h (1 + h) of sum |do v|, of which 2 h is there only
+    where the forward pass did not return v bit for bit, as is asserted for bfloat16; that times
+    scale, |k| and 1.1 (roundings of ds and of the result) bounds dq, and likewise dk. |lse| < 20:
+    scores are cap at most, or 64 products of normals over 8.
+    """
+    import sample_grad_norms_amd as dp
+    Hkv, D = 2, 64
+    q, k, v, do = make(sum(lengths), Hq, Hkv, D, dtype, 51)
+    kw = dict(kw)
+    if kw.pop("prefix", False):
+        kw["prefix"] = torch.tensor([1, 40, 0], dtype=torch.int32, device=dev())
+    kw.update(slopes=torch.full((Hq,), 2.0 ** 32, device=dev()), cu_seqlens=torch.tensor(offsets(lengths), dtype=torch.int32, device=dev()))
+    on = [x.to(dev()) for x in (q, k, v, do)]
+    o, lse = dp.attention_forward(*on[:3], **kw)
+    got = [x.double().cpu() for x in dp.attention_backward(on[3], *on[:3], o, lse, **kw)]
+    q, k, v, do = (x.double() for x in (q, k, v, do))
+    kr, vr = (x.repeat_interleave(Hq // Hkv, dim=1) for x in (k, v))
+    h, scale = half(dtype), D ** -0.5
+    s = (q * kr).sum(-1) * scale
+    size = (q * kr).abs().sum(-1) * scale
+    if "cap" in kw:
+        s = kw["cap"] * torch.tanh(s / kw["cap"])
+    assert float(s.abs().max()) < 20
+    err = (lse.double().cpu().t() - s).abs()
+    assert bool((err <= (D + 8) * U * size + 8 * U * (kw.get("cap", 0.0) + s.abs() + 1)).all())
+    if dtype == BF16:
+        assert torch.equal(o.double().cpu(), vr)
+    loose = 4 * 22 * U + (0 if dtype == BF16 else 2 * h)
+    assert bool(((o.double().cpu() - vr).abs() <= (4 * 22 * U + 2 * h) * vr.abs()).all())
+    ds = ((2 * D + 8) * U + loose) * (do * vr).abs().sum(-1, keepdim=True) * scale * 1.1
+    group = lambda x: x.view(x.shape[0], Hkv, Hq // Hkv, D).sum(2)
+    assert all(bool(torch.isfinite(x).all()) for x in got)
+    assert bool((got[0].abs() <= ds * kr.abs()).all())
+    assert bool((got[1].abs() <= group(ds * q.abs())).all())
+    again = 2 * U * ((D + 8) * float(size.max()) + 8 * (kw.get("cap", 0.0) + 20 + 1))
+    assert bool(((got[2] - group(do)).abs() <= (4 * 22 * U + again + 2 * h) * group(do.abs())).all())
