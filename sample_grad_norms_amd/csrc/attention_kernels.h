@@ -914,7 +914,7 @@ __device__ __forceinline__ void tile_again(const Args& a, const Change& ch, int3
 // work groups a CU so that one wave's run beside another's. B = 4, T = 2048, 32/8 heads,
 // D = 64: 104 us, 661 TF/s of the pairs u <= t; 12289 + 777 + 4100 rows, 16/2 heads,
 // D = 128: 713 us, 968 TF/s. A large bf16 matrix product reaches 1241 TF/s. Changed scores:
-// a bias is two more operations a score, 115 to 124 us at D = 64; a cap an exponential, a
+// a bias is two more operations a score, 115 to 127 us at D = 64; a cap an exponential, a
 // reciprocal and two operations, which with the softmax's own come to about 120 us of issue
 // slots there by count, 147 to 161 us in all (186 with the tanh written out and two waves a
 // SIMD instead of three).
@@ -1377,7 +1377,7 @@ __device__ __forceinline__ void backward_kv_pass(bool& careful, const Args& a, i
 // allow two waves a SIMD; the LDS is busy half of the time, and a fifth fewer reads (lse
 // and delta as a column of the first products) gained 2 % at D = 64 and lost 5 % at 128.
 // B = 4, T = 2048, 32/8 heads, D = 64: 229 us, 600 TF/s; 16/4 heads, D = 128: 285 us
-// (where 12 registers spill). Biased and capped 215 to 241 and 245 to 281 us at D = 64;
+// (where 12 registers spill). Biased and capped 215 to 242 and 245 to 281 us at D = 64;
 // 4 x 2048 rows, 16/4 heads, D = 128: 273 plain, 285 biased and capped.
 // SPLIT: a few such work groups share
 // the steps, as many as leave each wave kSteps of them, and the last to arrive adds
