@@ -146,8 +146,11 @@ int32_t key_splits(const attn::Args& a) {
   // chains are long (us, three against one: 4 x 2048, 16/4 heads D = 64 239 against 280,
   // D = 128 465 against 534; 1501 + 900 + 33 + 1200 rows 174 against 223; 8 x 1024 316
   // against 317; but 5 x 800, of 100 steps, 142 against 120, and twice as many keys 917
-  // against 904).
-  if (a.prefix && key_steps(a) > 104 && groups <= 1100) return 3;
+  // against 904). Two where chains are of 512 steps and more (two against three: 2 x 4096,
+  // 16/4 heads D = 64 405 against 412, 96 593 against 607, 128 793 against 835; 8192, 16/2
+  // heads 801 against 842, 1166 against 1219, 1571 against 1725; but 2 x 2048, 16/4 heads, of
+  // 256 steps, 158 against 147, 221 against 203, 279 against 261).
+  if (a.prefix && key_steps(a) > 104 && groups <= 1100) return key_steps(a) < 512 ? 3 : 2;
   if (BF16 && DC == 64) return (int32_t)splits;
   return key_steps(a) >= 256 && 4 * groups < 5 * places ? 3 : 1;
 }
