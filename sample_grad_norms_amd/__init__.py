@@ -711,7 +711,8 @@ def attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seql
 
     Scores may be changed before the softmax (dpnorm_attention_scores_forward):
     cap, in 1/1024 .. 1024, makes a score s cap * tanh(s / cap); slopes, float32
-    [Hq] on the GPU, of up to 2^32, adds -slopes[h] * |t - u| for row t and key u;
+    [Hq] on the GPU, of up to 2^32, adds -slopes[h] * |t - u| for row t and key u (below zero,
+    |slope| (length - 1) is at most 2^14; a steeper one gives NaN in its head and sequence);
     prefix, int32 [S] on the GPU, lets every row of a sequence see its first prefix[s] rows.
     """
     if (out is None) != (lse is None):

@@ -145,12 +145,25 @@ template <int MOD>
 __device__ __forceinline__ int32_t prefix_of(const Args& a, int32_t seq, int32_t len) {
   return MOD != kPlain && a.prefix ? min(max(uniform_load(a.prefix, seq), 0), len) : 0;
 }
-// The head's slope times f.
+// The steepest negative slope of a sequence of len rows, as bits. Such a slope raises far keys,
+// and a row's scores, their maximum and log-sum-exp with them: each of some ten roundings of
+// 2^-24 relative is an error of that much times |slope| distance in the exponent of a weight,
+// and past a bias of 2^31 the maximum's rounding alone is an infinite weight. Up to 2^14 a
+// weight is off by less than 2^-8 (0.18 % at most in 90 rows worked out with these
+// roundings), the half step to which bf16 weights are rounded. (Slopes above zero lower all
+// keys but the row's own: no limit.)
 template <int MOD>
-__device__ __forceinline__ float slope_of(const Args& a, int32_t h, float f) {
+__device__ __forceinline__ uint32_t steepest_of(int32_t len) {
+  if constexpr (!(MOD & kBiased)) return 0;
+  return __builtin_amdgcn_readfirstlane(__float_as_uint(len > 1 ? -0x1p14f / (float)(len - 1) : -0x1.fffffep127f));
+}
+// The head's slope times f; NaN for a steeper one, so that the head's results of the sequence
+// are. (Bits of negative numbers are in the order of their magnitudes, behind all positive ones.)
+template <int MOD>
+__device__ __forceinline__ float slope_of(const Args& a, int32_t h, uint32_t steepest, float f) {
   if constexpr (!(MOD & kBiased)) return 0.f;
-  const float m = uniform_load(a.slopes ? a.slopes : (const float*)a.k.p, a.slopes ? h : 0);   // (no branch in the loop)
-  return a.slopes ? m * f : 0.f;
+  const uint32_t m = uniform_load(a.slopes ? (const uint32_t*)a.slopes : (const uint32_t*)a.k.p, a.slopes ? h : 0);   // (no branch in the loop)
+  return a.slopes ? __uint_as_float(m > steepest ? 0x7fc00000u : m) * f : 0.f;
 }
 // What the softmax works on, times this, is in powers of two: products, or of capped
 // scores u (see squash), of which bf16's u is tanh / 2 up to a constant.
@@ -528,7 +541,8 @@ __device__ __forceinline__ constexpr bool natural() {
 // far) have weights of zero. A steep bias may lower a step's maximum so far that its product's
 // rounding, half a step of 2^8 from 2^31 on, is an infinite weight, which no later maximum
 // takes away: held at -2^31 there, where weights are zeros or right (a row's own key, without
-// bias, comes later or is in another split).
+// bias, comes later or is in another split). Maxima far above zero are of slopes that
+// steepest_of does not let pass.
 template <int MOD>
 __device__ __forceinline__ float in_powers(float m, float c) {
   if (m == -INFINITY) return 0.f;
@@ -769,7 +783,7 @@ __global__ __launch_bounds__(64 * NS, BF16 ? 2 : 1) void k_forward_rows(Args a) 
   uint4 q[G::kPairs];
   load_operand<BF16, DC>(a.q, start, h, w0, len, a.D, q);
   const float c = unit_of<BF16, MOD>(a);
-  const Change ch{prefix_of<MOD>(a, seq, len), slope_of<MOD>(a, h, bias_unit<BF16, MOD>(a))};
+  const Change ch{prefix_of<MOD>(a, seq, len), slope_of<MOD>(a, h, steepest_of<MOD>(len), bias_unit<BF16, MOD>(a))};
   float m, l;
   f32x16_t acc[G::kTiles];
   unsigned char* mine = lds + split * P::kBuffers * P::kBuf;
@@ -939,7 +953,7 @@ __global__ __launch_bounds__(256, !BF16 ? 1 : MOD != kPlain && DC == 64 ? 3 : 2)
   const int32_t w0 = tile * P::kRows + wv * 32;   // the wave's first query
   const int32_t query = w0 + (lane & 31);
   const uint32_t base = lds_address(lds);
-  const Change ch{prefix_of<MOD>(a, seq, len), slope_of<MOD>(a, h, bias_unit<BF16, MOD>(a))};
+  const Change ch{prefix_of<MOD>(a, seq, len), slope_of<MOD>(a, h, steepest_of<MOD>(len), bias_unit<BF16, MOD>(a))};
   const int32_t end = max(min(tile * P::kRows + P::kRows, len), ch.pre);   // keys that some query of the block sees
   const int32_t last = max(w0 + 32, ch.pre);                               // and of the wave
   const typename P::Rows ks(a.k, start, kh, a.D), vs(a.v, start, kh, a.D);
@@ -1093,7 +1107,7 @@ __global__ __launch_bounds__(256, !BF16 ? 1 : DC == 64 ? 3 : 2) void k_backward_
   const int32_t w0 = tile * P::kRows + wv * 32;
   const int32_t query = w0 + (lane & 31);
   const uint32_t base = lds_address(lds);
-  const Change ch{prefix_of<MOD>(a, seq, len), slope_of<MOD>(a, h, natural<BF16, MOD>() ? 1.f : kLog2e)};
+  const Change ch{prefix_of<MOD>(a, seq, len), slope_of<MOD>(a, h, steepest_of<MOD>(len), natural<BF16, MOD>() ? 1.f : kLog2e)};
   const int32_t end = max(min(tile * P::kRows + P::kRows, len), ch.pre), last = max(w0 + 32, ch.pre);
   const typename P::Rows ks(a.k, start, kh, a.D), vs(a.v, start, kh, a.D);
   ks.fetch(0, len, base);
@@ -1186,7 +1200,7 @@ __global__ __launch_bounds__(64 * NS, BF16 ? 2 : 1) void k_backward_q_rows(Args 
   const int lane = threadIdx.x & 63, g = lane >> 5;
   const int split = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int32_t w0 = tile * 32, query = w0 + (lane & 31);
-  const Change ch{prefix_of<MOD>(a, seq, len), slope_of<MOD>(a, h, natural<BF16, MOD>() ? 1.f : kLog2e)};
+  const Change ch{prefix_of<MOD>(a, seq, len), slope_of<MOD>(a, h, steepest_of<MOD>(len), natural<BF16, MOD>() ? 1.f : kLog2e)};
   const int32_t splits = SPLIT ? query_splits(a, w0, ch.pre, NS) : 1;
   if (SPLIT && z >= splits) return;
   uint4 q[G::kPairs], dO[G::kPairs];
@@ -1289,7 +1303,7 @@ __device__ __forceinline__ void backward_kv_pass(bool& careful, const Args& a, i
   using G = Geo<BF16, DC>;
   const int lane = threadIdx.x & 63, g = lane >> 5;
   const int32_t key = w0 + (lane & 31), rep = a.Hq / a.Hkv;
-  const uint32_t base = lds_address(mine);
+  const uint32_t base = lds_address(mine), steepest = steepest_of<MOD>(len);
   // 32 queries from q0 on of head h, with their lse and delta: zeros past the end
   // (whose weights are set to zero: against an infinity in a key they would be NaN)
   typename P::Rows qs(a.q, start, kh * rep, a.D), os(a.dO, start, kh * rep, a.D);
@@ -1345,7 +1359,7 @@ __device__ __forceinline__ void backward_kv_pass(bool& careful, const Args& a, i
         }
       }
     } else {
-      const Change ch{pre, slope_of<MOD>(a, h, natural<BF16, MOD>() ? 1.f : kLog2e)};
+      const Change ch{pre, slope_of<MOD>(a, h, steepest, natural<BF16, MOD>() ? 1.f : kLog2e)};
       weights_and_gradients<BF16, MOD>(p, ds, a, ch, key - q0 - 4 * g,
                                        [&](int r) { return *(const f32x4_t*)(words + 2 * result_row(r, g)); });
     }

@@ -149,7 +149,8 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: Opt
 
     cap: a score s becomes cap * tanh(s / cap). slopes, float32 [Hq]: row t and
     key u get a bias of -slopes[h] * |t - u|; it is fixed, and refused if it
-    requires a gradient. prefix, int32, one for each sequence: every row of a
+    requires a gradient (a slope below zero is at most 2^14 / (length - 1) steep; a
+    steeper one gives NaN). prefix, int32, one for each sequence: every row of a
     sequence sees its first prefix rows.
     """
     if slopes is not None and slopes.requires_grad:
