@@ -357,14 +357,16 @@ __global__ __launch_bounds__((64 * kSumWaves<BF16, NC, W>)) void k_backward(Args
     for (int i = 0; i < NC; ++i) {
       typename C::Floats wf;
       widen<BF16>(w[0][i], wf);
+      const bool in = (lane + 64 * W * i) * C::kN < a.d;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         typename C::Floats f, g;
         widen<BF16>(x[r][i], f);
         widen<BF16>(dy[r][i], g);
+        const float m = in ? mu[r] : 0.f;   // (0 times an h of infinity past d would be NaN in the row's sums)
 #pragma unroll
         for (int e = 0; e < C::kN; ++e) {
-          const float h = (RMS ? f[e] : f[e] - mu[r]) * rs[r];
+          const float h = (RMS ? f[e] : f[e] - m) * rs[r];
           const float gw = g[e] * wf[e], gc = g[e] * cf[r];
           if constexpr (!RMS) s[2 * r] += gw;
           s[2 * r + 1] = fmaf(gw, h, s[2 * r + 1]);
