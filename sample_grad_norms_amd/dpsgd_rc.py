@@ -115,7 +115,7 @@ class RandomizedClipping:
     sample, look like the positions of B samples of length B, which only the
     check can tell apart; without it they are refused ([B][1] is not). A norm
     layer's input is [B, ..., d], and [B, d] is taken with the check alone. Norm layers that share a gain or a bias share
-    both, and their eps and kind.
+    both, and their eps and kind; a layer's gain and bias are two parameters.
     """
 
     def __init__(self, model: nn.Module, C: float, noise_multiplier: float, k: int = 32,
@@ -165,6 +165,9 @@ class RandomizedClipping:
                              f"unclipped: {shared}")
         held: Dict[int, Tuple] = {}
         for m in self.norms:
+            if m.bias is m.weight and m.weight.requires_grad:
+                # (one gradient, of which the two norms are not parts)
+                raise ValueError("a norm layer's gain and bias must not be one parameter")
             for p in self._gain_and_bias(m):
                 if held.setdefault(id(p), self._norm_key(m)) != self._norm_key(m):
                     raise ValueError("norm layers that share a gain or a bias must share both, and their eps and kind")
@@ -188,7 +191,9 @@ class RandomizedClipping:
             if t.weight.requires_grad and all(p is not t.weight for p in self.params):
                 self.params.append(t.weight)
         for m in self.norms:
-            self.params += [p for p in self._gain_and_bias(m) if p.requires_grad and all(p is not q for q in self.params)]
+            for p in self._gain_and_bias(m):
+                if p.requires_grad and all(p is not q for q in self.params):
+                    self.params.append(p)
         self._names = {id(p): name for name, p in model.named_parameters()}
         self._capturing = False
         self._rec: Dict[nn.Module, List[Tuple[torch.Tensor, torch.Tensor]]] = {}
