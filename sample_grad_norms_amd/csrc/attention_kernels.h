@@ -538,15 +538,15 @@ __device__ __forceinline__ constexpr bool natural() {
 }
 
 // The running maximum in powers of two. Scores of -infinity alone (of a split, of the steps so
-// far) have weights of zero. A steep bias may lower a step's maximum so far that its product's
+// far) have weights of zero. A steep slope may lower a step's maximum so far that its product's
 // rounding, half a step of 2^8 from 2^31 on, is an infinite weight, which no later maximum
 // takes away: held at -2^31 there, where weights are zeros or right (a row's own key, without
-// bias, comes later or is in another split). Maxima far above zero are of slopes that
-// steepest_of does not let pass.
+// bias, comes later or is in another split). Without a slope above zero a maximum there is the
+// products' own, as in plain attention; those far above zero steepest_of does not let pass.
 template <int MOD>
-__device__ __forceinline__ float in_powers(float m, float c) {
+__device__ __forceinline__ float in_powers(const Change& ch, float m, float c) {
   if (m == -INFINITY) return 0.f;
-  return MOD & kBiased ? fmaxf(m * c, -0x1p31f) : m * c;
+  return MOD & kBiased ? fmaxf(m * c, ch.slope > 0.f ? -0x1p31f : -INFINITY) : m * c;
 }
 
 // In the backward pass: the products s of a column become the weights p = exp2(score - lse),
@@ -738,7 +738,7 @@ __device__ __forceinline__ void forward_pass(bool careful, const Args& a, const 
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[t][r] *= f;
     }
-    const float mc = in_powers<MOD>(m, c);
+    const float mc = in_powers<MOD>(ch, m, c);
     float sum[2] = {0.f, 0.f};
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
@@ -867,7 +867,7 @@ __device__ __forceinline__ float raise_maximum(f32x16_t (&s)[2], const Args& a, 
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[t][r] *= f;
   }
-  return in_powers<MOD>(m, c);
+  return in_powers<MOD>(ch, m, c);
 }
 
 // The step's scores become its weights, and join the sum.
