@@ -532,6 +532,8 @@ __device__ __forceinline__ float bias_unit(const Args& a) {
 
 // Capped scores in fp32 are differences from lse before they are in powers of two: a factor
 // on an lse of some tens, the cap's size, would round by more than the rest of the weight.
+// (Other scores in fp32 take the factor on lse first: 2^-24 of |lse|, as the products' own
+// errors are of |s|.)
 template <bool BF16, int MOD>
 __device__ __forceinline__ constexpr bool natural() {
   return !BF16 && (MOD & kCapped);
