@@ -150,7 +150,8 @@ int32_t key_splits(const attn::Args& a) {
   // against 120, 4 x 800 124 against 116, and twice as many keys 917 against 904). The host
   // does not see how many rows a prefix has: of 90 % three win the same (5 x 900 255 against
   // 299), of 5 % they win or lose little where lengths differ (1501 + .. 167 against 185) and
-  // lose where they do not (5 x 900 172 against 156, 8 x 480 174 against 162). Two where chains are of 512 steps and more (two against three: 2 x 4096,
+  // lose where they do not (5 x 900 172 against 156, 8 x 480 174 against 162). Two where
+  // chains are of 512 steps and more (two against three: 2 x 4096,
   // 16/4 heads D = 64 405 against 412, 96 593 against 607, 128 793 against 835; 8192, 16/2
   // heads 801 against 842, 1166 against 1219, 1571 against 1725; but 2 x 2048, 16/4 heads, of
   // 256 steps, 158 against 147, 221 against 203, 279 against 261).
