@@ -421,9 +421,10 @@ dpnorm_status dpnorm_attention_backward(const dpnorm_attn_shape* shape, const dp
  * sequence's length less 1 is at most 2^14, where a weight is off by less than 2^-8
  * relative (in proportion below). A steeper one makes all results of its head in that
  * sequence NaN (o, lse, dq, and dk and dv of its key head). prefix: device int32 [S].
- * cap is 0 or in 1/1024 .. 1024; scale is at least 2^-64 with slopes and at most 2^64 with a cap; else ERR_VALUE. The gradients are those of q, k and v: the
- * backward call is given what the forward call was, and ds has the factor 1 - tanh^2.
- * slopes and prefix must not overlap outputs or ws. scores may be NULL, and all its fields 0: then the calls are
+ * cap is 0 or in 1/1024 .. 1024; scale is at least 2^-64 with slopes and at most 2^64 with
+ * a cap; else ERR_VALUE. The gradients are those of q, k and v: the backward call is given
+ * what the forward call was, and ds has the factor 1 - tanh^2. slopes and prefix must not
+ * overlap outputs or ws. scores may be NULL, and all its fields 0: then the calls are
  * dpnorm_attention_forward and _backward, bit for bit, whose definitions and checks hold
  * for the rest. */
 typedef struct dpnorm_attn_scores {
